@@ -7,11 +7,12 @@ been built (``python -m combine_top_router_amd.build``).  There is no fallback p
 from . import lib
 from .lib import *  # noqa: F401,F403
 
-__all__ = list(lib.__all__) + ["MoeLayer"]
+_CLASSES = ("MoeLayer", "MoeNorm", "BalanceLoss", "Orthogonalizer")
+__all__ = list(lib.__all__) + list(_CLASSES)
 
 
 def __getattr__(name):
-    if name == "MoeLayer":
-        from .layer import MoeLayer
-        return MoeLayer
+    if name in _CLASSES:
+        from . import layer
+        return getattr(layer, name)
     raise AttributeError(name)

@@ -703,4 +703,132 @@ int moe_route_topk_bwd(const moe_shape* shape, const float* logits, const int32_
       launch_route_bwd(*shape, logits, topk_idx, topk_w, d_topk_w, d_logits, (hipStream_t)stream), __func__);
 }
 
+// ---- balance loss, norm, orthogonalised update ----
+int moe_balance_scratch_bytes(const moe_shape* shape, size_t* scratch_bytes) {
+  REQUIRE(scratch_bytes);
+  int rc = check_shape(shape);
+  if (rc) return rc;
+  const size_t W = (size_t)balance_parts(shape->T, shape->E), E = (size_t)shape->E;
+  *scratch_bytes = align_up(W * E * 4) + align_up(W * (E + 1) * 4);
+  return MOE_OK;
+}
+
+int moe_balance_fwd(const moe_shape* shape, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                    float coef, float* loss, int32_t* counts, float* prob, void* scratch, void* stream) {
+  int rc = check_shape(shape);
+  if (rc) return rc;
+  const moe_shape& s = *shape;
+  if (!isfinite(coef)) return fail(MOE_EINVAL, "coef is not finite");
+  REQUIRE(loss);
+  REQUIRE(counts);
+  REQUIRE(prob);
+  REQUIRE_WS(scratch);
+  if (s.T > 0) {
+    REQUIRE(logits);
+    REQUIRE(topk_idx);
+  }
+  const size_t off = align_up((size_t)balance_parts(s.T, s.E) * s.E * 4);
+  return hip_status(launch_balance_fwd(s, logits, topk_idx, mask, coef, loss, counts, prob, at<float>(scratch, 0),
+                                       at<int32_t>(scratch, off), (hipStream_t)stream),
+                    __func__);
+}
+
+int moe_balance_bwd(const moe_shape* shape, const float* logits, const int32_t* counts, const uint8_t* mask,
+                    float coef, const float* d_loss, const float* d_logits_in, float* d_logits, void* stream) {
+  int rc = check_shape(shape);
+  if (rc) return rc;
+  if (!isfinite(coef)) return fail(MOE_EINVAL, "coef is not finite");
+  if (shape->T == 0) return MOE_OK;
+  REQUIRE(logits);
+  REQUIRE(counts);
+  REQUIRE(d_logits);
+  if (d_logits == logits) return fail(MOE_EINVAL, "%s: d_logits is logits", __func__);
+  return hip_status(
+      launch_balance_bwd(*shape, logits, counts, mask, coef, d_loss, d_logits_in, d_logits, (hipStream_t)stream),
+      __func__);
+}
+
+static int check_norm(const moe_norm_shape* s) {
+  if (!s) return fail(MOE_EINVAL, "shape is NULL");
+  if (s->T < 0) return fail(MOE_EINVAL, "T = %d < 0", s->T);
+  if (s->H < 1 || s->H > (1 << 20)) return fail(MOE_EINVAL, "H = %d outside 1..2^20", s->H);
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) return fail(MOE_EINVAL, "dtype = %d", s->dtype);
+  if (s->kind != MOE_NORM_LAYER && s->kind != MOE_NORM_RMS) return fail(MOE_EINVAL, "kind = %d", s->kind);
+  if (!isfinite(s->eps) || s->eps < 0.f) return fail(MOE_EINVAL, "eps = %g must be finite and >= 0", (double)s->eps);
+  return MOE_OK;
+}
+
+int moe_norm_scratch_bytes(const moe_norm_shape* shape, size_t* scratch_bytes) {
+  REQUIRE(scratch_bytes);
+  int rc = check_norm(shape);
+  if (rc) return rc;
+  *scratch_bytes = align_up((size_t)norm_parts(*shape) * shape->H * 4 * 2 + 1);
+  return MOE_OK;
+}
+
+int moe_norm_fwd(const moe_norm_shape* shape, const void* x, const void* res, const void* w, const void* b,
+                 void* sum, void* y, float* mean, float* rstd, void* stream) {
+  int rc = check_norm(shape);
+  if (rc) return rc;
+  if ((res == nullptr) != (sum == nullptr)) return fail(MOE_EINVAL, "res and sum must both be given or both be NULL");
+  if (shape->T == 0) return MOE_OK;
+  REQUIRE(x);
+  REQUIRE(w);
+  REQUIRE(y);
+  REQUIRE(rstd);
+  if (shape->kind == MOE_NORM_LAYER) REQUIRE(mean);
+  if (y == sum) return fail(MOE_EINVAL, "%s: y is sum", __func__);
+  return hip_status(launch_norm_fwd(*shape, x, res, w, b, sum, y, mean, rstd, (hipStream_t)stream), __func__);
+}
+
+int moe_norm_bwd(const moe_norm_shape* shape, const void* dy, const void* s, const void* w, const float* mean,
+                 const float* rstd, const void* ds_in, void* dx, void* dw, void* db, void* scratch, void* stream) {
+  int rc = check_norm(shape);
+  if (rc) return rc;
+  REQUIRE(dw);
+  REQUIRE_WS(scratch);
+  if (shape->T > 0) {
+    REQUIRE(dy);
+    REQUIRE(s);
+    REQUIRE(w);
+    REQUIRE(rstd);
+    REQUIRE(dx);
+    if (shape->kind == MOE_NORM_LAYER) REQUIRE(mean);
+    if (dx == dy || dx == s) return fail(MOE_EINVAL, "%s: dx may be neither dy nor s", __func__);
+  }
+  return hip_status(launch_norm_bwd(*shape, dy, s, w, mean, rstd, ds_in, dx, dw, db, at<float>(scratch, 0),
+                                    (hipStream_t)stream),
+                    __func__);
+}
+
+static int check_orth(const moe_orth_shape* s) {
+  if (!s) return fail(MOE_EINVAL, "shape is NULL");
+  if (s->n < 0 || s->n > 65535) return fail(MOE_EINVAL, "n = %d outside 0..65535", s->n);
+  if (s->rows < 1 || s->cols < 1 || s->rows > 16384 || s->cols > 16384)
+    return fail(MOE_EINVAL, "rows = %d and cols = %d must lie in 1..16384", s->rows, s->cols);
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) return fail(MOE_EINVAL, "dtype = %d", s->dtype);
+  if (s->steps < 1 || s->steps > 6) return fail(MOE_EINVAL, "steps = %d outside 1..6", s->steps);
+  return MOE_OK;
+}
+
+int moe_orth_scratch_bytes(const moe_orth_shape* shape, size_t* scratch_bytes) {
+  REQUIRE(scratch_bytes);
+  int rc = check_orth(shape);
+  if (rc) return rc;
+  *scratch_bytes = align_up(orth_scratch_bytes(*shape) + 1);
+  return MOE_OK;
+}
+
+int moe_orthogonalize(const moe_orth_shape* shape, const void* g, void* o, float scale, void* scratch, void* stream) {
+  int rc = check_orth(shape);
+  if (rc) return rc;
+  if (!isfinite(scale)) return fail(MOE_EINVAL, "scale is not finite");
+  if (shape->n == 0) return MOE_OK;
+  REQUIRE(g);
+  REQUIRE(o);
+  REQUIRE_WS(scratch);
+  if (o == g && shape->dtype != MOE_BF16) return fail(MOE_EINVAL, "%s: o may be g only when g is bf16", __func__);
+  return hip_status(launch_orthogonalize(*shape, g, o, scale, scratch, (hipStream_t)stream), __func__);
+}
+
 }  // extern "C"

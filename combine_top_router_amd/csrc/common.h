@@ -132,6 +132,24 @@ hipError_t launch_router_fwd(const moe_shape& s, const bf16_t* x, const bf16_t* 
                              hipStream_t st);
 hipError_t launch_router_bwd(const moe_shape& s, const bf16_t* x, const bf16_t* w, const float* dl,
                              const bf16_t* dx_in, bf16_t* dx, bf16_t* dw, float* part, hipStream_t st);
+// load-balance loss (balance.hip): part_p [balance_parts, E], part_c [balance_parts, E + 1]
+int balance_parts(int T, int E);
+hipError_t launch_balance_fwd(const moe_shape& s, const float* logits, const int32_t* idx, const uint8_t* mask,
+                              float coef, float* loss, int32_t* counts, float* prob, float* part_p, int32_t* part_c,
+                              hipStream_t st);
+hipError_t launch_balance_bwd(const moe_shape& s, const float* logits, const int32_t* counts, const uint8_t* mask,
+                              float coef, const float* d_loss, const float* d_in, float* d_out, hipStream_t st);
+// layer / rms norm (norm.hip): part = fp32 shares of dw, then of db, [norm_parts, H] each
+int norm_parts(const moe_norm_shape& s);
+hipError_t launch_norm_fwd(const moe_norm_shape& s, const void* x, const void* res, const void* w, const void* b,
+                           void* sum, void* y, float* mean, float* rstd, hipStream_t st);
+hipError_t launch_norm_bwd(const moe_norm_shape& s, const void* dy, const void* sum, const void* w, const float* mean,
+                           const float* rstd, const void* ds_in, void* dx, void* dw, void* db, float* part,
+                           hipStream_t st);
+// orthogonalised updates (orth.hip)
+size_t orth_scratch_bytes(const moe_orth_shape& s);
+hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o, float scale, void* scratch,
+                                hipStream_t st);
 hipError_t launch_dtopk(const moe_shape& s, const float* dw_part, int nparts, const int32_t* row_of,
                         float* d_topk_w, hipStream_t st);
 

@@ -18,6 +18,150 @@ def stream_handle(stream=None) -> int:
     return s.cuda_stream
 
 
+def _device(device) -> torch.device:
+    d = torch.device(device)
+    if d.type == "cuda" and d.index is None:
+        d = torch.device("cuda", torch.cuda.current_device())
+    return d
+
+
+class _OnDevice:
+    """Checks and streams of the operators around the layer.  A call runs on `stream`, or on
+    the current stream of the operator's own device; its buffers are reused from call to
+    call, so calls of one operator on several streams have to be ordered by the caller."""
+
+    def _check(self, t, shape, dtype, name):
+        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+    def _call(self, func, *args, stream=None):
+        s = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        if torch.cuda.current_device() == self.device.index:
+            func(*args, s)
+        else:
+            with torch.cuda.device(self.device):
+                func(*args, s)
+
+
+class MoeNorm(_OnDevice):
+    """The norm in front of the layer (layer norm, or rms norm), with the residual sum before
+    it.  ``forward`` gives y, and leaves ``sum`` (with a residual), ``mean`` and ``rstd`` for
+    ``backward``, whose dx is the gradient of x and of the residual alike."""
+
+    def __init__(self, T, H, kind=L.MOE_NORM_LAYER, dtype=L.MOE_BF16, eps=1e-5, device="cuda"):
+        self.shape = L.MoeNormShape(T, H, dtype, kind, eps)
+        scratch_b = L.moe_norm_scratch_bytes(self.shape)
+        dev = self.device = _device(device)
+        dt = self.dtype = _DT[dtype]
+        self._row, self._vec = torch.Size((T, H)), torch.Size((H,))
+        self.y = torch.empty(T, H, dtype=dt, device=dev)
+        self._sum = torch.empty(T, H, dtype=dt, device=dev)
+        self.mean = torch.empty(T, dtype=torch.float32, device=dev) if kind == L.MOE_NORM_LAYER else None
+        self.rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        self.dx = torch.empty(T, H, dtype=dt, device=dev)
+        self.dw = torch.empty(H, dtype=dt, device=dev)
+        self.db = torch.empty(H, dtype=dt, device=dev)
+        self.scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
+        self.sum = None
+        self.inputs = None
+
+    def forward(self, x, w, b=None, res=None, stream=None):
+        self._check(x, self._row, self.dtype, "x")
+        self._check(w, self._vec, self.dtype, "w")
+        if b is not None:
+            self._check(b, self._vec, self.dtype, "b")
+        if res is not None:
+            self._check(res, self._row, self.dtype, "res")
+        self.sum = None if res is None else self._sum
+        self.inputs = (x if res is None else self._sum, w, b is not None)
+        self._call(L.moe_norm_fwd, self.shape, _p(x), _p(res), _p(w), _p(b), _p(self.sum), _p(self.y), _p(self.mean),
+                   _p(self.rstd), stream=stream)
+        return self.y
+
+    def backward(self, dy, ds_in=None, stream=None):
+        if self.inputs is None:
+            raise RuntimeError("backward without a forward")
+        self._check(dy, self._row, self.dtype, "dy")
+        if ds_in is not None:
+            self._check(ds_in, self._row, self.dtype, "ds_in")
+        s, w, bias = self.inputs
+        db = self.db if bias else None
+        self._call(L.moe_norm_bwd, self.shape, _p(dy), _p(s), _p(w), _p(self.mean), _p(self.rstd), _p(ds_in),
+                   _p(self.dx), _p(self.dw), _p(db), _p(self.scratch), stream=stream)
+        return {"dx": self.dx, "dw": self.dw, "db": db}
+
+
+class BalanceLoss(_OnDevice):
+    """The router's load-balance loss over all E experts.  ``forward`` gives the loss and
+    leaves ``counts`` [E + 1] (per expert, then the counted tokens) and ``prob`` [E];
+    ``backward`` gives d_logits, added to d_logits_in (in place if ``out`` is that)."""
+
+    def __init__(self, T, E, k, device="cuda"):
+        self.shape = L.MoeShape(T, 64, 64, E, k, 0, E, L.MOE_BF16, L.MOE_BWD_SAME, 1, L.MOE_FWD_SAME, 0, 0)
+        scratch_b = L.moe_balance_scratch_bytes(self.shape)
+        dev = self.device = _device(device)
+        f32 = torch.float32
+        self._logits, self._idx, self._mask = torch.Size((T, E)), torch.Size((T, k)), torch.Size((T,))
+        self.loss = torch.empty(1, dtype=f32, device=dev)
+        self.counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        self.prob = torch.empty(E, dtype=f32, device=dev)
+        self.d_logits = torch.empty(T, E, dtype=f32, device=dev)
+        self.scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
+        self.inputs = None
+
+    def forward(self, logits, topk_idx, coef, mask=None, stream=None):
+        self._check(logits, self._logits, torch.float32, "logits")
+        self._check(topk_idx, self._idx, torch.int32, "topk_idx")
+        if mask is not None:
+            self._check(mask, self._mask, torch.uint8, "mask")
+        self.inputs = (logits, mask, float(coef))
+        self._call(L.moe_balance_fwd, self.shape, _p(logits), _p(topk_idx), _p(mask), coef, _p(self.loss),
+                   _p(self.counts), _p(self.prob), _p(self.scratch), stream=stream)
+        return self.loss
+
+    def backward(self, d_loss=None, d_logits_in=None, out=None, stream=None):
+        if self.inputs is None:
+            raise RuntimeError("backward without a forward")
+        if d_loss is not None:
+            self._check(d_loss, self.loss.shape, torch.float32, "d_loss")
+        if d_logits_in is not None:
+            self._check(d_logits_in, self._logits, torch.float32, "d_logits_in")
+        if out is None:
+            out = self.d_logits
+        else:
+            self._check(out, self._logits, torch.float32, "out")
+        logits, mask, coef = self.inputs
+        self._call(L.moe_balance_bwd, self.shape, _p(logits), _p(self.counts), _p(mask), coef, _p(d_loss),
+                   _p(d_logits_in), _p(out), stream=stream)
+        return out
+
+
+class Orthogonalizer(_OnDevice):
+    """Orthogonalised updates of n weight matrices of one size (the experts' gradients, or
+    their momentum), by Newton-Schulz steps as in the Muon optimiser."""
+
+    def __init__(self, n, rows, cols, dtype=L.MOE_BF16, steps=5, device="cuda"):
+        self.shape = L.MoeOrthShape(n, rows, cols, dtype, steps)
+        scratch_b = L.moe_orth_scratch_bytes(self.shape)
+        dev = self.device = _device(device)
+        self.dtype = _DT[dtype]
+        self._size = torch.Size((n, rows, cols))
+        self.o = None
+        self.scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
+
+    def update(self, g, scale=1.0, out=None, stream=None):
+        self._check(g, self._size, self.dtype, "g")
+        if out is None:
+            if self.o is None:
+                self.o = torch.empty(self._size, dtype=torch.bfloat16, device=self.device)
+            out = self.o
+        else:
+            self._check(out, self._size, torch.bfloat16, "out")
+        self._call(L.moe_orthogonalize, self.shape, _p(g), _p(out), scale, _p(self.scratch), stream=stream)
+        return out
+
+
 class MoeLayer:
     """One GPU's share of a dropless MoE layer: experts [e_begin, e_begin + e_local) of E.
 
@@ -25,6 +169,10 @@ class MoeLayer:
     expert backward and the router backward.  ``recompute=1`` keeps nothing between the two
     (activation checkpointing: the backward recomputes the gate/up GEMM).  With ``fuse_gather`` the token rows are
     read from x through row_src inside the GEMMs instead of a gathered copy xp.
+
+    ``balance`` gives the load-balance loss of the last forward's routing; the backward then
+    adds its gradient to d_logits.  ``orthogonalize`` turns the last backward's weight
+    gradients into orthogonalised updates.  Both allocate their buffers on first use.
     """
 
     def __init__(self, T, H, I, E, k, e_begin=0, e_local=None, dtype=L.MOE_BF16, bwd=L.MOE_BWD_SAME,
@@ -57,6 +205,8 @@ class MoeLayer:
         self.d_topk_w = torch.empty(T, k, dtype=f32, device=dev)
         self.d_logits = torch.empty(T, E, dtype=f32, device=dev)
         self.inputs = None
+        self._balance, self._balanced = None, False
+        self._orth, self._updates = {}, {}
 
     def _check(self, t, shape, dtype, name):
         if t.device != self.device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
@@ -86,13 +236,48 @@ class MoeLayer:
         self._check(w_up, (s.e_local, s.H, s.I), self.dtype, "w_up")
         self._check(w_down, (s.e_local, s.I, s.H), self.dtype, "w_down")
         self.inputs = (logits, x, w_gate, w_up, w_down)
+        self._balanced = False
         self.route(logits, stream)
         self.dispatch(x, stream)
         self.experts(x, w_gate, w_up, w_down, stream)
         self.combine(stream)
         return self.y
 
-    def backward(self, dy, stream=None):
+    def balance(self, coef, mask=None, stream=None):
+        """The load-balance loss [1] of the last forward's routing, over all E experts and the
+        tokens with mask != 0 (uint8 [T]).  The per-expert counts are then in
+        ``balance_counts`` [E + 1]."""
+        if self.inputs is None:
+            raise RuntimeError("balance without a forward")
+        if self._balance is None:
+            self._balance = BalanceLoss(self.shape.T, self.shape.E, self.shape.k, device=self.device)
+        loss = self._balance.forward(self.inputs[0], self.topk_idx, coef, mask=mask, stream=stream)
+        self._balanced = True
+        return loss
+
+    @property
+    def balance_counts(self):
+        return None if self._balance is None else self._balance.counts
+
+    def orthogonalize(self, steps=5, scale=1.0, stream=None):
+        """Orthogonalised updates (bf16) of the last backward's dw_gate, dw_up and dw_down."""
+        s, code = self.shape, self.shape.dtype
+
+        def op(rows, cols):
+            key = (rows, cols, steps)
+            if key not in self._orth:
+                self._orth[key] = Orthogonalizer(s.e_local, rows, cols, code, steps, self.device)
+            return self._orth[key]
+
+        if not self._updates:
+            self._updates = {n: torch.empty(g.shape, dtype=torch.bfloat16, device=self.device)
+                             for n, g in (("gate", self.dw_gate), ("up", self.dw_up), ("down", self.dw_down))}
+        for n, g in (("gate", self.dw_gate), ("up", self.dw_up), ("down", self.dw_down)):
+            op(g.shape[1], g.shape[2]).update(g, scale, out=self._updates[n], stream=stream)
+        return dict(self._updates)
+
+    def backward(self, dy, stream=None, d_balance=None):
+        """``d_balance`` [1]: the upstream gradient of ``balance``'s loss (None: 1)."""
         s = self.shape
         self._check(dy, (s.T, s.H), self.dtype, "dy")
         logits, x, w_gate, w_up, w_down = self.inputs
@@ -102,5 +287,7 @@ class MoeLayer:
                   _p(self.dw_gate), _p(self.dw_up), _p(self.dw_down), _p(self.d_topk_w), _p(self.scratch), h)
         L.moe_route_topk_bwd(s, _p(logits), _p(self.topk_idx), _p(self.topk_w), _p(self.d_topk_w),
                              _p(self.d_logits), h)
+        if self._balanced:
+            self._balance.backward(d_balance, d_logits_in=self.d_logits, out=self.d_logits, stream=stream)
         return {"dx": self.dx, "dw_gate": self.dw_gate, "dw_up": self.dw_up, "dw_down": self.dw_down,
                 "d_topk_w": self.d_topk_w, "d_logits": self.d_logits}

@@ -9,17 +9,22 @@ import os
 __all__ = [
     "MOE_OK", "MOE_EINVAL", "MOE_EUNSUPPORTED", "MOE_EWORKSPACE", "MOE_EHIP",
     "MOE_F32", "MOE_BF16", "MOE_BWD_SAME", "MOE_BWD_MXFP8", "MOE_FWD_SAME", "MOE_FWD_MXFP8",
-    "MoeShape", "MoeError", "load", "lib_path", "EXPORTS",
+    "MOE_NORM_LAYER", "MOE_NORM_RMS",
+    "MoeShape", "MoeNormShape", "MoeOrthShape", "MoeError", "load", "lib_path", "EXPORTS",
     "moe_abi_version", "moe_last_error", "moe_workspace_bytes", "moe_route_topk",
     "moe_dispatch", "moe_dispatch_noscratch", "moe_fwd", "moe_combine", "moe_bwd", "moe_route_topk_bwd",
     "moe_mx_quantize", "moe_mx_quantize_cols", "moe_timing_enable", "moe_timing_read",
     "moe_router_fwd", "moe_router_bwd",
+    "moe_balance_scratch_bytes", "moe_balance_fwd", "moe_balance_bwd",
+    "moe_norm_scratch_bytes", "moe_norm_fwd", "moe_norm_bwd",
+    "moe_orth_scratch_bytes", "moe_orthogonalize",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4
 MOE_F32, MOE_BF16 = 0, 1
 MOE_BWD_SAME, MOE_BWD_MXFP8 = 0, 1
 MOE_FWD_SAME, MOE_FWD_MXFP8 = 0, 1
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -37,6 +42,14 @@ class MoeShape(ctypes.Structure):
         return "MoeShape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class MoeNormShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "dtype", "kind")] + [("eps", ctypes.c_float)]
+
+
+class MoeOrthShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "rows", "cols", "dtype", "steps")]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, func: str, msg: str):
         super().__init__(f"{func} failed with status {code}: {msg}")
@@ -45,6 +58,10 @@ class MoeError(RuntimeError):
 
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(MoeShape)
+_NS = ctypes.POINTER(MoeNormShape)
+_OS = ctypes.POINTER(MoeOrthShape)
+_SZ = ctypes.POINTER(ctypes.c_size_t)
+_F = ctypes.c_float
 _SIG = {
     "moe_abi_version": (ctypes.c_int, []),
     "moe_last_error": (ctypes.c_char_p, []),
@@ -61,6 +78,14 @@ _SIG = {
                                             _P, _P]),
     "moe_router_fwd": (ctypes.c_int, [_S] + [_P] * 7),
     "moe_router_bwd": (ctypes.c_int, [_S] + [_P] * 8),
+    "moe_balance_scratch_bytes": (ctypes.c_int, [_S, _SZ]),
+    "moe_balance_fwd": (ctypes.c_int, [_S, _P, _P, _P, _F] + [_P] * 5),
+    "moe_balance_bwd": (ctypes.c_int, [_S, _P, _P, _P, _F] + [_P] * 4),
+    "moe_norm_scratch_bytes": (ctypes.c_int, [_NS, _SZ]),
+    "moe_norm_fwd": (ctypes.c_int, [_NS] + [_P] * 9),
+    "moe_norm_bwd": (ctypes.c_int, [_NS] + [_P] * 11),
+    "moe_orth_scratch_bytes": (ctypes.c_int, [_OS, _SZ]),
+    "moe_orthogonalize": (ctypes.c_int, [_OS, _P, _P, _F, _P, _P]),
     "moe_timing_enable": (ctypes.c_int, [ctypes.c_int]),
     "moe_timing_read": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_char_p),
                                        ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int)]),
@@ -158,6 +183,47 @@ def moe_router_fwd(shape, x, w_r, logits, topk_idx, topk_w, scratch, stream=0):
 def moe_router_bwd(shape, x, w_r, d_logits, dx_in, dx, dw_r, scratch, stream=0):
     _check(load().moe_router_bwd(ctypes.byref(shape), x, w_r, d_logits, dx_in, dx, dw_r, scratch, stream),
            "moe_router_bwd")
+
+
+def _scratch_bytes(func, shape):
+    n = ctypes.c_size_t(0)
+    _check(getattr(load(), func)(ctypes.byref(shape), ctypes.byref(n)), func)
+    return n.value
+
+
+def moe_balance_scratch_bytes(shape: MoeShape) -> int:
+    return _scratch_bytes("moe_balance_scratch_bytes", shape)
+
+
+def moe_balance_fwd(shape, logits, topk_idx, mask, coef, loss, counts, prob, scratch, stream=0):
+    _check(load().moe_balance_fwd(ctypes.byref(shape), logits, topk_idx, mask, coef, loss, counts, prob, scratch,
+                                  stream), "moe_balance_fwd")
+
+
+def moe_balance_bwd(shape, logits, counts, mask, coef, d_loss, d_logits_in, d_logits, stream=0):
+    _check(load().moe_balance_bwd(ctypes.byref(shape), logits, counts, mask, coef, d_loss, d_logits_in, d_logits,
+                                  stream), "moe_balance_bwd")
+
+
+def moe_norm_scratch_bytes(shape: MoeNormShape) -> int:
+    return _scratch_bytes("moe_norm_scratch_bytes", shape)
+
+
+def moe_norm_fwd(shape, x, res, w, b, sum, y, mean, rstd, stream=0):
+    _check(load().moe_norm_fwd(ctypes.byref(shape), x, res, w, b, sum, y, mean, rstd, stream), "moe_norm_fwd")
+
+
+def moe_norm_bwd(shape, dy, s, w, mean, rstd, ds_in, dx, dw, db, scratch, stream=0):
+    _check(load().moe_norm_bwd(ctypes.byref(shape), dy, s, w, mean, rstd, ds_in, dx, dw, db, scratch, stream),
+           "moe_norm_bwd")
+
+
+def moe_orth_scratch_bytes(shape: MoeOrthShape) -> int:
+    return _scratch_bytes("moe_orth_scratch_bytes", shape)
+
+
+def moe_orthogonalize(shape, g, o, scale, scratch, stream=0):
+    _check(load().moe_orthogonalize(ctypes.byref(shape), g, o, scale, scratch, stream), "moe_orthogonalize")
 
 
 def moe_timing_enable(on: bool = True):

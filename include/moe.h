@@ -255,6 +255,92 @@ int moe_mx_quantize_cols(const void* x, int32_t N, const int32_t* offsets, int32
                          int32_t* poff, uint8_t* codes, uint8_t* scales, uint8_t* row_codes,
                          uint8_t* row_scales, void* stream);
 
+/* ---- around the layer in a training step: norm, balance loss, update ---- */
+
+/* Bytes of scratch of moe_balance_fwd for `shape` (T and E).  Never 0. */
+int moe_balance_scratch_bytes(const moe_shape* shape, size_t* scratch_bytes);
+
+/* Load-balance loss of the router with the per-expert counts, over all E experts and the
+ * N tokens that count: those with mask[t] != 0 (mask: uint8 [T], e.g. a padded batch), or
+ * all with mask == NULL.  With p_t = softmax(logits[t]):
+ *   counts[e] = slots (t, j) of counted tokens with topk_idx[t, j] = e (ids outside [0, E)
+ *               choose none), counts[E] = N           (int32 [E + 1])
+ *   prob[e]   = mean of p_te over the counted tokens  (fp32 [E])
+ *   loss[0]   = coef E / (k N) sum_e counts[e] prob[e]   (fp32; coef when the load is even)
+ * N = 0 gives zeros.  Logits of tokens that do not count are not read; a token whose
+ * logits are all -inf counts with p = 0.  coef must be finite.  Uses T, E and k of the
+ * shape.  Results do not change from run to run. */
+int moe_balance_fwd(const moe_shape* shape, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                    float coef, float* loss, int32_t* counts, float* prob, void* scratch, void* stream);
+
+/* Its gradient, the counts being constants (the selection is piecewise constant):
+ *   d_logits[t, j] = d_logits_in[t, j] + d_loss coef E / (k N^2) p_tj (c_j - sum_e c_e p_te)
+ * with c = counts and N = counts[E] as moe_balance_fwd wrote them, and the second term 0
+ * for tokens that do not count.  d_loss: device fp32 [1], the loss's upstream gradient;
+ * NULL is 1.  d_logits_in may be NULL (taken as 0) or equal to d_logits: what
+ * moe_route_topk_bwd wrote, so that d_logits goes on to moe_router_bwd whole. */
+int moe_balance_bwd(const moe_shape* shape, const float* logits, const int32_t* counts, const uint8_t* mask,
+                    float coef, const float* d_loss, const float* d_logits_in, float* d_logits, void* stream);
+
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+
+typedef struct {
+  int32_t T;      /* rows (tokens), >= 0 */
+  int32_t H;      /* columns, 1..2^20, any */
+  int32_t dtype;  /* moe_dtype of x, res, w, b, sum, y, dy, ds_in, dx, dw, db */
+  int32_t kind;   /* moe_norm_kind */
+  float eps;      /* finite, >= 0 */
+} moe_norm_shape;
+
+/* Bytes of scratch of moe_norm_bwd.  Never 0. */
+int moe_norm_scratch_bytes(const moe_norm_shape* shape, size_t* scratch_bytes);
+
+/* The norm in front of the layer, with the residual sum that comes before it:
+ *   s = x + res  (res == NULL: s = x), written to sum [T, H] when res is given
+ *   layer: mean = mean(s), rstd = 1 / sqrt(mean((s - mean)^2) + eps)
+ *   rms:   rstd = 1 / sqrt(mean(s^2) + eps); mean is not written and may be NULL
+ *   y = (s - mean) rstd w + b   (b may be NULL: no bias)
+ * over each row's H columns, in fp32, each output rounded once (y is the norm of the fp32
+ * sum, not of the rounded one).  mean and rstd: fp32 [T].  res and sum are given together;
+ * sum may be x or res. */
+int moe_norm_fwd(const moe_norm_shape* shape, const void* x, const void* res, const void* w, const void* b,
+                 void* sum, void* y, float* mean, float* rstd, void* stream);
+
+/* Its backward for the upstream dy [T, H], s = what was normalised (sum, or x without a
+ * residual) and the mean (NULL for rms) and rstd of the forward.  With xh = (s - mean) rstd
+ * and g = dy w:
+ *   dx = ds_in + rstd (g - mean(g) - xh mean(g xh))   (rms: without mean(g))
+ *   dw = sum_t dy xh,  db = sum_t dy   ([H])
+ * ds_in (the gradient that reaches s past the norm) may be NULL (taken as 0) or equal to
+ * dx; dx may not be dy or s.  dx is the gradient of x and of res alike.  db may be NULL.
+ * T = 0 gives dw = db = 0.  The sums over tokens run in fp32 in a fixed order.  Needs
+ * scratch. */
+int moe_norm_bwd(const moe_norm_shape* shape, const void* dy, const void* s, const void* w, const float* mean,
+                 const float* rstd, const void* ds_in, void* dx, void* dw, void* db, void* scratch, void* stream);
+
+typedef struct {
+  int32_t n;      /* matrices, 0..65535 (a layer's local experts) */
+  int32_t rows;   /* 1..16384 */
+  int32_t cols;   /* 1..16384 */
+  int32_t dtype;  /* moe_dtype of g */
+  int32_t steps;  /* Newton-Schulz steps, 1..6 (5 is usual) */
+} moe_orth_shape;
+
+/* Bytes of scratch of moe_orthogonalize (for bf16 or fp32 alike).  Never 0. */
+int moe_orth_scratch_bytes(const moe_orth_shape* shape, size_t* scratch_bytes);
+
+/* Orthogonalised update of n weight matrices (the Muon optimiser's step; e.g. the experts'
+ * dw_gate, dw_up or dw_down, or their momentum), each on its own:
+ *   X = G / (|G|_F + 1e-7), transposed if rows > cols;
+ *   steps times:  A = X X^T,  X = 3.4445 X + (-4.7750 A + 2.0315 A^2) X;
+ *   o = scale X, transposed back
+ * g: [n, rows, cols] of shape.dtype; o: [n, rows, cols] bf16, which may be g when that is
+ * bf16.  Inside, X and the products' factors are fp16 (the first iterates as a pair of
+ * fp16) and the sums fp32; the result is within about 2e-3 of its norm, besides o's
+ * rounding, for five steps.  A zero matrix gives zeros; one with a NaN or infinity gives
+ * NaN, and leaves the others alone.  scale must be finite.  Needs scratch. */
+int moe_orthogonalize(const moe_orth_shape* shape, const void* g, void* o, float scale, void* scratch, void* stream);
+
 /* Opt-in kernel timing for profilers and benchmarks (no effect on results).
  * moe_timing_enable(1) makes every kernel that this host thread launches through the
  * calls above carry two HIP events that the dispatch itself stamps at its start and end

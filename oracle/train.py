@@ -1,0 +1,113 @@
+"""The operators around the layer in a training step, in plain numpy fp64: the norm with its
+backward, the router's balance loss with its gradient, and the Newton-Schulz
+orthogonalisation of an update.  Shares no code with the HIP path."""
+from __future__ import annotations
+
+import numpy as np
+
+__all__ = ["norm_forward", "norm_backward", "balance_forward", "balance_backward", "orthogonalize",
+           "orthogonalize_rounded"]
+
+
+def norm_forward(x, res, w, b, eps, rms):
+    """(y, s, mean, rstd): s = x + res; y = (s - mean) rstd w + b, mean = 0 for rms."""
+    s = np.asarray(x, np.float64) + (0.0 if res is None else np.asarray(res, np.float64))
+    mean = np.zeros(s.shape[0]) if rms else s.mean(axis=1)
+    c = s - mean[:, None]
+    rstd = 1.0 / np.sqrt((c * c).mean(axis=1) + eps)
+    y = c * rstd[:, None] * np.asarray(w, np.float64)
+    return y + (0.0 if b is None else np.asarray(b, np.float64)), s, mean, rstd
+
+
+def norm_backward(dy, s, w, mean, rstd, ds_in, rms):
+    """(dx, dw, db) from the forward's s, mean and rstd."""
+    dy, s = np.asarray(dy, np.float64), np.asarray(s, np.float64)
+    xh = (s - mean[:, None]) * rstd[:, None]
+    g = dy * np.asarray(w, np.float64)
+    dx = g - xh * (g * xh).mean(axis=1, keepdims=True)
+    if not rms:
+        dx = dx - g.mean(axis=1, keepdims=True)
+    dx = dx * rstd[:, None]
+    if ds_in is not None:
+        dx = dx + np.asarray(ds_in, np.float64)
+    return dx, (dy * xh).sum(axis=0), dy.sum(axis=0)
+
+
+def _softmax(logits):
+    m = logits.max(axis=1, keepdims=True)
+    e = np.exp(logits - np.where(np.isneginf(m), 0.0, m))
+    z = e.sum(axis=1, keepdims=True)
+    return np.divide(e, z, out=np.zeros_like(e), where=z != 0)
+
+
+def balance_forward(logits, topk_idx, mask, coef):
+    """(loss, counts [E + 1], prob [E]) over the tokens with mask != 0 (None: all)."""
+    logits = np.asarray(logits, np.float64)
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    on = np.ones(T, bool) if mask is None else np.asarray(mask) != 0
+    n = int(on.sum())
+    counts = np.zeros(E + 1, np.int64)
+    for e in np.asarray(topk_idx)[on].reshape(-1):
+        if 0 <= e < E:
+            counts[e] += 1
+    counts[E] = n
+    if n == 0:
+        return 0.0, counts, np.zeros(E)
+    prob = _softmax(logits[on]).sum(axis=0) / n
+    return coef * E / (k * n) * float((counts[:E] * prob).sum()), counts, prob
+
+
+def balance_backward(logits, counts, k, mask, coef, d_loss, d_in):
+    logits = np.asarray(logits, np.float64)
+    T, E = logits.shape
+    d = np.zeros((T, E)) if d_in is None else np.asarray(d_in, np.float64).copy()
+    on = np.ones(T, bool) if mask is None else np.asarray(mask) != 0
+    n = int(counts[E])
+    if n > 0 and on.any():
+        c = np.asarray(counts[:E], np.float64)
+        p = _softmax(logits[on])
+        d[on] += d_loss * coef * E / (k * float(n) ** 2) * p * (c - (p * c).sum(axis=1, keepdims=True))
+    return d
+
+
+NS = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(g, steps, scale=1.0):
+    """One matrix."""
+    a, b, c = NS
+    x = np.asarray(g, np.float64)
+    x = x / (np.sqrt((x * x).sum()) + 1e-7)
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.T
+    for _ in range(steps):
+        q = x @ x.T
+        x = a * x + (b * q + c * (q @ q)) @ x
+    return scale * (x.T if tall else x)
+
+
+def orthogonalize_rounded(g, steps):
+    """The same with the iterates held in fp16: pairs hi + lo through the first three (hi in
+    the products, both in a X), A - I in place of A from the fourth step on, scales 2^15 (X)
+    and 2^14.  What this is off is what such a precision costs."""
+    def half(v, s):
+        return (v * s).astype(np.float16).astype(np.float64) / s
+
+    a, b, c = NS
+    x = np.asarray(g, np.float64)
+    x = x / (np.sqrt((x * x).sum()) + 1e-7)
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.T
+    hi = x
+    for i in range(steps):
+        t = 1.0 if i >= 3 else 0.0
+        d = half(hi @ hi.T - t * np.eye(len(x)), 2.0 ** 14)
+        p = half((b + 2 * c * t) * d + c * (d @ d), 2.0 ** 14)
+        x = (a + b * t + c * t * t) * x + p @ hi
+        if i < steps - 1:
+            hi = half(x, 2.0 ** 15)
+            x = hi + half(x - hi, 2.0 ** 15) if i < 3 else hi
+    return x.T if tall else x
