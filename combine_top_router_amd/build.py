@@ -41,7 +41,7 @@ FLAGS = [
 # The GEMM translation units: every kernel in them is sized to its register budget (256
 # registers per wave), and a spill (scratch memory traffic inside the MFMA loop or the
 # epilogue) fails the build.
-GEMM_SOURCES = ("gemm_fw256.hip", "gemm_fw320.hip")
+GEMM_SOURCES = ("gemm_fw256.hip", "gemm_fw320.hip", "orth.hip")
 
 
 def _check_no_spill(src: str, remarks: str) -> None:

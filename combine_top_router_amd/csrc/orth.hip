@@ -22,7 +22,8 @@
 // Against fp64 that is 0.7 to 2e-3 of the result's norm over spectra from flat to a
 // thousandfold spread, next to 1.7e-3 for the output's own rounding to bf16 (plain fp16
 // iterates: up to 4e-2, bf16 ones: up to 3e-1, on the same matrices).
-#include "common.h"
+#define MOE_GEMM_FW 256
+#include "gemm_engine.h"
 
 namespace moe {
 
@@ -30,6 +31,7 @@ namespace {
 
 typedef _Float16 f16;
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef i32x4 i32x4_a2 __attribute__((aligned(2)));   // 16 bytes at any element of bf16
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr double NS_EPS = 1e-7;
@@ -213,6 +215,255 @@ __global__ __launch_bounds__(256) void k_orth_tile(OrthArgs a) {
   }
 }
 
+// ---- the products on 256 x 256 tiles: jobs of the persistent tile stream ----
+__device__ __forceinline__ f16x8 as_f16(bf16x8 v) { return __builtin_bit_cast(f16x8, v); }
+
+// 8 fp32 values of one row <-> 16 bytes of fp16
+__device__ __forceinline__ f16x8 half8(const float (&v)[8]) {
+  f16x8 h;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = (f16)v[j];
+  return h;
+}
+
+struct OrthTile {
+  int z, i0, j0, nk;
+  int cnt, ncols;   // rows and columns of the product in the tile
+  float f;          // stored X -> X
+};
+
+struct OrthLd {
+  static constexpr bool GATHER = false;
+  int nk, pw;
+  const bf16_t* a[A_LP];   // the lane's chunk of its rows at K step 0 (K-major)
+  const bf16_t* b[B_LP];   // K-major rows, or MN-major k-rows
+  size_t bstep;            // elements from one K step of B to the next
+  __device__ __forceinline__ void fetch(int, int) const {}
+  template <class F>
+  __device__ __forceinline__ void issue(int kt, bf16_t* st, int, int, F&&) const {
+#pragma unroll
+    for (int q = 0; q < A_LP; ++q) dma16(a[q] + kt * BK, a_dst(st, q, pw));
+#pragma unroll
+    for (int q = 0; q < B_LP; ++q) dma16(b[q] + (size_t)kt * bstep, b_dst(st, q, pw));
+  }
+};
+
+template <int OP>
+struct JOrth {
+  using Tile = OrthTile;
+  using Ld = OrthLd;
+  static constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
+  static constexpr bool A_KMAJ = true, B_KMAJ = SYM;
+  static constexpr bool DYN = false, TRANS = false, EPI_LDS = true, NSPLIT = false, SIDE = false;
+  OrthArgs a;
+  int n, tm, tn;   // matrices; tiles along the rows and columns of a product
+  __device__ __forceinline__ static int ncol(int wn, int ni) { return wn * WCOLS + ni * 32; }
+  __device__ __forceinline__ int per() const { return SYM ? tm * (tm + 1) / 2 : tm * tn; }
+  __device__ __forceinline__ int items() const { return n * per(); }
+  __device__ __forceinline__ void tile(int v, Tile& p) const {
+    p.z = uni(v / per());
+    int rem = uni(v - p.z * per()), ti = 0;
+    if (SYM) {
+      while (rem > ti) rem -= ++ti;   // the lower triangle, row by row
+    } else {
+      ti = uni(rem % tm);             // down a column of tiles, which shares the tiles of X
+      rem = uni(rem / tm);
+    }
+    p.i0 = uni(ti * BM);
+    p.j0 = uni(rem * BN);
+    p.nk = uni((OP == ORTH_GRAM ? a.lp : a.mp) / BK);
+    p.cnt = uni(min(BM, a.mp - p.i0));
+    p.ncols = uni(min(BN, (SYM ? a.mp : a.lp) - p.j0));
+    p.f = a.step == 0 ? sload(a.factor + p.z) : 1.f / X_SCALE;
+  }
+  __device__ __forceinline__ WaveRows rows(const Tile& p, int wm) const { return wave_rows(p.cnt, wm); }
+  __device__ __forceinline__ void setup(int v, Ld& p, int pw, int lane) const {
+    Tile t;
+    tile(v, t);
+    p.pw = pw;
+    p.nk = t.nk;
+    const int K = OP == ORTH_GRAM ? a.lp : a.mp;
+    const size_t xo = (size_t)t.z * a.mp * a.lp, so = (size_t)t.z * a.mp * a.mp;
+    const bf16_t* pa = reinterpret_cast<const bf16_t*>(OP == ORTH_GRAM ? a.x + xo : OP == ORTH_POLY ? a.d + so : a.b + so);
+    const bf16_t* pb = reinterpret_cast<const bf16_t*>(OP == ORTH_POLY ? a.d + so : a.x + xo);
+#pragma unroll
+    for (int q = 0; q < A_LP; ++q) {
+      int r, c;
+      kmaj_slot(load_slot(q, pw, lane), r, c);
+      p.a[q] = pa + (size_t)min(t.i0 + r, a.mp - 1) * K + c * 8;
+    }
+#pragma unroll
+    for (int q = 0; q < B_LP; ++q) {
+      int r, c;
+      if (SYM) {
+        kmaj_slot(load_slot(q, pw, lane), r, c);
+        p.b[q] = pb + (size_t)min(t.j0 + r, a.mp - 1) * K + c * 8;
+      } else {
+        mnmaj_slot<BN>(load_slot(q, pw, lane), r, c);
+        const int col = t.j0 + c * 8;
+        p.b[q] = pb + (size_t)r * a.lp + (col < a.lp ? col : t.j0);   // past the edge: any column, not stored
+      }
+    }
+    p.bstep = SYM ? (size_t)BK : (size_t)BK * a.lp;
+  }
+  __device__ __forceinline__ void compute(const bf16_t* st, int, Acc& acc, int lane, const WaveRows& w, int wn) const {
+    const bf16_t* As = st;
+    const bf16_t* Bs = st + A_ELEMS;
+#pragma unroll
+    for (int kk = 0; kk < BK / 16; ++kk) {
+      bf16x8 af[MI], bf[NI];
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) af[mi] = frag_kmaj(As, w.base + mi * 32, kk, lane);
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+        bf[ni] = B_KMAJ ? frag_kmaj(Bs, ncol(wn, ni), kk, lane) : frag_mnmaj<BN>(Bs, ncol(wn, ni), kk, lane);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16(af[mi]), as_f16(bf[ni]), acc[mi][ni], 0, 0, 0);
+    }
+  }
+  // 16 rows at a time through the wave's fp32 staging: rows leave as they are, 8 columns a
+  // lane; a mirrored tile (or a transposed result) leaves as columns too, 16 rows a lane,
+  // from the finished values put back into the staging.
+  __device__ __forceinline__ void epilogue(const Tile& p, const Acc& acc, float* stage) const {
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int wm = (int)((unsigned)wv % WM), wn = (int)((unsigned)wv / WM);
+    float* wsm = stage + wv * EP_ROWS * EP_LD;
+    const StepCoef co = step_coef(a.step);
+    const size_t xo = (size_t)p.z * a.mp * a.lp, so = (size_t)p.z * a.mp * a.mp;
+    const bool tr = a.rows > a.cols;
+    const bool cols_out = SYM ? p.i0 != p.j0 : OP == ORTH_LAST && tr;
+    const int jw = p.j0 + wn * WCOLS;   // the wave's first column
+    if (jw - p.j0 >= p.ncols) return;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int rt = wm * WROWS + mi * 32 + h * 16;   // the piece's first row in the tile
+        if (rt < p.cnt) {
+          stage_quarter(wsm, acc, mi, h, lane);
+#pragma unroll
+          for (int jj = 0; jj < EP_ROWS / EP_RPP; ++jj) {
+            const int rr = lane / EP_LPR + EP_RPP * jj, cc = (lane % EP_LPR) * 8;
+            const int i = p.i0 + rt + rr, j = jw + cc;
+            float* const q = wsm + rr * EP_LD + cc;
+            float v[8];
+            read8(q, rr, v);
+            if constexpr (OP == ORTH_GRAM) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = v[e] * (p.f * p.f * D_SCALE) - (i == j + e ? co.t * D_SCALE : 0.f);
+              *reinterpret_cast<f16x8*>(a.d + so + (size_t)i * a.mp + j) = half8(v);
+            } else if constexpr (OP == ORTH_POLY) {
+              const f16x8 d = *reinterpret_cast<const f16x8*>(a.d + so + (size_t)i * a.mp + j);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[e] = v[e] * (NS_C * B_SCALE / (D_SCALE * D_SCALE)) + (float)d[e] * (co.beta * B_SCALE / D_SCALE);
+              *reinterpret_cast<f16x8*>(a.b + so + (size_t)i * a.mp + j) = half8(v);
+            } else {
+              const size_t o = xo + (size_t)i * a.lp + j;
+              const f16x8 xh = *reinterpret_cast<const f16x8*>(a.x + o);
+              float xv[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) xv[e] = (float)xh[e];
+              if (a.xlo) {
+                const f16x8 xl = *reinterpret_cast<const f16x8*>(a.xlo + o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xv[e] += (float)xl[e];
+              }
+              const float ca = co.alpha * p.f, cb = p.f / B_SCALE;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = xv[e] * ca + v[e] * cb;
+              if constexpr (OP == ORTH_APPLY) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= X_SCALE;
+                const f16x8 hi = half8(v);
+                *reinterpret_cast<f16x8*>(a.xn + o) = hi;
+                if (a.xnlo) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) v[e] -= (float)hi[e];
+                  *reinterpret_cast<f16x8*>(a.xnlo + o) = half8(v);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= a.scale;
+                if (!tr && i < a.m) {
+                  bf16_t* const out = a.out + (size_t)p.z * a.rows * a.cols + (size_t)i * a.cols + j;
+                  if (j + 8 <= a.l) {
+                    *reinterpret_cast<i32x4_a2*>(out) = pack8(v);
+                  } else {
+                    for (int e = 0; e < 8; ++e)
+                      if (j + e < a.l) out[e] = f2bf(v[e]);
+                  }
+                }
+              }
+            }
+            if (cols_out) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) q[e] = v[e];
+            }
+          }
+          staging_done();
+          if (cols_out) {
+            const int i = p.i0 + rt, j = jw + lane;   // rows i .. i + 15 of column j
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = wsm[e * EP_LD + lane];
+            if constexpr (SYM) {
+              f16* const d = (OP == ORTH_GRAM ? a.d : a.b) + so + (size_t)j * a.mp + i;
+              f16x8 lo, hi;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                lo[e] = (f16)v[e];
+                hi[e] = (f16)v[8 + e];
+              }
+              *reinterpret_cast<f16x8*>(d) = lo;
+              *reinterpret_cast<f16x8*>(d + 8) = hi;
+            } else if (j < a.l) {
+              bf16_t* const out = a.out + (size_t)p.z * a.rows * a.cols + (size_t)j * a.cols + i;
+              float lo[8], hi[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                lo[e] = v[e];
+                hi[e] = v[8 + e];
+              }
+              if (i + 16 <= a.m) {
+                *reinterpret_cast<i32x4_a2*>(out) = pack8(lo);
+                *reinterpret_cast<i32x4_a2*>(out + 8) = pack8(hi);
+              } else {
+                for (int e = 0; e < 16; ++e)
+                  if (i + e < a.m) out[e] = f2bf(v[e]);
+              }
+            }
+            staging_done();
+          }
+        }
+      }
+  }
+};
+
+template <int OP>
+__global__ __launch_bounds__(NTHR, 1) void k_orth_stream(OrthArgs a, int n, int tm, int tn) {
+  __shared__ __attribute__((aligned(16))) bf16_t lds[LDS_ELEMS];
+  JOrth<OP> job{a, n, tm, tn};
+  run_stream(job, lds);
+}
+
+template <int OP>
+static void orth_product(const char* name, const OrthArgs& a, int n, bool wide, hipStream_t st) {
+  constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
+  if (wide) {
+    const int tm = (int)ceil_div(a.mp, BM), tn = (int)ceil_div(a.lp, BN);
+    const int64_t items = (int64_t)n * (SYM ? tm * (tm + 1) / 2 : tm * tn);
+    MOE_LAUNCH(name, k_orth_stream<OP>, dim3((unsigned)grid_for(items)), dim3(NTHR), 0, st, a, n, tm, tn);
+  } else {
+    const int tm = a.mp / TB, tn = a.lp / TB;
+    const dim3 grid = SYM ? dim3((unsigned)(tm * (tm + 1) / 2), 1, (unsigned)n) : dim3((unsigned)tn, (unsigned)tm, (unsigned)n);
+    MOE_LAUNCH(name, k_orth_tile<OP>, grid, dim3(256), 0, st, a);
+  }
+}
+
 inline int pad64(int v) { return (v + 63) & ~63; }
 
 }  // namespace
@@ -276,13 +527,13 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   char* ws = reinterpret_cast<char*>(scratch);
   if (s.dtype == MOE_BF16) orth_enter(s, L, (const bf16_t*)g, ws, st);
   else orth_enter(s, L, (const float*)g, ws, st);
-  const int tm = L.mp / TB, tl = L.lp / TB;
+  const bool wide = L.mp >= 256;
   for (int i = 0; i < s.steps; ++i) {
     OrthArgs a{};
     a.mp = L.mp; a.lp = L.lp; a.m = L.m; a.l = L.l; a.rows = s.rows; a.cols = s.cols;
     a.step = i;
     a.x = reinterpret_cast<const f16*>(ws + L.off_x[i & 1]);
-    const bool lo_in = i == 0 ? s.dtype == MOE_F32 : i <= LO_STEPS, last = i == s.steps - 1;
+    const bool lo_in = i == 0 ? s.dtype == MOE_F32 : i <= LO_STEPS;
     a.xlo = lo_in ? reinterpret_cast<const f16*>(ws + L.off_lo[i & 1]) : nullptr;
     a.factor = reinterpret_cast<const float*>(ws + L.off_factor);
     a.d = reinterpret_cast<f16*>(ws + L.off_d);
@@ -291,11 +542,10 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
     a.xnlo = i < LO_STEPS ? reinterpret_cast<f16*>(ws + L.off_lo[(i + 1) & 1]) : nullptr;
     a.out = (bf16_t*)o;
     a.scale = scale;
-    const dim3 sym((unsigned)(tm * (tm + 1) / 2), 1, (unsigned)s.n), full((unsigned)tl, (unsigned)tm, (unsigned)s.n);
-    MOE_LAUNCH("orth_gram", k_orth_tile<ORTH_GRAM>, sym, dim3(256), 0, st, a);
-    MOE_LAUNCH("orth_poly", k_orth_tile<ORTH_POLY>, sym, dim3(256), 0, st, a);
-    if (last) MOE_LAUNCH("orth_last", k_orth_tile<ORTH_LAST>, full, dim3(256), 0, st, a);
-    else MOE_LAUNCH("orth_apply", k_orth_tile<ORTH_APPLY>, full, dim3(256), 0, st, a);
+    orth_product<ORTH_GRAM>("orth_gram", a, s.n, wide, st);
+    orth_product<ORTH_POLY>("orth_poly", a, s.n, wide, st);
+    if (i == s.steps - 1) orth_product<ORTH_LAST>("orth_last", a, s.n, wide, st);
+    else orth_product<ORTH_APPLY>("orth_apply", a, s.n, wide, st);
   }
   return hipGetLastError();
 }
