@@ -14,8 +14,9 @@
 // a = 3.4 a step, and so is the rounding noise that lands beside it.  So
 // * the step's a X is added in fp32 outside the matrix product (with a I inside the fp16
 //   factor, its rounded diagonal leaks the large directions into the small ones);
-// * X is kept as a pair hi + lo of fp16 through the first steps (the product reads hi, a X
-//   both), and enters as the exact bf16 values scaled by a power of two;
+// * the first iterates are kept as a pair, hi in fp16 and lo = the rest times 16 in E4M3 (a
+//   byte: 15 bits together; the product reads hi, a X both), and X enters as the exact bf16
+//   values scaled by a power of two;
 // * from step 3 on, when the singular values are near 1, A is kept as D = A - I:
 //   b A + c A^2 = (b + c) I + (b + 2c) D + c D^2, so the diagonal's rounding enters times
 //   b + 2c = -0.71 instead of b = -4.8.
@@ -32,16 +33,54 @@ namespace {
 typedef _Float16 f16;
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef i32x4 i32x4_a2 __attribute__((aligned(2)));   // 16 bytes at any element of bf16
+typedef i32x4 i32x4_a4 __attribute__((aligned(4)));   // or of fp32
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr double NS_EPS = 1e-7;
 constexpr int X_LOG2 = 15, D_LOG2 = 14, B_LOG2 = 14;
 constexpr float X_SCALE = 32768.f, D_SCALE = 16384.f, B_SCALE = 16384.f;
-constexpr int LO_STEPS = 3;      // the first iterates that are kept as hi + lo
+constexpr float LO_SCALE = 16.f;  // |lo| <= 16, half a step of fp16 at its top: 256 of E4M3's 448
+constexpr int LO_STEPS = 2;      // the first iterates that are kept as hi + lo
 constexpr int SHIFT_STEP = 3;    // from this step on, D = A - I
+
+__device__ __forceinline__ uint8_t lo_code(float rest) {
+  return (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(rest * LO_SCALE, 0.f, 0, false);
+}
+__device__ __forceinline__ float lo_value(uint8_t code) {
+  return __builtin_amdgcn_cvt_f32_fp8(code, 0) * (1.f / LO_SCALE);
+}
 
 // ---- norm and entry ----
 constexpr int NORM_CHUNKS = 64;   // workgroups a matrix at most
+
+// 8 elements at p, of which `left` are there (the rest read as 0); p at any element
+__device__ __forceinline__ void load8_any(const bf16_t* p, int left, float (&v)[8]) {
+  if (left >= 8) {
+    unpack8(*reinterpret_cast<const i32x4_a2*>(p), v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? bf2f(p[e]) : 0.f;
+  }
+}
+__device__ __forceinline__ void load8_any(const float* p, int left, float (&v)[8]) {
+  if (left >= 8) {
+    const i32x4 a = *reinterpret_cast<const i32x4_a4*>(p), b = *reinterpret_cast<const i32x4_a4*>(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __uint_as_float((uint32_t)a[e]);
+      v[4 + e] = __uint_as_float((uint32_t)b[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : 0.f;
+  }
+}
+
+__device__ __forceinline__ double wave_sum_f64(double a) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) a += __shfl_xor(a, off, 64);
+  return a;
+}
 
 // sums of squares of chunk blockIdx.x of matrix blockIdx.y, in fp64: neither a gradient of
 // 1e-30 nor one of 1e30 leaves the range
@@ -51,12 +90,14 @@ __global__ __launch_bounds__(256) void k_orth_sumsq(const T* __restrict__ g, int
   const T* p = g + (int64_t)blockIdx.y * count;
   const int64_t b = (int64_t)blockIdx.x * chunk, e = b + chunk < count ? b + chunk : count;
   double a = 0.0;
-  for (int64_t i = b + threadIdx.x; i < e; i += 256) {
-    const double v = (double)elem<T>::load(p + i);
-    a += v * v;
-  }
+#pragma unroll 4
+  for (int64_t i = b + threadIdx.x * 8; i < e; i += 256 * 8) {
+    float v[8];
+    load8_any(p + i, (int)(e - i < 8 ? e - i : 8), v);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) a += __shfl_xor(a, off, 64);
+    for (int q = 0; q < 8; ++q) a += (double)v[q] * (double)v[q];
+  }
+  a = wave_sum_f64(a);
   __shared__ double red[4];
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
   __syncthreads();
@@ -65,16 +106,18 @@ __global__ __launch_bounds__(256) void k_orth_sumsq(const T* __restrict__ g, int
 
 // X0 (hi, and lo for fp32 input) [m_p, l_p] of each matrix, padded with zeros, from g
 // [rows, cols] (transposed when rows > cols) times 2^e, where 2^e brings the norm into
-// [2^14, 2^15); factor[matrix] = 2^-e / (norm + eps) turns stored values into X0.
+// [2^14, 2^15); factor[matrix] = 2^-e / (norm + eps) turns stored values into X0.  One
+// workgroup makes 64 rows by up to ENTER_TILES tiles of 64 columns.
+constexpr int ENTER_TILES = 8;
 template <typename T, bool TR>
 __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int rows, int cols,
                                                     const double* __restrict__ part, int chunks, int mp, int lp,
-                                                    f16* __restrict__ hi, f16* __restrict__ lo,
+                                                    f16* __restrict__ hi, uint8_t* __restrict__ lo,
                                                     float* __restrict__ factor) {
-  __shared__ float tile[64][65];
-  double ss = 0.0;
-  for (int i = 0; i < chunks; ++i) ss += part[(size_t)blockIdx.z * chunks + i];
-  const double norm = sqrt(ss);
+  __shared__ float tile[TR ? 64 : 1][65];
+  static_assert(NORM_CHUNKS <= 64, "one lane a share");
+  const int lane = threadIdx.x & 63;
+  const double norm = sqrt(wave_sum_f64(lane < chunks ? part[(size_t)blockIdx.z * chunks + lane] : 0.0));
   int e = 0;
   if (norm > 0.0 && norm < 1e300) {
     frexp(norm, &e);   // norm = f 2^e, f in [1/2, 1)
@@ -82,25 +125,45 @@ __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int
   }
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
     factor[blockIdx.z] = (float)(ldexp(1.0, -e) / (norm + NS_EPS));
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // of X
+  const int tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;   // rows tr, tr + 32; 8 columns
+  const int r0 = blockIdx.y * 64;   // of X
   const T* p = g + (size_t)blockIdx.z * rows * cols;
-  const int m = TR ? cols : rows, l = TR ? rows : cols;
-  if (TR) {
-    for (int i = ty; i < 64; i += 4) {   // g row = X column c0 + i, g column = X row r0 + tx
-      const int r = c0 + i, c = r0 + tx;
-      tile[tx][i] = r < l && c < m ? elem<T>::load(p + (size_t)r * cols + c) : 0.f;
+  for (int ct = 0; ct < ENTER_TILES; ++ct) {
+    const int c0 = ((int)blockIdx.x * ENTER_TILES + ct) * 64;
+    if (c0 >= lp) break;
+    float v[2][8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      // TR: row c0 + .. of g is column c0 + .. of X, its columns r0 + .. are X's rows
+      const int r = (TR ? c0 : r0) + tr + 32 * q, c = (TR ? r0 : c0) + tc;
+      load8_any(p + (size_t)r * cols + c, r < rows ? cols - c : 0, v[q]);
     }
-    __syncthreads();
-  }
-  for (int i = ty; i < 64; i += 4) {
-    const int r = r0 + i, c = c0 + tx;
-    float v = TR ? tile[i][tx] : r < m && c < l ? elem<T>::load(p + (size_t)r * cols + c) : 0.f;
-    v = ldexpf(v, e);
-    const size_t o = ((size_t)blockIdx.z * mp + r) * lp + c;
-    const f16 h = (f16)v;
-    hi[o] = h;
-    if (lo) lo[o] = (f16)(v - (float)h);
+    if (TR) {
+      __syncthreads();   // the tile before has been read
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) tile[tc + x][tr + 32 * q] = v[q][x];
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[q][x] = tile[tr + 32 * q][tc + x];
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const size_t o = ((size_t)blockIdx.z * mp + r0 + tr + 32 * q) * lp + c0 + tc;
+      f16x8 h;
+      uint64_t codes = 0;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float s = ldexpf(v[q][x], e);
+        h[x] = (f16)s;
+        if (lo) codes |= (uint64_t)lo_code(s - (float)h[x]) << (8 * x);
+      }
+      *reinterpret_cast<f16x8*>(hi + o) = h;
+      if (lo) *reinterpret_cast<uint64_t*>(lo + o) = codes;
+    }
   }
 }
 
@@ -115,12 +178,12 @@ struct OrthArgs {
   int m, l, rows, cols;
   int step;
   const f16* x;           // X hi [n, mp, lp]
-  const f16* xlo;         // X lo, or null
+  const uint8_t* xlo;     // X lo, or null
   const float* factor;    // stored X -> X, per matrix (step 0)
   f16* d;                 // D [n, mp, mp]
   f16* b;                 // B = beta D + c D^2 [n, mp, mp]
   f16* xn;                // the next X
-  f16* xnlo;              // its lo, or null
+  uint8_t* xnlo;          // its lo, or null
   bf16_t* out;            // the last step's result [n, rows, cols]
   float scale;
 };
@@ -199,13 +262,13 @@ __global__ __launch_bounds__(256) void k_orth_tile(OrthArgs a) {
     } else {
       const size_t o = xo + (size_t)i * a.lp + j;
       float xv = (float)a.x[o];
-      if (a.xlo) xv += (float)a.xlo[o];
+      if (a.xlo) xv += lo_value(a.xlo[o]);
       const float v = xv * (co.alpha * f) + acc[r] * (f / B_SCALE);
       if (OP == ORTH_APPLY) {
         const float s = v * X_SCALE;
         const f16 h = (f16)s;
         a.xn[o] = h;
-        if (a.xnlo) a.xnlo[o] = (f16)(s - (float)h);
+        if (a.xnlo) a.xnlo[o] = lo_code(s - (float)h);
       } else if (i < a.m && j < a.l) {
         const size_t base = (size_t)z * a.rows * a.cols;
         const size_t oo = a.rows > a.cols ? (size_t)j * a.cols + i : (size_t)i * a.cols + j;
@@ -218,12 +281,98 @@ __global__ __launch_bounds__(256) void k_orth_tile(OrthArgs a) {
 // ---- the products on 256 x 256 tiles: jobs of the persistent tile stream ----
 __device__ __forceinline__ f16x8 as_f16(bf16x8 v) { return __builtin_bit_cast(f16x8, v); }
 
-// 8 fp32 values of one row <-> 16 bytes of fp16
-__device__ __forceinline__ f16x8 half8(const float (&v)[8]) {
-  f16x8 h;
+typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t pk_f16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, (f16x2){(f16)lo, (f16)hi});
+}
+// trans_chunks in fp16: 16 values of a transposed accumulator block (columns 8q + 4 (l / 32)
+// .. + 3 of row l % 32 in v[4q] .. v[4q + 3]) -> the row's chunks s = columns 16 s + 8 (l / 32)
+// .. + 7
+__device__ __forceinline__ void trans_chunks_f16(const float (&v)[16], i32x4 (&out)[2]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = (f16)v[j];
-  return h;
+  for (int s = 0; s < 2; ++s) {
+    uint32_t d[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const auto r = __builtin_amdgcn_permlane32_swap(pk_f16(v[8 * s + 2 * c], v[8 * s + 2 * c + 1]),
+                                                      pk_f16(v[8 * s + 4 + 2 * c], v[8 * s + 5 + 2 * c]), false, false);
+      d[0][c] = r[0];
+      d[1][c] = r[1];
+    }
+    out[s] = i32x4{(int)d[0][0], (int)d[0][1], (int)d[1][0], (int)d[1][1]};
+  }
+}
+// and back (the swap undoes itself)
+__device__ __forceinline__ void untrans_chunks_f16(const i32x4 (&ch)[2], float (&v)[16]) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)ch[s][c], (uint32_t)ch[s][2 + c], false, false);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f16x2 p = __builtin_bit_cast(f16x2, (uint32_t)r[h]);
+        v[8 * s + 4 * h + 2 * c] = (float)p[0];
+        v[8 * s + 4 * h + 2 * c + 1] = (float)p[1];
+      }
+    }
+}
+// The lo codes of such a block: 16 codes of row l % 32, columns 16 (l / 32) .. + 15, from the
+// lanes' values and back
+__device__ __forceinline__ i32x4 trans_codes(const float (&rest)[16]) {
+  uint32_t e[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(rest[4 * q] * LO_SCALE, rest[4 * q + 1] * LO_SCALE, 0, false);
+    e[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(rest[4 * q + 2] * LO_SCALE, rest[4 * q + 3] * LO_SCALE, lo, true);
+  }
+  const auto s02 = __builtin_amdgcn_permlane32_swap(e[0], e[2], false, false);
+  const auto s13 = __builtin_amdgcn_permlane32_swap(e[1], e[3], false, false);
+  return i32x4{(int)s02[0], (int)s02[1], (int)s13[0], (int)s13[1]};
+}
+__device__ __forceinline__ void add_codes(const i32x4& c, float (&v)[16]) {
+  const auto s02 = __builtin_amdgcn_permlane32_swap((uint32_t)c[0], (uint32_t)c[1], false, false);
+  const auto s13 = __builtin_amdgcn_permlane32_swap((uint32_t)c[2], (uint32_t)c[3], false, false);
+  const uint32_t e[4] = {s02[0], s13[0], s02[1], s13[1]};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)e[q], false);
+    const auto b = __builtin_amdgcn_cvt_pk_f32_fp8((int)e[q], true);
+    v[4 * q] += a[0] * (1.f / LO_SCALE);
+    v[4 * q + 1] += a[1] * (1.f / LO_SCALE);
+    v[4 * q + 2] += b[0] * (1.f / LO_SCALE);
+    v[4 * q + 3] += b[1] * (1.f / LO_SCALE);
+  }
+}
+
+// The columns of the 32 x 64 band that band_store has just passed through the wave's LDS
+// region, as rows of the transposed tile: store(column, row, chunk) gets rows row .. row + 7
+// of a column.  The transposing read hands a lane four rows of its column.
+template <class F>
+__device__ __forceinline__ void band_columns(const bf16_t* wreg, F&& store) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
+  i32x4 v[4];
+#pragma unroll
+  for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int col = 32 * ni + 16 * (g & 1) + 4 * q;
+      s16x4 t[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = kk * 16 + 8 * (g >> 1) + 4 * h + j;
+        t[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (MOE_LDS s16x4*)(wreg + r * WCOLS + (((col >> 3) ^ band_swz<8>(r)) << 3) + (col & 7)));
+      }
+      __builtin_memcpy(&v[ni * 2 + kk], t, 16);
+    }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the region is free for the next band
+#pragma unroll
+  for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) store(32 * ni + (lane & 31), kk * 16 + 8 * (lane >> 5), v[ni * 2 + kk]);
 }
 
 struct OrthTile {
@@ -248,13 +397,15 @@ struct OrthLd {
   }
 };
 
-template <int OP>
+// TALL: the last step of matrices that were transposed on entry, whose accumulators hold C,
+// so that the blocks leave as rows of C^T; all others hold C^T and leave as rows of C.
+template <int OP, bool TALL = false>
 struct JOrth {
   using Tile = OrthTile;
   using Ld = OrthLd;
   static constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
   static constexpr bool A_KMAJ = true, B_KMAJ = SYM;
-  static constexpr bool DYN = false, TRANS = false, EPI_LDS = true, NSPLIT = false, SIDE = false;
+  static constexpr bool DYN = false, TRANS = !TALL, EPI_LDS = true, NSPLIT = false, SIDE = false;
   OrthArgs a;
   int n, tm, tn;   // matrices; tiles along the rows and columns of a product
   __device__ __forceinline__ static int ncol(int wn, int ni) { return wn * WCOLS + ni * 32; }
@@ -321,132 +472,187 @@ struct JOrth {
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
-          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16(af[mi]), as_f16(bf[ni]), acc[mi][ni], 0, 0, 0);
+          acc[mi][ni] = TRANS ? __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16(bf[ni]), as_f16(af[mi]), acc[mi][ni], 0, 0, 0)
+                              : __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16(af[mi]), as_f16(bf[ni]), acc[mi][ni], 0, 0, 0);
     }
   }
-  // 16 rows at a time through the wave's fp32 staging: rows leave as they are, 8 columns a
-  // lane; a mirrored tile (or a transposed result) leaves as columns too, 16 rows a lane,
-  // from the finished values put back into the staging.
   __device__ __forceinline__ void epilogue(const Tile& p, const Acc& acc, float* stage) const {
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int wm = (int)((unsigned)wv % WM), wn = (int)((unsigned)wv / WM);
-    float* wsm = stage + wv * EP_ROWS * EP_LD;
+    const int tid = threadIdx.x, wv = tid >> 6, wm = (int)((unsigned)wv % WM), wn = (int)((unsigned)wv / WM);
+    if (wn * WCOLS >= p.ncols) return;   // the tile's sizes are multiples of 64
+    bf16_t* const wreg = reinterpret_cast<bf16_t*>(stage) + wv * BAND_ELEMS;
+    if constexpr (TALL) out_tall(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
+    else out_rows(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
+  }
+  // C^T accumulators: lane l holds row l % 32 of each band.  What the rows are combined with
+  // (D, or X hi and lo) is loaded in that layout two bands ahead (all four at once spill);
+  // finished bands leave through the wave's LDS region as whole row segments, and those of
+  // an off-diagonal tile of a symmetric product once more as columns.
+  __device__ __forceinline__ void out_rows(const Tile& p, const Acc& acc, bf16_t* wreg, int i0, int j0) const {
+    const int lane = threadIdx.x & 63;
     const StepCoef co = step_coef(a.step);
     const size_t xo = (size_t)p.z * a.mp * a.lp, so = (size_t)p.z * a.mp * a.mp;
-    const bool tr = a.rows > a.cols;
-    const bool cols_out = SYM ? p.i0 != p.j0 : OP == ORTH_LAST && tr;
-    const int jw = p.j0 + wn * WCOLS;   // the wave's first column
-    if (jw - p.j0 >= p.ncols) return;
+    const int ld = SYM ? a.mp : a.lp;
+    const f16* const side = OP == ORTH_POLY ? a.d + so : a.x + xo;
+    const uint8_t* const side_lo = !SYM && a.xlo ? a.xlo + xo : nullptr;
+    i32x4 xh[2][NI][2], xl[2][NI];
+    auto fetch = [&](int mi) {
+      const size_t row = (size_t)min(i0 + mi * 32 + (lane & 31), a.mp - 1) * ld + j0;
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
+      for (int ni = 0; ni < NI; ++ni) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rt = wm * WROWS + mi * 32 + h * 16;   // the piece's first row in the tile
-        if (rt < p.cnt) {
-          stage_quarter(wsm, acc, mi, h, lane);
+        for (int s = 0; s < 2; ++s)
+          xh[mi & 1][ni][s] = *reinterpret_cast<const i32x4*>(side + row + ni * 32 + 16 * s + 8 * (lane >> 5));
+        if (side_lo) xl[mi & 1][ni] = *reinterpret_cast<const i32x4*>(side_lo + row + ni * 32 + 16 * (lane >> 5));
+      }
+    };
+    if constexpr (OP != ORTH_GRAM) {
+      fetch(0);
+      fetch(1);
+    }
+    // v = acc cb + side ca
+    float ca, cb;
+    if (OP == ORTH_GRAM) { cb = p.f * p.f * D_SCALE; ca = 0.f; }
+    else if (OP == ORTH_POLY) { cb = NS_C * B_SCALE / (D_SCALE * D_SCALE); ca = co.beta * B_SCALE / D_SCALE; }
+    else { const float sc = OP == ORTH_APPLY ? X_SCALE : a.scale; cb = p.f / B_SCALE * sc; ca = co.alpha * p.f * sc; }
 #pragma unroll
-          for (int jj = 0; jj < EP_ROWS / EP_RPP; ++jj) {
-            const int rr = lane / EP_LPR + EP_RPP * jj, cc = (lane % EP_LPR) * 8;
-            const int i = p.i0 + rt + rr, j = jw + cc;
-            float* const q = wsm + rr * EP_LD + cc;
-            float v[8];
-            read8(q, rr, v);
-            if constexpr (OP == ORTH_GRAM) {
+    for (int mi = 0; mi < MI; ++mi) {
+      const int rb = i0 + mi * 32;
+      if (rb >= p.i0 + p.cnt) break;
+      i32x4 ch[NI][2], codes[NI];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = v[e] * (p.f * p.f * D_SCALE) - (i == j + e ? co.t * D_SCALE : 0.f);
-              *reinterpret_cast<f16x8*>(a.d + so + (size_t)i * a.mp + j) = half8(v);
-            } else if constexpr (OP == ORTH_POLY) {
-              const f16x8 d = *reinterpret_cast<const f16x8*>(a.d + so + (size_t)i * a.mp + j);
+      for (int ni = 0; ni < NI; ++ni) {
+        float v[16];
+        if constexpr (OP == ORTH_GRAM) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                v[e] = v[e] * (NS_C * B_SCALE / (D_SCALE * D_SCALE)) + (float)d[e] * (co.beta * B_SCALE / D_SCALE);
-              *reinterpret_cast<f16x8*>(a.b + so + (size_t)i * a.mp + j) = half8(v);
-            } else {
-              const size_t o = xo + (size_t)i * a.lp + j;
-              const f16x8 xh = *reinterpret_cast<const f16x8*>(a.x + o);
-              float xv[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) xv[e] = (float)xh[e];
-              if (a.xlo) {
-                const f16x8 xl = *reinterpret_cast<const f16x8*>(a.xlo + o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) xv[e] += (float)xl[e];
-              }
-              const float ca = co.alpha * p.f, cb = p.f / B_SCALE;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = xv[e] * ca + v[e] * cb;
-              if constexpr (OP == ORTH_APPLY) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= X_SCALE;
-                const f16x8 hi = half8(v);
-                *reinterpret_cast<f16x8*>(a.xn + o) = hi;
-                if (a.xnlo) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) v[e] -= (float)hi[e];
-                  *reinterpret_cast<f16x8*>(a.xnlo + o) = half8(v);
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= a.scale;
-                if (!tr && i < a.m) {
-                  bf16_t* const out = a.out + (size_t)p.z * a.rows * a.cols + (size_t)i * a.cols + j;
-                  if (j + 8 <= a.l) {
-                    *reinterpret_cast<i32x4_a2*>(out) = pack8(v);
-                  } else {
-                    for (int e = 0; e < 8; ++e)
-                      if (j + e < a.l) out[e] = f2bf(v[e]);
-                  }
-                }
-              }
-            }
-            if (cols_out) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) q[e] = v[e];
-            }
+          for (int r = 0; r < 16; ++r) {
+            v[r] = acc[mi][ni][r] * cb;
+            if (rb + (lane & 31) == j0 + ni * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= co.t * D_SCALE;
           }
-          staging_done();
-          if (cols_out) {
-            const int i = p.i0 + rt, j = jw + lane;   // rows i .. i + 15 of column j
-            float v[16];
+        } else {
+          untrans_chunks_f16(xh[mi & 1][ni], v);
+          if (side_lo) add_codes(xl[mi & 1][ni], v);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = wsm[e * EP_LD + lane];
-            if constexpr (SYM) {
-              f16* const d = (OP == ORTH_GRAM ? a.d : a.b) + so + (size_t)j * a.mp + i;
-              f16x8 lo, hi;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                lo[e] = (f16)v[e];
-                hi[e] = (f16)v[8 + e];
-              }
-              *reinterpret_cast<f16x8*>(d) = lo;
-              *reinterpret_cast<f16x8*>(d + 8) = hi;
-            } else if (j < a.l) {
-              bf16_t* const out = a.out + (size_t)p.z * a.rows * a.cols + (size_t)j * a.cols + i;
-              float lo[8], hi[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                lo[e] = v[e];
-                hi[e] = v[8 + e];
-              }
-              if (i + 16 <= a.m) {
-                *reinterpret_cast<i32x4_a2*>(out) = pack8(lo);
-                *reinterpret_cast<i32x4_a2*>(out + 8) = pack8(hi);
-              } else {
-                for (int e = 0; e < 16; ++e)
-                  if (i + e < a.m) out[e] = f2bf(v[e]);
-              }
-            }
-            staging_done();
-          }
+          for (int r = 0; r < 16; ++r) v[r] = acc[mi][ni][r] * cb + v[r] * ca;
         }
+        if constexpr (OP == ORTH_LAST) {
+          f32x16 b;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) b[r] = v[r];
+          trans_chunks(b, ch[ni]);
+        } else {
+          trans_chunks_f16(v, ch[ni]);
+        }
+        if (OP == ORTH_APPLY && a.xnlo) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] -= (float)(f16)v[r];
+          codes[ni] = trans_codes(v);
+        }
+      }
+      if (OP != ORTH_GRAM && mi + 2 < MI) fetch(mi + 2);
+      if (OP == ORTH_APPLY && a.xnlo) {
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+          *reinterpret_cast<i32x4*>(a.xnlo + xo + (size_t)(rb + (lane & 31)) * ld + j0 + ni * 32 + 16 * (lane >> 5)) = codes[ni];
+      }
+      if constexpr (OP == ORTH_LAST) {
+        bf16_t* const out = a.out + (size_t)p.z * a.rows * a.cols;
+        band_store(wreg, ch, [&](int rr, int cb_, i32x4 w) {
+          const int i = rb + rr, j = j0 + cb_;
+          if (i >= a.m || j >= a.l) return;
+          bf16_t* const q = out + (size_t)i * a.cols + j;
+          if (j + 8 <= a.l) {
+            *reinterpret_cast<i32x4_a2*>(q) = w;
+          } else {
+            for (int e = 0; e < 8; ++e)
+              if (j + e < a.l) q[e] = (bf16_t)((uint32_t)w[e >> 1] >> (16 * (e & 1)));
+          }
+        });
+      } else {
+        f16* const out = OP == ORTH_GRAM ? a.d + so : OP == ORTH_POLY ? a.b + so : a.xn + xo;
+        band_store(wreg, ch, [&](int rr, int cb_, i32x4 w) {
+          *reinterpret_cast<i32x4*>(out + (size_t)(rb + rr) * ld + j0 + cb_) = w;
+        });
+        if (SYM && p.i0 != p.j0)
+          band_columns(wreg, [&](int c, int r, i32x4 w) {
+            *reinterpret_cast<i32x4*>(out + (size_t)(j0 + c) * ld + rb + r) = w;
+          });
+      }
+    }
+  }
+  // The last step of transposed matrices: lane l holds column l % 32 of each block, whose X
+  // comes through the wave's LDS region and the transposing read; then rows of C^T leave.
+  __device__ __forceinline__ void out_tall(const Tile& p, const Acc& acc, bf16_t* wreg, int i0, int j0) const {
+    const int lane = threadIdx.x & 63, g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
+    const StepCoef co = step_coef(a.step);
+    const size_t xo = (size_t)p.z * a.mp * a.lp;
+    const float cb = p.f / B_SCALE * a.scale, ca = co.alpha * p.f * a.scale;
+    i32x4 xh[4];   // rows lane / 8 + 8 k of a 32 x 64 band, 16 bytes a lane, one band ahead
+    auto fetch = [&](int mi) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        xh[k] = *reinterpret_cast<const i32x4*>(
+            a.x + xo + (size_t)min(i0 + mi * 32 + (lane >> 3) + 8 * k, a.mp - 1) * a.lp + j0 + (lane & 7) * 8);
+    };
+    fetch(0);
+    Acc v;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = (lane >> 3) + 8 * k;
+        *reinterpret_cast<i32x4*>(wreg + r * WCOLS + (((lane & 7) ^ band_swz<8>(r)) << 3)) = xh[k];
+      }
+      if (mi + 1 < MI) fetch(mi + 1);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // rows 8 k + 4 (l / 32) .. + 3 of column l % 32
+          const int col = 32 * ni + 16 * (g & 1) + 4 * q, r = 8 * k + 4 * (g >> 1) + j;
+          const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (MOE_LDS s16x4*)(wreg + r * WCOLS + (((col >> 3) ^ band_swz<8>(r)) << 3) + (col & 7)));
+          const f16x4 x = __builtin_bit_cast(f16x4, t);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[mi][ni][4 * k + e] = acc[mi][ni][4 * k + e] * cb + (float)x[e] * ca;
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (a.xlo) {   // three steps or fewer
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int i = min(i0 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), a.mp - 1);
+            v[mi][ni][r] += lo_value(a.xlo[xo + (size_t)i * a.lp + j0 + ni * 32 + (lane & 31)]) * ca;
+          }
+      }
+    }
+    bf16_t* const out = a.out + (size_t)p.z * a.rows * a.cols;
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+      for (int mh = 0; mh < MI; mh += 2) {
+        i32x4 ch[2][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) trans_chunks(v[mh + b][ni], ch[b]);
+        band_store(wreg, ch, [&](int rr, int cb_, i32x4 w) {
+          const int r = j0 + ni * 32 + rr, c = i0 + mh * 32 + cb_;   // of the output
+          if (r >= a.l || c >= a.m) return;
+          bf16_t* const o = out + (size_t)r * a.cols + c;
+          if (c + 8 <= a.m) {
+            *reinterpret_cast<i32x4_a2*>(o) = w;
+          } else {
+            for (int e = 0; e < 8; ++e)
+              if (c + e < a.m) o[e] = (bf16_t)((uint32_t)w[e >> 1] >> (16 * (e & 1)));
+          }
+        });
       }
   }
 };
 
-template <int OP>
+template <int OP, bool TALL>
 __global__ __launch_bounds__(NTHR, 1) void k_orth_stream(OrthArgs a, int n, int tm, int tn) {
   __shared__ __attribute__((aligned(16))) bf16_t lds[LDS_ELEMS];
-  JOrth<OP> job{a, n, tm, tn};
+  JOrth<OP, TALL> job{a, n, tm, tn};
   run_stream(job, lds);
 }
 
@@ -456,7 +662,14 @@ static void orth_product(const char* name, const OrthArgs& a, int n, bool wide, 
   if (wide) {
     const int tm = (int)ceil_div(a.mp, BM), tn = (int)ceil_div(a.lp, BN);
     const int64_t items = (int64_t)n * (SYM ? tm * (tm + 1) / 2 : tm * tn);
-    MOE_LAUNCH(name, k_orth_stream<OP>, dim3((unsigned)grid_for(items)), dim3(NTHR), 0, st, a, n, tm, tn);
+    const dim3 grid((unsigned)grid_for(items));
+    if constexpr (OP == ORTH_LAST) {
+      if (a.rows > a.cols) {
+        MOE_LAUNCH(name, (k_orth_stream<OP, true>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
+        return;
+      }
+    }
+    MOE_LAUNCH(name, (k_orth_stream<OP, false>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
   } else {
     const int tm = a.mp / TB, tn = a.lp / TB;
     const dim3 grid = SYM ? dim3((unsigned)(tm * (tm + 1) / 2), 1, (unsigned)n) : dim3((unsigned)tn, (unsigned)tm, (unsigned)n);
@@ -493,7 +706,7 @@ static OrthLayout orth_layout(const moe_orth_shape& s) {
   L.off_factor = take((size_t)s.n * 4);
   for (int i = 0; i < 2; ++i) {
     L.off_x[i] = take(xb);
-    L.off_lo[i] = take(xb);
+    L.off_lo[i] = take(xb / 2);
   }
   L.off_d = take(db);
   L.off_b = take(db);
@@ -505,14 +718,14 @@ size_t orth_scratch_bytes(const moe_orth_shape& s) { return orth_layout(s).bytes
 template <typename T>
 static void orth_enter(const moe_orth_shape& s, const OrthLayout& L, const T* g, char* ws, hipStream_t st) {
   const int64_t count = (int64_t)s.rows * s.cols;
-  const int64_t chunk = ceil_div(count, L.chunks);
+  const int64_t chunk = ceil_div(ceil_div(count, L.chunks), 8) * 8;
   double* part = reinterpret_cast<double*>(ws + L.off_part);
   float* factor = reinterpret_cast<float*>(ws + L.off_factor);
   f16* hi = reinterpret_cast<f16*>(ws + L.off_x[0]);
-  f16* lo = s.dtype == MOE_F32 ? reinterpret_cast<f16*>(ws + L.off_lo[0]) : nullptr;
+  uint8_t* lo = s.dtype == MOE_F32 ? reinterpret_cast<uint8_t*>(ws + L.off_lo[0]) : nullptr;
   MOE_LAUNCH("orth_sumsq", k_orth_sumsq<T>, dim3((unsigned)L.chunks, (unsigned)s.n), dim3(256), 0, st, g, count, chunk,
              part);
-  const dim3 grid((unsigned)(L.lp / 64), (unsigned)(L.mp / 64), (unsigned)s.n);
+  const dim3 grid((unsigned)ceil_div(L.lp / 64, ENTER_TILES), (unsigned)(L.mp / 64), (unsigned)s.n);
   if (s.rows > s.cols)
     MOE_LAUNCH("orth_enter", (k_orth_enter<T, true>), grid, dim3(256), 0, st, g, s.rows, s.cols, part, L.chunks, L.mp,
                L.lp, hi, lo, factor);
@@ -534,12 +747,12 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
     a.step = i;
     a.x = reinterpret_cast<const f16*>(ws + L.off_x[i & 1]);
     const bool lo_in = i == 0 ? s.dtype == MOE_F32 : i <= LO_STEPS;
-    a.xlo = lo_in ? reinterpret_cast<const f16*>(ws + L.off_lo[i & 1]) : nullptr;
+    a.xlo = lo_in ? reinterpret_cast<const uint8_t*>(ws + L.off_lo[i & 1]) : nullptr;
     a.factor = reinterpret_cast<const float*>(ws + L.off_factor);
     a.d = reinterpret_cast<f16*>(ws + L.off_d);
     a.b = reinterpret_cast<f16*>(ws + L.off_b);
     a.xn = reinterpret_cast<f16*>(ws + L.off_x[(i + 1) & 1]);
-    a.xnlo = i < LO_STEPS ? reinterpret_cast<f16*>(ws + L.off_lo[(i + 1) & 1]) : nullptr;
+    a.xnlo = i < LO_STEPS ? reinterpret_cast<uint8_t*>(ws + L.off_lo[(i + 1) & 1]) : nullptr;
     a.out = (bf16_t*)o;
     a.scale = scale;
     orth_product<ORTH_GRAM>("orth_gram", a, s.n, wide, st);
