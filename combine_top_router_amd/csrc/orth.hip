@@ -677,6 +677,175 @@ static void orth_product(const char* name, const OrthArgs& a, int n, bool wide, 
   }
 }
 
+// ---- small matrices: the whole iteration in one workgroup ----
+// X [MP, lp] (at most SMALL_ELEMS) stays in one CU: as fp32 in the accumulator layout of its
+// eight waves (so no iterate is rounded but for the products), and as fp16 in LDS beside D and
+// B.  One launch instead of 2 + 3 a step, which is what bounds matrices this small: eight of
+// 128 x 64, five steps, took 84 us in 17 launches.
+constexpr int SMALL_ELEMS = 32768, SMALL_MP = 128;
+constexpr int SMALL_BLOCKS = SMALL_ELEMS / 1024 / NW;   // 32 x 32 blocks of X a wave
+constexpr int small_lds(int mp) {   // elements: X (rows of lp + 8), D and B (rows of mp + 8)
+  return SMALL_ELEMS + 8 * mp + 2 * mp * (mp + 8);
+}
+
+// 32 x 32 block of P Q^T, K-major rows of ldp and ldq in LDS, transposed in the accumulator
+__device__ __forceinline__ f32x16 small_block(const f16* p, int ldp, const f16* q, int ldq, int K, int lane) {
+  f32x16 acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  const f16 *pa = p + (lane & 31) * ldp + 8 * (lane >> 5), *pb = q + (lane & 31) * ldq + 8 * (lane >> 5);
+#pragma unroll 4
+  for (int k = 0; k < K; k += 16)
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(pb + k),
+                                                 *reinterpret_cast<const f16x8*>(pa + k), acc, 0, 0, 0);
+  return acc;
+}
+// 32 x 32 block of B X: K-major rows of B; X as it lies, [K][ldx], through the transposing read
+__device__ __forceinline__ f32x16 small_block_x(const f16* b, int ldb, const f16* x, int ldx, int K, int lane) {
+  f32x16 acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  const f16* pa = b + (lane & 31) * ldb + 8 * (lane >> 5);
+  const int g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
+  const f16* px = x + (8 * (g >> 1) + j) * ldx + 16 * (g & 1) + 4 * q;
+#pragma unroll 4
+  for (int k = 0; k < K; k += 16) {
+    s16x4 t[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) t[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(px + (k + 4 * h) * ldx));
+    f16x8 xf;
+    __builtin_memcpy(&xf, t, 16);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, *reinterpret_cast<const f16x8*>(pa + k), acc, 0, 0, 0);
+  }
+  return acc;
+}
+// 16 values in the transposed accumulator layout -> the block at dst, rows of ld
+__device__ __forceinline__ void small_put(f16* dst, int ld, const float (&v)[16], int lane) {
+  f16* const row = dst + (lane & 31) * ld + 4 * (lane >> 5);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<f16x4*>(row + 8 * q) = f16x4{(f16)v[4 * q], (f16)v[4 * q + 1], (f16)v[4 * q + 2], (f16)v[4 * q + 3]};
+}
+
+template <typename T, int MP>
+__global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out, int rows, int cols, int lp,
+                                                        int steps, float scale) {
+  __shared__ __attribute__((aligned(16))) f16 small[small_lds(MP)];
+  __shared__ double red[NW];
+  constexpr int LDM = MP + 8, RB = MP / 32;
+  const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), ldx = lp + 8;
+  f16* const xs = small;
+  f16* const ds = xs + MP * ldx;
+  f16* const bs = ds + MP * LDM;
+  const bool tall = rows > cols;
+  const int m = tall ? cols : rows, l = tall ? rows : cols;
+  const size_t si = tall ? 1 : cols, sj = tall ? cols : 1;   // strides of X in g and out
+  const int nb = RB * (lp / 32);
+  const size_t base = (size_t)blockIdx.x * rows * cols;
+  float x[SMALL_BLOCKS][16];
+  double ss = 0.0;
+#pragma unroll
+  for (int b = 0; b < SMALL_BLOCKS; ++b) {
+    const int blk = wv + NW * b, i = (blk % RB) * 32 + (lane & 31), j0 = (blk / RB) * 32 + 4 * (lane >> 5);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int j = j0 + 8 * (r >> 2) + (r & 3);
+      const bool in = blk < nb && i < m && j < l;
+      x[b][r] = in ? elem<T>::load(g + base + i * si + j * sj) : 0.f;
+      ss += (double)x[b][r] * (double)x[b][r];
+    }
+  }
+  ss = wave_sum_f64(ss);
+  if (lane == 0) red[wv] = ss;
+  __syncthreads();
+  ss = 0.0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) ss += red[w];
+  const double norm = sqrt(ss);
+  int e = 0;
+  if (norm > 0.0 && norm < 1e300) {
+    frexp(norm, &e);
+    e = -e;
+  }
+  const float f = (float)(ldexp(1.0, -e) / (norm + NS_EPS));   // through 2^e: no factor leaves fp32's range
+#pragma unroll
+  for (int b = 0; b < SMALL_BLOCKS; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x[b][r] = ldexpf(x[b][r], e) * f;
+  for (int step = 0; step < steps; ++step) {
+    const StepCoef co = step_coef(step);
+#pragma unroll
+    for (int b = 0; b < SMALL_BLOCKS; ++b) {
+      const int blk = wv + NW * b;
+      if (blk < nb) {
+        float v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = x[b][r] * X_SCALE;
+        small_put(xs + (blk % RB) * 32 * ldx + (blk / RB) * 32, ldx, v, lane);
+      }
+    }
+    __syncthreads();
+    for (int blk = wv; blk < RB * RB; blk += NW) {
+      const int bi = blk % RB * 32, bj = blk / RB * 32;
+      const f32x16 acc = small_block(xs + bi * ldx, ldx, xs + bj * ldx, ldx, lp, lane);
+      float v[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        v[r] = acc[r] * (D_SCALE / (X_SCALE * X_SCALE));
+        if (bi + (lane & 31) == bj + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= co.t * D_SCALE;
+      }
+      small_put(ds + bi * LDM + bj, LDM, v, lane);
+    }
+    __syncthreads();
+    for (int blk = wv; blk < RB * RB; blk += NW) {
+      const int bi = blk % RB * 32, bj = blk / RB * 32;
+      const f32x16 acc = small_block(ds + bi * LDM, LDM, ds + bj * LDM, LDM, MP, lane);
+      float v[16];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f16x4 d = *reinterpret_cast<const f16x4*>(ds + (bi + (lane & 31)) * LDM + bj + 8 * q + 4 * (lane >> 5));
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[4 * q + c] = acc[4 * q + c] * (NS_C * B_SCALE / (D_SCALE * D_SCALE)) + (float)d[c] * (co.beta * B_SCALE / D_SCALE);
+      }
+      small_put(bs + bi * LDM + bj, LDM, v, lane);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < SMALL_BLOCKS; ++b) {
+      const int blk = wv + NW * b;
+      if (blk < nb) {
+        const f32x16 acc = small_block_x(bs + (blk % RB) * 32 * LDM, LDM, xs + (blk / RB) * 32, ldx, MP, lane);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[b][r] = x[b][r] * co.alpha + acc[r] * (1.f / (X_SCALE * B_SCALE));
+      }
+    }
+    __syncthreads();   // xs, ds and bs have been read
+  }
+#pragma unroll
+  for (int b = 0; b < SMALL_BLOCKS; ++b) {
+    const int blk = wv + NW * b, i = (blk % RB) * 32 + (lane & 31), j0 = (blk / RB) * 32 + 4 * (lane >> 5);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int j = j0 + 8 * (r >> 2) + (r & 3);
+      if (blk < nb && i < m && j < l) out[base + i * si + j * sj] = f2bf(x[b][r] * scale);
+    }
+  }
+}
+
+inline bool orth_small(int mp, int lp) { return mp <= SMALL_MP && mp * lp <= SMALL_ELEMS; }
+
+template <typename T>
+static hipError_t launch_small(const moe_orth_shape& s, const T* g, bf16_t* o, int mp, int lp, float scale,
+                               hipStream_t st) {
+  const dim3 grid((unsigned)s.n), block(NTHR);
+  if (mp == 64)
+    MOE_LAUNCH("orth_small", (k_orth_small<T, 64>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, scale);
+  else
+    MOE_LAUNCH("orth_small", (k_orth_small<T, 128>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, scale);
+  return hipGetLastError();
+}
+
 inline int pad64(int v) { return (v + 63) & ~63; }
 
 }  // namespace
@@ -737,6 +906,9 @@ static void orth_enter(const moe_orth_shape& s, const OrthLayout& L, const T* g,
 hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o, float scale, void* scratch,
                                 hipStream_t st) {
   const OrthLayout L = orth_layout(s);
+  if (orth_small(L.mp, L.lp))
+    return s.dtype == MOE_BF16 ? launch_small(s, (const bf16_t*)g, (bf16_t*)o, L.mp, L.lp, scale, st)
+                               : launch_small(s, (const float*)g, (bf16_t*)o, L.mp, L.lp, scale, st);
   char* ws = reinterpret_cast<char*>(scratch);
   if (s.dtype == MOE_BF16) orth_enter(s, L, (const bf16_t*)g, ws, st);
   else orth_enter(s, L, (const float*)g, ws, st);

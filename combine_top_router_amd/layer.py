@@ -25,23 +25,35 @@ def _device(device) -> torch.device:
     return d
 
 
+# the raw handle of a device's current stream, without the Stream object that
+# torch.cuda.current_stream builds around it (2 us of a call of 8)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _OnDevice:
     """Checks and streams of the operators around the layer.  A call runs on `stream`, or on
     the current stream of the operator's own device; its buffers are reused from call to
     call, so calls of one operator on several streams have to be ordered by the caller."""
 
+    def _place(self, device):
+        self.device = _device(device)
+        self._index = self.device.index
+        L.load()
+
     def _check(self, t, shape, dtype, name):
-        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+        if t.dtype != dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
-    def _call(self, func, *args, stream=None):
-        s = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
-        if torch.cuda.current_device() == self.device.index:
-            func(*args, s)
+    def _stream(self, stream):
+        return _raw_stream(self._index) if stream is None else stream.cuda_stream
+
+    def _call(self, func, *args):
+        if torch.cuda.current_device() == self._index:
+            func(*args)
         else:
-            with torch.cuda.device(self.device):
-                func(*args, s)
+            with torch.cuda.device(self._index):
+                func(*args)
 
 
 class MoeNorm(_OnDevice):
@@ -52,7 +64,8 @@ class MoeNorm(_OnDevice):
     def __init__(self, T, H, kind=L.MOE_NORM_LAYER, dtype=L.MOE_BF16, eps=1e-5, device="cuda"):
         self.shape = L.MoeNormShape(T, H, dtype, kind, eps)
         scratch_b = L.moe_norm_scratch_bytes(self.shape)
-        dev = self.device = _device(device)
+        self._place(device)
+        dev = self.device
         dt = self.dtype = _DT[dtype]
         self._row, self._vec = torch.Size((T, H)), torch.Size((H,))
         self.y = torch.empty(T, H, dtype=dt, device=dev)
@@ -76,7 +89,7 @@ class MoeNorm(_OnDevice):
         self.sum = None if res is None else self._sum
         self.inputs = (x if res is None else self._sum, w, b is not None)
         self._call(L.moe_norm_fwd, self.shape, _p(x), _p(res), _p(w), _p(b), _p(self.sum), _p(self.y), _p(self.mean),
-                   _p(self.rstd), stream=stream)
+                   _p(self.rstd), self._stream(stream))
         return self.y
 
     def backward(self, dy, ds_in=None, stream=None):
@@ -88,7 +101,7 @@ class MoeNorm(_OnDevice):
         s, w, bias = self.inputs
         db = self.db if bias else None
         self._call(L.moe_norm_bwd, self.shape, _p(dy), _p(s), _p(w), _p(self.mean), _p(self.rstd), _p(ds_in),
-                   _p(self.dx), _p(self.dw), _p(db), _p(self.scratch), stream=stream)
+                   _p(self.dx), _p(self.dw), _p(db), _p(self.scratch), self._stream(stream))
         return {"dx": self.dx, "dw": self.dw, "db": db}
 
 
@@ -100,7 +113,8 @@ class BalanceLoss(_OnDevice):
     def __init__(self, T, E, k, device="cuda"):
         self.shape = L.MoeShape(T, 64, 64, E, k, 0, E, L.MOE_BF16, L.MOE_BWD_SAME, 1, L.MOE_FWD_SAME, 0, 0)
         scratch_b = L.moe_balance_scratch_bytes(self.shape)
-        dev = self.device = _device(device)
+        self._place(device)
+        dev = self.device
         f32 = torch.float32
         self._logits, self._idx, self._mask = torch.Size((T, E)), torch.Size((T, k)), torch.Size((T,))
         self.loss = torch.empty(1, dtype=f32, device=dev)
@@ -117,7 +131,7 @@ class BalanceLoss(_OnDevice):
             self._check(mask, self._mask, torch.uint8, "mask")
         self.inputs = (logits, mask, float(coef))
         self._call(L.moe_balance_fwd, self.shape, _p(logits), _p(topk_idx), _p(mask), coef, _p(self.loss),
-                   _p(self.counts), _p(self.prob), _p(self.scratch), stream=stream)
+                   _p(self.counts), _p(self.prob), _p(self.scratch), self._stream(stream))
         return self.loss
 
     def backward(self, d_loss=None, d_logits_in=None, out=None, stream=None):
@@ -133,7 +147,7 @@ class BalanceLoss(_OnDevice):
             self._check(out, self._logits, torch.float32, "out")
         logits, mask, coef = self.inputs
         self._call(L.moe_balance_bwd, self.shape, _p(logits), _p(self.counts), _p(mask), coef, _p(d_loss),
-                   _p(d_logits_in), _p(out), stream=stream)
+                   _p(d_logits_in), _p(out), self._stream(stream))
         return out
 
 
@@ -144,7 +158,8 @@ class Orthogonalizer(_OnDevice):
     def __init__(self, n, rows, cols, dtype=L.MOE_BF16, steps=5, device="cuda"):
         self.shape = L.MoeOrthShape(n, rows, cols, dtype, steps)
         scratch_b = L.moe_orth_scratch_bytes(self.shape)
-        dev = self.device = _device(device)
+        self._place(device)
+        dev = self.device
         self.dtype = _DT[dtype]
         self._size = torch.Size((n, rows, cols))
         self.o = None
@@ -158,7 +173,8 @@ class Orthogonalizer(_OnDevice):
             out = self.o
         else:
             self._check(out, self._size, torch.bfloat16, "out")
-        self._call(L.moe_orthogonalize, self.shape, _p(g), _p(out), scale, _p(self.scratch), stream=stream)
+        self._call(L.moe_orthogonalize, self.shape, _p(g), _p(out), scale, _p(self.scratch),
+                   self._stream(stream))
         return out
 
 
