@@ -24,6 +24,8 @@
 // thousandfold spread, next to 1.7e-3 for the output's own rounding to bf16 (plain fp16
 // iterates: up to 4e-2, bf16 ones: up to 3e-1, on the same matrices).
 #define MOE_GEMM_FW 256
+#include <math.h>
+
 #include "gemm_engine.h"
 
 namespace moe {
@@ -168,9 +170,6 @@ __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int
 }
 
 // ---- the products ----
-// C = P Q^T (NT) or P Q, one 64 x 64 tile a workgroup of four waves
-constexpr int TB = 64, TK = 64, TLD = TK + 8;
-
 enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_APPLY = 2, ORTH_LAST = 3 };
 
 struct OrthArgs {
@@ -194,88 +193,6 @@ struct StepCoef {
 __host__ __device__ inline StepCoef step_coef(int step) {
   const float t = step >= SHIFT_STEP ? 1.f : 0.f;
   return {t, NS_A + NS_B * t + NS_C * t * t, NS_B + 2.f * NS_C * t};
-}
-
-template <int OP>
-__global__ __launch_bounds__(256) void k_orth_tile(OrthArgs a) {
-  __shared__ __attribute__((aligned(16))) f16 ps[TB * TLD];
-  __shared__ __attribute__((aligned(16))) f16 qs[TB * TLD];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int z = blockIdx.z;
-  int i0, j0;
-  if (OP == ORTH_GRAM || OP == ORTH_POLY) {   // lower triangle of tiles
-    int ti = 0, rem = blockIdx.x;
-    while (rem > ti) rem -= ++ti;
-    i0 = ti * TB;
-    j0 = rem * TB;
-  } else {
-    i0 = blockIdx.y * TB;
-    j0 = blockIdx.x * TB;
-  }
-  const int K = OP == ORTH_GRAM ? a.lp : a.mp;
-  const size_t xo = (size_t)z * a.mp * a.lp, so = (size_t)z * a.mp * a.mp;
-  const f16* P = OP == ORTH_GRAM ? a.x + xo : OP == ORTH_POLY ? a.d + so : a.b + so;
-  const f16* Q = OP == ORTH_GRAM ? a.x + xo : OP == ORTH_POLY ? a.d + so : a.x + xo;
-  f32x16 acc;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-  const int wi = (wv & 1) * 32, wj = (wv >> 1) * 32;
-  for (int k0 = 0; k0 < K; k0 += TK) {
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int r = (tid >> 3) + 32 * q, c = (tid & 7) * 8;
-      *reinterpret_cast<f16x8*>(&ps[r * TLD + c]) = *reinterpret_cast<const f16x8*>(P + (size_t)(i0 + r) * K + k0 + c);
-      if (OP <= ORTH_POLY) {
-        *reinterpret_cast<f16x8*>(&qs[r * TLD + c]) =
-            *reinterpret_cast<const f16x8*>(Q + (size_t)(j0 + r) * K + k0 + c);
-      } else {
-        const f16x8 v = *reinterpret_cast<const f16x8*>(Q + (size_t)(k0 + r) * a.lp + j0 + c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) qs[(c + j) * TLD + r] = v[j];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < TK / 16; ++kk) {
-      const int kt = kk * 16 + (lane >> 5) * 8;
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-          *reinterpret_cast<const f16x8*>(&ps[(wi + (lane & 31)) * TLD + kt]),
-          *reinterpret_cast<const f16x8*>(&qs[(wj + (lane & 31)) * TLD + kt]), acc, 0, 0, 0);
-    }
-  }
-  const StepCoef co = step_coef(a.step);
-  const float f = a.step == 0 ? a.factor[z] : 1.f / X_SCALE;
-  const int j = j0 + wj + (lane & 31);
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int i = i0 + wi + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-    if (OP == ORTH_GRAM) {
-      const f16 v = (f16)(acc[r] * (f * f * D_SCALE) - (i == j ? co.t * D_SCALE : 0.f));
-      a.d[so + (size_t)i * a.mp + j] = v;
-      if (i0 != j0) a.d[so + (size_t)j * a.mp + i] = v;
-    } else if (OP == ORTH_POLY) {
-      const float dv = (float)a.d[so + (size_t)i * a.mp + j];
-      const f16 v = (f16)(acc[r] * (NS_C * B_SCALE / (D_SCALE * D_SCALE)) + dv * (co.beta * B_SCALE / D_SCALE));
-      a.b[so + (size_t)i * a.mp + j] = v;
-      if (i0 != j0) a.b[so + (size_t)j * a.mp + i] = v;
-    } else {
-      const size_t o = xo + (size_t)i * a.lp + j;
-      float xv = (float)a.x[o];
-      if (a.xlo) xv += lo_value(a.xlo[o]);
-      const float v = xv * (co.alpha * f) + acc[r] * (f / B_SCALE);
-      if (OP == ORTH_APPLY) {
-        const float s = v * X_SCALE;
-        const f16 h = (f16)s;
-        a.xn[o] = h;
-        if (a.xnlo) a.xnlo[o] = lo_code(s - (float)h);
-      } else if (i < a.m && j < a.l) {
-        const size_t base = (size_t)z * a.rows * a.cols;
-        const size_t oo = a.rows > a.cols ? (size_t)j * a.cols + i : (size_t)i * a.cols + j;
-        a.out[base + oo] = f2bf(v * a.scale);
-      }
-    }
-  }
 }
 
 // ---- the products on 256 x 256 tiles: jobs of the persistent tile stream ----
@@ -656,25 +573,238 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_stream(OrthArgs a, int n, int 
   run_stream(job, lds);
 }
 
-template <int OP>
-static void orth_product(const char* name, const OrthArgs& a, int n, bool wide, hipStream_t st) {
+// ---- the products on 128 x 128 and 64 x 64 tiles: one tile a workgroup ----
+// For matrices whose 256-row tiles leave CUs idle or mostly padding.  Such launches wait for
+// loads, not for MFMAs: the K steps ring through NS stages of LDS, so NS - 1 steps of
+// direct-to-LDS loads are in flight, with one barrier a step.
+template <int TILE> struct TileCfg;
+template <> struct TileCfg<64> { static constexpr int NS = 8, WAVES = 4, TMI = 1; };    // 2 x 2 waves of 32 x 32
+template <> struct TileCfg<128> { static constexpr int NS = 4, WAVES = 8, TMI = 2; };   // 2 x 4 waves of 64 x 32
+
+// MN-major rows of 64 (8 chunks): rows two apart in other halves of a row's 128 bytes, so the
+// four rows of a transposing read meet no bank twice; wider rows as in the engine
+template <int W>
+__device__ __forceinline__ int tile_mn_chunk(int r, int c) {
+  return W == 64 ? c ^ (((r >> 1) & 1) << 2) : mnmaj_chunk(r, c);
+}
+template <int W>
+__device__ __forceinline__ f16x8 tile_frag_mn(const bf16_t* s, int base, int kk, int lane) {
+  const int g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3, col = base + 16 * (g & 1) + 4 * q;
+  s16x4 v[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = kk * 16 + 8 * (g >> 1) + 4 * h + j;
+    v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(s + r * W + (tile_mn_chunk<W>(r, col >> 3) << 3) + (col & 7)));
+  }
+  f16x8 out;
+  __builtin_memcpy(&out, v, 16);
+  return out;
+}
+
+template <int OP, int TILE>
+__global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, 1) void k_orth_tile(OrthArgs a, int tm, int tn) {
+  using C = TileCfg<TILE>;
   constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
-  if (wide) {
-    const int tm = (int)ceil_div(a.mp, BM), tn = (int)ceil_div(a.lp, BN);
-    const int64_t items = (int64_t)n * (SYM ? tm * (tm + 1) / 2 : tm * tn);
-    const dim3 grid((unsigned)grid_for(items));
+  constexpr int OPER = TILE * BK, STAGE = 2 * OPER;                  // elements
+  constexpr int LP = OPER * 2 / 1024 / C::WAVES;                     // 1 KB loads of one operand a wave and step
+  static_assert(LP * C::WAVES * 512 == OPER, "wave loads divide among the waves");
+  __shared__ __attribute__((aligned(16))) bf16_t lds[C::NS * STAGE];
+  const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
+  const int per = SYM ? tm * (tm + 1) / 2 : tm * tn;
+  const int z = uni(blockIdx.x / per);
+  int rem = uni(blockIdx.x - z * per), ti = 0;
+  if (SYM) {
+    while (rem > ti) rem -= ++ti;
+  } else {
+    ti = uni(rem % tm);
+    rem = uni(rem / tm);
+  }
+  const int i0 = ti * TILE, j0 = rem * TILE, ldn = SYM ? a.mp : a.lp;
+  const int K = OP == ORTH_GRAM ? a.lp : a.mp, nk = K / BK;
+  const size_t xo = (size_t)z * a.mp * a.lp, so = (size_t)z * a.mp * a.mp;
+  const bf16_t* pa = reinterpret_cast<const bf16_t*>(OP == ORTH_GRAM ? a.x + xo : OP == ORTH_POLY ? a.d + so : a.b + so);
+  const bf16_t* pb = reinterpret_cast<const bf16_t*>(OP == ORTH_POLY ? a.d + so : a.x + xo);
+  const bf16_t *la[LP], *lb[LP];
+#pragma unroll
+  for (int q = 0; q < LP; ++q) {
+    const int slot = (q * C::WAVES + wv) * 64 + lane;
+    int r, c;
+    kmaj_slot(slot, r, c);
+    la[q] = pa + (size_t)min(i0 + r, a.mp - 1) * K + c * 8;
+    if (SYM) {
+      lb[q] = pb + (size_t)min(j0 + r, a.mp - 1) * K + c * 8;
+    } else {
+      r = slot / (TILE / 8);
+      c = tile_mn_chunk<TILE>(r, slot % (TILE / 8));
+      lb[q] = pb + (size_t)r * a.lp + min(j0 + c * 8, a.lp - 8);   // past the edge: any columns, not stored
+    }
+  }
+  const size_t bstep = SYM ? (size_t)BK : (size_t)BK * a.lp;
+  auto issue = [&](int kt) {
+    bf16_t* const st = lds + (kt % C::NS) * STAGE;
+#pragma unroll
+    for (int q = 0; q < LP; ++q) {
+      dma16(la[q] + kt * BK, st + (q * C::WAVES + wv) * 512);
+      dma16(lb[q] + kt * bstep, st + OPER + (q * C::WAVES + wv) * 512);
+    }
+  };
+  const int wm = wv & 1, wn = wv >> 1, ib = wm * 32 * C::TMI, jb = wn * 32;   // the wave's first row and column
+  f32x16 acc[C::TMI];
+#pragma unroll
+  for (int mi = 0; mi < C::TMI; ++mi)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[mi][r] = 0.f;
+#pragma unroll
+  for (int kt = 0; kt < C::NS - 1; ++kt)
+    if (kt < nk) issue(kt);
+  for (int kt = 0; kt < nk; ++kt) {
+    // step kt has landed when at most the NS - 2 later steps' loads are out
+    if (nk - 1 - kt >= C::NS - 2) {
+      static_assert(2 * LP * (C::NS - 2) < 64, "vmcnt counts to 63");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * LP * (C::NS - 2)) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    if (kt + C::NS - 1 < nk) issue(kt + C::NS - 1);   // into the stage read one step ago
+    const bf16_t* const as = lds + (kt % C::NS) * STAGE;
+    const bf16_t* const bs = as + OPER;
+#pragma unroll
+    for (int kk = 0; kk < BK / 16; ++kk) {
+      const f16x8 bf = SYM ? as_f16(frag_kmaj(bs, jb, kk, lane)) : tile_frag_mn<TILE>(bs, jb, kk, lane);
+#pragma unroll
+      for (int mi = 0; mi < C::TMI; ++mi)
+        acc[mi] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf, as_f16(frag_kmaj(as, ib + mi * 32, kk, lane)), acc[mi], 0, 0, 0);
+    }
+  }
+  // lane l: row l % 32 of each block, columns 8q + 4 (l / 32) .. + 3
+  if (j0 + jb >= ldn) return;
+  const StepCoef co = step_coef(a.step);
+  const float f = a.step == 0 ? a.factor[z] : 1.f / X_SCALE;
+  float ca, cb;
+  if (OP == ORTH_GRAM) { cb = f * f * D_SCALE; ca = 0.f; }
+  else if (OP == ORTH_POLY) { cb = NS_C * B_SCALE / (D_SCALE * D_SCALE); ca = co.beta * B_SCALE / D_SCALE; }
+  else { const float sc = OP == ORTH_APPLY ? X_SCALE : a.scale; cb = f / B_SCALE * sc; ca = co.alpha * f * sc; }
+#pragma unroll
+  for (int mi = 0; mi < C::TMI; ++mi) {
+    const int i = i0 + ib + mi * 32 + (lane & 31), j = j0 + jb;
+    if (i0 + ib + mi * 32 >= a.mp) break;
+    const size_t at = (size_t)i * ldn + j;
+    float v[16];
+    if constexpr (OP == ORTH_GRAM) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        v[r] = acc[mi][r] * cb;
+        if (i == j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= co.t * D_SCALE;
+      }
+    } else {
+      const f16* const side = OP == ORTH_POLY ? a.d + so : a.x + xo;
+      i32x4 ch[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) ch[s] = *reinterpret_cast<const i32x4*>(side + at + 16 * s + 8 * (lane >> 5));
+      untrans_chunks_f16(ch, v);
+      if (!SYM && a.xlo) add_codes(*reinterpret_cast<const i32x4*>(a.xlo + xo + at + 16 * (lane >> 5)), v);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] = acc[mi][r] * cb + v[r] * ca;
+    }
     if constexpr (OP == ORTH_LAST) {
-      if (a.rows > a.cols) {
-        MOE_LAUNCH(name, (k_orth_stream<OP, true>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
-        return;
+      bf16_t* const out = a.out + (size_t)z * a.rows * a.cols;
+      if (a.rows > a.cols) {   // transposed back: 32 lanes write 64 bytes of a row
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int jj = j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+          if (i < a.m && jj < a.l) out[(size_t)jj * a.cols + i] = f2bf(v[r]);
+        }
+      } else {
+        f32x16 b;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) b[r] = v[r];
+        i32x4 ch[2];
+        trans_chunks(b, ch);
+        if (i < a.m) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int jj = j + 16 * s + 8 * (lane >> 5);
+            bf16_t* const q = out + (size_t)i * a.cols + jj;
+            if (jj + 8 <= a.l) {
+              *reinterpret_cast<i32x4_a2*>(q) = ch[s];
+            } else {
+              for (int e = 0; e < 8; ++e)
+                if (jj + e < a.l) q[e] = (bf16_t)((uint32_t)ch[s][e >> 1] >> (16 * (e & 1)));
+            }
+          }
+        }
+      }
+    } else {
+      f16* const out = OP == ORTH_GRAM ? a.d + so : OP == ORTH_POLY ? a.b + so : a.xn + xo;
+      i32x4 ch[2];
+      trans_chunks_f16(v, ch);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) *reinterpret_cast<i32x4*>(out + at + 16 * s + 8 * (lane >> 5)) = ch[s];
+      if (SYM && i0 != j0) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          out[(size_t)(j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * ldn + i] = (f16)v[r];
+      }
+      if (OP == ORTH_APPLY && a.xnlo) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] -= (float)(f16)v[r];
+        *reinterpret_cast<i32x4*>(a.xnlo + xo + at + 16 * (lane >> 5)) = trans_codes(v);
       }
     }
-    MOE_LAUNCH(name, (k_orth_stream<OP, false>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
-  } else {
-    const int tm = a.mp / TB, tn = a.lp / TB;
-    const dim3 grid = SYM ? dim3((unsigned)(tm * (tm + 1) / 2), 1, (unsigned)n) : dim3((unsigned)tn, (unsigned)tm, (unsigned)n);
-    MOE_LAUNCH(name, k_orth_tile<OP>, grid, dim3(256), 0, st, a);
   }
+}
+
+// The tile of a product, M x N over K in n matrices (M x M by halves when symmetric): the one
+// of least estimated time.  A tile of a round (one on each CU) takes a start and an end, e,
+// and c a K step of 64; measured on one MI355X, in us:
+//            64 rows        128 rows       256 rows
+//   e        3.2 / 4.5      6 / 8          12           (symmetric / not)
+//   c        0.27           0.53           1.25 on a few CUs, 2.15 on all (the stream is
+//                                          then bound by what the L2s and the MFMAs deliver)
+// Both sides, whole products: 5 of 384 over K = 1024, symmetric, 7.4 / 11.6 / 27.3; 32 of 384
+// over 1024: 26 / 15 / 28; 8 of 768 x 2048 over 768: 68 / 44 / 33; 128 of 768 over 2048,
+// symmetric: 218 with 256 rows.
+static int orth_tile_size(bool sym, int n, int M, int N, int K) {
+  const double steps = K / 64.0, cus = num_cus();
+  int best = 256;
+  double least = 0.0;
+  for (int t = 256; t >= 64; t /= 2) {
+    const int64_t tm = ceil_div(M, t), tn = ceil_div(N, t), items = n * (sym ? tm * (tm + 1) / 2 : tm * tn);
+    const double fill = items < cus ? items / cus : 1.0;
+    const double e = t == 256 ? 12.0 : t == 128 ? (sym ? 6.0 : 8.0) : (sym ? 3.2 : 4.5);
+    const double c = t == 256 ? 1.25 + 0.9 * fill : t == 128 ? 0.53 : 0.27;
+    const double us = ceil((double)items / cus) * (e + c * steps);
+    if (t == 256 || us < least) {
+      best = t;
+      least = us;
+    }
+  }
+  return best;
+}
+
+template <int OP, int TILE>
+static void orth_tiles(const char* name, const OrthArgs& a, int n, hipStream_t st) {
+  constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
+  const int tm = (int)ceil_div(a.mp, TILE), tn = (int)ceil_div(a.lp, TILE);
+  const int per = SYM ? tm * (tm + 1) / 2 : tm * tn;
+  MOE_LAUNCH(name, (k_orth_tile<OP, TILE>), dim3((unsigned)n * per), dim3(64 * TileCfg<TILE>::WAVES), 0, st, a, tm, tn);
+}
+
+template <int OP>
+static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t st) {
+  constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
+  const int tile = orth_tile_size(SYM, n, a.mp, SYM ? a.mp : a.lp, OP == ORTH_GRAM ? a.lp : a.mp);
+  if (tile == 64) return orth_tiles<OP, 64>(name, a, n, st);
+  if (tile == 128) return orth_tiles<OP, 128>(name, a, n, st);
+  const int tm = (int)ceil_div(a.mp, BM), tn = (int)ceil_div(a.lp, BN);
+  const dim3 grid((unsigned)grid_for((int64_t)n * (SYM ? tm * (tm + 1) / 2 : tm * tn)));
+  if constexpr (OP == ORTH_LAST) {
+    if (a.rows > a.cols) {
+      MOE_LAUNCH(name, (k_orth_stream<OP, true>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
+      return;
+    }
+  }
+  MOE_LAUNCH(name, (k_orth_stream<OP, false>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
 }
 
 // ---- small matrices: the whole iteration in one workgroup ----
@@ -912,7 +1042,6 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   char* ws = reinterpret_cast<char*>(scratch);
   if (s.dtype == MOE_BF16) orth_enter(s, L, (const bf16_t*)g, ws, st);
   else orth_enter(s, L, (const float*)g, ws, st);
-  const bool wide = L.mp >= 256;
   for (int i = 0; i < s.steps; ++i) {
     OrthArgs a{};
     a.mp = L.mp; a.lp = L.lp; a.m = L.m; a.l = L.l; a.rows = s.rows; a.cols = s.cols;
@@ -927,10 +1056,10 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
     a.xnlo = i < LO_STEPS ? reinterpret_cast<uint8_t*>(ws + L.off_lo[(i + 1) & 1]) : nullptr;
     a.out = (bf16_t*)o;
     a.scale = scale;
-    orth_product<ORTH_GRAM>("orth_gram", a, s.n, wide, st);
-    orth_product<ORTH_POLY>("orth_poly", a, s.n, wide, st);
-    if (i == s.steps - 1) orth_product<ORTH_LAST>("orth_last", a, s.n, wide, st);
-    else orth_product<ORTH_APPLY>("orth_apply", a, s.n, wide, st);
+    orth_product<ORTH_GRAM>("orth_gram", a, s.n, st);
+    orth_product<ORTH_POLY>("orth_poly", a, s.n, st);
+    if (i == s.steps - 1) orth_product<ORTH_LAST>("orth_last", a, s.n, st);
+    else orth_product<ORTH_APPLY>("orth_apply", a, s.n, st);
   }
   return hipGetLastError();
 }
