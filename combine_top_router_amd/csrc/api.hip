@@ -781,8 +781,9 @@ int moe_norm_fwd(const moe_norm_shape* shape, const void* x, const void* res, co
   return hip_status(launch_norm_fwd(*shape, x, res, w, b, sum, y, mean, rstd, (hipStream_t)stream), __func__);
 }
 
-int moe_norm_bwd(const moe_norm_shape* shape, const void* dy, const void* s, const void* w, const float* mean,
-                 const float* rstd, const void* ds_in, void* dx, void* dw, void* db, void* scratch, void* stream) {
+int moe_norm_bwd(const moe_norm_shape* shape, const void* dy, const void* s, const void* res, const void* w,
+                 const float* mean, const float* rstd, const void* ds_in, void* dx, void* dw, void* db, void* scratch,
+                 void* stream) {
   int rc = check_norm(shape);
   if (rc) return rc;
   REQUIRE(dw);
@@ -794,9 +795,9 @@ int moe_norm_bwd(const moe_norm_shape* shape, const void* dy, const void* s, con
     REQUIRE(rstd);
     REQUIRE(dx);
     if (shape->kind == MOE_NORM_LAYER) REQUIRE(mean);
-    if (dx == dy || dx == s) return fail(MOE_EINVAL, "%s: dx may be neither dy nor s", __func__);
+    if (dx == dy || dx == s || dx == res) return fail(MOE_EINVAL, "%s: dx may be none of dy, s and res", __func__);
   }
-  return hip_status(launch_norm_bwd(*shape, dy, s, w, mean, rstd, ds_in, dx, dw, db, at<float>(scratch, 0),
+  return hip_status(launch_norm_bwd(*shape, dy, s, res, w, mean, rstd, ds_in, dx, dw, db, at<float>(scratch, 0),
                                     (hipStream_t)stream),
                     __func__);
 }

@@ -108,7 +108,7 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float (*red)[2]) {
 }
 
 template <int TPR>
-constexpr int wg_threads() { return TPR > 256 ? TPR : 256; }
+constexpr int wg_threads() { return TPR > 64 ? TPR : 256; }
 
 // Forward, a row in the registers of TPR threads (H <= TPR EPT).  The norm is taken of the
 // fp32 sum, not of the sum rounded to the stored type: y then carries one rounding instead
@@ -248,22 +248,25 @@ __global__ __launch_bounds__(LONG_T) void k_norm_fwd_long(const T* x, const T* r
 
 // Backward, rows in registers: workgroup g takes rows g, g + gridDim.x, ... (times the rows
 // it holds at once) and leaves its share of dw and db in part[g] and part[G + g].
-template <typename T, int TPR, int EPT, bool RMS>
+template <typename T, int TPR, int EPT, bool RMS, bool HAS_B>
 __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_bwd(const T* __restrict__ dy, const T* __restrict__ s,
-                                                               const T* __restrict__ w,
+                                                               const T* __restrict__ res, const T* __restrict__ w,
                                                                const float* __restrict__ mean,
                                                                const float* __restrict__ rstd, const T* ds_in, int T_,
-                                                               int H, T* dx, float* __restrict__ part, int has_b) {
+                                                               int H, T* dx, float* __restrict__ part) {
   constexpr int V = rowvec<T>::V, NV = EPT / V, GROUPS = wg_threads<TPR>() / TPR;
   __shared__ float red[2][TPR / 64][2];
   __shared__ float fold[GROUPS > 1 ? GROUPS * TPR * EPT : 1];
   const int group = (int)threadIdx.x / TPR, lane = threadIdx.x % TPR;
-  float wv[NV][V], dwa[NV][V], dba[NV][V];
+  float wv[NV][V], dwa[NV][V], dba[HAS_B ? NV : 1][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     load_cols(w, (lane + i * TPR) * V, H, wv[i]);
 #pragma unroll
-    for (int j = 0; j < V; ++j) dwa[i][j] = dba[i][j] = 0.f;
+    for (int j = 0; j < V; ++j) {
+      dwa[i][j] = 0.f;
+      if (HAS_B) dba[i][j] = 0.f;
+    }
   }
   const float inv_h = 1.f / (float)H;
   int par = 0;
@@ -276,6 +279,15 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_bwd(const T* __restr
       load_cols(dy + off, (lane + i * TPR) * V, H, g[i]);
     }
     const float mu = RMS ? 0.f : mean[t], rs = rstd[t];
+    if (res) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float r[V];
+        load_cols(res + off, (lane + i * TPR) * V, H, r);
+#pragma unroll
+        for (int j = 0; j < V; ++j) xh[i][j] += r[j];
+      }
+    }
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -283,7 +295,7 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_bwd(const T* __restr
       for (int j = 0; j < V; ++j) {   // columns at or past H hold dy = 0
         xh[i][j] = (xh[i][j] - mu) * rs;
         dwa[i][j] += g[i][j] * xh[i][j];
-        dba[i][j] += g[i][j];
+        if (HAS_B) dba[i][j] += g[i][j];
         g[i][j] *= wv[i][j];
         s1 += g[i][j];
         s2 += g[i][j] * xh[i][j];
@@ -326,21 +338,19 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_bwd(const T* __restr
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int c = (lane + i * TPR) * V + j;
-          if (c < H) out[c] = a[i][j];
-        }
+        for (int q = 0; q < V; q += 4)
+          store_cols<float>(out, (lane + i * TPR) * V + q, H, *reinterpret_cast<float(*)[4]>(&a[i][q]));
     }
   };
   leave(dwa, part + (size_t)blockIdx.x * H);
-  if (has_b) leave(dba, part + ((size_t)gridDim.x + blockIdx.x) * H);
+  if constexpr (HAS_B) leave(dba, part + ((size_t)gridDim.x + blockIdx.x) * H);
 }
 
 // Backward of the long rows: dx row by row, then dw and db column by column over slices of
 // the rows.
 template <typename T, bool RMS>
 __global__ __launch_bounds__(LONG_T) void k_norm_dx_long(const T* __restrict__ dy, const T* __restrict__ s,
-                                                         const T* __restrict__ w, const float* __restrict__ mean,
+                                                         const T* __restrict__ res, const T* __restrict__ w, const float* __restrict__ mean,
                                                          const float* __restrict__ rstd, const T* ds_in, int T_, int H,
                                                          T* dx) {
   constexpr int V = rowvec<T>::V;
@@ -349,10 +359,19 @@ __global__ __launch_bounds__(LONG_T) void k_norm_dx_long(const T* __restrict__ d
   for (int64_t t = blockIdx.x; t < T_; t += gridDim.x, par ^= 1) {
     const size_t off = (size_t)t * H;
     const float mu = RMS ? 0.f : mean[t], rs = rstd[t];
+    auto row = [&](int c, float (&v)[V]) {
+      load_cols(s + off, c, H, v);
+      if (res) {
+        float r[V];
+        load_cols(res + off, c, H, r);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] += r[j];
+      }
+    };
     float s1 = 0.f, s2 = 0.f;
     for (int c = threadIdx.x * V; c < H; c += LONG_T * V) {
       float xv[V], g[V], wv[V];
-      load_cols(s + off, c, H, xv);
+      row(c, xv);
       load_cols(dy + off, c, H, g);
       load_cols(w, c, H, wv);
 #pragma unroll
@@ -367,7 +386,7 @@ __global__ __launch_bounds__(LONG_T) void k_norm_dx_long(const T* __restrict__ d
     s2 /= (float)H;
     for (int c = threadIdx.x * V; c < H; c += LONG_T * V) {
       float xv[V], g[V], wv[V];
-      load_cols(s + off, c, H, xv);
+      row(c, xv);
       load_cols(dy + off, c, H, g);
       load_cols(w, c, H, wv);
 #pragma unroll
@@ -385,6 +404,7 @@ __global__ __launch_bounds__(LONG_T) void k_norm_dx_long(const T* __restrict__ d
 
 template <typename T, bool RMS>
 __global__ __launch_bounds__(256) void k_norm_dw_long(const T* __restrict__ dy, const T* __restrict__ s,
+                                                      const T* __restrict__ res,
                                                       const float* __restrict__ mean, const float* __restrict__ rstd,
                                                       int T_, int H, float* __restrict__ part, int has_b) {
   const int c = (int)blockIdx.x * 256 + (int)threadIdx.x;
@@ -392,7 +412,8 @@ __global__ __launch_bounds__(256) void k_norm_dw_long(const T* __restrict__ dy, 
   float a = 0.f, d = 0.f;
   for (int64_t t = blockIdx.y; t < T_; t += gridDim.y) {
     const float g = elem<T>::load(dy + (size_t)t * H + c);
-    a += g * ((elem<T>::load(s + (size_t)t * H + c) - (RMS ? 0.f : mean[t])) * rstd[t]);
+    const float v = elem<T>::load(s + (size_t)t * H + c) + (res ? elem<T>::load(res + (size_t)t * H + c) : 0.f);
+    a += g * ((v - (RMS ? 0.f : mean[t])) * rstd[t]);
     d += g;
   }
   part[(size_t)blockIdx.y * H + c] = a;
@@ -427,24 +448,39 @@ inline unsigned row_grid(int64_t wgs) { return (unsigned)(wgs < (1 << 20) ? wgs 
 
 }  // namespace
 
-// Shares of dw: workgroups of the backward, or row slices of the long rows
+// Shares of dw: workgroups of the backward, or row slices of the long rows.  1024 (512 of
+// four times the threads): at 16384 x 4096 bf16 with a residual 256 / 512 / 1024 / 2048 take
+// 320 / 198 / 136 / 145 us, too few rows in flight on one side and more shares than rows are
+// worth on the other.
 int norm_parts(const moe_norm_shape& s) {
   if (s.T == 0) return 0;
   const int rows = s.H <= 1024 ? 4 : 1;   // rows a workgroup holds at once
-  const int64_t most = s.H > NORM_REG_COLS ? 16 : 512;
+  const int64_t most = s.H > NORM_REG_COLS ? 16 : s.H > 4096 ? 512 : 1024;
   const int64_t g = ceil_div(s.T, rows);
   return (int)(g < most ? g : most);
 }
 
 // Threads and registers of a row: 16 values a thread at most, so that the backward's rows,
 // weights and two sums (5 x 16) fit without spilling; one wave up to 1024 columns, then 256
-// threads to 4096 and 1024 threads to 16384.
-#define NORM_REG_DISPATCH(H, CALL)             \
+// threads to 4096 and 1024 threads to 16384.  32 values in fewer threads, with fewer barriers,
+// lose: 16384 x 4096 with 128 threads takes 109 us forward and 195 backward, against 95 and
+// 136.  The forward holds less and takes 512 threads from 2048 to 4096 columns: 95 us against
+// 100 with 256.
+#define NORM_BWD_DISPATCH(H, CALL)             \
   do {                                         \
     if ((H) <= 512) { CALL(64, 8); }           \
     else if ((H) <= 1024) { CALL(64, 16); }    \
     else if ((H) <= 2048) { CALL(256, 8); }    \
     else if ((H) <= 4096) { CALL(256, 16); }   \
+    else if ((H) <= 8192) { CALL(1024, 8); }   \
+    else { CALL(1024, 16); }                   \
+  } while (0)
+#define NORM_FWD_DISPATCH(H, CALL)             \
+  do {                                         \
+    if ((H) <= 512) { CALL(64, 8); }           \
+    else if ((H) <= 1024) { CALL(64, 16); }    \
+    else if ((H) <= 2048) { CALL(256, 8); }    \
+    else if ((H) <= 4096) { CALL(512, 8); }    \
     else if ((H) <= 8192) { CALL(1024, 8); }   \
     else { CALL(1024, 16); }                   \
   } while (0)
@@ -462,31 +498,31 @@ static hipError_t norm_fwd(const moe_norm_shape& s, const void* x_, const void* 
 #define CALL(TPR, EPT)                                                                                          \
   MOE_LAUNCH("norm_fwd", (k_norm_fwd<T, TPR, EPT, RMS>), dim3(row_grid(ceil_div(s.T, wg_threads<TPR>() / TPR))), \
              dim3(wg_threads<TPR>()), 0, st, x, res, w, b, s.T, s.H, s.eps, sum, y, mean, rstd)
-  NORM_REG_DISPATCH(s.H, CALL);
+  NORM_FWD_DISPATCH(s.H, CALL);
 #undef CALL
   return hipGetLastError();
 }
 
-template <typename T, bool RMS>
-static hipError_t norm_bwd(const moe_norm_shape& s, const void* dy_, const void* sum_, const void* w_,
-                           const float* mean, const float* rstd, const void* ds_in_, void* dx_, void* dw, void* db,
-                           float* part, hipStream_t st) {
-  const T *dy = (const T*)dy_, *sum = (const T*)sum_, *w = (const T*)w_, *ds_in = (const T*)ds_in_;
+template <typename T, bool RMS, bool HAS_B>
+static hipError_t norm_bwd(const moe_norm_shape& s, const void* dy_, const void* sum_, const void* res_,
+                           const void* w_, const float* mean, const float* rstd, const void* ds_in_, void* dx_,
+                           void* dw, void* db, float* part, hipStream_t st) {
+  const T *dy = (const T*)dy_, *sum = (const T*)sum_, *res = (const T*)res_, *w = (const T*)w_, *ds_in = (const T*)ds_in_;
   T* dx = (T*)dx_;
-  const int G = norm_parts(s), has_b = db != nullptr;
+  const int G = norm_parts(s);
   if (s.T > 0 && s.H > NORM_REG_COLS) {
-    MOE_LAUNCH("norm_dx", (k_norm_dx_long<T, RMS>), dim3(row_grid(s.T)), dim3(LONG_T), 0, st, dy, sum, w, mean, rstd,
-               ds_in, s.T, s.H, dx);
+    MOE_LAUNCH("norm_dx", (k_norm_dx_long<T, RMS>), dim3(row_grid(s.T)), dim3(LONG_T), 0, st, dy, sum, res, w, mean,
+               rstd, ds_in, s.T, s.H, dx);
     MOE_LAUNCH("norm_dw", (k_norm_dw_long<T, RMS>), dim3((unsigned)ceil_div(s.H, 256), (unsigned)G), dim3(256), 0, st,
-               dy, sum, mean, rstd, s.T, s.H, part, has_b);
+               dy, sum, res, mean, rstd, s.T, s.H, part, HAS_B);
   } else if (s.T > 0) {
-#define CALL(TPR, EPT)                                                                                       \
-  MOE_LAUNCH("norm_bwd", (k_norm_bwd<T, TPR, EPT, RMS>), dim3((unsigned)G), dim3(wg_threads<TPR>()), 0, st, dy, \
-             sum, w, mean, rstd, ds_in, s.T, s.H, dx, part, has_b)
-    NORM_REG_DISPATCH(s.H, CALL);
+#define CALL(TPR, EPT)                                                                                              \
+  MOE_LAUNCH("norm_bwd", (k_norm_bwd<T, TPR, EPT, RMS, HAS_B>), dim3((unsigned)G), dim3(wg_threads<TPR>()), 0, st, dy, \
+             sum, res, w, mean, rstd, ds_in, s.T, s.H, dx, part)
+    NORM_BWD_DISPATCH(s.H, CALL);
 #undef CALL
   }
-  MOE_LAUNCH("norm_fold", k_norm_fold<T>, dim3((unsigned)ceil_div(s.H, FOLD_COLS), has_b ? 2u : 1u),
+  MOE_LAUNCH("norm_fold", k_norm_fold<T>, dim3((unsigned)ceil_div(s.H, FOLD_COLS), HAS_B ? 2u : 1u),
              dim3(FOLD_COLS * FOLD_GROUPS), 0, st, part, G, s.H, (T*)dw, (T*)db);
   return hipGetLastError();
 }
@@ -501,15 +537,19 @@ hipError_t launch_norm_fwd(const moe_norm_shape& s, const void* x, const void* r
              : norm_fwd<float, false>(s, x, res, w, b, sum, y, mean, rstd, st);
 }
 
-hipError_t launch_norm_bwd(const moe_norm_shape& s, const void* dy, const void* sum, const void* w, const float* mean,
-                           const float* rstd, const void* ds_in, void* dx, void* dw, void* db, float* part,
-                           hipStream_t st) {
-  const bool rms = s.kind == MOE_NORM_RMS;
+template <typename T, bool RMS, class... A>
+static hipError_t norm_bwd_b(bool has_b, A... a) {
+  return has_b ? norm_bwd<T, RMS, true>(a...) : norm_bwd<T, RMS, false>(a...);
+}
+hipError_t launch_norm_bwd(const moe_norm_shape& s, const void* dy, const void* sum, const void* res, const void* w,
+                           const float* mean, const float* rstd, const void* ds_in, void* dx, void* dw, void* db,
+                           float* part, hipStream_t st) {
+  const bool rms = s.kind == MOE_NORM_RMS, b = db != nullptr;
   if (s.dtype == MOE_BF16)
-    return rms ? norm_bwd<bf16_t, true>(s, dy, sum, w, mean, rstd, ds_in, dx, dw, db, part, st)
-               : norm_bwd<bf16_t, false>(s, dy, sum, w, mean, rstd, ds_in, dx, dw, db, part, st);
-  return rms ? norm_bwd<float, true>(s, dy, sum, w, mean, rstd, ds_in, dx, dw, db, part, st)
-             : norm_bwd<float, false>(s, dy, sum, w, mean, rstd, ds_in, dx, dw, db, part, st);
+    return rms ? norm_bwd_b<bf16_t, true>(b, s, dy, sum, res, w, mean, rstd, ds_in, dx, dw, db, part, st)
+               : norm_bwd_b<bf16_t, false>(b, s, dy, sum, res, w, mean, rstd, ds_in, dx, dw, db, part, st);
+  return rms ? norm_bwd_b<float, true>(b, s, dy, sum, res, w, mean, rstd, ds_in, dx, dw, db, part, st)
+             : norm_bwd_b<float, false>(b, s, dy, sum, res, w, mean, rstd, ds_in, dx, dw, db, part, st);
 }
 
 }  // namespace moe

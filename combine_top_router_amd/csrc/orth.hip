@@ -109,12 +109,11 @@ __global__ __launch_bounds__(256) void k_orth_sumsq(const T* __restrict__ g, int
 // X0 (hi, and lo for fp32 input) [m_p, l_p] of each matrix, padded with zeros, from g
 // [rows, cols] (transposed when rows > cols) times 2^e, where 2^e brings the norm into
 // [2^14, 2^15); factor[matrix] = 2^-e / (norm + eps) turns stored values into X0.  One
-// workgroup makes 64 rows by up to ENTER_TILES tiles of 64 columns.
-constexpr int ENTER_TILES = 8;
+// workgroup makes 64 rows by `tiles` tiles of 64 columns.
 template <typename T, bool TR>
 __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int rows, int cols,
                                                     const double* __restrict__ part, int chunks, int mp, int lp,
-                                                    f16* __restrict__ hi, uint8_t* __restrict__ lo,
+                                                    int tiles, f16* __restrict__ hi, uint8_t* __restrict__ lo,
                                                     float* __restrict__ factor) {
   __shared__ float tile[TR ? 64 : 1][65];
   static_assert(NORM_CHUNKS <= 64, "one lane a share");
@@ -130,8 +129,8 @@ __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int
   const int tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;   // rows tr, tr + 32; 8 columns
   const int r0 = blockIdx.y * 64;   // of X
   const T* p = g + (size_t)blockIdx.z * rows * cols;
-  for (int ct = 0; ct < ENTER_TILES; ++ct) {
-    const int c0 = ((int)blockIdx.x * ENTER_TILES + ct) * 64;
+  for (int ct = 0; ct < tiles; ++ct) {
+    const int c0 = ((int)blockIdx.x * tiles + ct) * 64;
     if (c0 >= lp) break;
     float v[2][8];
 #pragma unroll
@@ -1024,13 +1023,17 @@ static void orth_enter(const moe_orth_shape& s, const OrthLayout& L, const T* g,
   uint8_t* lo = s.dtype == MOE_F32 ? reinterpret_cast<uint8_t*>(ws + L.off_lo[0]) : nullptr;
   MOE_LAUNCH("orth_sumsq", k_orth_sumsq<T>, dim3((unsigned)L.chunks, (unsigned)s.n), dim3(256), 0, st, g, count, chunk,
              part);
-  const dim3 grid((unsigned)ceil_div(L.lp / 64, ENTER_TILES), (unsigned)(L.mp / 64), (unsigned)s.n);
+  // up to 8 tiles a workgroup (the norm's shares are read once for them) where that leaves
+  // 4096 workgroups
+  const int64_t all = (int64_t)s.n * (L.lp / 64) * (L.mp / 64);
+  const int tiles = (int)(all < 4096 ? 1 : all > 8 * 4096 ? 8 : all / 4096);
+  const dim3 grid((unsigned)ceil_div(L.lp / 64, tiles), (unsigned)(L.mp / 64), (unsigned)s.n);
   if (s.rows > s.cols)
     MOE_LAUNCH("orth_enter", (k_orth_enter<T, true>), grid, dim3(256), 0, st, g, s.rows, s.cols, part, L.chunks, L.mp,
-               L.lp, hi, lo, factor);
+               L.lp, tiles, hi, lo, factor);
   else
     MOE_LAUNCH("orth_enter", (k_orth_enter<T, false>), grid, dim3(256), 0, st, g, s.rows, s.cols, part, L.chunks, L.mp,
-               L.lp, hi, lo, factor);
+               L.lp, tiles, hi, lo, factor);
 }
 
 hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o, float scale, void* scratch,

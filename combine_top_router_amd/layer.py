@@ -58,8 +58,9 @@ class _OnDevice:
 
 class MoeNorm(_OnDevice):
     """The norm in front of the layer (layer norm, or rms norm), with the residual sum before
-    it.  ``forward`` gives y, and leaves ``sum`` (with a residual), ``mean`` and ``rstd`` for
-    ``backward``, whose dx is the gradient of x and of the residual alike."""
+    it.  ``forward`` gives y, and leaves ``sum`` (with a residual), ``mean`` and ``rstd``;
+    ``backward`` reads its x, residual and weight again, which have to be as they were (the
+    stored sum has been rounded).  dx is the gradient of x and of the residual alike."""
 
     def __init__(self, T, H, kind=L.MOE_NORM_LAYER, dtype=L.MOE_BF16, eps=1e-5, device="cuda"):
         self.shape = L.MoeNormShape(T, H, dtype, kind, eps)
@@ -87,7 +88,7 @@ class MoeNorm(_OnDevice):
         if res is not None:
             self._check(res, self._row, self.dtype, "res")
         self.sum = None if res is None else self._sum
-        self.inputs = (x if res is None else self._sum, w, b is not None)
+        self.inputs = (x, res, w, b is not None)
         self._call(L.moe_norm_fwd, self.shape, _p(x), _p(res), _p(w), _p(b), _p(self.sum), _p(self.y), _p(self.mean),
                    _p(self.rstd), self._stream(stream))
         return self.y
@@ -98,9 +99,9 @@ class MoeNorm(_OnDevice):
         self._check(dy, self._row, self.dtype, "dy")
         if ds_in is not None:
             self._check(ds_in, self._row, self.dtype, "ds_in")
-        s, w, bias = self.inputs
+        x, res, w, bias = self.inputs
         db = self.db if bias else None
-        self._call(L.moe_norm_bwd, self.shape, _p(dy), _p(s), _p(w), _p(self.mean), _p(self.rstd), _p(ds_in),
+        self._call(L.moe_norm_bwd, self.shape, _p(dy), _p(x), _p(res), _p(w), _p(self.mean), _p(self.rstd), _p(ds_in),
                    _p(self.dx), _p(self.dw), _p(db), _p(self.scratch), self._stream(stream))
         return {"dx": self.dx, "dw": self.dw, "db": db}
 

@@ -83,7 +83,7 @@ _SIG = {
     "moe_balance_bwd": (ctypes.c_int, [_S, _P, _P, _P, _F] + [_P] * 4),
     "moe_norm_scratch_bytes": (ctypes.c_int, [_NS, _SZ]),
     "moe_norm_fwd": (ctypes.c_int, [_NS] + [_P] * 9),
-    "moe_norm_bwd": (ctypes.c_int, [_NS] + [_P] * 11),
+    "moe_norm_bwd": (ctypes.c_int, [_NS] + [_P] * 12),
     "moe_orth_scratch_bytes": (ctypes.c_int, [_OS, _SZ]),
     "moe_orthogonalize": (ctypes.c_int, [_OS, _P, _P, _F, _P, _P]),
     "moe_timing_enable": (ctypes.c_int, [ctypes.c_int]),
@@ -213,8 +213,8 @@ def moe_norm_fwd(shape, x, res, w, b, sum, y, mean, rstd, stream=0):
     _check(load().moe_norm_fwd(ctypes.byref(shape), x, res, w, b, sum, y, mean, rstd, stream), "moe_norm_fwd")
 
 
-def moe_norm_bwd(shape, dy, s, w, mean, rstd, ds_in, dx, dw, db, scratch, stream=0):
-    _check(load().moe_norm_bwd(ctypes.byref(shape), dy, s, w, mean, rstd, ds_in, dx, dw, db, scratch, stream),
+def moe_norm_bwd(shape, dy, s, res, w, mean, rstd, ds_in, dx, dw, db, scratch, stream=0):
+    _check(load().moe_norm_bwd(ctypes.byref(shape), dy, s, res, w, mean, rstd, ds_in, dx, dw, db, scratch, stream),
            "moe_norm_bwd")
 
 

@@ -267,8 +267,8 @@ int moe_balance_scratch_bytes(const moe_shape* shape, size_t* scratch_bytes);
  *               choose none), counts[E] = N           (int32 [E + 1])
  *   prob[e]   = mean of p_te over the counted tokens  (fp32 [E])
  *   loss[0]   = coef E / (k N) sum_e counts[e] prob[e]   (fp32; coef when the load is even)
- * N = 0 gives zeros.  Logits of tokens that do not count are not read; a token whose
- * logits are all -inf counts with p = 0.  coef must be finite.  Uses T, E and k of the
+ * N = 0 gives zeros.  Tokens that do not count may hold anything; a token whose logits
+ * are all -inf counts with p = 0.  coef must be finite.  Uses T, E and k of the
  * shape.  Results do not change from run to run. */
 int moe_balance_fwd(const moe_shape* shape, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                     float coef, float* loss, int32_t* counts, float* prob, void* scratch, void* stream);
@@ -306,17 +306,19 @@ int moe_norm_scratch_bytes(const moe_norm_shape* shape, size_t* scratch_bytes);
 int moe_norm_fwd(const moe_norm_shape* shape, const void* x, const void* res, const void* w, const void* b,
                  void* sum, void* y, float* mean, float* rstd, void* stream);
 
-/* Its backward for the upstream dy [T, H], s = what was normalised (sum, or x without a
- * residual) and the mean (NULL for rms) and rstd of the forward.  With xh = (s - mean) rstd
- * and g = dy w:
+/* Its backward for the upstream dy [T, H] and the mean (NULL for rms) and rstd of the
+ * forward.  What was normalised is s + res, in fp32: s = x and the forward's res, or, with
+ * res = NULL, s = x without a residual or the stored sum (one read less, but dw and dx then
+ * carry the sum's rounding).  With xh = (s + res - mean) rstd and g = dy w:
  *   dx = ds_in + rstd (g - mean(g) - xh mean(g xh))   (rms: without mean(g))
  *   dw = sum_t dy xh,  db = sum_t dy   ([H])
  * ds_in (the gradient that reaches s past the norm) may be NULL (taken as 0) or equal to
- * dx; dx may not be dy or s.  dx is the gradient of x and of res alike.  db may be NULL.
+ * dx; dx may not be dy, s or res.  dx is the gradient of x and of res alike.  db may be NULL.
  * T = 0 gives dw = db = 0.  The sums over tokens run in fp32 in a fixed order.  Needs
  * scratch. */
-int moe_norm_bwd(const moe_norm_shape* shape, const void* dy, const void* s, const void* w, const float* mean,
-                 const float* rstd, const void* ds_in, void* dx, void* dw, void* db, void* scratch, void* stream);
+int moe_norm_bwd(const moe_norm_shape* shape, const void* dy, const void* s, const void* res, const void* w,
+                 const float* mean, const float* rstd, const void* ds_in, void* dx, void* dw, void* db, void* scratch,
+                 void* stream);
 
 typedef struct {
   int32_t n;      /* matrices, 0..65535 (a layer's local experts) */

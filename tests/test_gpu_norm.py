@@ -75,20 +75,22 @@ def _verify(T, H, dt, rms, with_res, with_b, op, c, y, g):
     _near(y, want, e_xh * np.abs(w) + 4 * U * (np.abs(xh * w) + (0 if b is None else np.abs(b))), dt, "y")
     if with_res:
         _near(op.sum, s, 2 * U * np.abs(s), dt, "sum")
-    # the backward from the stored sum and the forward's own statistics
-    s_in = _n(op.sum) if with_res else x
+    # the backward from the forward's own statistics
+    s_in = s
     mean = _n(op.mean) if not rms else np.zeros(T)
     rstd = _n(op.rstd)
     dx, dw, db = ot.norm_backward(_n(c["dy"]), s_in, w, mean, rstd, _n(c["ds"]) if with_res else None, rms)
     xh = (s_in - mean[:, None]) * rstd[:, None]
+    big = (2 * U * np.abs(s_in) + U * np.abs(mean[:, None])) * rstd[:, None]   # xh's own error
     gg = np.abs(_n(c["dy"]) * w)
     gx = np.abs(_n(c["dy"]) * w * xh)
     e = 48 * U * rstd[:, None] * (gg + gg.mean(axis=1, keepdims=True) + np.abs(xh) * gx.mean(axis=1, keepdims=True))
+    e = e + rstd[:, None] * (big * gx.mean(axis=1, keepdims=True) + np.abs(xh) * (gg * big).mean(axis=1, keepdims=True))
     _near(g["dx"], dx, e + 2 * U * np.abs(dx), dt, "dx")
     # a column's sum: at most T / 16 rows in sequence in a share, then the shares
     seq = 16 + T // 4
     dyx = np.abs(_n(c["dy"]) * xh).sum(axis=0)
-    _near(g["dw"], dw, (seq + 8) * U * dyx, dt, "dw")
+    _near(g["dw"], dw, (seq + 8) * U * dyx + (np.abs(_n(c["dy"])) * big).sum(axis=0), dt, "dw")
     if with_b:
         _near(g["db"], db, (seq + 8) * U * np.abs(_n(c["dy"])).sum(axis=0), dt, "db")
     else:
@@ -139,10 +141,17 @@ def test_norm_in_place_sum_and_gradient():
     p = lambda t: t.data_ptr()  # noqa: E731
     lib.moe_norm_fwd(s, p(x), p(c["res"]), p(c["w"]), 0, p(x), p(y2), p(mean), p(rstd), st)      # sum is x
     dw = torch.empty_like(c["w"])
-    lib.moe_norm_bwd(s, p(c["dy"]), p(x), p(c["w"]), p(mean), p(rstd), p(dx), p(dx), p(dw), 0, p(op.scratch), st)
+    lib.moe_norm_bwd(s, p(c["dy"]), p(c["x"]), p(c["res"]), p(c["w"]), p(mean), p(rstd), p(dx), p(dx), p(dw), 0,
+                     p(op.scratch), st)
     torch.cuda.synchronize()
     assert torch.equal(y2, y) and torch.equal(x, op.sum)
     assert torch.equal(dx, g["dx"]) and torch.equal(dw, g["dw"])
+    # from the stored sum: what the oracle gives for that
+    lib.moe_norm_bwd(s, p(c["dy"]), p(x), 0, p(c["w"]), p(mean), p(rstd), 0, p(dx), p(dw), 0, p(op.scratch), st)
+    torch.cuda.synchronize()
+    dx64, dw64, _ = ot.norm_backward(_n(c["dy"]), _n(x), _n(c["w"]), _n(mean), _n(rstd), None, False)
+    assert np.linalg.norm(_n(dx) - dx64) < 2.0 ** -8 * np.linalg.norm(dx64)
+    assert np.linalg.norm(_n(dw) - dw64) < 2.0 ** -8 * np.linalg.norm(dw64)
 
 
 def test_norm_rows_apart():
@@ -176,7 +185,7 @@ def test_norm_without_rows():
     dw = torch.full((70,), 3.0, device="cuda")
     db = torch.full((70,), 3.0, device="cuda")
     ws = torch.empty(lib.moe_norm_scratch_bytes(s), dtype=torch.uint8, device="cuda")
-    lib.moe_norm_bwd(s, 0, 0, 0, 0, 0, 0, 0, dw.data_ptr(), db.data_ptr(), ws.data_ptr(),
+    lib.moe_norm_bwd(s, 0, 0, 0, 0, 0, 0, 0, 0, dw.data_ptr(), db.data_ptr(), ws.data_ptr(),
                      torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert not dw.any() and not db.any()
@@ -196,7 +205,7 @@ def test_norm_writes_nothing_past_its_outputs():
     ws = torch.full((nb + 256,), 7, dtype=torch.uint8, device="cuda")
     lib.moe_norm_fwd(s, p(c["x"]), p(c["res"]), p(c["w"]), p(c["b"]), p(buf["sum"]), p(buf["y"]), p(stat["mean"]),
                      p(stat["rstd"]), st)
-    lib.moe_norm_bwd(s, p(c["dy"]), p(buf["sum"]), p(c["w"]), p(stat["mean"]), p(stat["rstd"]), 0, p(buf["dx"]),
+    lib.moe_norm_bwd(s, p(c["dy"]), p(buf["sum"]), 0, p(c["w"]), p(stat["mean"]), p(stat["rstd"]), 0, p(buf["dx"]),
                      p(vec["dw"]), p(vec["db"]), p(ws), st)
     torch.cuda.synchronize()
     for t in buf.values():

@@ -74,7 +74,7 @@ def test_step_is_its_parts():
     want = ot.balance_backward(n(s.logits), counts, K, s.mask.cpu().numpy(), COEF, 1.0, routing)
     assert rel(n(out["d_logits"]), want) < 1e-4
     # the norm's backward of what the router's backward gave
-    dx, dw, _ = ot.norm_backward(n(s.dx), n(s.norm.sum), n(s.w), np.zeros(T), n(s.norm.rstd), n(s.ds), True)
+    dx, dw, _ = ot.norm_backward(n(s.dx), n(s.h) + n(s.attn), n(s.w), np.zeros(T), n(s.norm.rstd), n(s.ds), True)
     assert rel(n(out["dh"]), dx) < BF16_TOL and rel(n(out["dw"]), dw) < BF16_TOL
     for name, g in (("o_gate", lay.dw_gate), ("o_up", lay.dw_up), ("o_down", lay.dw_down)):
         for e in (0, E - 1):

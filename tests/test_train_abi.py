@@ -47,7 +47,7 @@ def test_norm_shapes(bad):
     s = _norm(L, **bad)
     assert _code(lambda: L.moe_norm_scratch_bytes(s)) == L.MOE_EINVAL
     assert _code(lambda: L.moe_norm_fwd(s, P, 0, P, 0, 0, P, P, P)) == L.MOE_EINVAL
-    assert _code(lambda: L.moe_norm_bwd(s, P, P, P, P, P, 0, P, P, 0, P)) == L.MOE_EINVAL
+    assert _code(lambda: L.moe_norm_bwd(s, P, P, 0, P, P, P, 0, P, P, 0, P)) == L.MOE_EINVAL
 
 
 def test_norm_pointers():
@@ -60,13 +60,14 @@ def test_norm_pointers():
     assert _code(lambda: L.moe_norm_fwd(s, *dict(good, res=P).values())) == L.MOE_EINVAL      # res without sum
     assert _code(lambda: L.moe_norm_fwd(s, *dict(good, sum=P).values())) == L.MOE_EINVAL      # sum without res
     assert _code(lambda: L.moe_norm_fwd(s, *dict(good, res=P, sum=2 * P).values())) == L.MOE_EINVAL   # y is sum
-    good = dict(dy=P, s=2 * P, w=P, mean=P, rstd=P, ds_in=0, dx=3 * P, dw=P, db=0, scratch=P)
+    good = dict(dy=P, s=2 * P, res=0, w=P, mean=P, rstd=P, ds_in=0, dx=3 * P, dw=P, db=0, scratch=P)
     for name in ("dy", "s", "w", "mean", "rstd", "dx", "dw"):
         a = dict(good, **{name: 0})
         assert _code(lambda: L.moe_norm_bwd(s, *a.values())) == L.MOE_EINVAL, name
     assert _code(lambda: L.moe_norm_bwd(s, *dict(good, scratch=0).values())) == L.MOE_EWORKSPACE
-    for name in ("dy", "s"):
-        a = dict(good, dx=good[name])
+    for name in ("dy", "s", "res"):
+        a = dict(good, res=4 * P)
+        a["dx"] = a[name]
         assert _code(lambda: L.moe_norm_bwd(s, *a.values())) == L.MOE_EINVAL
     L.moe_norm_fwd(_norm(L, T=0), 0, 0, 0, 0, 0, 0, 0, 0)   # no rows: nothing to do
 
