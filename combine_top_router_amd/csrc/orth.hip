@@ -574,11 +574,12 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_stream(OrthArgs a, int n, int 
 
 // ---- the products on 128 x 128 and 64 x 64 tiles: one tile a workgroup ----
 // For matrices whose 256-row tiles leave CUs idle or mostly padding.  Such launches wait for
-// loads, not for MFMAs: the K steps ring through NS stages of LDS, so NS - 1 steps of
-// direct-to-LDS loads are in flight, with one barrier a step.
+// loads, not for MFMAs.  The K steps ring through NS stages of LDS, so NS - 1 steps of
+// direct-to-LDS loads are in flight, with one barrier a step: eight stages where a CU gets one
+// tile, two where several workgroups on a CU cover each other's waits.
 template <int TILE> struct TileCfg;
-template <> struct TileCfg<64> { static constexpr int NS = 8, WAVES = 4, TMI = 1; };    // 2 x 2 waves of 32 x 32
-template <> struct TileCfg<128> { static constexpr int NS = 4, WAVES = 8, TMI = 2; };   // 2 x 4 waves of 64 x 32
+template <> struct TileCfg<64> { static constexpr int WAVES = 4, TMI = 1; };    // 2 x 2 waves of 32 x 32
+template <> struct TileCfg<128> { static constexpr int WAVES = 8, TMI = 2; };   // 2 x 4 waves of 64 x 32
 
 // MN-major rows of 64 (8 chunks): rows two apart in other halves of a row's 128 bytes, so the
 // four rows of a transposing read meet no bank twice; wider rows as in the engine
@@ -600,18 +601,22 @@ __device__ __forceinline__ f16x8 tile_frag_mn(const bf16_t* s, int base, int kk,
   return out;
 }
 
-template <int OP, int TILE>
-__global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, 1) void k_orth_tile(OrthArgs a, int tm, int tn) {
+template <int OP, int TILE, int NS>
+__global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_orth_tile(OrthArgs a, int tm, int tn, int items) {
   using C = TileCfg<TILE>;
   constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
   constexpr int OPER = TILE * BK, STAGE = 2 * OPER;                  // elements
   constexpr int LP = OPER * 2 / 1024 / C::WAVES;                     // 1 KB loads of one operand a wave and step
   static_assert(LP * C::WAVES * 512 == OPER, "wave loads divide among the waves");
-  __shared__ __attribute__((aligned(16))) bf16_t lds[C::NS * STAGE];
+  __shared__ __attribute__((aligned(16))) bf16_t lds[NS * STAGE];
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
   const int per = SYM ? tm * (tm + 1) / 2 : tm * tn;
-  const int z = uni(blockIdx.x / per);
-  int rem = uni(blockIdx.x - z * per), ti = 0;
+  // workgroup b runs on XCD b % 8: contiguous ranges of tiles, so that an XCD's L2 holds the
+  // matrices its tiles share
+  const int share = (int)(gridDim.x >> 3), v = (int)(blockIdx.x & 7) * share + (int)(blockIdx.x >> 3);
+  if (v >= items) return;
+  const int z = uni(v / per);
+  int rem = uni(v - z * per), ti = 0;
   if (SYM) {
     while (rem > ti) rem -= ++ti;
   } else {
@@ -640,7 +645,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, 1) void k_orth_tile(Orth
   }
   const size_t bstep = SYM ? (size_t)BK : (size_t)BK * a.lp;
   auto issue = [&](int kt) {
-    bf16_t* const st = lds + (kt % C::NS) * STAGE;
+    bf16_t* const st = lds + (kt % NS) * STAGE;
 #pragma unroll
     for (int q = 0; q < LP; ++q) {
       dma16(la[q] + kt * BK, st + (q * C::WAVES + wv) * 512);
@@ -654,18 +659,18 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, 1) void k_orth_tile(Orth
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[mi][r] = 0.f;
 #pragma unroll
-  for (int kt = 0; kt < C::NS - 1; ++kt)
+  for (int kt = 0; kt < NS - 1; ++kt)
     if (kt < nk) issue(kt);
   for (int kt = 0; kt < nk; ++kt) {
     // step kt has landed when at most the NS - 2 later steps' loads are out
-    if (nk - 1 - kt >= C::NS - 2) {
-      static_assert(2 * LP * (C::NS - 2) < 64, "vmcnt counts to 63");
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * LP * (C::NS - 2)) : "memory");
+    if (NS > 2 && nk - 1 - kt >= NS - 2) {
+      static_assert(2 * LP * (NS - 2) < 64, "vmcnt counts to 63");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * LP * (NS - 2)) : "memory");
     } else {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
-    if (kt + C::NS - 1 < nk) issue(kt + C::NS - 1);   // into the stage read one step ago
-    const bf16_t* const as = lds + (kt % C::NS) * STAGE;
+    if (kt + NS - 1 < nk) issue(kt + NS - 1);   // into the stage read one step ago
+    const bf16_t* const as = lds + (kt % NS) * STAGE;
     const bf16_t* const bs = as + OPER;
 #pragma unroll
     for (int kk = 0; kk < BK / 16; ++kk) {
@@ -754,47 +759,51 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, 1) void k_orth_tile(Orth
 }
 
 // The tile of a product, M x N over K in n matrices (M x M by halves when symmetric): the one
-// of least estimated time.  A tile of a round (one on each CU) takes a start and an end, e,
-// and c a K step of 64; measured on one MI355X, in us:
-//            64 rows        128 rows       256 rows
-//   e        3.2 / 4.5      6 / 8          12           (symmetric / not)
-//   c        0.27           0.53           1.25 on a few CUs, 2.15 on all (the stream is
-//                                          then bound by what the L2s and the MFMAs deliver)
-// Both sides, whole products: 5 of 384 over K = 1024, symmetric, 7.4 / 11.6 / 27.3; 32 of 384
-// over 1024: 26 / 15 / 28; 8 of 768 x 2048 over 768: 68 / 44 / 33; 128 of 768 over 2048,
-// symmetric: 218 with 256 rows.
-static int orth_tile_size(bool sym, int n, int M, int N, int K) {
-  const double steps = K / 64.0, cus = num_cus();
-  int best = 256;
-  double least = 0.0;
-  for (int t = 256; t >= 64; t /= 2) {
-    const int64_t tm = ceil_div(M, t), tn = ceil_div(N, t), items = n * (sym ? tm * (tm + 1) / 2 : tm * tn);
-    const double fill = items < cus ? items / cus : 1.0;
-    const double e = t == 256 ? 12.0 : t == 128 ? (sym ? 6.0 : 8.0) : (sym ? 3.2 : 4.5);
-    const double c = t == 256 ? 1.25 + 0.9 * fill : t == 128 ? 0.53 : 0.27;
-    const double us = ceil((double)items / cus) * (e + c * steps);
-    if (t == 256 || us < least) {
-      best = t;
-      least = us;
-    }
-  }
-  return best;
+// of least estimated time, from what the four kernels were measured to take on one MI355X, in
+// us, for t tiles a CU and k steps of 64:
+//   64 rows, deep ring    3 + 0.27 k                        one tile a CU at most
+//   64 rows               3 + max(0.40 k, t (0.8 + 0.18 k))  five workgroups share a CU
+//   128 rows              4 + max(0.58 k, t (1.9 + 0.70 k))  two share a CU
+//   256 rows              5 + ceil(t) (7 + c k)              c = 1.25 on few CUs, 2.15 on all
+// Whole updates, bf16, with 64 deep / 64 / 128 / 256 rows throughout: 100 of 64 x 1024 148 /
+// 124 / 145 / 246 us; 11 of 362 x 362 113 / 103 / 131 / 264; 8 of 768 x 2048 576 / 384 / 351 /
+// 586; 128 of 320 x 640 783 / 486 / 478 / 625; the symmetric product of 20 of 256 over K =
+// 1024 7.4 / 9.4 / 12.5 / 27.5; 128 of 768 x 2048 take 4.1 ms with 256 rows.
+enum OrthTileKind { TILE_64_DEEP, TILE_64, TILE_128, TILE_256 };
+static OrthTileKind orth_tile_kind(bool sym, int n, int M, int N, int K) {
+  const double k = K / 64.0, cus = num_cus();
+  auto load = [&](int t) {
+    const int64_t tm = ceil_div(M, t), tn = ceil_div(N, t);
+    return n * (sym ? tm * (tm + 1) / 2 : tm * tn) / cus;
+  };
+  const double t64 = load(64), t128 = load(128), t256 = load(256);
+  const double us[4] = {t64 <= 1.0 ? 3.0 + 0.27 * k : 1e30, 3.0 + fmax(0.40 * k, t64 * (0.8 + 0.18 * k)),
+                        4.0 + fmax(0.58 * k, t128 * (1.9 + 0.70 * k)),
+                        5.0 + ceil(t256) * (7.0 + (1.25 + 0.9 * fmin(t256, 1.0)) * k)};
+  int best = TILE_256;
+  for (int i = 0; i < 3; ++i)
+    if (us[i] < us[best]) best = i;
+  return (OrthTileKind)best;
 }
 
-template <int OP, int TILE>
+template <int OP, int TILE, int NS>
 static void orth_tiles(const char* name, const OrthArgs& a, int n, hipStream_t st) {
   constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
   const int tm = (int)ceil_div(a.mp, TILE), tn = (int)ceil_div(a.lp, TILE);
-  const int per = SYM ? tm * (tm + 1) / 2 : tm * tn;
-  MOE_LAUNCH(name, (k_orth_tile<OP, TILE>), dim3((unsigned)n * per), dim3(64 * TileCfg<TILE>::WAVES), 0, st, a, tm, tn);
+  const int items = n * (SYM ? tm * (tm + 1) / 2 : tm * tn);
+  MOE_LAUNCH(name, (k_orth_tile<OP, TILE, NS>), dim3((unsigned)(items + 7) & ~7u), dim3(64 * TileCfg<TILE>::WAVES), 0, st,
+             a, tm, tn, items);
 }
 
 template <int OP>
 static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t st) {
   constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
-  const int tile = orth_tile_size(SYM, n, a.mp, SYM ? a.mp : a.lp, OP == ORTH_GRAM ? a.lp : a.mp);
-  if (tile == 64) return orth_tiles<OP, 64>(name, a, n, st);
-  if (tile == 128) return orth_tiles<OP, 128>(name, a, n, st);
+  switch (orth_tile_kind(SYM, n, a.mp, SYM ? a.mp : a.lp, OP == ORTH_GRAM ? a.lp : a.mp)) {
+    case TILE_64_DEEP: return orth_tiles<OP, 64, 8>(name, a, n, st);
+    case TILE_64: return orth_tiles<OP, 64, 2>(name, a, n, st);
+    case TILE_128: return orth_tiles<OP, 128, 2>(name, a, n, st);
+    default: break;
+  }
   const int tm = (int)ceil_div(a.mp, BM), tn = (int)ceil_div(a.lp, BN);
   const dim3 grid((unsigned)grid_for((int64_t)n * (SYM ? tm * (tm + 1) / 2 : tm * tn)));
   if constexpr (OP == ORTH_LAST) {
