@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 # gemm.hip is compiled twice, through gemm_fw256.hip and gemm_fw320.hip (one tile height each)
 SOURCES = ["api.hip", "route.hip", "index.hip", "gemm_fw256.hip", "gemm_fw320.hip", "gemm_f32.hip", "mx_quant.hip",
-           "router_gemm.hip", "norm.hip", "balance.hip", "orth.hip"]
+           "router_gemm.hip", "norm.hip", "balance.hip", "gemm_orth.hip"]
 ARCH = "gfx950"
 
 
@@ -41,7 +41,7 @@ FLAGS = [
 # The GEMM translation units: every kernel in them is sized to its register budget (256
 # registers per wave), and a spill (scratch memory traffic inside the MFMA loop or the
 # epilogue) fails the build.
-GEMM_SOURCES = ("gemm_fw256.hip", "gemm_fw320.hip", "orth.hip")
+GEMM_SOURCES = ("gemm_fw256.hip", "gemm_fw320.hip", "gemm_orth.hip")
 
 
 def _check_no_spill(src: str, remarks: str) -> None:

@@ -146,7 +146,7 @@ hipError_t launch_norm_fwd(const moe_norm_shape& s, const void* x, const void* r
 hipError_t launch_norm_bwd(const moe_norm_shape& s, const void* dy, const void* sum, const void* res, const void* w,
                            const float* mean, const float* rstd, const void* ds_in, void* dx, void* dw, void* db,
                            float* part, hipStream_t st);
-// orthogonalised updates (orth.hip)
+// orthogonalised updates (gemm_orth.hip)
 size_t orth_scratch_bytes(const moe_orth_shape& s);
 hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o, float scale, void* scratch,
                                 hipStream_t st);

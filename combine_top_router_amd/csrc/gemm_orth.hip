@@ -41,6 +41,8 @@ constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr double NS_EPS = 1e-7;
 constexpr int X_LOG2 = 15, D_LOG2 = 14, B_LOG2 = 14;
 constexpr float X_SCALE = 32768.f, D_SCALE = 16384.f, B_SCALE = 16384.f;
+// of two merged steps: |S| <= 2.8, and P's eigenvalues lie in [-11.5, 0]
+constexpr float S_SCALE = 16384.f, P_SCALE = 4096.f;
 constexpr float LO_SCALE = 16.f;  // |lo| <= 16, half a step of fp16 at its top: 256 of E4M3's 448
 constexpr int LO_STEPS = 2;      // the first iterates that are kept as hi + lo
 constexpr int SHIFT_STEP = 3;    // from this step on, D = A - I
@@ -169,21 +171,27 @@ __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int
 }
 
 // ---- the products ----
-enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_APPLY = 2, ORTH_LAST = 3 };
+// What a product is for.  SYM0..2: a symmetric one C = c0 P Q^T - diag I, + c1 S1, + c2 S2, of
+// which the lower triangle of tiles is computed and mirrored; APPLY: X' = c0 P X + c1 X; LAST:
+// the same into the result.
+enum { ORTH_SYM0 = 0, ORTH_SYM1 = 1, ORTH_SYM2 = 2, ORTH_APPLY = 3, ORTH_LAST = 4 };
+constexpr bool orth_sym(int op) { return op <= ORTH_SYM2; }
 
 struct OrthArgs {
   int mp, lp;             // padded sizes, multiples of 64
+  int K;                  // the contraction: rows of P (and Q) are K long
   int m, l, rows, cols;
-  int step;
-  const f16* x;           // X hi [n, mp, lp]
+  const f16* p;           // [n, mp, K]
+  const f16* q;           // symmetric: [n, mp, K]; else X hi [n, mp, lp]
+  const f16* s1;          // [n, mp, mp]
+  const f16* s2;
+  float c0, c1, c2, diag;
+  const float* factor;    // per matrix, stored X -> X, in every X (the first products); null: 1
+  f16* c;                 // symmetric: C [n, mp, mp]
   const uint8_t* xlo;     // X lo, or null
-  const float* factor;    // stored X -> X, per matrix (step 0)
-  f16* d;                 // D [n, mp, mp]
-  f16* b;                 // B = beta D + c D^2 [n, mp, mp]
-  f16* xn;                // the next X
+  f16* xn;                // X'
   uint8_t* xnlo;          // its lo, or null
-  bf16_t* out;            // the last step's result [n, rows, cols]
-  float scale;
+  bf16_t* out;            // the result [n, rows, cols]
 };
 
 struct StepCoef {
@@ -319,7 +327,7 @@ template <int OP, bool TALL = false>
 struct JOrth {
   using Tile = OrthTile;
   using Ld = OrthLd;
-  static constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
+  static constexpr bool SYM = orth_sym(OP);
   static constexpr bool A_KMAJ = true, B_KMAJ = SYM;
   static constexpr bool DYN = false, TRANS = !TALL, EPI_LDS = true, NSPLIT = false, SIDE = false;
   OrthArgs a;
@@ -338,10 +346,10 @@ struct JOrth {
     }
     p.i0 = uni(ti * BM);
     p.j0 = uni(rem * BN);
-    p.nk = uni((OP == ORTH_GRAM ? a.lp : a.mp) / BK);
+    p.nk = uni(a.K / BK);
     p.cnt = uni(min(BM, a.mp - p.i0));
     p.ncols = uni(min(BN, (SYM ? a.mp : a.lp) - p.j0));
-    p.f = a.step == 0 ? sload(a.factor + p.z) : 1.f / X_SCALE;
+    p.f = a.factor ? sload(a.factor + p.z) : 1.f;
   }
   __device__ __forceinline__ WaveRows rows(const Tile& p, int wm) const { return wave_rows(p.cnt, wm); }
   __device__ __forceinline__ void setup(int v, Ld& p, int pw, int lane) const {
@@ -349,10 +357,9 @@ struct JOrth {
     tile(v, t);
     p.pw = pw;
     p.nk = t.nk;
-    const int K = OP == ORTH_GRAM ? a.lp : a.mp;
-    const size_t xo = (size_t)t.z * a.mp * a.lp, so = (size_t)t.z * a.mp * a.mp;
-    const bf16_t* pa = reinterpret_cast<const bf16_t*>(OP == ORTH_GRAM ? a.x + xo : OP == ORTH_POLY ? a.d + so : a.b + so);
-    const bf16_t* pb = reinterpret_cast<const bf16_t*>(OP == ORTH_POLY ? a.d + so : a.x + xo);
+    const int K = a.K;
+    const bf16_t* pa = reinterpret_cast<const bf16_t*>(a.p + (size_t)t.z * a.mp * K);
+    const bf16_t* pb = reinterpret_cast<const bf16_t*>(a.q + (size_t)t.z * a.mp * (SYM ? K : a.lp));
 #pragma unroll
     for (int q = 0; q < A_LP; ++q) {
       int r, c;
@@ -400,36 +407,36 @@ struct JOrth {
     else out_rows(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
   }
   // C^T accumulators: lane l holds row l % 32 of each band.  What the rows are combined with
-  // (D, or X hi and lo) is loaded in that layout two bands ahead (all four at once spill);
-  // finished bands leave through the wave's LDS region as whole row segments, and those of
-  // an off-diagonal tile of a symmetric product once more as columns.
+  // (S1 and S2, or X hi and lo) is loaded in that layout two bands ahead, S1 and S2
+  // one (more spill); finished bands leave through the wave's LDS region as whole row segments, and
+  // those of an off-diagonal tile of a symmetric product once more as columns.
   __device__ __forceinline__ void out_rows(const Tile& p, const Acc& acc, bf16_t* wreg, int i0, int j0) const {
     const int lane = threadIdx.x & 63;
-    const StepCoef co = step_coef(a.step);
     const size_t xo = (size_t)p.z * a.mp * a.lp, so = (size_t)p.z * a.mp * a.mp;
     const int ld = SYM ? a.mp : a.lp;
-    const f16* const side = OP == ORTH_POLY ? a.d + so : a.x + xo;
+    const f16* const side = SYM ? a.s1 + so : a.q + xo;
+    const f16* const side2 = a.s2 + so;
     const uint8_t* const side_lo = !SYM && a.xlo ? a.xlo + xo : nullptr;
-    i32x4 xh[2][NI][2], xl[2][NI];
+    constexpr int AHEAD = OP == ORTH_SYM2 ? 1 : 2;
+    i32x4 xh[AHEAD][NI][2], xl[AHEAD][NI], x2[AHEAD][NI][2];
     auto fetch = [&](int mi) {
       const size_t row = (size_t)min(i0 + mi * 32 + (lane & 31), a.mp - 1) * ld + j0;
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          xh[mi & 1][ni][s] = *reinterpret_cast<const i32x4*>(side + row + ni * 32 + 16 * s + 8 * (lane >> 5));
-        if (side_lo) xl[mi & 1][ni] = *reinterpret_cast<const i32x4*>(side_lo + row + ni * 32 + 16 * (lane >> 5));
+        for (int s = 0; s < 2; ++s) {
+          xh[mi % AHEAD][ni][s] = *reinterpret_cast<const i32x4*>(side + row + ni * 32 + 16 * s + 8 * (lane >> 5));
+          if (OP == ORTH_SYM2)
+            x2[mi % AHEAD][ni][s] = *reinterpret_cast<const i32x4*>(side2 + row + ni * 32 + 16 * s + 8 * (lane >> 5));
+        }
+        if (side_lo) xl[mi % AHEAD][ni] = *reinterpret_cast<const i32x4*>(side_lo + row + ni * 32 + 16 * (lane >> 5));
       }
     };
-    if constexpr (OP != ORTH_GRAM) {
+    if constexpr (OP != ORTH_SYM0) {
       fetch(0);
-      fetch(1);
+      if (AHEAD > 1) fetch(1);
     }
-    // v = acc cb + side ca
-    float ca, cb;
-    if (OP == ORTH_GRAM) { cb = p.f * p.f * D_SCALE; ca = 0.f; }
-    else if (OP == ORTH_POLY) { cb = NS_C * B_SCALE / (D_SCALE * D_SCALE); ca = co.beta * B_SCALE / D_SCALE; }
-    else { const float sc = OP == ORTH_APPLY ? X_SCALE : a.scale; cb = p.f / B_SCALE * sc; ca = co.alpha * p.f * sc; }
+    const float c0 = SYM ? a.c0 * p.f * p.f : a.c0 * p.f, c1 = SYM ? a.c1 : a.c1 * p.f;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       const int rb = i0 + mi * 32;
@@ -438,17 +445,23 @@ struct JOrth {
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
         float v[16];
-        if constexpr (OP == ORTH_GRAM) {
+        if constexpr (OP == ORTH_SYM0) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            v[r] = acc[mi][ni][r] * cb;
-            if (rb + (lane & 31) == j0 + ni * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= co.t * D_SCALE;
+            v[r] = acc[mi][ni][r] * c0;
+            if (rb + (lane & 31) == j0 + ni * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= a.diag;
           }
         } else {
-          untrans_chunks_f16(xh[mi & 1][ni], v);
-          if (side_lo) add_codes(xl[mi & 1][ni], v);
+          untrans_chunks_f16(xh[mi % AHEAD][ni], v);
+          if (side_lo) add_codes(xl[mi % AHEAD][ni], v);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] = acc[mi][ni][r] * cb + v[r] * ca;
+          for (int r = 0; r < 16; ++r) v[r] = acc[mi][ni][r] * c0 + v[r] * c1;
+          if constexpr (OP == ORTH_SYM2) {
+            float u[16];
+            untrans_chunks_f16(x2[mi % AHEAD][ni], u);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) v[r] += u[r] * a.c2;
+          }
         }
         if constexpr (OP == ORTH_LAST) {
           f32x16 b;
@@ -464,7 +477,7 @@ struct JOrth {
           codes[ni] = trans_codes(v);
         }
       }
-      if (OP != ORTH_GRAM && mi + 2 < MI) fetch(mi + 2);
+      if (OP != ORTH_SYM0 && mi + AHEAD < MI) fetch(mi + AHEAD);
       if (OP == ORTH_APPLY && a.xnlo) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
@@ -484,7 +497,7 @@ struct JOrth {
           }
         });
       } else {
-        f16* const out = OP == ORTH_GRAM ? a.d + so : OP == ORTH_POLY ? a.b + so : a.xn + xo;
+        f16* const out = SYM ? a.c + so : a.xn + xo;
         band_store(wreg, ch, [&](int rr, int cb_, i32x4 w) {
           *reinterpret_cast<i32x4*>(out + (size_t)(rb + rr) * ld + j0 + cb_) = w;
         });
@@ -499,15 +512,14 @@ struct JOrth {
   // comes through the wave's LDS region and the transposing read; then rows of C^T leave.
   __device__ __forceinline__ void out_tall(const Tile& p, const Acc& acc, bf16_t* wreg, int i0, int j0) const {
     const int lane = threadIdx.x & 63, g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
-    const StepCoef co = step_coef(a.step);
     const size_t xo = (size_t)p.z * a.mp * a.lp;
-    const float cb = p.f / B_SCALE * a.scale, ca = co.alpha * p.f * a.scale;
+    const float c0 = a.c0 * p.f, c1 = a.c1 * p.f;
     i32x4 xh[4];   // rows lane / 8 + 8 k of a 32 x 64 band, 16 bytes a lane, one band ahead
     auto fetch = [&](int mi) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         xh[k] = *reinterpret_cast<const i32x4*>(
-            a.x + xo + (size_t)min(i0 + mi * 32 + (lane >> 3) + 8 * k, a.mp - 1) * a.lp + j0 + (lane & 7) * 8);
+            a.q + xo + (size_t)min(i0 + mi * 32 + (lane >> 3) + 8 * k, a.mp - 1) * a.lp + j0 + (lane & 7) * 8);
     };
     fetch(0);
     Acc v;
@@ -529,7 +541,7 @@ struct JOrth {
               (MOE_LDS s16x4*)(wreg + r * WCOLS + (((col >> 3) ^ band_swz<8>(r)) << 3) + (col & 7)));
           const f16x4 x = __builtin_bit_cast(f16x4, t);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[mi][ni][4 * k + e] = acc[mi][ni][4 * k + e] * cb + (float)x[e] * ca;
+          for (int e = 0; e < 4; ++e) v[mi][ni][4 * k + e] = acc[mi][ni][4 * k + e] * c0 + (float)x[e] * c1;
         }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (a.xlo) {   // three steps or fewer
@@ -538,7 +550,7 @@ struct JOrth {
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int i = min(i0 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), a.mp - 1);
-            v[mi][ni][r] += lo_value(a.xlo[xo + (size_t)i * a.lp + j0 + ni * 32 + (lane & 31)]) * ca;
+            v[mi][ni][r] += lo_value(a.xlo[xo + (size_t)i * a.lp + j0 + ni * 32 + (lane & 31)]) * c1;
           }
       }
     }
@@ -604,7 +616,7 @@ __device__ __forceinline__ f16x8 tile_frag_mn(const bf16_t* s, int base, int kk,
 template <int OP, int TILE, int NS>
 __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_orth_tile(OrthArgs a, int tm, int tn, int items) {
   using C = TileCfg<TILE>;
-  constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
+  constexpr bool SYM = orth_sym(OP);
   constexpr int OPER = TILE * BK, STAGE = 2 * OPER;                  // elements
   constexpr int LP = OPER * 2 / 1024 / C::WAVES;                     // 1 KB loads of one operand a wave and step
   static_assert(LP * C::WAVES * 512 == OPER, "wave loads divide among the waves");
@@ -624,10 +636,10 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     rem = uni(rem / tm);
   }
   const int i0 = ti * TILE, j0 = rem * TILE, ldn = SYM ? a.mp : a.lp;
-  const int K = OP == ORTH_GRAM ? a.lp : a.mp, nk = K / BK;
+  const int K = a.K, nk = K / BK;
   const size_t xo = (size_t)z * a.mp * a.lp, so = (size_t)z * a.mp * a.mp;
-  const bf16_t* pa = reinterpret_cast<const bf16_t*>(OP == ORTH_GRAM ? a.x + xo : OP == ORTH_POLY ? a.d + so : a.b + so);
-  const bf16_t* pb = reinterpret_cast<const bf16_t*>(OP == ORTH_POLY ? a.d + so : a.x + xo);
+  const bf16_t* pa = reinterpret_cast<const bf16_t*>(a.p + (size_t)z * a.mp * K);
+  const bf16_t* pb = reinterpret_cast<const bf16_t*>(a.q + (SYM ? (size_t)z * a.mp * K : xo));
   const bf16_t *la[LP], *lb[LP];
 #pragma unroll
   for (int q = 0; q < LP; ++q) {
@@ -682,33 +694,37 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
   }
   // lane l: row l % 32 of each block, columns 8q + 4 (l / 32) .. + 3
   if (j0 + jb >= ldn) return;
-  const StepCoef co = step_coef(a.step);
-  const float f = a.step == 0 ? a.factor[z] : 1.f / X_SCALE;
-  float ca, cb;
-  if (OP == ORTH_GRAM) { cb = f * f * D_SCALE; ca = 0.f; }
-  else if (OP == ORTH_POLY) { cb = NS_C * B_SCALE / (D_SCALE * D_SCALE); ca = co.beta * B_SCALE / D_SCALE; }
-  else { const float sc = OP == ORTH_APPLY ? X_SCALE : a.scale; cb = f / B_SCALE * sc; ca = co.alpha * f * sc; }
+  const float f = a.factor ? a.factor[z] : 1.f;
+  const float c0 = SYM ? a.c0 * f * f : a.c0 * f, c1 = SYM ? a.c1 : a.c1 * f;
 #pragma unroll
   for (int mi = 0; mi < C::TMI; ++mi) {
     const int i = i0 + ib + mi * 32 + (lane & 31), j = j0 + jb;
     if (i0 + ib + mi * 32 >= a.mp) break;
     const size_t at = (size_t)i * ldn + j;
     float v[16];
-    if constexpr (OP == ORTH_GRAM) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        v[r] = acc[mi][r] * cb;
-        if (i == j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= co.t * D_SCALE;
-      }
-    } else {
-      const f16* const side = OP == ORTH_POLY ? a.d + so : a.x + xo;
+    auto side = [&](const f16* from, float (&u)[16]) {
       i32x4 ch[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) ch[s] = *reinterpret_cast<const i32x4*>(side + at + 16 * s + 8 * (lane >> 5));
-      untrans_chunks_f16(ch, v);
+      for (int s = 0; s < 2; ++s) ch[s] = *reinterpret_cast<const i32x4*>(from + at + 16 * s + 8 * (lane >> 5));
+      untrans_chunks_f16(ch, u);
+    };
+    if constexpr (OP == ORTH_SYM0) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        v[r] = acc[mi][r] * c0;
+        if (i == j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= a.diag;
+      }
+    } else {
+      side(SYM ? a.s1 + so : a.q + xo, v);
       if (!SYM && a.xlo) add_codes(*reinterpret_cast<const i32x4*>(a.xlo + xo + at + 16 * (lane >> 5)), v);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) v[r] = acc[mi][r] * cb + v[r] * ca;
+      for (int r = 0; r < 16; ++r) v[r] = acc[mi][r] * c0 + v[r] * c1;
+      if constexpr (OP == ORTH_SYM2) {
+        float u[16];
+        side(a.s2 + so, u);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] += u[r] * a.c2;
+      }
     }
     if constexpr (OP == ORTH_LAST) {
       bf16_t* const out = a.out + (size_t)z * a.rows * a.cols;
@@ -739,7 +755,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
         }
       }
     } else {
-      f16* const out = OP == ORTH_GRAM ? a.d + so : OP == ORTH_POLY ? a.b + so : a.xn + xo;
+      f16* const out = SYM ? a.c + so : a.xn + xo;
       i32x4 ch[2];
       trans_chunks_f16(v, ch);
 #pragma unroll
@@ -770,7 +786,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
 // 586; 128 of 320 x 640 783 / 486 / 478 / 625; the symmetric product of 20 of 256 over K =
 // 1024 7.4 / 9.4 / 12.5 / 27.5; 128 of 768 x 2048 take 4.1 ms with 256 rows.
 enum OrthTileKind { TILE_64_DEEP, TILE_64, TILE_128, TILE_256 };
-static OrthTileKind orth_tile_kind(bool sym, int n, int M, int N, int K) {
+static OrthTileKind orth_tile_kind(bool sym, int n, int M, int N, int K, double* time = nullptr) {
   const double k = K / 64.0, cus = num_cus();
   auto load = [&](int t) {
     const int64_t tm = ceil_div(M, t), tn = ceil_div(N, t);
@@ -783,12 +799,13 @@ static OrthTileKind orth_tile_kind(bool sym, int n, int M, int N, int K) {
   int best = TILE_256;
   for (int i = 0; i < 3; ++i)
     if (us[i] < us[best]) best = i;
+  if (time) *time = us[best];
   return (OrthTileKind)best;
 }
 
 template <int OP, int TILE, int NS>
 static void orth_tiles(const char* name, const OrthArgs& a, int n, hipStream_t st) {
-  constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
+  constexpr bool SYM = orth_sym(OP);
   const int tm = (int)ceil_div(a.mp, TILE), tn = (int)ceil_div(a.lp, TILE);
   const int items = n * (SYM ? tm * (tm + 1) / 2 : tm * tn);
   MOE_LAUNCH(name, (k_orth_tile<OP, TILE, NS>), dim3((unsigned)(items + 7) & ~7u), dim3(64 * TileCfg<TILE>::WAVES), 0, st,
@@ -797,8 +814,8 @@ static void orth_tiles(const char* name, const OrthArgs& a, int n, hipStream_t s
 
 template <int OP>
 static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t st) {
-  constexpr bool SYM = OP == ORTH_GRAM || OP == ORTH_POLY;
-  switch (orth_tile_kind(SYM, n, a.mp, SYM ? a.mp : a.lp, OP == ORTH_GRAM ? a.lp : a.mp)) {
+  constexpr bool SYM = orth_sym(OP);
+  switch (orth_tile_kind(SYM, n, a.mp, SYM ? a.mp : a.lp, a.K)) {
     case TILE_64_DEEP: return orth_tiles<OP, 64, 8>(name, a, n, st);
     case TILE_64: return orth_tiles<OP, 64, 2>(name, a, n, st);
     case TILE_128: return orth_tiles<OP, 128, 2>(name, a, n, st);
@@ -988,10 +1005,28 @@ inline int pad64(int v) { return (v + 63) & ~63; }
 
 }  // namespace
 
-// Scratch: norm shares and factors, then X (two iterates, hi and lo), D and B
+// The first two steps as one: with R = A of the first step and B_i = b A_i + c A_i^2 of both,
+//   A_1 = (a I + B_0) R (a I + B_0) = a^2 R + 2a S + B_0 S,  S = B_0 R  (all commute),
+//   X_2 = (a^2 I + P) X_0,  P = a B_0 + a B_1 + B_1 B_0,
+// three symmetric m^3 products in place of X_1 (its product, its A, and its rounding: no lo of
+// it is kept either).  It pays where matrices are long: 128 of 768 x 2048 bf16 take 4.1 ms step
+// by step and 3.7 merged; at 1 : 1 the two are alike.  Merging further pairs in this way
+// costs precision (A_3 out of A_2 has its rounding multiplied by up to a^2: 3 to 4e-3 in all).
+static bool merge_pays(int n, int mp, int lp) {
+  double gram, apply, sym;
+  orth_tile_kind(true, n, mp, mp, lp, &gram);
+  orth_tile_kind(false, n, mp, lp, mp, &apply);
+  orth_tile_kind(true, n, mp, mp, mp, &sym);
+  return gram + apply > 3.0 * sym;
+}
+
+// Scratch: norm shares and factors, then X (two iterates, hi and lo), and the square matrices:
+// D and B of a step, or R (which A_1 replaces in off_s[3]), B_0, S, A_1, B_1 of two merged
+// ones, whose P takes S's place
 struct OrthLayout {
   int m, l, mp, lp, chunks;
-  size_t off_part, off_factor, off_x[2], off_lo[2], off_d, off_b, bytes;
+  bool merge;
+  size_t off_part, off_factor, off_x[2], off_lo[2], off_s[5], bytes;
 };
 static OrthLayout orth_layout(const moe_orth_shape& s) {
   OrthLayout L{};
@@ -1015,8 +1050,8 @@ static OrthLayout orth_layout(const moe_orth_shape& s) {
     L.off_x[i] = take(xb);
     L.off_lo[i] = take(xb / 2);
   }
-  L.off_d = take(db);
-  L.off_b = take(db);
+  L.merge = s.steps >= 2 && merge_pays(s.n, L.mp, L.lp);
+  for (int i = 0; i < (L.merge ? 5 : 2); ++i) L.off_s[i] = take(db);
   L.bytes = off;
   return L;
 }
@@ -1054,24 +1089,69 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   char* ws = reinterpret_cast<char*>(scratch);
   if (s.dtype == MOE_BF16) orth_enter(s, L, (const bf16_t*)g, ws, st);
   else orth_enter(s, L, (const float*)g, ws, st);
-  for (int i = 0; i < s.steps; ++i) {
-    OrthArgs a{};
-    a.mp = L.mp; a.lp = L.lp; a.m = L.m; a.l = L.l; a.rows = s.rows; a.cols = s.cols;
-    a.step = i;
-    a.x = reinterpret_cast<const f16*>(ws + L.off_x[i & 1]);
-    const bool lo_in = i == 0 ? s.dtype == MOE_F32 : i <= LO_STEPS;
-    a.xlo = lo_in ? reinterpret_cast<const uint8_t*>(ws + L.off_lo[i & 1]) : nullptr;
-    a.factor = reinterpret_cast<const float*>(ws + L.off_factor);
-    a.d = reinterpret_cast<f16*>(ws + L.off_d);
-    a.b = reinterpret_cast<f16*>(ws + L.off_b);
-    a.xn = reinterpret_cast<f16*>(ws + L.off_x[(i + 1) & 1]);
-    a.xnlo = i < LO_STEPS ? reinterpret_cast<uint8_t*>(ws + L.off_lo[(i + 1) & 1]) : nullptr;
-    a.out = (bf16_t*)o;
-    a.scale = scale;
-    orth_product<ORTH_GRAM>("orth_gram", a, s.n, st);
-    orth_product<ORTH_POLY>("orth_poly", a, s.n, st);
-    if (i == s.steps - 1) orth_product<ORTH_LAST>("orth_last", a, s.n, st);
+  f16* const x[2] = {reinterpret_cast<f16*>(ws + L.off_x[0]), reinterpret_cast<f16*>(ws + L.off_x[1])};
+  uint8_t* const xlo[2] = {reinterpret_cast<uint8_t*>(ws + L.off_lo[0]), reinterpret_cast<uint8_t*>(ws + L.off_lo[1])};
+  f16* sq[5];
+  for (int i = 0; i < 5; ++i) sq[i] = reinterpret_cast<f16*>(ws + L.off_s[i]);
+  OrthArgs base{};
+  base.mp = L.mp; base.lp = L.lp; base.m = L.m; base.l = L.l; base.rows = s.rows; base.cols = s.cols;
+  base.out = (bf16_t*)o;
+  const float* factor = reinterpret_cast<const float*>(ws + L.off_factor);
+  int cur = 0;                              // X's buffer
+  bool has_lo = s.dtype == MOE_F32;
+  int los = L.merge ? LO_STEPS - 1 : LO_STEPS;   // iterates still to be kept with their lo
+  // C = c0 P Q^T + c1 S1 + c2 S2 - diag I
+  auto sym = [&](const char* name, const f16* p, const f16* q, int K, f16* c, float c0, float diag, const f16* s1,
+                 float c1, const f16* s2, float c2, const float* f) {
+    OrthArgs a = base;
+    a.p = p; a.q = q; a.K = K; a.c = c; a.c0 = c0; a.diag = diag; a.s1 = s1; a.c1 = c1; a.s2 = s2; a.c2 = c2;
+    a.factor = f;
+    if (s2) orth_product<ORTH_SYM2>(name, a, s.n, st);
+    else if (s1) orth_product<ORTH_SYM1>(name, a, s.n, st);
+    else orth_product<ORTH_SYM0>(name, a, s.n, st);
+  };
+  // D = A - t I of the current X, and B = beta D + c D^2
+  auto gram_poly = [&](f16* d, f16* b, const StepCoef& co, const float* f) {
+    sym("orth_gram", x[cur], x[cur], L.lp, d, f ? D_SCALE : D_SCALE / (X_SCALE * X_SCALE), co.t * D_SCALE, nullptr, 0.f,
+        nullptr, 0.f, f);
+    sym("orth_poly", d, d, L.mp, b, NS_C * B_SCALE / (D_SCALE * D_SCALE), 0.f, d, co.beta * B_SCALE / D_SCALE, nullptr,
+        0.f, nullptr);
+  };
+  // X <- alpha X + P X (P at p_scale); the last one into the result
+  auto apply = [&](const f16* p, float p_scale, float alpha, const float* f, bool last) {
+    OrthArgs a = base;
+    const float out = (last ? scale : X_SCALE) * (f ? 1.f : 1.f / X_SCALE);
+    a.p = p; a.q = x[cur]; a.K = L.mp;
+    a.c0 = out / p_scale;
+    a.c1 = out * alpha;
+    a.factor = f;
+    a.xlo = has_lo ? xlo[cur] : nullptr;
+    has_lo = los-- > 0;
+    a.xn = x[cur ^ 1];
+    a.xnlo = has_lo ? xlo[cur ^ 1] : nullptr;
+    if (last) orth_product<ORTH_LAST>("orth_last", a, s.n, st);
     else orth_product<ORTH_APPLY>("orth_apply", a, s.n, st);
+    cur ^= 1;
+  };
+  int step = 0;
+  if (L.merge) {
+    f16 *r = sq[0], *b0 = sq[1], *sp = sq[2], *a1 = sq[3], *b1 = sq[4];
+    constexpr float BB = 1.f / (B_SCALE * B_SCALE), BD = 1.f / (B_SCALE * D_SCALE);
+    gram_poly(r, b0, step_coef(0), factor);
+    sym("orth_s", b0, r, L.mp, sp, S_SCALE * BD, 0.f, nullptr, 0.f, nullptr, 0.f, nullptr);
+    sym("orth_a1", b0, sp, L.mp, a1, D_SCALE / (B_SCALE * S_SCALE), 0.f, r, NS_A * NS_A, sp, 2.f * NS_A * D_SCALE / S_SCALE,
+        nullptr);
+    sym("orth_poly", a1, a1, L.mp, b1, NS_C * B_SCALE / (D_SCALE * D_SCALE), 0.f, a1, NS_B * B_SCALE / D_SCALE, nullptr,
+        0.f, nullptr);
+    sym("orth_p", b1, b0, L.mp, sp, P_SCALE * BB, 0.f, b0, NS_A * P_SCALE / B_SCALE, b1, NS_A * P_SCALE / B_SCALE, nullptr);
+    apply(sp, P_SCALE, NS_A * NS_A, factor, s.steps == 2);
+    step = 2;
+  }
+  for (; step < s.steps; ++step) {
+    const StepCoef co = step_coef(step);
+    const float* f = step == 0 ? factor : nullptr;
+    gram_poly(sq[0], sq[1], co, f);
+    apply(sq[1], B_SCALE, co.alpha, f, step == s.steps - 1);
   }
   return hipGetLastError();
 }

@@ -5,6 +5,8 @@ from __future__ import annotations
 
 import numpy as np
 
+from . import mx
+
 __all__ = ["norm_forward", "norm_backward", "balance_forward", "balance_backward", "orthogonalize",
            "orthogonalize_rounded"]
 
@@ -88,12 +90,18 @@ def orthogonalize(g, steps, scale=1.0):
     return scale * (x.T if tall else x)
 
 
-def orthogonalize_rounded(g, steps):
-    """The same with the iterates held in fp16: pairs hi + lo through the first three (hi in
-    the products, both in a X), A - I in place of A from the fourth step on, scales 2^15 (X)
-    and 2^14.  What this is off is what such a precision costs."""
+def orthogonalize_rounded(g, steps, merged=False):
+    """The same with the iterates held in fp16: the first two as pairs hi + lo, lo in E4M3
+    times 16 (hi in the products, both in a X), A - I in place of A from the fourth step on,
+    scales 2^15 (X) and 2^14; merged: the first two steps as one, in the square matrices.
+    What this is off is what such a precision costs."""
     def half(v, s):
         return (v * s).astype(np.float16).astype(np.float64) / s
+
+    def pair(v):
+        hi = half(v, 2.0 ** 15)
+        lo = mx.e4m3_decode(mx.e4m3_encode((v - hi) * 2.0 ** 19)) / 2.0 ** 19
+        return hi, hi + lo
 
     a, b, c = NS
     x = np.asarray(g, np.float64)
@@ -101,13 +109,26 @@ def orthogonalize_rounded(g, steps):
     tall = x.shape[0] > x.shape[1]
     if tall:
         x = x.T
-    hi = x
-    for i in range(steps):
+    hi, first, los = x, 0, 2
+    if merged:
+        r = half(hi @ hi.T, 2.0 ** 14)
+        b0 = half(b * r + c * (r @ r), 2.0 ** 14)
+        s = half(b0 @ r, 2.0 ** 14)
+        a1 = half(a * a * r + 2 * a * s + b0 @ s, 2.0 ** 14)
+        b1 = half(b * a1 + c * (a1 @ a1), 2.0 ** 14)
+        p = half(a * b0 + a * b1 + b1 @ b0, 2.0 ** 12)
+        x = a * a * x + p @ hi
+        if steps > 2:
+            hi, x = pair(x)
+        first, los = 2, 1
+    for i in range(first, steps):
         t = 1.0 if i >= 3 else 0.0
         d = half(hi @ hi.T - t * np.eye(len(x)), 2.0 ** 14)
         p = half((b + 2 * c * t) * d + c * (d @ d), 2.0 ** 14)
         x = (a + b * t + c * t * t) * x + p @ hi
         if i < steps - 1:
-            hi = half(x, 2.0 ** 15)
-            x = hi + half(x - hi, 2.0 ** 15) if i < 3 else hi
+            if i - first < los - (1 if merged else 0):
+                hi, x = pair(x)
+            else:
+                hi = x = half(x, 2.0 ** 15)
     return x.T if tall else x

@@ -16,7 +16,7 @@ from test_oracle_train import spectra
 pytestmark = pytest.mark.gpu
 
 TOL = 2.0 ** -8 + 3e-3
-SIZES = [(1, 1), (1, 9), (9, 1), (2, 2), (17, 33), (64, 64), (65, 64), (63, 130), (128, 64), (130, 257), (257, 130),
+SIZES = [(64, 700), (700, 64), (130, 1100), (1, 1), (1, 9), (9, 1), (2, 2), (17, 33), (64, 64), (65, 64), (63, 130), (128, 64), (130, 257), (257, 130),
          (256, 256), (300, 700), (768, 256), (520, 520), (333, 1000), (1000, 333)]
 
 
@@ -84,11 +84,13 @@ def test_orth_matrices_apart():
     assert torch.equal(alone[0], clean[2])
 
 
-def test_orth_in_place_and_within_bounds():
+# one launch; step by step on small tiles; two steps merged; 256-row tiles (40 matrices)
+@pytest.mark.parametrize("n,rows,cols", [(2, 70, 33), (2, 260, 250), (2, 70, 700), (2, 700, 70), (40, 500, 610)])
+def test_orth_in_place_and_within_bounds(n, rows, cols):
     import combine_top_router_amd.lib as L
-    s = L.MoeOrthShape(2, 70, 33, L.MOE_BF16, 5)
-    g = torch.stack([torch.from_numpy(spectra("flat", 70, 33, i)) for i in range(2)]).to(torch.bfloat16).cuda()
-    want = _op(2, 70, 33, torch.bfloat16).update(g)
+    s = L.MoeOrthShape(n, rows, cols, L.MOE_BF16, 5)
+    g = torch.randn(n, rows, cols, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda()
+    want = _op(n, rows, cols, torch.bfloat16).update(g)
     count = g.numel()
     buf = torch.full((count + 128,), 9.0, dtype=torch.bfloat16, device="cuda")
     buf[:count] = g.reshape(-1)
@@ -96,8 +98,22 @@ def test_orth_in_place_and_within_bounds():
     ws = torch.full((nb + 256,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN in every type: all of it is written first
     L.moe_orthogonalize(s, buf.data_ptr(), buf.data_ptr(), 1.0, ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
-    assert torch.equal(buf[:count].view(2, 70, 33), want)
+    assert torch.equal(buf[:count].view(n, rows, cols), want)
     assert (buf[count:] == 9).all() and (ws[nb:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("n,rows,cols", [(40, 512, 640), (40, 640, 512), (36, 300, 1500), (36, 1500, 300), (48, 260, 520)])
+@pytest.mark.parametrize("steps", [2, 3, 5])
+def test_orth_of_many_matrices(n, rows, cols, steps):
+    """Enough of them for the larger tiles, step by step and merged; three of them looked at."""
+    gen = torch.Generator().manual_seed(rows)
+    g = torch.randn(n, rows, cols, generator=gen).to(torch.bfloat16)
+    for i, k in enumerate(("flat", "low_rank", "power")):
+        g[i * (n // 3)] = torch.from_numpy(spectra(k, rows, cols, i)).to(torch.bfloat16)
+    o = _op(n, rows, cols, torch.bfloat16, steps).update(g.cuda())
+    torch.cuda.synchronize()
+    for i in (0, n // 3, 2 * (n // 3), n - 1):
+        assert _off(o[i], ot.orthogonalize(g[i].double().numpy(), steps)) < TOL, i
 
 
 def test_orth_refuses_other_tensors():

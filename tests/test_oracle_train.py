@@ -92,10 +92,11 @@ def spectra(kind, m, l, seed):
     return (u * np.arange(1, min(m, l) + 1.0) ** -1) @ v.T
 
 
+@pytest.mark.parametrize("merged", [False, True])
 @pytest.mark.parametrize("kind", ["flat", "low_rank", "power"])
-@pytest.mark.parametrize("m,l", [(64, 64), (96, 200), (200, 96)])
-def test_the_precision_of_the_iterates_costs_little(kind, m, l):
+@pytest.mark.parametrize("m,l", [(64, 64), (96, 200), (200, 96), (64, 512)])
+def test_the_precision_of_the_iterates_costs_little(kind, m, l, merged):
     g = spectra(kind, m, l, 5)
     want = ot.orthogonalize(g, 5)
-    off = np.linalg.norm(ot.orthogonalize_rounded(g, 5) - want) / np.linalg.norm(want)
+    off = np.linalg.norm(ot.orthogonalize_rounded(g, 5, merged) - want) / np.linalg.norm(want)
     assert off < 2e-3
