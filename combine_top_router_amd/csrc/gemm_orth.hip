@@ -838,42 +838,70 @@ static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t
 // B.  One launch instead of 2 + 3 a step, which is what bounds matrices this small: eight of
 // 128 x 64, five steps, took 84 us in 17 launches.
 constexpr int SMALL_ELEMS = 32768, SMALL_MP = 128;
-constexpr int SMALL_BLOCKS = SMALL_ELEMS / 1024 / NW;   // 32 x 32 blocks of X a wave
 constexpr int small_lds(int mp) {   // elements: X (rows of lp + 8), D and B (rows of mp + 8)
   return SMALL_ELEMS + 8 * mp + 2 * mp * (mp + 8);
 }
 
-// 32 x 32 block of P Q^T, K-major rows of ldp and ldq in LDS, transposed in the accumulator
-__device__ __forceinline__ f32x16 small_block(const f16* p, int ldp, const f16* q, int ldq, int K, int lane) {
-  f32x16 acc;
+// NB 32 x 32 blocks of P Q^T, K-major rows of ldp and ldq in LDS, transposed in the
+// accumulators; the blocks lie qs columns of it apart in one row of blocks, so that a fragment
+// of P serves all of them (LDS reads are what such a step waits for)
+template <int NB>
+__device__ __forceinline__ void small_blocks(const f16* p, int ldp, const f16* q, int ldq, int qs, int K, int lane,
+                                             f32x16 (&acc)[NB]) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
   const f16 *pa = p + (lane & 31) * ldp + 8 * (lane >> 5), *pb = q + (lane & 31) * ldq + 8 * (lane >> 5);
 #pragma unroll 4
-  for (int k = 0; k < K; k += 16)
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(pb + k),
-                                                 *reinterpret_cast<const f16x8*>(pa + k), acc, 0, 0, 0);
-  return acc;
-}
-// 32 x 32 block of B X: K-major rows of B; X as it lies, [K][ldx], through the transposing read
-__device__ __forceinline__ f32x16 small_block_x(const f16* b, int ldb, const f16* x, int ldx, int K, int lane) {
-  f32x16 acc;
+  for (int k = 0; k < K; k += 16) {
+    const f16x8 pf = *reinterpret_cast<const f16x8*>(pa + k);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-  const f16* pa = b + (lane & 31) * ldb + 8 * (lane >> 5);
+    for (int b = 0; b < NB; ++b)
+      acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(pb + b * qs * ldq + k), pf, acc[b], 0, 0, 0);
+  }
+}
+// the same of B X, at xo[b] columns of it: X as it lies, [K][ldx], through the transposing
+// read
+template <int NB>
+__device__ __forceinline__ void small_blocks_x(const f16* p, int ldp, const f16* x, int ldx, const int (&xo)[NB], int K,
+                                               int lane, f32x16 (&acc)[NB]) {
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
+  const f16* pa = p + (lane & 31) * ldp + 8 * (lane >> 5);
   const int g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
   const f16* px = x + (8 * (g >> 1) + j) * ldx + 16 * (g & 1) + 4 * q;
-#pragma unroll 4
+#pragma unroll 2
   for (int k = 0; k < K; k += 16) {
-    s16x4 t[2];
+    const f16x8 pf = *reinterpret_cast<const f16x8*>(pa + k);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) t[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(px + (k + 4 * h) * ldx));
-    f16x8 xf;
-    __builtin_memcpy(&xf, t, 16);
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, *reinterpret_cast<const f16x8*>(pa + k), acc, 0, 0, 0);
+    for (int b = 0; b < NB; ++b) {
+      s16x4 t[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        t[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(px + (k + 4 * h) * ldx + xo[b]));
+      f16x8 xf;
+      __builtin_memcpy(&xf, t, 16);
+      acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, pf, acc[b], 0, 0, 0);
+    }
   }
-  return acc;
 }
+// four elements at p, at any element's address
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef i32x2 i32x2_a2 __attribute__((aligned(2)));
+__device__ __forceinline__ f32x4 load4(const bf16_t* p) {
+  const i32x2 u = *reinterpret_cast<const i32x2_a2*>(p);
+  return f32x4{__uint_as_float((uint32_t)u[0] << 16), __uint_as_float((uint32_t)u[0] & 0xffff0000u),
+               __uint_as_float((uint32_t)u[1] << 16), __uint_as_float((uint32_t)u[1] & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4 load4(const float* p) {
+  const i32x4 u = *reinterpret_cast<const i32x4_a4*>(p);
+  return f32x4{__uint_as_float((uint32_t)u[0]), __uint_as_float((uint32_t)u[1]), __uint_as_float((uint32_t)u[2]),
+               __uint_as_float((uint32_t)u[3])};
+}
+
 // 16 values in the transposed accumulator layout -> the block at dst, rows of ld
 __device__ __forceinline__ void small_put(f16* dst, int ld, const float (&v)[16], int lane) {
   f16* const row = dst + (lane & 31) * ld + 4 * (lane >> 5);
@@ -882,12 +910,15 @@ __device__ __forceinline__ void small_put(f16* dst, int ld, const float (&v)[16]
     *reinterpret_cast<f16x4*>(row + 8 * q) = f16x4{(f16)v[4 * q], (f16)v[4 * q + 1], (f16)v[4 * q + 2], (f16)v[4 * q + 3]};
 }
 
-template <typename T, int MP>
+// XB: 32 x 32 blocks of X a wave, 1, 2 or 4 (one launch runs its code cold: the instructions
+// of blocks that are not there cost more than the work of those that are)
+template <typename T, int MP, int XB>
 __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out, int rows, int cols, int lp,
                                                         int steps, float scale) {
   __shared__ __attribute__((aligned(16))) f16 small[small_lds(MP)];
   __shared__ double red[NW];
   constexpr int LDM = MP + 8, RB = MP / 32;
+  constexpr int SB = RB * RB > NW ? RB * RB / NW : 1;   // blocks of D and B a wave
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), ldx = lp + 8;
   f16* const xs = small;
   f16* const ds = xs + MP * ldx;
@@ -897,19 +928,30 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
   const size_t si = tall ? 1 : cols, sj = tall ? cols : 1;   // strides of X in g and out
   const int nb = RB * (lp / 32);
   const size_t base = (size_t)blockIdx.x * rows * cols;
-  float x[SMALL_BLOCKS][16];
+  float x[XB][16];
   double ss = 0.0;
 #pragma unroll
-  for (int b = 0; b < SMALL_BLOCKS; ++b) {
+  for (int b = 0; b < XB; ++b) {
     const int blk = wv + NW * b, i = (blk % RB) * 32 + (lane & 31), j0 = (blk / RB) * 32 + 4 * (lane >> 5);
+    const T* const row = g + base + i * si;
+    const bool in = blk < nb && i < m;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int j = j0 + 8 * (r >> 2) + (r & 3);
-      const bool in = blk < nb && i < m && j < l;
-      x[b][r] = in ? elem<T>::load(g + base + i * si + j * sj) : 0.f;
-      ss += (double)x[b][r] * (double)x[b][r];
+    for (int q = 0; q < 4; ++q) {
+      const int j = j0 + 8 * q;
+      if (!tall && in && j + 4 <= l) {   // four of a row at once; transposed, a load takes 32 neighbours
+        const f32x4 u = load4(row + j);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[b][4 * q + c] = u[c];
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[b][4 * q + c] = in && j + c < l ? elem<T>::load(row + (j + c) * sj) : 0.f;
+      }
     }
   }
+#pragma unroll
+  for (int b = 0; b < XB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) ss += (double)x[b][r] * (double)x[b][r];
   ss = wave_sum_f64(ss);
   if (lane == 0) red[wv] = ss;
   __syncthreads();
@@ -924,81 +966,111 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
   }
   const float f = (float)(ldexp(1.0, -e) / (norm + NS_EPS));   // through 2^e: no factor leaves fp32's range
 #pragma unroll
-  for (int b = 0; b < SMALL_BLOCKS; ++b)
+  for (int b = 0; b < XB; ++b)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) x[b][r] = ldexpf(x[b][r], e) * f;
+    for (int r = 0; r < 16; ++r) x[b][r] = ldexpf(x[b][r], e) * (f * X_SCALE);   // X 2^15, as in LDS
   for (int step = 0; step < steps; ++step) {
     const StepCoef co = step_coef(step);
 #pragma unroll
-    for (int b = 0; b < SMALL_BLOCKS; ++b) {
+    for (int b = 0; b < XB; ++b) {
       const int blk = wv + NW * b;
-      if (blk < nb) {
+      if (blk < nb) small_put(xs + (blk % RB) * 32 * ldx + (blk / RB) * 32, ldx, x[b], lane);
+    }
+    __syncthreads();
+    // a wave's blocks of D and B, and of X, share a row of blocks: NW is a multiple of RB
+    static_assert(NW % RB == 0, "block rows");
+    const int bi = wv % RB * 32, bj0 = wv / RB * 32;
+    if (wv < RB * RB) {
+      f32x16 acc[SB];
+      small_blocks<SB>(xs + bi * ldx, ldx, xs + bj0 * ldx, ldx, NW / RB * 32, lp, lane, acc);
+#pragma unroll
+      for (int b = 0; b < SB; ++b) {
+        const int bj = bj0 + b * (NW / RB) * 32;
         float v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = x[b][r] * X_SCALE;
-        small_put(xs + (blk % RB) * 32 * ldx + (blk / RB) * 32, ldx, v, lane);
+        for (int r = 0; r < 16; ++r) v[r] = acc[b][r] * (D_SCALE / (X_SCALE * X_SCALE));
+        if (bi == bj) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if ((lane & 31) == 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= co.t * D_SCALE;
+        }
+        small_put(ds + bi * LDM + bj, LDM, v, lane);
       }
     }
     __syncthreads();
-    for (int blk = wv; blk < RB * RB; blk += NW) {
-      const int bi = blk % RB * 32, bj = blk / RB * 32;
-      const f32x16 acc = small_block(xs + bi * ldx, ldx, xs + bj * ldx, ldx, lp, lane);
-      float v[16];
+    if (wv < RB * RB) {
+      f32x16 acc[SB];
+      small_blocks<SB>(ds + bi * LDM, LDM, ds + bj0 * LDM, LDM, NW / RB * 32, MP, lane, acc);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        v[r] = acc[r] * (D_SCALE / (X_SCALE * X_SCALE));
-        if (bi + (lane & 31) == bj + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= co.t * D_SCALE;
+      for (int b = 0; b < SB; ++b) {
+        const int bj = bj0 + b * (NW / RB) * 32;
+        float v[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f16x4 d = *reinterpret_cast<const f16x4*>(ds + (bi + (lane & 31)) * LDM + bj + 8 * q + 4 * (lane >> 5));
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            v[4 * q + c] = acc[b][4 * q + c] * (NS_C * B_SCALE / (D_SCALE * D_SCALE)) + (float)d[c] * (co.beta * B_SCALE / D_SCALE);
+        }
+        small_put(bs + bi * LDM + bj, LDM, v, lane);
       }
-      small_put(ds + bi * LDM + bj, LDM, v, lane);
     }
     __syncthreads();
-    for (int blk = wv; blk < RB * RB; blk += NW) {
-      const int bi = blk % RB * 32, bj = blk / RB * 32;
-      const f32x16 acc = small_block(ds + bi * LDM, LDM, ds + bj * LDM, LDM, MP, lane);
-      float v[16];
+    {
+      f32x16 acc[XB];
+      int xo[XB];   // a block past the last reads the wave's first again; its x goes nowhere
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f16x4 d = *reinterpret_cast<const f16x4*>(ds + (bi + (lane & 31)) * LDM + bj + 8 * q + 4 * (lane >> 5));
+      for (int b = 0; b < XB; ++b) xo[b] = wv + NW * b < nb ? b * (NW / RB) * 32 : 0;
+      if (wv < nb) {
+        small_blocks_x<XB>(bs + bi * LDM, LDM, xs + wv / RB * 32, ldx, xo, MP, lane, acc);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          v[4 * q + c] = acc[4 * q + c] * (NS_C * B_SCALE / (D_SCALE * D_SCALE)) + (float)d[c] * (co.beta * B_SCALE / D_SCALE);
-      }
-      small_put(bs + bi * LDM + bj, LDM, v, lane);
-    }
-    __syncthreads();
+        for (int b = 0; b < XB; ++b)
 #pragma unroll
-    for (int b = 0; b < SMALL_BLOCKS; ++b) {
-      const int blk = wv + NW * b;
-      if (blk < nb) {
-        const f32x16 acc = small_block_x(bs + (blk % RB) * 32 * LDM, LDM, xs + (blk / RB) * 32, ldx, MP, lane);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[b][r] = x[b][r] * co.alpha + acc[r] * (1.f / (X_SCALE * B_SCALE));
+          for (int r = 0; r < 16; ++r) x[b][r] = x[b][r] * co.alpha + acc[b][r] * (1.f / B_SCALE);
       }
     }
     __syncthreads();   // xs, ds and bs have been read
   }
+  scale *= 1.f / X_SCALE;
 #pragma unroll
-  for (int b = 0; b < SMALL_BLOCKS; ++b) {
+  for (int b = 0; b < XB; ++b) {
     const int blk = wv + NW * b, i = (blk % RB) * 32 + (lane & 31), j0 = (blk / RB) * 32 + 4 * (lane >> 5);
+    bf16_t* const row = out + base + i * si;
+    if (blk >= nb || i >= m) continue;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int j = j0 + 8 * (r >> 2) + (r & 3);
-      if (blk < nb && i < m && j < l) out[base + i * si + j * sj] = f2bf(x[b][r] * scale);
+    for (int q = 0; q < 4; ++q) {
+      const int j = j0 + 8 * q;
+      if (!tall && j + 4 <= l) {
+        *reinterpret_cast<i32x2_a2*>(row + j) =
+            i32x2{(int)pk_bf16(x[b][4 * q] * scale, x[b][4 * q + 1] * scale),
+                  (int)pk_bf16(x[b][4 * q + 2] * scale, x[b][4 * q + 3] * scale)};
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (j + c < l) row[(j + c) * sj] = f2bf(x[b][4 * q + c] * scale);
+      }
     }
   }
 }
 
 inline bool orth_small(int mp, int lp) { return mp <= SMALL_MP && mp * lp <= SMALL_ELEMS; }
 
+template <typename T, int MP>
+static hipError_t launch_small(const moe_orth_shape& s, const T* g, bf16_t* o, int lp, float scale, hipStream_t st) {
+  const dim3 grid((unsigned)s.n), block(NTHR);
+  const int blocks = (int)ceil_div(MP / 32 * (lp / 32), NW);
+#define CALL(XB) \
+  MOE_LAUNCH("orth_small", (k_orth_small<T, MP, XB>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, scale)
+  if (blocks == 1) CALL(1);
+  else if (blocks == 2) CALL(2);
+  else CALL(4);
+#undef CALL
+  return hipGetLastError();
+}
 template <typename T>
 static hipError_t launch_small(const moe_orth_shape& s, const T* g, bf16_t* o, int mp, int lp, float scale,
                                hipStream_t st) {
-  const dim3 grid((unsigned)s.n), block(NTHR);
-  if (mp == 64)
-    MOE_LAUNCH("orth_small", (k_orth_small<T, 64>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, scale);
-  else
-    MOE_LAUNCH("orth_small", (k_orth_small<T, 128>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, scale);
-  return hipGetLastError();
+  return mp == 64 ? launch_small<T, 64>(s, g, o, lp, scale, st) : launch_small<T, 128>(s, g, o, lp, scale, st);
 }
 
 inline int pad64(int v) { return (v + 63) & ~63; }

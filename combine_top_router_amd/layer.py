@@ -38,22 +38,19 @@ class _OnDevice:
     def _place(self, device):
         self.device = _device(device)
         self._index = self.device.index
-        L.load()
 
     def _check(self, t, shape, dtype, name):
         if t.dtype != dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
-    def _stream(self, stream):
-        return _raw_stream(self._index) if stream is None else stream.cuda_stream
-
-    def _call(self, func, *args):
+    def _call(self, func, stream, *args):
+        s = _raw_stream(self._index) if stream is None else stream.cuda_stream
         if torch.cuda.current_device() == self._index:
-            func(*args)
+            func(*args, s)
         else:
             with torch.cuda.device(self._index):
-                func(*args)
+                func(*args, s)
 
 
 class MoeNorm(_OnDevice):
@@ -77,6 +74,9 @@ class MoeNorm(_OnDevice):
         self.dw = torch.empty(H, dtype=dt, device=dev)
         self.db = torch.empty(H, dtype=dt, device=dev)
         self.scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
+        # the buffers stay where they are
+        self._p_sum, self._p_y, self._p_mean, self._p_rstd = _p(self._sum), _p(self.y), _p(self.mean), _p(self.rstd)
+        self._p_dx, self._p_dw, self._p_scratch = _p(self.dx), _p(self.dw), _p(self.scratch)
         self.sum = None
         self.inputs = None
 
@@ -89,8 +89,8 @@ class MoeNorm(_OnDevice):
             self._check(res, self._row, self.dtype, "res")
         self.sum = None if res is None else self._sum
         self.inputs = (x, res, w, b is not None)
-        self._call(L.moe_norm_fwd, self.shape, _p(x), _p(res), _p(w), _p(b), _p(self.sum), _p(self.y), _p(self.mean),
-                   _p(self.rstd), self._stream(stream))
+        self._call(L.moe_norm_fwd, stream, self.shape, _p(x), _p(res), _p(w), _p(b), 0 if res is None else self._p_sum,
+                   self._p_y, self._p_mean, self._p_rstd)
         return self.y
 
     def backward(self, dy, ds_in=None, stream=None):
@@ -101,8 +101,8 @@ class MoeNorm(_OnDevice):
             self._check(ds_in, self._row, self.dtype, "ds_in")
         x, res, w, bias = self.inputs
         db = self.db if bias else None
-        self._call(L.moe_norm_bwd, self.shape, _p(dy), _p(x), _p(res), _p(w), _p(self.mean), _p(self.rstd), _p(ds_in),
-                   _p(self.dx), _p(self.dw), _p(db), _p(self.scratch), self._stream(stream))
+        self._call(L.moe_norm_bwd, stream, self.shape, _p(dy), _p(x), _p(res), _p(w), self._p_mean, self._p_rstd,
+                   _p(ds_in), self._p_dx, self._p_dw, _p(db), self._p_scratch)
         return {"dx": self.dx, "dw": self.dw, "db": db}
 
 
@@ -123,6 +123,7 @@ class BalanceLoss(_OnDevice):
         self.prob = torch.empty(E, dtype=f32, device=dev)
         self.d_logits = torch.empty(T, E, dtype=f32, device=dev)
         self.scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
+        self._p_fwd = (_p(self.loss), _p(self.counts), _p(self.prob), _p(self.scratch))
         self.inputs = None
 
     def forward(self, logits, topk_idx, coef, mask=None, stream=None):
@@ -131,8 +132,7 @@ class BalanceLoss(_OnDevice):
         if mask is not None:
             self._check(mask, self._mask, torch.uint8, "mask")
         self.inputs = (logits, mask, float(coef))
-        self._call(L.moe_balance_fwd, self.shape, _p(logits), _p(topk_idx), _p(mask), coef, _p(self.loss),
-                   _p(self.counts), _p(self.prob), _p(self.scratch), self._stream(stream))
+        self._call(L.moe_balance_fwd, stream, self.shape, _p(logits), _p(topk_idx), _p(mask), coef, *self._p_fwd)
         return self.loss
 
     def backward(self, d_loss=None, d_logits_in=None, out=None, stream=None):
@@ -147,8 +147,8 @@ class BalanceLoss(_OnDevice):
         else:
             self._check(out, self._logits, torch.float32, "out")
         logits, mask, coef = self.inputs
-        self._call(L.moe_balance_bwd, self.shape, _p(logits), _p(self.counts), _p(mask), coef, _p(d_loss),
-                   _p(d_logits_in), _p(out), self._stream(stream))
+        self._call(L.moe_balance_bwd, stream, self.shape, _p(logits), self._p_fwd[1], _p(mask), coef, _p(d_loss),
+                   _p(d_logits_in), _p(out))
         return out
 
 
@@ -174,8 +174,7 @@ class Orthogonalizer(_OnDevice):
             out = self.o
         else:
             self._check(out, self._size, torch.bfloat16, "out")
-        self._call(L.moe_orthogonalize, self.shape, _p(g), _p(out), scale, _p(self.scratch),
-                   self._stream(stream))
+        self._call(L.moe_orthogonalize, stream, self.shape, _p(g), _p(out), scale, _p(self.scratch))
         return out
 
 

@@ -16,7 +16,7 @@ from test_oracle_train import spectra
 pytestmark = pytest.mark.gpu
 
 TOL = 2.0 ** -8 + 3e-3
-SIZES = [(64, 700), (700, 64), (130, 1100), (1, 1), (1, 9), (9, 1), (2, 2), (17, 33), (64, 64), (65, 64), (63, 130), (128, 64), (130, 257), (257, 130),
+SIZES = [(100, 200), (128, 150), (60, 320), (40, 500), (64, 700), (700, 64), (130, 1100), (1, 1), (1, 9), (9, 1), (2, 2), (17, 33), (64, 64), (65, 64), (63, 130), (128, 64), (130, 257), (257, 130),
          (256, 256), (300, 700), (768, 256), (520, 520), (333, 1000), (1000, 333)]
 
 
