@@ -8,7 +8,7 @@
 //
 // Both passes are bound by HBM: about ten flops an element against 8 bytes (forward with a
 // residual, bf16) or 8 to 10 (backward).  So a row is read once and held in registers, as
-// EPT fp32 values in each of the TPR threads that share it: the statistics are two passes
+// EPT fp32 values in each of the threads that share it: the statistics are two passes
 // over registers (the variance about the mean itself, not E[s^2] - mu^2, which cancels),
 // and the backward keeps each thread's columns of dw and db in registers over all its rows.
 #include "common.h"
@@ -18,7 +18,7 @@ namespace moe {
 namespace {
 
 // 16 bytes at an address of any element: gfx950 global loads and stores run in unaligned
-// mode, so rows of an odd width take the same wide accesses as aligned ones
+// mode, so rows of an odd width take wide accesses too
 typedef i32x4 i32x4_a2 __attribute__((aligned(2)));
 typedef i32x4 i32x4_a4 __attribute__((aligned(4)));
 
@@ -55,8 +55,8 @@ template <> struct rowvec<float> {
   }
 };
 
-// V elements at column c of a row of H: whole vectors where they fit, element by element in
-// the row's last, partial one; columns at or past H read as 0 and are not written
+// V elements at column c of a row of H: whole vectors where they fit, element by element
+// over the row's end (the kernels of long and of very short rows)
 template <typename T>
 __device__ __forceinline__ void load_cols(const T* row, int c, int H, float (&v)[rowvec<T>::V]) {
   constexpr int V = rowvec<T>::V;
@@ -79,64 +79,135 @@ __device__ __forceinline__ void store_cols(T* row, int c, int H, const float (&v
   }
 }
 
-// Sums of a and b over the TPR threads of a row, in every one of them.  TPR = 64 is one
-// wave; larger groups are the whole workgroup and meet in red, which the caller gives anew
-// (another slot) for each call between two barriers.
-template <int TPR>
+// The same for the rows held in registers: columns c .. c + V - 1, c >= -1; columns outside
+// [0, H) read as 0 and are not written.  EDGE: H is no multiple of V.  A vector over a row's
+// end is then read whole, with the neighbour rows' elements (which may be changing: they are
+// dropped); at the tensor's own ends the vector is moved to columns lo .. hi, inside it, and
+// its elements moved back.  (Element by element, the ends made the rows of 4095 bf16 take three
+// times as long as those of 4096.)
+struct RowEnds {
+  int lo, hi;
+};
+// of row t of T, V <= H
+template <int V>
+__device__ __forceinline__ RowEnds row_ends(int64_t t, int64_t T, int H) {
+  const int64_t left = (T - t) * H - V;
+  return {t > 0 ? -1 : 0, left < (1 << 30) ? (int)left : 1 << 30};
+}
+template <bool EDGE, typename T>
+__device__ __forceinline__ void load_row(const T* row, RowEnds ends, int c, int H, float (&v)[rowvec<T>::V]) {
+  constexpr int V = rowvec<T>::V;
+  if (c < H) {
+    if constexpr (EDGE) {
+      const int from = min(max(c, ends.lo), ends.hi), d = c - from;   // d: -1 .. V - 1
+      rowvec<T>::load(row + from, v);
+      if (c < 0 || c + V > H) {
+        if (d < 0) {
+#pragma unroll
+          for (int j = V - 1; j > 0; --j) v[j] = v[j - 1];
+        }
+#pragma unroll
+        for (int b = V / 2; b >= 1; b >>= 1)
+          if (d > 0 && (d & b)) {
+#pragma unroll
+            for (int j = 0; j + b < V; ++j) v[j] = v[j + b];
+          }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (c + j < 0 || c + j >= H) v[j] = 0.f;
+      }
+    } else {
+      rowvec<T>::load(row + c, v);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = 0.f;
+  }
+}
+template <bool EDGE, typename T>
+__device__ __forceinline__ void store_row(T* row, int c, int H, const float (&v)[rowvec<T>::V]) {
+  constexpr int V = rowvec<T>::V;
+  if (!EDGE || (c >= 0 && c + V <= H)) {
+    if (c < H) rowvec<T>::store(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (c + j >= 0 && c + j < H) elem<T>::store(row + c + j, v[j]);
+  }
+}
+
+// Columns by which a row's vectors start early, so that a bf16 row at an odd element is read
+// at whole words (16 bytes at an odd one cost twice as much).  Any value gives the same
+// results up to the order of the row's sums; cap: the columns that the row's threads hold.
+template <bool EDGE, typename T>
+__device__ __forceinline__ int col_shift(const T* row, int H, int cap) {
+  return EDGE && sizeof(T) == 2 && H < cap ? (int)(((uintptr_t)row >> 1) & 1) : 0;
+}
+
+// The threads of a row: one wave (WAVE; four rows a workgroup) or the whole workgroup, of
+// as many waves as the row fills.
+template <bool WAVE>
+__device__ __forceinline__ int row_threads() { return WAVE ? 64 : (int)blockDim.x; }
+
+// Sums of a and b over the threads of a row, in every one of them.  Workgroups meet in red,
+// of which the caller gives another slot for each call between two barriers.
+template <bool WAVE>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float (*red)[2]) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
     a += __shfl_xor(a, off, 64);
     b += __shfl_xor(b, off, 64);
   }
-  if constexpr (TPR > 64) {
-    constexpr int NWV = TPR / 64;
-    const int wv = threadIdx.x >> 6;
+  if constexpr (!WAVE) {
+    const int wv = threadIdx.x >> 6, nw = (int)(blockDim.x >> 6);
     if ((threadIdx.x & 63) == 0) {
       red[wv][0] = a;
       red[wv][1] = b;
     }
     __syncthreads();
-    a = 0.f;
-    b = 0.f;
-#pragma unroll
-    for (int i = 0; i < NWV; ++i) {
+    a = red[0][0];
+    b = red[0][1];
+#pragma unroll 4
+    for (int i = 1; i < nw; ++i) {
       a += red[i][0];
       b += red[i][1];
     }
   }
 }
 
-template <int TPR>
-constexpr int wg_threads() { return TPR > 64 ? TPR : 256; }
+constexpr int MAX_WAVES = 16;
+template <bool WAVE>
+constexpr int wg_most() { return WAVE ? 256 : 64 * MAX_WAVES; }
 
-// Forward, a row in the registers of TPR threads (H <= TPR EPT).  The norm is taken of the
-// fp32 sum, not of the sum rounded to the stored type: y then carries one rounding instead
-// of two.
-template <typename T, int TPR, int EPT, bool RMS>
-__global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_fwd(const T* x, const T* res,
-                                                               const T* __restrict__ w, const T* __restrict__ b,
-                                                               int T_, int H, float eps, T* sum, T* y, float* mean,
-                                                               float* rstd) {
-  constexpr int V = rowvec<T>::V, NV = EPT / V, GROUPS = wg_threads<TPR>() / TPR;
-  __shared__ float red[4][TPR / 64][2];
-  const int lane = threadIdx.x % TPR;
+// Forward, a row in registers.  The norm is taken of the fp32 sum, not of the sum rounded to
+// the stored type: y then carries one rounding instead of two.
+template <typename T, bool WAVE, int EPT, bool EDGE, bool RMS>
+__global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_fwd(const T* x, const T* res, const T* __restrict__ w,
+                                                             const T* __restrict__ b, int T_, int H, float eps,
+                                                             T* sum, T* y, float* mean, float* rstd) {
+  constexpr int V = rowvec<T>::V, NV = EPT / V, GROUPS = WAVE ? 4 : 1;
+  __shared__ float red[4][MAX_WAVES][2];
+  const int tpr = row_threads<WAVE>(), lane = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  const RowEnds vec = row_ends<V>(0, 1, H);   // of w and b
   int par = 0;   // the row's slots in red: those of the row before may still be read
-  for (int64_t t = (int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR; t < T_; t += (int64_t)gridDim.x * GROUPS, par ^= 2) {
+  for (int64_t t = (int64_t)blockIdx.x * GROUPS + (WAVE ? threadIdx.x >> 6 : 0); t < T_;
+       t += (int64_t)gridDim.x * GROUPS, par ^= 2) {
     const size_t off = (size_t)t * H;
+    const RowEnds ends = row_ends<V>(t, T_, H);
+    const int c0 = lane * V - col_shift<EDGE>(x + off, H, tpr * EPT);
     float v[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load_cols(x + off, (lane + i * TPR) * V, H, v[i]);
+    for (int i = 0; i < NV; ++i) load_row<EDGE>(x + off, ends, c0 + i * tpr * V, H, v[i]);
     if (res) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float r[V];
-        load_cols(res + off, (lane + i * TPR) * V, H, r);
+        load_row<EDGE>(res + off, ends, c0 + i * tpr * V, H, r);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[i][j] += r[j];
       }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) store_cols(sum + off, (lane + i * TPR) * V, H, v[i]);
+      for (int i = 0; i < NV; ++i) store_row<EDGE>(sum + off, c0 + i * tpr * V, H, v[i]);
     }
     float mu = 0.f;
     if constexpr (!RMS) {
@@ -145,7 +216,7 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_fwd(const T* x, cons
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) s += v[i][j];
-      row_sum2<TPR>(s, unused, red[par]);
+      row_sum2<WAVE>(s, unused, red[par]);
       mu = s / (float)H;
     }
     float q = 0.f, unused = 0.f;
@@ -153,25 +224,26 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_fwd(const T* x, cons
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
+        const int c = c0 + i * tpr * V + (EDGE ? j : 0);   // else vectors lie inside or outside whole
         v[i][j] -= mu;
-        if ((lane + i * TPR) * V + j < H) q += v[i][j] * v[i][j];
+        if (RMS || (c >= 0 && c < H)) q += v[i][j] * v[i][j];
       }
-    row_sum2<TPR>(q, unused, red[par + 1]);
+    row_sum2<WAVE>(q, unused, red[par + 1]);
     const float rs = 1.f / sqrtf(q / (float)H + eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * TPR) * V;
+      const int c = c0 + i * tpr * V;
       float wv[V];
-      load_cols(w, c, H, wv);
+      load_row<EDGE>(w, vec, c, H, wv);
 #pragma unroll
       for (int j = 0; j < V; ++j) v[i][j] *= rs * wv[j];
       if (b) {
         float bv[V];
-        load_cols(b, c, H, bv);
+        load_row<EDGE>(b, vec, c, H, bv);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[i][j] += bv[j];
       }
-      store_cols(y + off, c, H, v[i]);
+      store_row<EDGE>(y + off, c, H, v[i]);
     }
     if (lane == 0) {
       if constexpr (!RMS) mean[t] = mu;
@@ -188,7 +260,7 @@ __global__ __launch_bounds__(LONG_T) void k_norm_fwd_long(const T* x, const T* r
                                                           const T* __restrict__ w, const T* __restrict__ b, int T_,
                                                           int H, float eps, T* sum, T* y, float* mean, float* rstd) {
   constexpr int V = rowvec<T>::V;
-  __shared__ float red[4][LONG_T / 64][2];
+  __shared__ float red[4][MAX_WAVES][2];
   int par = 0;
   for (int64_t t = blockIdx.x; t < T_; t += gridDim.x, par ^= 2) {
     const size_t off = (size_t)t * H;
@@ -210,7 +282,7 @@ __global__ __launch_bounds__(LONG_T) void k_norm_fwd_long(const T* x, const T* r
 #pragma unroll
         for (int j = 0; j < V; ++j) s += v[j];
       }
-      row_sum2<LONG_T>(s, unused, red[par]);
+      row_sum2<false>(s, unused, red[par]);
       mu = s / (float)H;
     }
     float q = 0.f;
@@ -222,7 +294,7 @@ __global__ __launch_bounds__(LONG_T) void k_norm_fwd_long(const T* x, const T* r
       for (int j = 0; j < V; ++j)
         if (c + j < H) q += (v[j] - mu) * (v[j] - mu);
     }
-    row_sum2<LONG_T>(q, unused, red[par + 1]);
+    row_sum2<false>(q, unused, red[par + 1]);
     const float rs = 1.f / sqrtf(q / (float)H + eps);
     for (int c = threadIdx.x * V; c < H; c += LONG_T * V) {
       float v[V], wv[V];
@@ -248,20 +320,25 @@ __global__ __launch_bounds__(LONG_T) void k_norm_fwd_long(const T* x, const T* r
 
 // Backward, rows in registers: workgroup g takes rows g, g + gridDim.x, ... (times the rows
 // it holds at once) and leaves its share of dw and db in part[g] and part[G + g].
-template <typename T, int TPR, int EPT, bool RMS, bool HAS_B>
-__global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_bwd(const T* __restrict__ dy, const T* __restrict__ s,
-                                                               const T* __restrict__ res, const T* __restrict__ w,
-                                                               const float* __restrict__ mean,
-                                                               const float* __restrict__ rstd, const T* ds_in, int T_,
-                                                               int H, T* dx, float* __restrict__ part) {
-  constexpr int V = rowvec<T>::V, NV = EPT / V, GROUPS = wg_threads<TPR>() / TPR;
-  __shared__ float red[2][TPR / 64][2];
-  __shared__ float fold[GROUPS > 1 ? GROUPS * TPR * EPT : 1];
-  const int group = (int)threadIdx.x / TPR, lane = threadIdx.x % TPR;
+template <typename T, bool WAVE, int EPT, bool EDGE, bool RMS, bool HAS_B>
+__global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_bwd(const T* __restrict__ dy, const T* __restrict__ s,
+                                                             const T* __restrict__ res, const T* __restrict__ w,
+                                                             const float* __restrict__ mean,
+                                                             const float* __restrict__ rstd, const T* ds_in, int T_,
+                                                             int H, T* dx, float* __restrict__ part) {
+  constexpr int V = rowvec<T>::V, NV = EPT / V, GROUPS = WAVE ? 4 : 1;
+  __shared__ float red[2][MAX_WAVES][2];
+  __shared__ float fold[WAVE ? GROUPS * 64 * EPT : 1];
+  const int tpr = row_threads<WAVE>(), lane = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  const int group = WAVE ? (int)(threadIdx.x >> 6) : 0;
+  const RowEnds vec = row_ends<V>(0, 1, H);   // of w and b
+  // one shift for all the rows of the group, whose columns stay with their threads (their
+  // parities agree: the rows of a step are a multiple of 4, or the grid is even)
+  const int c0 = lane * V - col_shift<EDGE>(s + ((size_t)blockIdx.x * GROUPS + group) * H, H, tpr * EPT);
   float wv[NV][V], dwa[NV][V], dba[HAS_B ? NV : 1][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    load_cols(w, (lane + i * TPR) * V, H, wv[i]);
+    load_row<EDGE>(w, vec, c0 + i * tpr * V, H, wv[i]);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       dwa[i][j] = 0.f;
@@ -272,18 +349,19 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_bwd(const T* __restr
   int par = 0;
   for (int64_t t = (int64_t)blockIdx.x * GROUPS + group; t < T_; t += (int64_t)gridDim.x * GROUPS, par ^= 1) {
     const size_t off = (size_t)t * H;
+    const RowEnds ends = row_ends<V>(t, T_, H);
     float xh[NV][V], g[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      load_cols(s + off, (lane + i * TPR) * V, H, xh[i]);
-      load_cols(dy + off, (lane + i * TPR) * V, H, g[i]);
+      load_row<EDGE>(s + off, ends, c0 + i * tpr * V, H, xh[i]);
+      load_row<EDGE>(dy + off, ends, c0 + i * tpr * V, H, g[i]);
     }
     const float mu = RMS ? 0.f : mean[t], rs = rstd[t];
     if (res) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float r[V];
-        load_cols(res + off, (lane + i * TPR) * V, H, r);
+        load_row<EDGE>(res + off, ends, c0 + i * tpr * V, H, r);
 #pragma unroll
         for (int j = 0; j < V; ++j) xh[i][j] += r[j];
       }
@@ -292,7 +370,7 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_bwd(const T* __restr
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) {   // columns at or past H hold dy = 0
+      for (int j = 0; j < V; ++j) {   // columns outside the row hold dy = 0
         xh[i][j] = (xh[i][j] - mu) * rs;
         dwa[i][j] += g[i][j] * xh[i][j];
         if (HAS_B) dba[i][j] += g[i][j];
@@ -300,46 +378,47 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void k_norm_bwd(const T* __restr
         s1 += g[i][j];
         s2 += g[i][j] * xh[i][j];
       }
-    row_sum2<TPR>(s1, s2, red[par]);
+    row_sum2<WAVE>(s1, s2, red[par]);
     s1 = RMS ? 0.f : s1 * inv_h;
     s2 *= inv_h;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * TPR) * V;
+      const int c = c0 + i * tpr * V;
 #pragma unroll
       for (int j = 0; j < V; ++j) g[i][j] = rs * (g[i][j] - s1 - xh[i][j] * s2);
       if (ds_in) {
         float d[V];
-        load_cols(ds_in + off, c, H, d);
+        load_row<EDGE>(ds_in + off, ends, c, H, d);
 #pragma unroll
         for (int j = 0; j < V; ++j) g[i][j] += d[j];
       }
-      store_cols(dx + off, c, H, g[i]);
+      store_row<EDGE>(dx + off, c, H, g[i]);
     }
   }
   // the row groups' shares, added in group order
   auto leave = [&](float (&a)[NV][V], float* out) {
-    if constexpr (GROUPS > 1) {
+    if constexpr (WAVE) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) fold[((group * NV + i) * V + j) * TPR + lane] = a[i][j];
+        for (int j = 0; j < V; ++j) {
+          const int c = c0 + i * tpr * V + j;
+          if (c >= 0 && c < H) fold[group * 64 * EPT + c] = a[i][j];
+        }
       __syncthreads();
-      if (group == 0) {
+      for (int c = threadIdx.x; c < H; c += 256) {
+        float sum = fold[c];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int j = 0; j < V; ++j)
-            for (int o = 1; o < GROUPS; ++o) a[i][j] += fold[((o * NV + i) * V + j) * TPR + lane];
+        for (int o = 1; o < GROUPS; ++o) sum += fold[o * 64 * EPT + c];
+        out[c] = sum;
       }
-    }
-    if (group == 0) {
+    } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int q = 0; q < V; q += 4)
-          store_cols<float>(out, (lane + i * TPR) * V + q, H, *reinterpret_cast<float(*)[4]>(&a[i][q]));
+          store_row<EDGE>(out, c0 + i * tpr * V + q, H, *reinterpret_cast<float(*)[4]>(&a[i][q]));
     }
   };
   leave(dwa, part + (size_t)blockIdx.x * H);
@@ -354,7 +433,7 @@ __global__ __launch_bounds__(LONG_T) void k_norm_dx_long(const T* __restrict__ d
                                                          const float* __restrict__ rstd, const T* ds_in, int T_, int H,
                                                          T* dx) {
   constexpr int V = rowvec<T>::V;
-  __shared__ float red[2][LONG_T / 64][2];
+  __shared__ float red[2][MAX_WAVES][2];
   int par = 0;
   for (int64_t t = blockIdx.x; t < T_; t += gridDim.x, par ^= 1) {
     const size_t off = (size_t)t * H;
@@ -381,7 +460,7 @@ __global__ __launch_bounds__(LONG_T) void k_norm_dx_long(const T* __restrict__ d
         s2 += g[j] * ((xv[j] - mu) * rs);
       }
     }
-    row_sum2<LONG_T>(s1, s2, red[par]);
+    row_sum2<false>(s1, s2, red[par]);
     s1 = RMS ? 0.f : s1 / (float)H;
     s2 /= (float)H;
     for (int c = threadIdx.x * V; c < H; c += LONG_T * V) {
@@ -421,7 +500,7 @@ __global__ __launch_bounds__(256) void k_norm_dw_long(const T* __restrict__ dy, 
 }
 
 // dw (and db, blockIdx.y = 1): the G shares added in a fixed order, rounded once
-constexpr int FOLD_COLS = 64, FOLD_GROUPS = 16;
+constexpr int FOLD_COLS = 32, FOLD_GROUPS = 32;
 template <typename T>
 __global__ __launch_bounds__(FOLD_COLS* FOLD_GROUPS) void k_norm_fold(const float* __restrict__ part, int G, int H,
                                                                      T* __restrict__ dw, T* __restrict__ db) {
@@ -448,41 +527,41 @@ inline unsigned row_grid(int64_t wgs) { return (unsigned)(wgs < (1 << 20) ? wgs 
 
 }  // namespace
 
-// Shares of dw: workgroups of the backward, or row slices of the long rows.  1024 (512 of
-// four times the threads): at 16384 x 4096 bf16 with a residual 256 / 512 / 1024 / 2048 take
-// 320 / 198 / 136 / 145 us, too few rows in flight on one side and more shares than rows are
-// worth on the other.
+// Threads of a row.  One wave up to 1024 columns (8 or 16 values a thread); then a workgroup
+// of as many waves as 8 values a thread fill, to 8192 columns, and 1024 threads of 16 to
+// 16384.  More values in fewer threads, with fewer barriers, lose: 16384 x 4096 bf16 with 128
+// threads of 32 takes 109 us forward and 195 backward, with 512 of 8 95 and 136.
+inline int norm_threads(int H) {
+  return H <= 1024 ? 256 : H > 8192 ? 1024 : (int)(ceil_div(ceil_div(H, 8), 64) * 64);
+}
+
+// Shares of dw: workgroups of the backward, or row slices of the long rows.  About four rows
+// each, as far as that leaves 256 workgroups and asks for at most 256 K threads (512
+// workgroups at least): at 16384 x 4096 bf16 with a residual, 256 threads, 256 / 512 / 1024 /
+// 2048 shares take 320 / 198 / 136 / 145 us, too few rows in flight on one side and more
+// shares than rows are worth on the other.
 int norm_parts(const moe_norm_shape& s) {
   if (s.T == 0) return 0;
   const int rows = s.H <= 1024 ? 4 : 1;   // rows a workgroup holds at once
-  const int64_t most = s.H > NORM_REG_COLS ? 16 : s.H > 4096 ? 512 : 1024;
-  const int64_t g = ceil_div(s.T, rows);
-  return (int)(g < most ? g : most);
+  int64_t most = s.H > NORM_REG_COLS ? 16 : 262144 / norm_threads(s.H);
+  if (s.H <= NORM_REG_COLS && most < 512) most = 512;
+  const int64_t all = ceil_div(s.T, rows), want = ceil_div(all, 4) > 256 ? ceil_div(all, 4) : 256;
+  int64_t g = all < want ? all : want;
+  if (g > most) g = most;
+  if (g < all && (g & 1)) ++g;   // even: see k_norm_bwd's columns
+  return (int)g;
 }
 
-// Threads and registers of a row: 16 values a thread at most, so that the backward's rows,
-// weights and two sums (5 x 16) fit without spilling; one wave up to 1024 columns, then 256
-// threads to 4096 and 1024 threads to 16384.  32 values in fewer threads, with fewer barriers,
-// lose: 16384 x 4096 with 128 threads takes 109 us forward and 195 backward, against 95 and
-// 136.  The forward holds less and takes 512 threads from 2048 to 4096 columns: 95 us against
-// 100 with 256.
-#define NORM_BWD_DISPATCH(H, CALL)             \
-  do {                                         \
-    if ((H) <= 512) { CALL(64, 8); }           \
-    else if ((H) <= 1024) { CALL(64, 16); }    \
-    else if ((H) <= 2048) { CALL(256, 8); }    \
-    else if ((H) <= 4096) { CALL(256, 16); }   \
-    else if ((H) <= 8192) { CALL(1024, 8); }   \
-    else { CALL(1024, 16); }                   \
-  } while (0)
-#define NORM_FWD_DISPATCH(H, CALL)             \
-  do {                                         \
-    if ((H) <= 512) { CALL(64, 8); }           \
-    else if ((H) <= 1024) { CALL(64, 16); }    \
-    else if ((H) <= 2048) { CALL(256, 8); }    \
-    else if ((H) <= 4096) { CALL(512, 8); }    \
-    else if ((H) <= 8192) { CALL(1024, 8); }   \
-    else { CALL(1024, 16); }                   \
+// rows held in registers: at least one vector, at most 1024 threads of 16 values
+template <typename T>
+inline bool in_registers(int H) { return H >= rowvec<T>::V && H <= NORM_REG_COLS; }
+
+#define NORM_DISPATCH(H, EDGE, CALL)               \
+  do {                                             \
+    if ((H) <= 512) { CALL(true, 8, EDGE); }       \
+    else if ((H) <= 1024) { CALL(true, 16, EDGE); } \
+    else if ((H) <= 8192) { CALL(false, 8, EDGE); } \
+    else { CALL(false, 16, EDGE); }                \
   } while (0)
 
 template <typename T, bool RMS>
@@ -490,15 +569,16 @@ static hipError_t norm_fwd(const moe_norm_shape& s, const void* x_, const void* 
                            void* sum_, void* y_, float* mean, float* rstd, hipStream_t st) {
   const T *x = (const T*)x_, *res = (const T*)res_, *w = (const T*)w_, *b = (const T*)b_;
   T *sum = (T*)sum_, *y = (T*)y_;
-  if (s.H > NORM_REG_COLS) {
+  if (!in_registers<T>(s.H)) {
     MOE_LAUNCH("norm_fwd", (k_norm_fwd_long<T, RMS>), dim3(row_grid(s.T)), dim3(LONG_T), 0, st, x, res, w, b, s.T,
                s.H, s.eps, sum, y, mean, rstd);
     return hipGetLastError();
   }
-#define CALL(TPR, EPT)                                                                                          \
-  MOE_LAUNCH("norm_fwd", (k_norm_fwd<T, TPR, EPT, RMS>), dim3(row_grid(ceil_div(s.T, wg_threads<TPR>() / TPR))), \
-             dim3(wg_threads<TPR>()), 0, st, x, res, w, b, s.T, s.H, s.eps, sum, y, mean, rstd)
-  NORM_FWD_DISPATCH(s.H, CALL);
+#define CALL(WAVE, EPT, EDGE)                                                                                        \
+  MOE_LAUNCH("norm_fwd", (k_norm_fwd<T, WAVE, EPT, EDGE, RMS>), dim3(row_grid(WAVE ? ceil_div(s.T, 4) : s.T)),          \
+             dim3((unsigned)norm_threads(s.H)), 0, st, x, res, w, b, s.T, s.H, s.eps, sum, y, mean, rstd)
+  if (s.H % rowvec<T>::V) NORM_DISPATCH(s.H, true, CALL);
+  else NORM_DISPATCH(s.H, false, CALL);
 #undef CALL
   return hipGetLastError();
 }
@@ -510,16 +590,17 @@ static hipError_t norm_bwd(const moe_norm_shape& s, const void* dy_, const void*
   const T *dy = (const T*)dy_, *sum = (const T*)sum_, *res = (const T*)res_, *w = (const T*)w_, *ds_in = (const T*)ds_in_;
   T* dx = (T*)dx_;
   const int G = norm_parts(s);
-  if (s.T > 0 && s.H > NORM_REG_COLS) {
+  if (s.T > 0 && !in_registers<T>(s.H)) {
     MOE_LAUNCH("norm_dx", (k_norm_dx_long<T, RMS>), dim3(row_grid(s.T)), dim3(LONG_T), 0, st, dy, sum, res, w, mean,
                rstd, ds_in, s.T, s.H, dx);
     MOE_LAUNCH("norm_dw", (k_norm_dw_long<T, RMS>), dim3((unsigned)ceil_div(s.H, 256), (unsigned)G), dim3(256), 0, st,
                dy, sum, res, mean, rstd, s.T, s.H, part, HAS_B);
   } else if (s.T > 0) {
-#define CALL(TPR, EPT)                                                                                              \
-  MOE_LAUNCH("norm_bwd", (k_norm_bwd<T, TPR, EPT, RMS, HAS_B>), dim3((unsigned)G), dim3(wg_threads<TPR>()), 0, st, dy, \
-             sum, res, w, mean, rstd, ds_in, s.T, s.H, dx, part)
-    NORM_BWD_DISPATCH(s.H, CALL);
+#define CALL(WAVE, EPT, EDGE)                                                                                          \
+  MOE_LAUNCH("norm_bwd", (k_norm_bwd<T, WAVE, EPT, EDGE, RMS, HAS_B>), dim3((unsigned)G), dim3((unsigned)norm_threads(s.H)), \
+             0, st, dy, sum, res, w, mean, rstd, ds_in, s.T, s.H, dx, part)
+    if (s.H % rowvec<T>::V) NORM_DISPATCH(s.H, true, CALL);
+    else NORM_DISPATCH(s.H, false, CALL);
 #undef CALL
   }
   MOE_LAUNCH("norm_fold", k_norm_fold<T>, dim3((unsigned)ceil_div(s.H, FOLD_COLS), HAS_B ? 2u : 1u),

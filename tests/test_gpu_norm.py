@@ -13,7 +13,7 @@ from oracle import train as ot
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
-SIZES = [(1, 1), (3, 7), (1, 64), (5, 100), (64, 128), (7, 512), (9, 513), (33, 769), (6, 1000), (5, 1024), (5, 1032),
+SIZES = [(1, 1), (3, 7), (40, 3), (5, 8), (6, 9), (1, 64), (2, 511), (2, 1023), (700, 1001), (2, 2047), (3, 2049), (2, 8191), (2, 16383), (5, 100), (64, 128), (7, 512), (9, 513), (33, 769), (6, 1000), (5, 1024), (5, 1032),
          (300, 2048), (3, 2056), (4, 4095), (4, 4096), (3, 5000), (3, 8192), (2, 8200), (2, 16384), (2, 16385),
          (3, 20000), (1030, 96)]
 
