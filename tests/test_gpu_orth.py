@@ -116,6 +116,39 @@ def test_orth_of_many_matrices(n, rows, cols, steps):
         assert _off(o[i], ot.orthogonalize(g[i].double().numpy(), steps)) < TOL, i
 
 
+@pytest.mark.parametrize("rows,cols,steps", [(1536, 768, 3), (768, 1536, 3), (1500, 700, 5), (700, 1500, 1), (1500, 700, 1)])
+def test_orth_on_the_largest_tiles(rows, cols, steps):
+    """64 of them go to the 256-row tiles: both orientations, the lo part read by the last step
+    (three steps), sizes off the tiles, and a NaN that stays in its matrix."""
+    n = 64
+    g = torch.randn(n, rows, cols, generator=torch.Generator().manual_seed(rows)).to(torch.bfloat16)
+    g[1] = torch.from_numpy(spectra("low_rank", rows, cols, 1)).to(torch.bfloat16)
+    g[2, 5, 7] = float("nan")
+    g[3] = 0
+    o = _op(n, rows, cols, torch.bfloat16, steps).update(g.cuda(), scale=2.0)
+    torch.cuda.synchronize()
+    for i in (0, 1, n - 1):
+        assert _off(o[i], ot.orthogonalize(g[i].double().numpy(), steps, 2.0)) < TOL, i
+    assert torch.isnan(o[2]).all() and not o[3].any()
+    assert torch.isfinite(torch.cat([o[:2], o[3:]])).all()
+
+
+def test_orth_two_at_once():
+    """Two operators on two streams, over several calls each."""
+    a, b = _op(3, 300, 520, torch.bfloat16), _op(8, 128, 64, torch.bfloat16)
+    ga = torch.randn(3, 300, 520, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    gb = torch.randn(8, 128, 64, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    wa, wb = a.update(ga).clone(), b.update(gb).clone()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (sa, sb):
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        oa = a.update(ga, stream=sa)
+        ob = b.update(gb, stream=sb)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, wa) and torch.equal(ob, wb)
+
+
 def test_orth_refuses_other_tensors():
     op = _op(2, 8, 16, torch.bfloat16)
     g = torch.zeros(2, 8, 16, dtype=torch.bfloat16, device="cuda")
