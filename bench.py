@@ -68,6 +68,9 @@ def kernel_work(name, T, H, I, k, R, El, E_all=0):
         # router GEMM (E = all experts): x, W_r, fp32 logits / d_logits
         "router_logits": (T * H * b + H * E_all * b + T * E_all * 4, 2.0 * T * H * E_all),
         "router_dx": (T * E_all * 4 + H * E_all * b + 2 * T * H * b, 2.0 * T * H * E_all),
+        # load-balance loss: logits; logits, d_logits in and out
+        "balance_sum": (T * E_all * 4 + T * k * 4, 0.0),
+        "balance_bwd": (3 * T * E_all * 4, 0.0),
         "combine": (row_h + T * H * b, 0.0),
         "unpermute_dx": (row_h + T * H * b + R * 4 * ((I + 255) // 256) * 4 + T * k * 4, 0.0),
         # MXFP8 GEMMs: fp8 operands, bf16 side inputs and outputs
@@ -251,6 +254,8 @@ def main():
                          "gate/up GEMM (value still counts the 18RHI of the layer, not the 4RHI recomputed)")
     ap.add_argument("--router", action="store_true",
                     help="logits from the router GEMM x W_r inside the step (and its backward into dx and dW_r)")
+    ap.add_argument("--balance", action="store_true",
+                    help="the router's load-balance loss inside the step, its gradient added to d_logits")
     ap.add_argument("--gather-copy", action="store_true",
                     help="the dispatch writes the gathered token rows Xp, which the GEMMs then read densely "
                          "(default: the GEMM loaders read x through row_src)")
@@ -289,8 +294,12 @@ def main():
         sh, scr = layer.shape, layer.scratch.data_ptr()
 
     def fwd(st=None):
-        if not args.router:
-            return layer.forward(logits, x, wg, wu, wd, st)
+        y = layer.forward(logits, x, wg, wu, wd, st) if not args.router else router_fwd(st)
+        if args.balance:
+            layer.balance(1e-2, stream=st)
+        return y
+
+    def router_fwd(st):
         h = stream_handle(st)
         L.moe_router_fwd(sh, x.data_ptr(), w_r.data_ptr(), router_logits.data_ptr(), layer.topk_idx.data_ptr(),
                          layer.topk_w.data_ptr(), scr, h)
@@ -450,6 +459,7 @@ def main():
         "config": {"workload": WORKLOADS[args.workload] + (", activation checkpointing (backward recomputes "
                                                             "the gate/up GEMM)" if args.recompute else "")
                    + (", router GEMM x W_r in the step" if args.router else "")
+                   + (", load-balance loss in the step" if args.balance else "")
                    + (", gathered rows Xp written by the dispatch" if args.gather_copy else ""),
                    "T": cfg.T, "H": cfg.H, "I": cfg.I, "E": cfg.E, "k": cfg.k, "e_local": cfg.e_local, "rows": R},
         # the layer's algorithmic flops (router GEMM included with --router) over the step

@@ -23,6 +23,13 @@
 // Against fp64 that is 0.7 to 2e-3 of the result's norm over spectra from flat to a
 // thousandfold spread, next to 1.7e-3 for the output's own rounding to bf16 (plain fp16
 // iterates: up to 4e-2, bf16 ones: up to 3e-1, on the same matrices).
+//
+// Cost.  A step is 3 m^2 l + m^3 multiply-adds (A and A^2 by halves), which binds from a few
+// matrices of some hundred rows on; below, launches and latencies do.  Measured on one MI355X,
+// five steps, bf16: 128 of 2048 x 768 3.64 ms (2.6 PFLOP of such work in 2.4 ms at the 1.08
+// PFLOP/s of a large library fp16 product), of it 0.24 reading g twice and writing X (5.1
+// TB/s); the symmetric products over l run at 0.95 PFLOP/s of executed work (diagonal tiles
+// are computed whole), those with X at 0.7 to 0.82 beside what their epilogues move.
 #define MOE_GEMM_FW 256
 #include <math.h>
 
@@ -39,7 +46,7 @@ typedef i32x4 i32x4_a4 __attribute__((aligned(4)));   // or of fp32
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr double NS_EPS = 1e-7;
-constexpr int X_LOG2 = 15, D_LOG2 = 14, B_LOG2 = 14;
+constexpr int X_LOG2 = 15;
 constexpr float X_SCALE = 32768.f, D_SCALE = 16384.f, B_SCALE = 16384.f;
 // of two merged steps: |S| <= 2.8, and P's eigenvalues lie in [-11.5, 0]
 constexpr float S_SCALE = 16384.f, P_SCALE = 4096.f;
@@ -407,9 +414,9 @@ struct JOrth {
     else out_rows(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
   }
   // C^T accumulators: lane l holds row l % 32 of each band.  What the rows are combined with
-  // (S1 and S2, or X hi and lo) is loaded in that layout two bands ahead, S1 and S2
-  // one (more spill); finished bands leave through the wave's LDS region as whole row segments, and
-  // those of an off-diagonal tile of a symmetric product once more as columns.
+  // is loaded in that layout two bands ahead (S1, or X hi and lo) or one (S1 and S2), as far
+  // as the registers go; finished bands leave through the wave's LDS region as whole row
+  // segments, and those of an off-diagonal tile of a symmetric product once more as columns.
   __device__ __forceinline__ void out_rows(const Tile& p, const Acc& acc, bf16_t* wreg, int i0, int j0) const {
     const int lane = threadIdx.x & 63;
     const size_t xo = (size_t)p.z * a.mp * a.lp, so = (size_t)p.z * a.mp * a.mp;
@@ -836,7 +843,7 @@ static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t
 // X [MP, lp] (at most SMALL_ELEMS) stays in one CU: as fp32 in the accumulator layout of its
 // eight waves (so no iterate is rounded but for the products), and as fp16 in LDS beside D and
 // B.  One launch instead of 2 + 3 a step, which is what bounds matrices this small: eight of
-// 128 x 64, five steps, took 84 us in 17 launches.
+// 128 x 64, five steps, take 13.6 us and took 84 in 17 launches.
 constexpr int SMALL_ELEMS = 32768, SMALL_MP = 128;
 constexpr int small_lds(int mp) {   // elements: X (rows of lp + 8), D and B (rows of mp + 8)
   return SMALL_ELEMS + 8 * mp + 2 * mp * (mp + 8);
@@ -1093,8 +1100,7 @@ static bool merge_pays(int n, int mp, int lp) {
 }
 
 // Scratch: norm shares and factors, then X (two iterates, hi and lo), and the square matrices:
-// D and B of a step, or R (which A_1 replaces in off_s[3]), B_0, S, A_1, B_1 of two merged
-// ones, whose P takes S's place
+// D and B of a step, or R, B_0, S, A_1 and B_1 of two merged ones, whose P takes S's place
 struct OrthLayout {
   int m, l, mp, lp, chunks;
   bool merge;
@@ -1116,6 +1122,7 @@ static OrthLayout orth_layout(const moe_orth_shape& s) {
     return at;
   };
   const size_t xb = (size_t)s.n * L.mp * L.lp * 2, db = (size_t)s.n * L.mp * L.mp * 2;
+  if (orth_small(L.mp, L.lp)) return L;   // no scratch
   L.off_part = take((size_t)s.n * L.chunks * 8);
   L.off_factor = take((size_t)s.n * 4);
   for (int i = 0; i < 2; ++i) {

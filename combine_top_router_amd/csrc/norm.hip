@@ -11,6 +11,10 @@
 // EPT fp32 values in each of the threads that share it: the statistics are two passes
 // over registers (the variance about the mean itself, not E[s^2] - mu^2, which cancels),
 // and the backward keeps each thread's columns of dw and db in registers over all its rows.
+// Measured on one MI355X at 16384 x 4096 bf16 with a residual: forward 93 us for 537 MB,
+// backward 99 us for 671 MB (x, res, dy, ds_in, dx), 5.8 and 6.8 TB/s beside the 5.1 TB/s of a
+// large copy (part of each array is still in the 256 MB cache); 4096 x 2048 forward 13.4 us;
+// one row 2.5 us, a launch.
 #include "common.h"
 
 namespace moe {

@@ -235,6 +235,7 @@ class MoeLayer:
         L.moe_route_topk(s, _p(logits), _p(self.topk_idx), _p(self.topk_w), stream_handle(stream))
 
     def dispatch(self, x, stream=None):
+        self._balanced = False   # a new pass
         L.moe_dispatch(self.shape, _p(self.topk_idx), _p(x), _p(self.counts), _p(self.offsets), _p(self.row_src),
                        _p(self.row_of), _p(self.xp), _p(self.scratch), stream_handle(stream))
 
@@ -252,7 +253,6 @@ class MoeLayer:
         self._check(w_up, (s.e_local, s.H, s.I), self.dtype, "w_up")
         self._check(w_down, (s.e_local, s.I, s.H), self.dtype, "w_down")
         self.inputs = (logits, x, w_gate, w_up, w_down)
-        self._balanced = False
         self.route(logits, stream)
         self.dispatch(x, stream)
         self.experts(x, w_gate, w_up, w_down, stream)
@@ -261,8 +261,8 @@ class MoeLayer:
 
     def balance(self, coef, mask=None, stream=None):
         """The load-balance loss [1] of the last forward's routing, over all E experts and the
-        tokens with mask != 0 (uint8 [T]).  The per-expert counts are then in
-        ``balance_counts`` [E + 1]."""
+        tokens with mask != 0 (uint8 [T]); called between the forward and the backward.  The
+        per-expert counts are then in ``balance_counts`` [E + 1]."""
         if self.inputs is None:
             raise RuntimeError("balance without a forward")
         if self._balance is None:
@@ -296,6 +296,8 @@ class MoeLayer:
         """``d_balance`` [1]: the upstream gradient of ``balance``'s loss (None: 1)."""
         s = self.shape
         self._check(dy, (s.T, s.H), self.dtype, "dy")
+        if d_balance is not None and not self._balanced:
+            raise RuntimeError("d_balance without a balance loss in this pass")
         logits, x, w_gate, w_up, w_down = self.inputs
         h = stream_handle(stream)
         L.moe_bwd(s, _p(dy), _p(x), _p(self.xp), _p(self.offsets), _p(self.row_src), _p(self.row_of),

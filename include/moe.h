@@ -337,9 +337,10 @@ int moe_orth_scratch_bytes(const moe_orth_shape* shape, size_t* scratch_bytes);
  *   steps times:  A = X X^T,  X = 3.4445 X + (-4.7750 A + 2.0315 A^2) X;
  *   o = scale X, transposed back
  * g: [n, rows, cols] of shape.dtype; o: [n, rows, cols] bf16, which may be g when that is
- * bf16.  Inside, X and the products' factors are fp16 (the first iterates as a pair of
- * fp16) and the sums fp32; the result is within about 2e-3 of its norm, besides o's
- * rounding, for five steps.  A zero matrix gives zeros; one with a NaN or infinity gives
+ * bf16.  Inside, X and the products' factors are fp16 (the first iterates with a byte
+ * more) and the sums fp32; the result is within about 2e-3 of its norm, besides o's
+ * rounding, for five steps.  Directions far below a matrix's largest are multiplied by 3.4 a
+ * step, g's own rounding errors with them.  A zero matrix gives zeros; one with a NaN or infinity gives
  * NaN, and leaves the others alone.  scale must be finite.  Needs scratch. */
 int moe_orthogonalize(const moe_orth_shape* shape, const void* g, void* o, float scale, void* scratch, void* stream);
 
