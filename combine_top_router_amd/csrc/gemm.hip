@@ -270,7 +270,7 @@ struct JGateUp {
   static constexpr bool A_KMAJ = true, B_KMAJ = MX;
   static constexpr bool DYN = false, TRANS = true, EPI_LDS = true;
   static constexpr bool NSPLIT = false;   // column halves of a last round (Sched)
-  static constexpr bool SIDE = QW;
+  static constexpr bool SIDE = QW, DIAG = false;
   static_assert(!(MX && QW), "the weight codes come from bf16 B stages");
   __device__ __forceinline__ static int ncol(int wn, int ni) {
     return (ni < NI / 2 ? 0 : BN / 2) + wn * (WCOLS / 2) + (ni % (NI / 2)) * 32;
@@ -429,7 +429,7 @@ struct JDown {
   static constexpr bool A_KMAJ = true, B_KMAJ = MX;
   static constexpr bool DYN = false, TRANS = true, EPI_LDS = true;
   static constexpr bool NSPLIT = false;   // column halves of a last round (Sched)
-  static constexpr bool SIDE = QW;
+  static constexpr bool SIDE = QW, DIAG = false;
   static_assert(!(MX && QW), "the weight codes come from bf16 B stages");
   __device__ __forceinline__ static int ncol(int wn, int ni) { return wn * WCOLS + ni * 32; }
   FwdArgs a;
@@ -561,7 +561,7 @@ struct JDa {
   static constexpr bool A_KMAJ = true, B_KMAJ = true;
   static constexpr bool DYN = false, TRANS = false, EPI_LDS = true;
   static constexpr bool NSPLIT = !MX;   // column halves of a last round (Sched)
-  static constexpr bool SIDE = false;   // no extra per-step work
+  static constexpr bool SIDE = false, DIAG = false;   // no extra per-step work
   __device__ __forceinline__ static int ncol(int wn, int ni) { return wn * WCOLS + ni * 32; }
   BwdArgs a;
   MxArgs m;
@@ -685,7 +685,7 @@ struct JDx {
   static constexpr bool A_KMAJ = true, B_KMAJ = true;
   static constexpr bool DYN = false, TRANS = true, EPI_LDS = true;
   static constexpr bool NSPLIT = false;   // column halves of a last round (Sched)
-  static constexpr bool SIDE = false;   // no extra per-step work
+  static constexpr bool SIDE = false, DIAG = false;   // no extra per-step work
   __device__ __forceinline__ static int ncol(int wn, int ni) { return wn * WCOLS + ni * 32; }
   BwdArgs a;
   MxArgs m;
@@ -836,7 +836,7 @@ struct JWgrad {
   // the accumulators hold C^T; the epilogue writes them as bf16 row bands (band_store)
   static constexpr bool DYN = true, TRANS = true, EPI_LDS = true;
   static constexpr bool NSPLIT = false;   // column halves of a last round (Sched)
-  static constexpr bool SIDE = false;   // no extra per-step work
+  static constexpr bool SIDE = false, DIAG = false;   // no extra per-step work
   __device__ __forceinline__ bool dynamic() const { return sload(a.order + a.El) != 0; }
   __device__ __forceinline__ int32_t* counter() const { return a.order + a.El + 1 + WHICH; }
   __device__ __forceinline__ static int ncol(int wn, int ni) { return wn * WCOLS + ni * 32; }

@@ -382,9 +382,10 @@ struct Sched {
 //
 // A job J supplies: items(); the compute side -- Tile, tile(v, Tile&) (what the epilogue
 // needs, scalar loads only), rows(const Tile&, wm) (the WaveRows of wave row wm),
-// compute(stage pointer, stage index, acc, lane, WaveRows, wn) and epilogue(const Tile&,
-// acc, staging); and the load side -- Ld, setup(v, Ld&, pw, lane) and Ld::GATHER,
-// Ld::issue(kt, stage pointer, stage index, parity, fetch_next) and Ld::fetch(kt,
+// compute(stage pointer, stage index, acc, lane, WaveRows, wn), with J::DIAG also
+// diagonal(stage pointer, const Tile&, K step, acc, lane, WaveRows, wn) after it, and
+// epilogue(const Tile&, acc, staging); and the load side -- Ld, setup(v, Ld&, pw, lane) and
+// Ld::GATHER, Ld::issue(kt, stage pointer, stage index, parity, fetch_next) and Ld::fetch(kt,
 // parity) (fetch_next, when the loader calls it, fetches the row indices of the next
 // position into the other index slot); a gathering loader's job also supplies
 // fetch_first(v, pw, lane, parity), the row indices of item v's first step.
@@ -468,7 +469,10 @@ __device__ __forceinline__ void fused_stream(const J& job, bf16_t* lds, S sc, in
       // stores are on their way long before the next position's wait
       if constexpr (J::SIDE)
         if (kc < cur.nk) job.side(lds + cs * STAGE_ELEMS, cur, kc, wv * 64 + lane);
-      if (kc < cur.nk && wr.nblk > 0) job.compute(lds + cs * STAGE_ELEMS, cs, acc, lane, wr, wn);
+      if (kc < cur.nk && wr.nblk > 0) {
+        job.compute(lds + cs * STAGE_ELEMS, cs, acc, lane, wr, wn);
+        if constexpr (J::DIAG) job.diagonal(lds + cs * STAGE_ELEMS, cur, kc, acc, lane, wr, wn);
+      }
       if (sc.dyn && kc == 0 && wv == 0) {   // published after the MFMAs, read after a barrier
         const int n = uni(grabbed);
         if (lane == 0) slot[t & 1] = n;

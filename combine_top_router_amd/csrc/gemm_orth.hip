@@ -12,8 +12,9 @@
 //   X * 2^15 (<= 39400), A * 2^14 (<= 23700), (b A + c A^2) * 2^14 (<= 46000).
 // An early rounding is what hurts: a singular value far below the largest is multiplied by
 // a = 3.4 a step, and so is the rounding noise that lands beside it.  So
-// * the step's a X is added in fp32 outside the matrix product (with a I inside the fp16
-//   factor, its rounded diagonal leaks the large directions into the small ones);
+// * the step's a X is added to the fp32 sums by itself (with a I inside the fp16 factor, the
+//   rounded diagonal leaks the large directions into the small ones); where matrix
+//   instructions add it, a times the factor's scale is made an fp16 number by that scale;
 // * the first iterates are kept as a pair, hi in fp16 and lo = the rest times 16 in E4M3 (a
 //   byte: 15 bits together; the product reads hi, a X both), and X enters as the exact bf16
 //   values scaled by a power of two;
@@ -178,11 +179,11 @@ __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int
 }
 
 // ---- the products ----
-// What a product is for.  SYM0..2: a symmetric one C = c0 P Q^T - diag I, + c1 S1, + c2 S2, of
-// which the lower triangle of tiles is computed and mirrored; APPLY: X' = c0 P X + c1 X; LAST:
-// the same into the result.
-enum { ORTH_SYM0 = 0, ORTH_SYM1 = 1, ORTH_SYM2 = 2, ORTH_APPLY = 3, ORTH_LAST = 4 };
-constexpr bool orth_sym(int op) { return op <= ORTH_SYM2; }
+// What a product is for.  SYM0..3: a symmetric one, of which the lower triangle of tiles is
+// computed and mirrored: C = c0 P Q^T - diag I; c0 P Q^T + c1 Q; + c2 P; + c2 R.  APPLY: X' =
+// c0 P X + c1 X; LAST: the same into the result.
+enum { ORTH_SYM0 = 0, ORTH_SYM1 = 1, ORTH_SYM2 = 2, ORTH_SYM3 = 3, ORTH_APPLY = 4, ORTH_LAST = 5 };
+constexpr bool orth_sym(int op) { return op <= ORTH_SYM3; }
 
 struct OrthArgs {
   int mp, lp;             // padded sizes, multiples of 64
@@ -190,9 +191,9 @@ struct OrthArgs {
   int m, l, rows, cols;
   const f16* p;           // [n, mp, K]
   const f16* q;           // symmetric: [n, mp, K]; else X hi [n, mp, lp]
-  const f16* s1;          // [n, mp, mp]
-  const f16* s2;
+  const f16* side;        // P or R of SYM2 and SYM3 [n, mp, mp]
   float c0, c1, c2, diag;
+  f16 r1, r2;             // c1 / c0 and SYM2's c2 / c0, which the scales make fp16 numbers
   const float* factor;    // per matrix, stored X -> X, in every X (the first products); null: 1
   f16* c;                 // symmetric: C [n, mp, mp]
   const uint8_t* xlo;     // X lo, or null
@@ -330,13 +331,15 @@ struct OrthLd {
 
 // TALL: the last step of matrices that were transposed on entry, whose accumulators hold C,
 // so that the blocks leave as rows of C^T; all others hold C^T and leave as rows of C.
-template <int OP, bool TALL = false>
+// LO: X comes with its lo.
+template <int OP, bool TALL, bool LO>
 struct JOrth {
   using Tile = OrthTile;
   using Ld = OrthLd;
   static constexpr bool SYM = orth_sym(OP);
   static constexpr bool A_KMAJ = true, B_KMAJ = SYM;
   static constexpr bool DYN = false, TRANS = !TALL, EPI_LDS = true, NSPLIT = false, SIDE = false;
+  static constexpr bool DIAG = OP != ORTH_SYM0;
   OrthArgs a;
   int n, tm, tn;   // matrices; tiles along the rows and columns of a product
   __device__ __forceinline__ static int ncol(int wn, int ni) { return wn * WCOLS + ni * 32; }
@@ -426,6 +429,55 @@ struct JOrth {
       }
     __builtin_amdgcn_sched_group_barrier(MFMA, MI * NI, 0);
   }
+  // c1 Q (of which X is one) and SYM2's c2 P are part of the products: the tile's own block of
+  // Q passes through LDS as the K steps of the tile's rows, where a fragment of r1 I multiplies
+  // it (Q is symmetric or X), the block of P at those of its columns.  r1 = c1 / c0 is fp16 and
+  // the sums are fp32, so nothing is rounded that an addition in the epilogue would not round.
+  // Read and added there, the blocks cost 8% of a product with X at K = 768 (433 and 405 us,
+  // 128 of 768 x 2048) and 3% at 1536, 6% of one with a Q, 20% of one with P and Q.
+  __device__ __forceinline__ static f16x8 scaled_identity(f16 r, int half, int lane) {   // 16 of 32 rows
+    const int at = (lane & 31) - 16 * half - 8 * (lane >> 5);
+    f16x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e == at ? r : (f16)0.f;
+    return v;
+  }
+  __device__ __forceinline__ void diagonal(const bf16_t* st, const Tile& p, int kc, Acc& acc, int lane, const WaveRows& w,
+                                           int wn) const {
+    const bf16_t* As = st;
+    const bf16_t* Bs = st + A_ELEMS;
+    const int k0 = kc * BK;
+#pragma unroll
+    for (int half = 0; half < MI / 2; ++half) {   // 64 of the wave's rows
+      if (k0 != p.i0 + w.base + 64 * half) continue;
+      int ln = lane;
+      asm volatile("" : "+v"(ln));   // its addresses are not kept in registers over the K steps
+#pragma unroll
+      for (int kk = 0; kk < BK / 16; ++kk) {
+        const f16x8 e = scaled_identity(a.r1, kk & 1, ln);
+        const int mi = 2 * half + (kk >> 1);
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) {
+          const f16x8 b = as_f16(B_KMAJ ? frag_kmaj(Bs, ncol(wn, ni), kk, ln) : frag_mnmaj<BN>(Bs, ncol(wn, ni), kk, ln));
+          acc[mi][ni] = TRANS ? __builtin_amdgcn_mfma_f32_32x32x16_f16(b, e, acc[mi][ni], 0, 0, 0)
+                              : __builtin_amdgcn_mfma_f32_32x32x16_f16(e, b, acc[mi][ni], 0, 0, 0);
+        }
+      }
+    }
+    if (OP == ORTH_SYM2 && k0 == p.j0 + wn * WCOLS) {
+      static_assert(WCOLS == BK, "a wave's columns are one K step");
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+#pragma unroll
+      for (int kk = 0; kk < BK / 16; ++kk) {
+        const f16x8 e = scaled_identity(a.r2, kk & 1, ln);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+          acc[mi][kk >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e, as_f16(frag_kmaj(As, w.base + mi * 32, kk, ln)),
+                                                                    acc[mi][kk >> 1], 0, 0, 0);
+      }
+    }
+  }
   __device__ __forceinline__ void epilogue(const Tile& p, const Acc& acc, float* stage) const {
     const int tid = threadIdx.x, wv = tid >> 6, wm = (int)((unsigned)wv % WM), wn = (int)((unsigned)wv / WM);
     if (wn * WCOLS >= p.ncols) return;   // the tile's sizes are multiples of 64
@@ -433,62 +485,68 @@ struct JOrth {
     if constexpr (TALL) out_tall(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
     else out_rows(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
   }
-  // C^T accumulators: lane l holds row l % 32 of each band.  What the rows are combined with
-  // is loaded in that layout two bands ahead (S1, or X hi and lo) or one (S1 and S2), as far
-  // as the registers go; finished bands leave through the wave's LDS region as whole row
-  // segments, and those of an off-diagonal tile of a symmetric product once more as columns.
+  // C^T accumulators: lane l holds row l % 32 of each band.  What the products do not hold (R,
+  // X lo) is loaded in that layout two bands ahead; finished bands leave through the wave's LDS
+  // region as whole row segments, and those of an off-diagonal tile of a symmetric product once
+  // more as columns.
   __device__ __forceinline__ void out_rows(const Tile& p, const Acc& acc, bf16_t* wreg, int i0, int j0) const {
     const int lane = threadIdx.x & 63;
     const size_t xo = (size_t)p.z * a.mp * a.lp, so = (size_t)p.z * a.mp * a.mp;
     const int ld = SYM ? a.mp : a.lp;
-    const f16* const side = SYM ? a.s1 + so : a.q + xo;
-    const f16* const side2 = a.s2 + so;
-    const uint8_t* const side_lo = !SYM && a.xlo ? a.xlo + xo : nullptr;
-    constexpr int AHEAD = OP == ORTH_SYM2 ? 1 : 2;
-    i32x4 xh[AHEAD][NI][2], xl[AHEAD][NI], x2[AHEAD][NI][2];
+    constexpr int AHEAD = 2;
+    i32x4 xl[AHEAD][NI], xr[AHEAD][NI][2];
     auto fetch = [&](int mi) {
       const size_t row = (size_t)min(i0 + mi * 32 + (lane & 31), a.mp - 1) * ld + j0;
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
+        if constexpr (OP == ORTH_SYM3) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          xh[mi % AHEAD][ni][s] = *reinterpret_cast<const i32x4*>(side + row + ni * 32 + 16 * s + 8 * (lane >> 5));
-          if (OP == ORTH_SYM2)
-            x2[mi % AHEAD][ni][s] = *reinterpret_cast<const i32x4*>(side2 + row + ni * 32 + 16 * s + 8 * (lane >> 5));
+          for (int s = 0; s < 2; ++s)
+            xr[mi % AHEAD][ni][s] = *reinterpret_cast<const i32x4*>(a.side + so + row + ni * 32 + 16 * s + 8 * (lane >> 5));
         }
-        if (side_lo) xl[mi % AHEAD][ni] = *reinterpret_cast<const i32x4*>(side_lo + row + ni * 32 + 16 * (lane >> 5));
+        if constexpr (LO) xl[mi % AHEAD][ni] = *reinterpret_cast<const i32x4*>(a.xlo + xo + row + ni * 32 + 16 * (lane >> 5));
       }
     };
-    if constexpr (OP != ORTH_SYM0) {
-      fetch(0);
-      if (AHEAD > 1) fetch(1);
-    }
-    const float c0 = SYM ? a.c0 * p.f * p.f : a.c0 * p.f, c1 = SYM ? a.c1 : a.c1 * p.f;
+    fetch(0);
+    fetch(1);
+    const float c0 = SYM ? a.c0 * p.f * p.f : a.c0 * p.f, c1 = a.c1 * p.f;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       const int rb = i0 + mi * 32;
-      if (rb >= p.i0 + p.cnt) break;
+      if (rb >= p.i0 + p.cnt) {
+        // the bands already on their way: a load that is never waited for here would be waited
+        // for where its registers are next written, in the K loop
+#pragma unroll
+        for (int k = 0; k < AHEAD && mi + k < MI; ++k)
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni) {
+            if constexpr (OP == ORTH_SYM3) asm volatile("" ::"v"(xr[(mi + k) % AHEAD][ni][0]), "v"(xr[(mi + k) % AHEAD][ni][1]));
+            if constexpr (LO) asm volatile("" ::"v"(xl[(mi + k) % AHEAD][ni]));
+          }
+        break;
+      }
       i32x4 ch[NI][2], codes[NI];
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
         float v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = acc[mi][ni][r] * c0;
         if constexpr (OP == ORTH_SYM0) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            v[r] = acc[mi][ni][r] * c0;
+          for (int r = 0; r < 16; ++r)
             if (rb + (lane & 31) == j0 + ni * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= a.diag;
-          }
-        } else {
-          untrans_chunks_f16(xh[mi % AHEAD][ni], v);
-          if (side_lo) add_codes(xl[mi % AHEAD][ni], v);
+        }
+        if constexpr (OP == ORTH_SYM3) {
+          float u[16];
+          untrans_chunks_f16(xr[mi % AHEAD][ni], u);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] = acc[mi][ni][r] * c0 + v[r] * c1;
-          if constexpr (OP == ORTH_SYM2) {
-            float u[16];
-            untrans_chunks_f16(x2[mi % AHEAD][ni], u);
+          for (int r = 0; r < 16; ++r) v[r] += u[r] * a.c2;
+        }
+        if constexpr (LO) {
+          float u[16] = {};
+          add_codes(xl[mi % AHEAD][ni], u);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) v[r] += u[r] * a.c2;
-          }
+          for (int r = 0; r < 16; ++r) v[r] += u[r] * c1;
         }
         if constexpr (OP == ORTH_LAST) {
           f32x16 b;
@@ -504,7 +562,7 @@ struct JOrth {
           codes[ni] = trans_codes(v);
         }
       }
-      if (OP != ORTH_SYM0 && mi + AHEAD < MI) fetch(mi + AHEAD);
+      if (mi + AHEAD < MI) fetch(mi + AHEAD);
       if (OP == ORTH_APPLY && a.xnlo) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
@@ -535,52 +593,12 @@ struct JOrth {
       }
     }
   }
-  // The last step of transposed matrices: lane l holds column l % 32 of each block, whose X
-  // comes through the wave's LDS region and the transposing read; then rows of C^T leave.
+  // The last step of transposed matrices: lane l holds column l % 32 of each block, and rows of
+  // C^T leave.
   __device__ __forceinline__ void out_tall(const Tile& p, const Acc& acc, bf16_t* wreg, int i0, int j0) const {
-    const int lane = threadIdx.x & 63, g = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
+    const int lane = threadIdx.x & 63;
     const size_t xo = (size_t)p.z * a.mp * a.lp;
     const float c0 = a.c0 * p.f, c1 = a.c1 * p.f;
-    i32x4 xh[4];   // rows lane / 8 + 8 k of a 32 x 64 band, 16 bytes a lane, one band ahead
-    auto fetch = [&](int mi) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        xh[k] = *reinterpret_cast<const i32x4*>(
-            a.q + xo + (size_t)min(i0 + mi * 32 + (lane >> 3) + 8 * k, a.mp - 1) * a.lp + j0 + (lane & 7) * 8);
-    };
-    fetch(0);
-    Acc v;
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = (lane >> 3) + 8 * k;
-        *reinterpret_cast<i32x4*>(wreg + r * WCOLS + (((lane & 7) ^ band_swz<8>(r)) << 3)) = xh[k];
-      }
-      if (mi + 1 < MI) fetch(mi + 1);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {   // rows 8 k + 4 (l / 32) .. + 3 of column l % 32
-          const int col = 32 * ni + 16 * (g & 1) + 4 * q, r = 8 * k + 4 * (g >> 1) + j;
-          const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (MOE_LDS s16x4*)(wreg + r * WCOLS + (((col >> 3) ^ band_swz<8>(r)) << 3) + (col & 7)));
-          const f16x4 x = __builtin_bit_cast(f16x4, t);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[mi][ni][4 * k + e] = acc[mi][ni][4 * k + e] * c0 + (float)x[e] * c1;
-        }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (a.xlo) {   // three steps or fewer
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int i = min(i0 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), a.mp - 1);
-            v[mi][ni][r] += lo_value(a.xlo[xo + (size_t)i * a.lp + j0 + ni * 32 + (lane & 31)]) * c1;
-          }
-      }
-    }
     bf16_t* const out = a.out + (size_t)p.z * a.rows * a.cols;
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni)
@@ -588,7 +606,20 @@ struct JOrth {
       for (int mh = 0; mh < MI; mh += 2) {
         i32x4 ch[2][2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) trans_chunks(v[mh + b][ni], ch[b]);
+        for (int b = 0; b < 2; ++b) {
+          f32x16 v;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] = acc[mh + b][ni][r] * c0;
+          if constexpr (LO) {   // three steps or fewer
+            int ln = lane;
+            asm volatile("" : "+v"(ln) : : "memory");   // one block's addresses and loads at a time
+            const uint8_t* q = a.xlo + xo + (size_t)(min(i0 + (mh + b) * 32, a.mp - 32) + 4 * (ln >> 5)) * a.lp + j0 +
+                               ni * 32 + (ln & 31);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) v[r] += lo_value(q[(size_t)(8 * (r >> 2) + (r & 3)) * a.lp]) * c1;
+          }
+          trans_chunks(v, ch[b]);
+        }
         band_store(wreg, ch, [&](int rr, int cb_, i32x4 w) {
           const int r = j0 + ni * 32 + rr, c = i0 + mh * 32 + cb_;   // of the output
           if (r >= a.l || c >= a.m) return;
@@ -604,10 +635,10 @@ struct JOrth {
   }
 };
 
-template <int OP, bool TALL>
+template <int OP, bool TALL, bool LO>
 __global__ __launch_bounds__(NTHR, 1) void k_orth_stream(OrthArgs a, int n, int tm, int tn) {
   __shared__ __attribute__((aligned(16))) bf16_t lds[LDS_ELEMS];
-  JOrth<OP, TALL> job{a, n, tm, tn};
+  JOrth<OP, TALL, LO> job{a, n, tm, tn};
   run_stream(job, lds);
 }
 
@@ -742,13 +773,13 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
         if (i == j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= a.diag;
       }
     } else {
-      side(SYM ? a.s1 + so : a.q + xo, v);
+      side(a.q + (SYM ? so : xo), v);
       if (!SYM && a.xlo) add_codes(*reinterpret_cast<const i32x4*>(a.xlo + xo + at + 16 * (lane >> 5)), v);
 #pragma unroll
       for (int r = 0; r < 16; ++r) v[r] = acc[mi][r] * c0 + v[r] * c1;
       if constexpr (OP == ORTH_SYM2) {
         float u[16];
-        side(a.s2 + so, u);
+        side(a.side + so, u);
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] += u[r] * a.c2;
       }
@@ -839,6 +870,24 @@ static void orth_tiles(const char* name, const OrthArgs& a, int n, hipStream_t s
              a, tm, tn, items);
 }
 
+template <int OP, bool TALL, bool LO>
+static void orth_stream(const char* name, const OrthArgs& a, int n, hipStream_t st) {
+  constexpr bool SYM = orth_sym(OP);
+  const int tm = (int)ceil_div(a.mp, BM), tn = (int)ceil_div(a.lp, BN);
+  const dim3 grid((unsigned)grid_for((int64_t)n * (SYM ? tm * (tm + 1) / 2 : tm * tn)));
+  MOE_LAUNCH(name, (k_orth_stream<OP, TALL, LO>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
+}
+template <int OP>
+static void orth_stream(const char* name, const OrthArgs& a, int n, hipStream_t st) {
+  if constexpr (orth_sym(OP)) {
+    orth_stream<OP, false, false>(name, a, n, st);
+  } else {
+    if constexpr (OP == ORTH_LAST)
+      if (a.rows > a.cols) return a.xlo ? orth_stream<OP, true, true>(name, a, n, st) : orth_stream<OP, true, false>(name, a, n, st);
+    a.xlo ? orth_stream<OP, false, true>(name, a, n, st) : orth_stream<OP, false, false>(name, a, n, st);
+  }
+}
+
 template <int OP>
 static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t st) {
   constexpr bool SYM = orth_sym(OP);
@@ -848,17 +897,14 @@ static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t
     case TILE_128: return orth_tiles<OP, 128, 2>(name, a, n, st);
     default: break;
   }
-  const int tm = (int)ceil_div(a.mp, BM), tn = (int)ceil_div(a.lp, BN);
-  const dim3 grid((unsigned)grid_for((int64_t)n * (SYM ? tm * (tm + 1) / 2 : tm * tn)));
-  if constexpr (OP == ORTH_LAST) {
-    if (a.rows > a.cols) {
-      MOE_LAUNCH(name, (k_orth_stream<OP, true>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
-      return;
-    }
-  }
-  MOE_LAUNCH(name, (k_orth_stream<OP, false>), grid, dim3(NTHR), 0, st, a, n, tm, tn);
+  orth_stream<OP>(name, a, n, st);
 }
-
+// SYM3 differs from SYM2 in the streamed kernel only
+template <>
+void orth_product<ORTH_SYM3>(const char* name, const OrthArgs& a, int n, hipStream_t st) {
+  if (orth_tile_kind(true, n, a.mp, a.mp, a.K) == TILE_256) orth_stream<ORTH_SYM3>(name, a, n, st);
+  else orth_product<ORTH_SYM2>(name, a, n, st);
+}
 // ---- small matrices: the whole iteration in one workgroup ----
 // X [MP, lp] (at most SMALL_ELEMS) stays in one CU: as fp32 in the accumulator layout of its
 // eight waves (so no iterate is rounded but for the products), and as fp16 in LDS beside D and
@@ -1100,6 +1146,9 @@ static hipError_t launch_small(const moe_orth_shape& s, const T* g, bf16_t* o, i
   return mp == 64 ? launch_small<T, 64>(s, g, o, lp, scale, st) : launch_small<T, 128>(s, g, o, lp, scale, st);
 }
 
+// The scale next to `scale` with which k * scale is an fp16 number
+inline float fit_scale(float k, float scale) { return (float)(f16)(k * scale) / k; }
+
 inline int pad64(int v) { return (v + 63) & ~63; }
 
 }  // namespace
@@ -1199,22 +1248,25 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   int cur = 0;                              // X's buffer
   bool has_lo = s.dtype == MOE_F32;
   int los = L.merge ? LO_STEPS - 1 : LO_STEPS;   // iterates still to be kept with their lo
-  // C = c0 P Q^T + c1 S1 + c2 S2 - diag I
-  auto sym = [&](const char* name, const f16* p, const f16* q, int K, f16* c, float c0, float diag, const f16* s1,
-                 float c1, const f16* s2, float c2, const float* f) {
+  // C = c0 P Q^T + c1 Q + c2 side - diag I, side P or another
+  auto sym = [&](const char* name, const f16* p, const f16* q, int K, f16* c, float c0, float diag, const float* f,
+                 float c1 = 0.f, const f16* side = nullptr, float c2 = 0.f) {
     OrthArgs a = base;
-    a.p = p; a.q = q; a.K = K; a.c = c; a.c0 = c0; a.diag = diag; a.s1 = s1; a.c1 = c1; a.s2 = s2; a.c2 = c2;
+    a.p = p; a.q = q; a.K = K; a.c = c; a.c0 = c0; a.diag = diag; a.c1 = c1; a.side = side; a.c2 = c2;
+    a.r1 = (f16)(c1 / c0);
+    a.r2 = (f16)(c2 / c0);
     a.factor = f;
-    if (s2) orth_product<ORTH_SYM2>(name, a, s.n, st);
-    else if (s1) orth_product<ORTH_SYM1>(name, a, s.n, st);
+    if (side && side == p) orth_product<ORTH_SYM2>(name, a, s.n, st);
+    else if (side) orth_product<ORTH_SYM3>(name, a, s.n, st);
+    else if (c1 != 0.f) orth_product<ORTH_SYM1>(name, a, s.n, st);
     else orth_product<ORTH_SYM0>(name, a, s.n, st);
   };
   // D = A - t I of the current X, and B = beta D + c D^2
-  auto gram_poly = [&](f16* d, f16* b, const StepCoef& co, const float* f) {
-    sym("orth_gram", x[cur], x[cur], L.lp, d, f ? D_SCALE : D_SCALE / (X_SCALE * X_SCALE), co.t * D_SCALE, nullptr, 0.f,
-        nullptr, 0.f, f);
-    sym("orth_poly", d, d, L.mp, b, NS_C * B_SCALE / (D_SCALE * D_SCALE), 0.f, d, co.beta * B_SCALE / D_SCALE, nullptr,
-        0.f, nullptr);
+  auto gram = [&](f16* d, float ds, float t, const float* f) {
+    sym("orth_gram", x[cur], x[cur], L.lp, d, f ? ds : ds / (X_SCALE * X_SCALE), t * ds, f);
+  };
+  auto poly = [&](f16* d, float ds, f16* b, float bs, float beta) {
+    sym("orth_poly", d, d, L.mp, b, NS_C * bs / (ds * ds), 0.f, nullptr, beta * bs / ds);
   };
   // X <- alpha X + P X (P at p_scale); the last one into the result
   auto apply = [&](const f16* p, float p_scale, float alpha, const float* f, bool last) {
@@ -1223,6 +1275,7 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
     a.p = p; a.q = x[cur]; a.K = L.mp;
     a.c0 = out / p_scale;
     a.c1 = out * alpha;
+    a.r1 = (f16)(alpha * p_scale);
     a.factor = f;
     a.xlo = has_lo ? xlo[cur] : nullptr;
     has_lo = los-- > 0;
@@ -1235,22 +1288,24 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   int step = 0;
   if (L.merge) {
     f16 *r = sq[0], *b0 = sq[1], *sp = sq[2], *a1 = sq[3], *b1 = sq[4];
-    constexpr float BB = 1.f / (B_SCALE * B_SCALE), BD = 1.f / (B_SCALE * D_SCALE);
-    gram_poly(r, b0, step_coef(0), factor);
-    sym("orth_s", b0, r, L.mp, sp, S_SCALE * BD, 0.f, nullptr, 0.f, nullptr, 0.f, nullptr);
-    sym("orth_a1", b0, sp, L.mp, a1, D_SCALE / (B_SCALE * S_SCALE), 0.f, r, NS_A * NS_A, sp, 2.f * NS_A * D_SCALE / S_SCALE,
-        nullptr);
-    sym("orth_poly", a1, a1, L.mp, b1, NS_C * B_SCALE / (D_SCALE * D_SCALE), 0.f, a1, NS_B * B_SCALE / D_SCALE, nullptr,
-        0.f, nullptr);
-    sym("orth_p", b1, b0, L.mp, sp, P_SCALE * BB, 0.f, b0, NS_A * P_SCALE / B_SCALE, b1, NS_A * P_SCALE / B_SCALE, nullptr);
-    apply(sp, P_SCALE, NS_A * NS_A, factor, s.steps == 2);
+    const float ds = fit_scale(NS_B / NS_C, D_SCALE), bs = fit_scale(NS_A, 0.5f * B_SCALE);   // 2 a bs is fp16, too
+    const float ps = fit_scale(NS_A * NS_A, P_SCALE);
+    gram(r, ds, 0.f, factor);
+    poly(r, ds, b0, bs, NS_B);
+    sym("orth_s", b0, r, L.mp, sp, S_SCALE / (bs * ds), 0.f, nullptr);
+    sym("orth_a1", b0, sp, L.mp, a1, ds / (bs * S_SCALE), 0.f, nullptr, 2.f * NS_A * ds / S_SCALE, r, NS_A * NS_A);
+    poly(a1, ds, b1, bs, NS_B);
+    sym("orth_p", b1, b0, L.mp, sp, ps / (bs * bs), 0.f, nullptr, NS_A * ps / bs, b1, NS_A * ps / bs);
+    apply(sp, ps, NS_A * NS_A, factor, s.steps == 2);
     step = 2;
   }
   for (; step < s.steps; ++step) {
     const StepCoef co = step_coef(step);
     const float* f = step == 0 ? factor : nullptr;
-    gram_poly(sq[0], sq[1], co, f);
-    apply(sq[1], B_SCALE, co.alpha, f, step == s.steps - 1);
+    const float ds = fit_scale(co.beta / NS_C, D_SCALE), bs = fit_scale(co.alpha, B_SCALE);
+    gram(sq[0], ds, co.t, f);
+    poly(sq[0], ds, sq[1], bs, co.beta);
+    apply(sq[1], bs, co.alpha, f, step == s.steps - 1);
   }
   return hipGetLastError();
 }
