@@ -27,10 +27,11 @@
 //
 // Cost.  A step is 3 m^2 l + m^3 multiply-adds (A and A^2 by halves), which binds from a few
 // matrices of some hundred rows on; below, launches and latencies do.  Measured on one MI355X,
-// five steps, bf16: 128 of 2048 x 768 3.64 ms (2.6 PFLOP of such work in 2.4 ms at the 1.08
-// PFLOP/s of a large library fp16 product), of it 0.24 reading g twice and writing X (5.1
-// TB/s); the symmetric products over l run at 0.95 PFLOP/s of executed work (diagonal tiles
-// are computed whole), those with X at 0.7 to 0.82 beside what their epilogues move.
+// five steps, bf16, one call after another: 128 of 2048 x 768 3.42 ms, 16 of 1536 x 4096 3.04
+// (2.6 PFLOP of such work each, 2.4 ms at the 1.08 PFLOP/s of a large library fp16 product;
+// both run at the clock that their power leaves).  Of the former 0.23 read g twice and write X
+// (5.1 TB/s); the products with X run at 0.77 PFLOP/s (0.95 at 1536 rows), the symmetric ones
+// at 0.84 of what they execute, which is 5.25 of 9 tiles at 768 rows where 4.5 are needed.
 #define MOE_GEMM_FW 256
 #include <math.h>
 
@@ -361,7 +362,17 @@ struct JOrth {
     p.ncols = uni(min(BN, (SYM ? a.mp : a.lp) - p.j0));
     p.f = a.factor ? sload(a.factor + p.z) : 1.f;
   }
-  __device__ __forceinline__ WaveRows rows(const Tile& p, int wm) const { return wave_rows(p.cnt, wm); }
+  // A diagonal tile's waves that lie above the diagonal: mirrored from those below it, which
+  // leaves out two of eight (all of them computed: 3503 and 3060 us for the two batches above,
+  // 3423 and 3042 so)
+  __device__ __forceinline__ static bool above(const Tile& p, int wm, int wn) {
+    return SYM && p.i0 == p.j0 && wn * WCOLS >= (wm + 1) * WROWS;
+  }
+  __device__ __forceinline__ WaveRows rows(const Tile& p, int wm) const {
+    WaveRows w = wave_rows(p.cnt, wm);
+    if (above(p, wm, (int)((unsigned)uni(threadIdx.x >> 6) / WM))) w.nblk = 0;
+    return w;
+  }
   __device__ __forceinline__ void setup(int v, Ld& p, int pw, int lane) const {
     Tile t;
     tile(v, t);
@@ -480,7 +491,7 @@ struct JOrth {
   }
   __device__ __forceinline__ void epilogue(const Tile& p, const Acc& acc, float* stage) const {
     const int tid = threadIdx.x, wv = tid >> 6, wm = (int)((unsigned)wv % WM), wn = (int)((unsigned)wv / WM);
-    if (wn * WCOLS >= p.ncols) return;   // the tile's sizes are multiples of 64
+    if (wn * WCOLS >= p.ncols || above(p, wm, wn)) return;   // the tile's sizes are multiples of 64
     bf16_t* const wreg = reinterpret_cast<bf16_t*>(stage) + wv * BAND_ELEMS;
     if constexpr (TALL) out_tall(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
     else out_rows(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
@@ -586,7 +597,7 @@ struct JOrth {
         band_store(wreg, ch, [&](int rr, int cb_, i32x4 w) {
           *reinterpret_cast<i32x4*>(out + (size_t)(rb + rr) * ld + j0 + cb_) = w;
         });
-        if (SYM && p.i0 != p.j0)
+        if (SYM && i0 >= j0 + WCOLS)   // off the diagonal
           band_columns(wreg, [&](int c, int r, i32x4 w) {
             *reinterpret_cast<i32x4*>(out + (size_t)(j0 + c) * ld + rb + r) = w;
           });
@@ -723,6 +734,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     }
   };
   const int wm = wv & 1, wn = wv >> 1, ib = wm * 32 * C::TMI, jb = wn * 32;   // the wave's first row and column
+  const bool above = SYM && i0 == j0 && jb >= ib + 32 * C::TMI;   // mirrored from below the diagonal
   f32x16 acc[C::TMI];
 #pragma unroll
   for (int mi = 0; mi < C::TMI; ++mi)
@@ -742,6 +754,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     if (kt + NS - 1 < nk) issue(kt + NS - 1);   // into the stage read one step ago
     const bf16_t* const as = lds + (kt % NS) * STAGE;
     const bf16_t* const bs = as + OPER;
+    if (above) continue;
 #pragma unroll
     for (int kk = 0; kk < BK / 16; ++kk) {
       const f16x8 bf = SYM ? as_f16(frag_kmaj(bs, jb, kk, lane)) : tile_frag_mn<TILE>(bs, jb, kk, lane);
@@ -751,7 +764,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     }
   }
   // lane l: row l % 32 of each block, columns 8q + 4 (l / 32) .. + 3
-  if (j0 + jb >= ldn) return;
+  if (j0 + jb >= ldn || above) return;
   const float f = a.factor ? a.factor[z] : 1.f;
   const float c0 = SYM ? a.c0 * f * f : a.c0 * f, c1 = SYM ? a.c1 : a.c1 * f;
 #pragma unroll
@@ -818,7 +831,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
       trans_chunks_f16(v, ch);
 #pragma unroll
       for (int s = 0; s < 2; ++s) *reinterpret_cast<i32x4*>(out + at + 16 * s + 8 * (lane >> 5)) = ch[s];
-      if (SYM && i0 != j0) {
+      if (SYM && i0 + ib >= j0 + jb + 32) {   // off the diagonal
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           out[(size_t)(j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * ldn + i] = (f16)v[r];
