@@ -734,7 +734,10 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     }
   };
   const int wm = wv & 1, wn = wv >> 1, ib = wm * 32 * C::TMI, jb = wn * 32;   // the wave's first row and column
-  const bool above = SYM && i0 == j0 && jb >= ib + 32 * C::TMI;   // mirrored from below the diagonal
+  // above the diagonal: mirrored from below.  Not in the deep ring, whose lone workgroups wait
+  // for loads: there the branch costs more than the products (5 of 333 x 1000 117 us, 128 with
+  // it; 128 of 320 x 640, in the short ring, 463 us without and 452 with)
+  const bool above = SYM && NS == 2 && i0 == j0 && jb >= ib + 32 * C::TMI;
   f32x16 acc[C::TMI];
 #pragma unroll
   for (int mi = 0; mi < C::TMI; ++mi)
@@ -831,7 +834,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
       trans_chunks_f16(v, ch);
 #pragma unroll
       for (int s = 0; s < 2; ++s) *reinterpret_cast<i32x4*>(out + at + 16 * s + 8 * (lane >> 5)) = ch[s];
-      if (SYM && i0 + ib >= j0 + jb + 32) {   // off the diagonal
+      if (SYM && (NS == 2 ? i0 + ib >= j0 + jb + 32 : i0 != j0)) {   // what no wave computes
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           out[(size_t)(j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * ldn + i] = (f16)v[r];
