@@ -88,37 +88,43 @@ __device__ __forceinline__ void store_cols(T* row, int c, int H, const float (&v
 // end is then read whole, with the neighbour rows' elements (which may be changing: they are
 // dropped); at the tensor's own ends the vector is moved to columns lo .. hi, inside it, and
 // its elements moved back.  (Element by element, the ends made the rows of 4095 bf16 take three
-// times as long as those of 4096.)
+// times as long as those of 4096.)  What a row's end asks for is the same for all of its
+// threads (the vector over it holds `tail` of the row's elements), so it is decided by scalar
+// branches, and moving back is left to the last row.
 struct RowEnds {
-  int lo, hi;
+  int lo, hi, tail;
 };
-// of row t of T, V <= H
+// of row t of T, V <= H, with vectors that start `shift` columns early
 template <int V>
-__device__ __forceinline__ RowEnds row_ends(int64_t t, int64_t T, int H) {
+__device__ __forceinline__ RowEnds row_ends(int64_t t, int64_t T, int H, int shift) {
   const int64_t left = (T - t) * H - V;
-  return {t > 0 ? -1 : 0, left < (1 << 30) ? (int)left : 1 << 30};
+  return {t > 0 ? -1 : 0, left < (1 << 30) ? (int)left : 1 << 30, (H + shift) & (V - 1)};
 }
 template <bool EDGE, typename T>
 __device__ __forceinline__ void load_row(const T* row, RowEnds ends, int c, int H, float (&v)[rowvec<T>::V]) {
   constexpr int V = rowvec<T>::V;
   if (c < H) {
     if constexpr (EDGE) {
-      const int from = min(max(c, ends.lo), ends.hi), d = c - from;   // d: -1 .. V - 1
-      rowvec<T>::load(row + from, v);
-      if (c < 0 || c + V > H) {
-        if (d < 0) {
+      rowvec<T>::load(row + min(max(c, ends.lo), ends.hi), v);
+      if (c + V > H) {
+        if (ends.hi < H) {   // the last row: moved by V - tail
+#pragma unroll
+          for (int b = V / 2; b >= 1; b >>= 1)
+            if ((V - ends.tail) & b) {
+#pragma unroll
+              for (int j = 0; j + b < V; ++j) v[j] = v[j + b];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (j >= ends.tail) v[j] = 0.f;
+      }
+      if (sizeof(T) == 2 && c < 0) {
+        if (ends.lo == 0) {
 #pragma unroll
           for (int j = V - 1; j > 0; --j) v[j] = v[j - 1];
         }
-#pragma unroll
-        for (int b = V / 2; b >= 1; b >>= 1)
-          if (d > 0 && (d & b)) {
-#pragma unroll
-            for (int j = 0; j + b < V; ++j) v[j] = v[j + b];
-          }
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (c + j < 0 || c + j >= H) v[j] = 0.f;
+        v[0] = 0.f;
       }
     } else {
       rowvec<T>::load(row + c, v);
@@ -129,14 +135,17 @@ __device__ __forceinline__ void load_row(const T* row, RowEnds ends, int c, int 
   }
 }
 template <bool EDGE, typename T>
-__device__ __forceinline__ void store_row(T* row, int c, int H, const float (&v)[rowvec<T>::V]) {
+__device__ __forceinline__ void store_row(T* row, int c, int H, int tail, const float (&v)[rowvec<T>::V]) {
   constexpr int V = rowvec<T>::V;
   if (!EDGE || (c >= 0 && c + V <= H)) {
     if (c < H) rowvec<T>::store(row + c, v);
-  } else {
+  } else if (c < 0) {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (c + j >= 0 && c + j < H) elem<T>::store(row + c + j, v[j]);
+    for (int j = 1; j < V; ++j) elem<T>::store(row + c + j, v[j]);
+  } else if (c < H) {
+#pragma unroll
+    for (int j = 0; j < V - 1; ++j)
+      if (j < tail) elem<T>::store(row + c + j, v[j]);
   }
 }
 
@@ -192,13 +201,13 @@ __global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_fwd(const T* x, const 
   constexpr int V = rowvec<T>::V, NV = EPT / V, GROUPS = WAVE ? 4 : 1;
   __shared__ float red[4][MAX_WAVES][2];
   const int tpr = row_threads<WAVE>(), lane = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
-  const RowEnds vec = row_ends<V>(0, 1, H);   // of w and b
   int par = 0;   // the row's slots in red: those of the row before may still be read
-  for (int64_t t = (int64_t)blockIdx.x * GROUPS + (WAVE ? threadIdx.x >> 6 : 0); t < T_;
+  for (int64_t t = (int64_t)blockIdx.x * GROUPS + (WAVE ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : 0); t < T_;
        t += (int64_t)gridDim.x * GROUPS, par ^= 2) {
     const size_t off = (size_t)t * H;
-    const RowEnds ends = row_ends<V>(t, T_, H);
-    const int c0 = lane * V - col_shift<EDGE>(x + off, H, tpr * EPT);
+    const int shift = col_shift<EDGE>(x + off, H, tpr * EPT);
+    const RowEnds ends = row_ends<V>(t, T_, H, shift), vec = row_ends<V>(0, 1, H, shift);   // vec: w and b
+    const int c0 = lane * V - shift;
     float v[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) load_row<EDGE>(x + off, ends, c0 + i * tpr * V, H, v[i]);
@@ -211,7 +220,7 @@ __global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_fwd(const T* x, const 
         for (int j = 0; j < V; ++j) v[i][j] += r[j];
       }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) store_row<EDGE>(sum + off, c0 + i * tpr * V, H, v[i]);
+      for (int i = 0; i < NV; ++i) store_row<EDGE>(sum + off, c0 + i * tpr * V, H, ends.tail, v[i]);
     }
     float mu = 0.f;
     if constexpr (!RMS) {
@@ -247,7 +256,7 @@ __global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_fwd(const T* x, const 
 #pragma unroll
         for (int j = 0; j < V; ++j) v[i][j] += bv[j];
       }
-      store_row<EDGE>(y + off, c, H, v[i]);
+      store_row<EDGE>(y + off, c, H, ends.tail, v[i]);
     }
     if (lane == 0) {
       if constexpr (!RMS) mean[t] = mu;
@@ -334,11 +343,12 @@ __global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_bwd(const T* __restric
   __shared__ float red[2][MAX_WAVES][2];
   __shared__ float fold[WAVE ? GROUPS * 64 * EPT : 1];
   const int tpr = row_threads<WAVE>(), lane = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
-  const int group = WAVE ? (int)(threadIdx.x >> 6) : 0;
-  const RowEnds vec = row_ends<V>(0, 1, H);   // of w and b
+  const int group = WAVE ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : 0;
   // one shift for all the rows of the group, whose columns stay with their threads (their
   // parities agree: the rows of a step are a multiple of 4, or the grid is even)
-  const int c0 = lane * V - col_shift<EDGE>(s + ((size_t)blockIdx.x * GROUPS + group) * H, H, tpr * EPT);
+  const int shift = col_shift<EDGE>(s + ((size_t)blockIdx.x * GROUPS + group) * H, H, tpr * EPT);
+  const int c0 = lane * V - shift;
+  const RowEnds vec = row_ends<V>(0, 1, H, shift);   // of w
   float wv[NV][V], dwa[NV][V], dba[HAS_B ? NV : 1][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -353,7 +363,7 @@ __global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_bwd(const T* __restric
   int par = 0;
   for (int64_t t = (int64_t)blockIdx.x * GROUPS + group; t < T_; t += (int64_t)gridDim.x * GROUPS, par ^= 1) {
     const size_t off = (size_t)t * H;
-    const RowEnds ends = row_ends<V>(t, T_, H);
+    const RowEnds ends = row_ends<V>(t, T_, H, shift);
     float xh[NV][V], g[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -396,7 +406,7 @@ __global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_bwd(const T* __restric
 #pragma unroll
         for (int j = 0; j < V; ++j) g[i][j] += d[j];
       }
-      store_row<EDGE>(dx + off, c, H, g[i]);
+      store_row<EDGE>(dx + off, c, H, ends.tail, g[i]);
     }
   }
   // the row groups' shares, added in group order
@@ -422,7 +432,7 @@ __global__ __launch_bounds__(wg_most<WAVE>()) void k_norm_bwd(const T* __restric
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int q = 0; q < V; q += 4)
-          store_row<EDGE>(out, c0 + i * tpr * V + q, H, *reinterpret_cast<float(*)[4]>(&a[i][q]));
+          store_row<EDGE>(out, c0 + i * tpr * V + q, H, (H + shift) & 3, *reinterpret_cast<float(*)[4]>(&a[i][q]));
     }
   };
   leave(dwa, part + (size_t)blockIdx.x * H);
