@@ -999,6 +999,149 @@ __device__ __forceinline__ void small_put(f16* dst, int ld, const float (&v)[16]
     *reinterpret_cast<f16x4*>(row + 8 * q) = f16x4{(f16)v[4 * q], (f16)v[4 * q + 1], (f16)v[4 * q + 2], (f16)v[4 * q + 3]};
 }
 
+// ---- few rows: a step's square matrices in one workgroup ----
+// With m at most 128 a matrix's squares fit in one CU's LDS, so one launch makes A of X, passed
+// through a ring of K steps that serves as both factors, and of it B; or, for the first two
+// steps as one, all of R, B_0, S, A_1, B_1 and P.  That is 2 launches a step in place of 3, and
+// 1 in place of 6 for the merged ones.  What is left is the read of X by a lone CU (0.2 us a K
+// step of 8 KB, 0.4 of 16 KB) and 4 to 6 us a launch.  A by the lower triangle alone, a wave a
+// 16-deep slice of K (a third of the LDS reads, but shares to join), was slower up to K =
+// 4096 at 128 rows, and faster past 2048 at 64.
+struct SquareArgs {
+  const f16* x;          // [n, MP, K]
+  int K;
+  const float* factor;   // per matrix, stored X -> X; null: 1
+  float c0, diag;        // D = c0 X X^T - diag I
+  float sq, lin;         // B = sq D^2 + lin D, and B_1 of A_1
+  float s, a0, as, ar;   // S = s B_0 R;  A_1 = a0 B_0 S + as S + ar R
+  float p0, p1;          // P = p0 B_1 B_0 + p1 (B_0 + B_1)
+  f16* out;              // B or P [n, MP, MP]
+};
+template <int MP, bool MERGED>
+__global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
+  constexpr int NS = 8, OPER = MP * BK, LP = OPER * 2 / 1024 / NW;   // 1 KB loads a wave and K step
+  static_assert(LP * NW * 512 == OPER && LP * (NS - 2) < 64, "wave loads divide among the waves");
+  constexpr int LDM = MP + 8, RB = MP / 32, BLOCKS = RB * RB;
+  constexpr int SB = BLOCKS > NW ? BLOCKS / NW : 1;       // 32 x 32 blocks a wave
+  constexpr int SPLIT = BLOCKS < NW ? NW / BLOCKS : 1;    // waves that share a block's K steps
+  constexpr int MAT = MP * LDM, ELEMS = NS * OPER > 4 * MAT ? NS * OPER : 4 * MAT;
+  static_assert(SPLIT == 1 || 4 * MAT + BLOCKS * 1024 * 2 * (SPLIT - 1) <= ELEMS, "shares behind the matrices");
+  __shared__ __attribute__((aligned(16))) f16 lds[ELEMS];
+  const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), w = wv % BLOCKS, part = wv / BLOCKS;
+  const int bi = w % RB * 32, bj0 = w / RB * 32;
+  constexpr int BSTEP = NW / RB * 32;   // columns from one of a wave's blocks to the next
+  const size_t z = blockIdx.x;
+  const int K = a.K, nk = K / BK;
+  const bf16_t* la[LP];
+#pragma unroll
+  for (int q = 0; q < LP; ++q) {
+    int r, c;
+    kmaj_slot((q * NW + wv) * 64 + lane, r, c);
+    la[q] = reinterpret_cast<const bf16_t*>(a.x) + (z * MP + r) * K + c * 8;
+  }
+  bf16_t* const ring = reinterpret_cast<bf16_t*>(lds);
+  auto issue = [&](int kt) {
+#pragma unroll
+    for (int q = 0; q < LP; ++q) dma16(la[q] + kt * BK, ring + (kt % NS) * OPER + (q * NW + wv) * 512);
+  };
+  f32x16 acc[SB];
+#pragma unroll
+  for (int b = 0; b < SB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
+#pragma unroll 1
+  for (int kt = 0; kt < min(NS - 1, nk); ++kt) issue(kt);
+#pragma unroll 1
+  for (int kt = 0; kt < nk; ++kt) {
+    // step kt has landed when at most the NS - 2 later steps' loads are out
+    if (nk - 1 - kt >= NS - 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LP * (NS - 2)) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kt + NS - 1 < nk) issue(kt + NS - 1);   // into the stage read one step ago
+    const bf16_t* const st = ring + (kt % NS) * OPER;
+#pragma unroll
+    for (int k = 0; k < BK / 16 / SPLIT; ++k) {
+      const int kk = part * (BK / 16 / SPLIT) + k;
+      const f16x8 pf = as_f16(frag_kmaj(st, bi, kk, lane));
+#pragma unroll
+      for (int b = 0; b < SB; ++b)
+        acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16(frag_kmaj(st, bj0 + b * BSTEP, kk, lane)), pf, acc[b], 0, 0, 0);
+    }
+  }
+  __syncthreads();   // the ring's space is the matrices' from here on
+  if constexpr (SPLIT > 1) {
+    float* const share = reinterpret_cast<float*>(lds + 4 * MAT) + w * 1024 + lane;
+    static_assert(SPLIT == 2, "one share a block");
+    if (part == 1) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) share[r * 64] = acc[0][r];
+    }
+    __syncthreads();
+    if (part == 0) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[0][r] += share[r * 64];
+    }
+  }
+  const bool on = part == 0;
+  // dst (the next matrix, or the result) = c acc + c1 S1 + c2 S2, blocks in this wave's layout:
+  // lane l holds row bi + l % 32, columns 8 q + 4 (l / 32) .. + 3 of each block
+  auto finish = [&](f16* dst, float c, float diag, const f16* s1, float c1, const f16* s2, float c2) {
+    if (!on) return;
+#pragma unroll
+    for (int b = 0; b < SB; ++b) {
+      const int bj = bj0 + b * BSTEP;
+      float v[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] = acc[b][r] * c;
+      if (diag != 0.f && bi == bj) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if ((lane & 31) == 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= diag;
+      }
+      auto add = [&](const f16* side, float k) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f16x4 u = *reinterpret_cast<const f16x4*>(side + (bi + (lane & 31)) * LDM + bj + 8 * q + 4 * (lane >> 5));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * q + e] += (float)u[e] * k;
+        }
+      };
+      if (s1) add(s1, c1);
+      if (s2) add(s2, c2);
+      if (dst) {
+        small_put(dst + bi * LDM + bj, LDM, v, lane);
+      } else {
+        i32x4 ch[2];
+        trans_chunks_f16(v, ch);
+        f16* const o = a.out + (z * MP + bi + (lane & 31)) * MP + bj + 8 * (lane >> 5);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<i32x4*>(o + 16 * h) = ch[h];
+      }
+    }
+  };
+  auto product = [&](const f16* p, const f16* q) {
+    __syncthreads();
+    if (on) small_blocks<SB>(p + bi * LDM, LDM, q + bj0 * LDM, LDM, BSTEP, MP, lane, acc);
+  };
+  f16 *const d = lds, *const b0 = lds + MAT, *const sm = lds + 2 * MAT, *const a1 = lds + 3 * MAT;
+  const float f = a.factor ? a.factor[z] : 1.f;
+  finish(d, a.c0 * f * f, a.diag, nullptr, 0.f, nullptr, 0.f);
+  product(d, d);
+  if constexpr (!MERGED) {
+    finish(nullptr, a.sq, 0.f, d, a.lin, nullptr, 0.f);
+  } else {
+    f16* const b1 = d;
+    finish(b0, a.sq, 0.f, d, a.lin, nullptr, 0.f);
+    product(b0, d);
+    finish(sm, a.s, 0.f, nullptr, 0.f, nullptr, 0.f);
+    product(b0, sm);
+    finish(a1, a.a0, 0.f, sm, a.as, d, a.ar);
+    product(a1, a1);   // its barrier also ends the reads of d, whose place B_1 takes
+    finish(b1, a.sq, 0.f, a1, a.lin, nullptr, 0.f);
+    product(b1, b0);
+    finish(nullptr, a.p0, 0.f, b0, a.p1, b1, a.p1);
+  }
+}
+
 // XB: 32 x 32 blocks of X a wave, 1, 2 or 4 (one launch runs its code cold: the instructions
 // of blocks that are not there cost more than the work of those that are)
 template <typename T, int MP, int XB>
@@ -1186,9 +1329,24 @@ static bool merge_pays(int n, int mp, int lp) {
 
 // Scratch: norm shares and factors, then X (two iterates, hi and lo), and the square matrices:
 // D and B of a step, or R, B_0, S, A_1 and B_1 of two merged ones, whose P takes S's place
+// Whether a step's squares are made by k_orth_square (mp <= 128).  A lone workgroup reads its
+// matrix at 40 to 80 GB/s, so the products by tiles win where K is long and matrices are few:
+// whole updates, squares in one launch / by tiles, 5 of 64 x 1024 48 / 79 us, 100 of them 74 /
+// 105, 1 of 64 x 4096 86 / 124, 2 of 128 x 512 56 / 75, 1 of 128 x 2048 99 / 99, 128 of 128 x
+// 4096 538 / 644, 300 of 128 x 600 234 / 246, 1 of 96 x 4096 156 / 137.  Estimated time of a
+// step's squares, in us, with two workgroups a CU for 64 rows and one for 128; the factor is
+// what the merged steps (1 launch for 6) add.
+static bool square_pays(int n, int mp, int lp) {
+  if (mp > 128) return false;
+  double gram, poly;
+  orth_tile_kind(true, n, mp, mp, lp, &gram);
+  orth_tile_kind(true, n, mp, mp, mp, &poly);
+  const double k = lp / 64.0, rounds = ceil(n / ((mp == 64 ? 2.0 : 1.0) * num_cus()));
+  return rounds * (mp == 64 ? 4.0 + 0.20 * k : 6.0 + 0.42 * k) <= 1.3 * (gram + poly);
+}
 struct OrthLayout {
   int m, l, mp, lp, chunks;
-  bool merge;
+  bool square, merge;   // k_orth_square; the first two steps as one
   size_t off_part, off_factor, off_x[2], off_lo[2], off_s[5], bytes;
 };
 static OrthLayout orth_layout(const moe_orth_shape& s) {
@@ -1214,8 +1372,9 @@ static OrthLayout orth_layout(const moe_orth_shape& s) {
     L.off_x[i] = take(xb);
     L.off_lo[i] = take(xb / 2);
   }
-  L.merge = s.steps >= 2 && merge_pays(s.n, L.mp, L.lp);
-  for (int i = 0; i < (L.merge ? 5 : 2); ++i) L.off_s[i] = take(db);
+  L.square = square_pays(s.n, L.mp, L.lp);
+  L.merge = s.steps >= 2 && (L.square || merge_pays(s.n, L.mp, L.lp));
+  for (int i = 0; i < (L.square ? 1 : L.merge ? 5 : 2); ++i) L.off_s[i] = take(db);
   L.bytes = off;
   return L;
 }
@@ -1301,8 +1460,34 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
     else orth_product<ORTH_APPLY>("orth_apply", a, s.n, st);
     cur ^= 1;
   };
+  auto square = [&](SquareArgs& a, bool merged, float ds, float bs, float beta, const float* f) {
+    a.x = x[cur]; a.K = L.lp; a.factor = f; a.out = sq[0];
+    a.c0 = f ? ds : ds / (X_SCALE * X_SCALE);
+    a.sq = NS_C * bs / (ds * ds);
+    a.lin = beta * bs / ds;
+    const dim3 grid((unsigned)s.n), block(NTHR);
+#define CALL(MP)                                                                               \
+  if (merged) MOE_LAUNCH("orth_square2", (k_orth_square<MP, true>), grid, block, 0, st, a);    \
+  else MOE_LAUNCH("orth_square", (k_orth_square<MP, false>), grid, block, 0, st, a)
+    if (L.mp == 64) {
+      CALL(64);
+    } else {
+      CALL(128);
+    }
+#undef CALL
+  };
   int step = 0;
-  if (L.merge) {
+  if (L.merge && L.square) {
+    const float ds = fit_scale(NS_B / NS_C, D_SCALE), bs = fit_scale(NS_A, 0.5f * B_SCALE);
+    const float ps = fit_scale(NS_A * NS_A, P_SCALE);
+    SquareArgs a{};
+    a.s = S_SCALE / (bs * ds);
+    a.a0 = ds / (bs * S_SCALE); a.as = 2.f * NS_A * ds / S_SCALE; a.ar = NS_A * NS_A;
+    a.p0 = ps / (bs * bs); a.p1 = NS_A * ps / bs;
+    square(a, true, ds, bs, NS_B, factor);
+    apply(sq[0], ps, NS_A * NS_A, factor, s.steps == 2);
+    step = 2;
+  } else if (L.merge) {
     f16 *r = sq[0], *b0 = sq[1], *sp = sq[2], *a1 = sq[3], *b1 = sq[4];
     const float ds = fit_scale(NS_B / NS_C, D_SCALE), bs = fit_scale(NS_A, 0.5f * B_SCALE);   // 2 a bs is fp16, too
     const float ps = fit_scale(NS_A * NS_A, P_SCALE);
@@ -1319,9 +1504,16 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
     const StepCoef co = step_coef(step);
     const float* f = step == 0 ? factor : nullptr;
     const float ds = fit_scale(co.beta / NS_C, D_SCALE), bs = fit_scale(co.alpha, B_SCALE);
-    gram(sq[0], ds, co.t, f);
-    poly(sq[0], ds, sq[1], bs, co.beta);
-    apply(sq[1], bs, co.alpha, f, step == s.steps - 1);
+    f16* const b = L.square ? sq[0] : sq[1];
+    if (L.square) {
+      SquareArgs a{};
+      a.diag = co.t * ds;
+      square(a, false, ds, bs, co.beta, f);
+    } else {
+      gram(sq[0], ds, co.t, f);
+      poly(sq[0], ds, b, bs, co.beta);
+    }
+    apply(b, bs, co.alpha, f, step == s.steps - 1);
   }
   return hipGetLastError();
 }

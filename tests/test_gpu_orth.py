@@ -133,6 +133,25 @@ def test_orth_on_the_largest_tiles(rows, cols, steps):
     assert torch.isfinite(torch.cat([o[:2], o[3:]])).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(64, 640), (33, 1999), (100, 600), (700, 128), (1100, 97)])
+@pytest.mark.parametrize("steps,dt", [(1, torch.bfloat16), (2, torch.float32), (3, torch.bfloat16), (4, torch.float32),
+                                      (6, torch.bfloat16)])
+def test_orth_of_few_rows(rows, cols, steps, dt):
+    """A step's squares in one launch: zero, NaN and ordinary matrices side by side, each as it
+    is alone, bit for bit."""
+    g = torch.stack([torch.from_numpy(spectra(k, rows, cols, i)) for i, k in enumerate(("flat", "low_rank", "power", "flat"))])
+    g = g.to(dt)
+    g[3, 1, 2] = float("nan")
+    g = torch.cat([g, torch.zeros_like(g[:1])])
+    o = _op(5, rows, cols, dt, steps).update(g.cuda(), scale=1.5)
+    alone = _op(1, rows, cols, dt, steps).update(g[2:3].cuda(), scale=1.5)
+    torch.cuda.synchronize()
+    for i in range(3):
+        assert _off(o[i], ot.orthogonalize(g[i].double().numpy(), steps, 1.5)) < TOL, i
+    assert torch.isnan(o[3]).all() and not o[4].any()
+    assert torch.equal(o[2], alone[0])
+
+
 def test_orth_two_at_once():
     """Two operators on two streams, over several calls each."""
     a, b = _op(3, 300, 520, torch.bfloat16), _op(8, 128, 64, torch.bfloat16)
