@@ -152,6 +152,31 @@ def test_orth_of_few_rows(rows, cols, steps, dt):
     assert torch.equal(o[2], alone[0])
 
 
+# one launch; squares in one launch a step; small tiles; the largest tiles
+@pytest.mark.parametrize("n,rows,cols", [(8, 128, 64), (5, 600, 100), (3, 300, 520), (64, 520, 1100)])
+def test_orth_as_graphs_that_share_an_operator(n, rows, cols):
+    """Two graphs on one operator's scratch, replayed in turn with eager calls in between."""
+    gen = torch.Generator().manual_seed(n)
+    op = _op(n, rows, cols, torch.bfloat16)
+    g = [torch.randn(n, rows, cols, generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+    want = [op.update(x).clone() for x in g]
+    out = [torch.empty_like(x) for x in g]
+    graphs = []
+    for x, o in zip(g, out):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            op.update(x, out=o)
+        graphs.append(graph)
+    for _ in range(3):
+        for o in out:
+            o.zero_()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+        assert torch.equal(op.update(g[1]), want[1])
+
+
 def test_orth_two_at_once():
     """Two operators on two streams, over several calls each."""
     a, b = _op(3, 300, 520, torch.bfloat16), _op(8, 128, 64, torch.bfloat16)
