@@ -925,7 +925,7 @@ void orth_product<ORTH_SYM3>(const char* name, const OrthArgs& a, int n, hipStre
 // X [MP, lp] (at most SMALL_ELEMS) stays in one CU: as fp32 in the accumulator layout of its
 // eight waves (so no iterate is rounded but for the products), and as fp16 in LDS beside D and
 // B.  One launch instead of 2 + 3 a step, which is what bounds matrices this small: eight of
-// 128 x 64, five steps, take 13.6 us and took 84 in 17 launches.
+// 128 x 64, five steps, take 12.7 us and took 84 in 17 launches.
 constexpr int SMALL_ELEMS = 32768, SMALL_MP = 128;
 constexpr int small_lds(int mp) {   // elements: X (rows of lp + 8), D and B (rows of mp + 8)
   return SMALL_ELEMS + 8 * mp + 2 * mp * (mp + 8);
@@ -951,8 +951,8 @@ __device__ __forceinline__ void small_blocks(const f16* p, int ldp, const f16* q
   }
 }
 // the same of B X, at xo[b] columns of it: X as it lies, [K][ldx], through the transposing
-// read
-template <int NB>
+// read; TALL: not transposed in the accumulators
+template <int NB, bool TALL>
 __device__ __forceinline__ void small_blocks_x(const f16* p, int ldp, const f16* x, int ldx, const int (&xo)[NB], int K,
                                                int lane, f32x16 (&acc)[NB]) {
 #pragma unroll
@@ -973,7 +973,8 @@ __device__ __forceinline__ void small_blocks_x(const f16* p, int ldp, const f16*
         t[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(px + (k + 4 * h) * ldx + xo[b]));
       f16x8 xf;
       __builtin_memcpy(&xf, t, 16);
-      acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, pf, acc[b], 0, 0, 0);
+      acc[b] = TALL ? __builtin_amdgcn_mfma_f32_32x32x16_f16(pf, xf, acc[b], 0, 0, 0)
+                    : __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, pf, acc[b], 0, 0, 0);
     }
   }
 }
@@ -1143,8 +1144,11 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
 }
 
 // XB: 32 x 32 blocks of X a wave, 1, 2 or 4 (one launch runs its code cold: the instructions
-// of blocks that are not there cost more than the work of those that are)
-template <typename T, int MP, int XB>
+// of blocks that are not there cost more than the work of those that are).  TALL: rows > cols.
+// A lane holds 16 elements of one row of g in each block, four at a time side by side, so of a
+// row of X or, TALL, of a column (read element by element across g, 128 x 64 took 13.4 us
+// where 64 x 128 took 12.2).
+template <typename T, int MP, int XB, bool TALL>
 __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out, int rows, int cols, int lp,
                                                         int steps, float scale) {
   __shared__ __attribute__((aligned(16))) f16 small[small_lds(MP)];
@@ -1155,28 +1159,28 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
   f16* const xs = small;
   f16* const ds = xs + MP * ldx;
   f16* const bs = ds + MP * LDM;
-  const bool tall = rows > cols;
-  const int m = tall ? cols : rows, l = tall ? rows : cols;
-  const size_t si = tall ? 1 : cols, sj = tall ? cols : 1;   // strides of X in g and out
   const int nb = RB * (lp / 32);
+  // of block blk: the lane's row of g, and its first column
+  auto g_row = [&](int blk) { return (TALL ? blk / RB : blk % RB) * 32 + (lane & 31); };
+  auto g_col = [&](int blk) { return (TALL ? blk % RB : blk / RB) * 32 + 4 * (lane >> 5); };
   const size_t base = (size_t)blockIdx.x * rows * cols;
   float x[XB][16];
   double ss = 0.0;
 #pragma unroll
   for (int b = 0; b < XB; ++b) {
-    const int blk = wv + NW * b, i = (blk % RB) * 32 + (lane & 31), j0 = (blk / RB) * 32 + 4 * (lane >> 5);
-    const T* const row = g + base + i * si;
-    const bool in = blk < nb && i < m;
+    const int blk = wv + NW * b, i = g_row(blk), j0 = g_col(blk);
+    const T* const row = g + base + (size_t)i * cols;
+    const bool in = blk < nb && i < rows;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int j = j0 + 8 * q;
-      if (!tall && in && j + 4 <= l) {   // four of a row at once; transposed, a load takes 32 neighbours
+      if (in && j + 4 <= cols) {
         const f32x4 u = load4(row + j);
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[b][4 * q + c] = u[c];
       } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[b][4 * q + c] = in && j + c < l ? elem<T>::load(row + (j + c) * sj) : 0.f;
+        for (int c = 0; c < 4; ++c) x[b][4 * q + c] = in && j + c < cols ? elem<T>::load(row + j + c) : 0.f;
       }
     }
   }
@@ -1206,7 +1210,16 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
 #pragma unroll
     for (int b = 0; b < XB; ++b) {
       const int blk = wv + NW * b;
-      if (blk < nb) small_put(xs + (blk % RB) * 32 * ldx + (blk / RB) * 32, ldx, x[b], lane);
+      f16* const dst = xs + (blk % RB) * 32 * ldx + (blk / RB) * 32;
+      if (blk >= nb) continue;
+      if constexpr (TALL) {
+        int ln = lane;
+        asm volatile("" : "+v"(ln));   // its 16 addresses are not kept over the steps
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dst[(8 * (r >> 2) + 4 * (ln >> 5) + (r & 3)) * ldx + (ln & 31)] = (f16)x[b][r];
+      } else {
+        small_put(dst, ldx, x[b], lane);
+      }
     }
     __syncthreads();
     // a wave's blocks of D and B, and of X, share a row of blocks: NW is a multiple of RB
@@ -1254,7 +1267,7 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
 #pragma unroll
       for (int b = 0; b < XB; ++b) xo[b] = wv + NW * b < nb ? b * (NW / RB) * 32 : 0;
       if (wv < nb) {
-        small_blocks_x<XB>(bs + bi * LDM, LDM, xs + wv / RB * 32, ldx, xo, MP, lane, acc);
+        small_blocks_x<XB, TALL>(bs + bi * LDM, LDM, xs + wv / RB * 32, ldx, xo, MP, lane, acc);
 #pragma unroll
         for (int b = 0; b < XB; ++b)
 #pragma unroll
@@ -1266,20 +1279,20 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
   scale *= 1.f / X_SCALE;
 #pragma unroll
   for (int b = 0; b < XB; ++b) {
-    const int blk = wv + NW * b, i = (blk % RB) * 32 + (lane & 31), j0 = (blk / RB) * 32 + 4 * (lane >> 5);
-    bf16_t* const row = out + base + i * si;
-    if (blk >= nb || i >= m) continue;
+    const int blk = wv + NW * b, i = g_row(blk), j0 = g_col(blk);
+    bf16_t* const row = out + base + (size_t)i * cols;
+    if (blk >= nb || i >= rows) continue;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int j = j0 + 8 * q;
-      if (!tall && j + 4 <= l) {
+      if (j + 4 <= cols) {
         *reinterpret_cast<i32x2_a2*>(row + j) =
             i32x2{(int)pk_bf16(x[b][4 * q] * scale, x[b][4 * q + 1] * scale),
                   (int)pk_bf16(x[b][4 * q + 2] * scale, x[b][4 * q + 3] * scale)};
       } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (j + c < l) row[(j + c) * sj] = f2bf(x[b][4 * q + c] * scale);
+          if (j + c < cols) row[j + c] = f2bf(x[b][4 * q + c] * scale);
       }
     }
   }
@@ -1287,12 +1300,12 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
 
 inline bool orth_small(int mp, int lp) { return mp <= SMALL_MP && mp * lp <= SMALL_ELEMS; }
 
-template <typename T, int MP>
+template <typename T, int MP, bool TALL>
 static hipError_t launch_small(const moe_orth_shape& s, const T* g, bf16_t* o, int lp, float scale, hipStream_t st) {
   const dim3 grid((unsigned)s.n), block(NTHR);
   const int blocks = (int)ceil_div(MP / 32 * (lp / 32), NW);
 #define CALL(XB) \
-  MOE_LAUNCH("orth_small", (k_orth_small<T, MP, XB>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, scale)
+  MOE_LAUNCH("orth_small", (k_orth_small<T, MP, XB, TALL>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, scale)
   if (blocks == 1) CALL(1);
   else if (blocks == 2) CALL(2);
   else CALL(4);
@@ -1302,7 +1315,9 @@ static hipError_t launch_small(const moe_orth_shape& s, const T* g, bf16_t* o, i
 template <typename T>
 static hipError_t launch_small(const moe_orth_shape& s, const T* g, bf16_t* o, int mp, int lp, float scale,
                                hipStream_t st) {
-  return mp == 64 ? launch_small<T, 64>(s, g, o, lp, scale, st) : launch_small<T, 128>(s, g, o, lp, scale, st);
+  if (s.rows > s.cols)
+    return mp == 64 ? launch_small<T, 64, true>(s, g, o, lp, scale, st) : launch_small<T, 128, true>(s, g, o, lp, scale, st);
+  return mp == 64 ? launch_small<T, 64, false>(s, g, o, lp, scale, st) : launch_small<T, 128, false>(s, g, o, lp, scale, st);
 }
 
 // The scale next to `scale` with which k * scale is an fp16 number
