@@ -26,8 +26,10 @@ def _device(device) -> torch.device:
 
 
 # the raw handle of a device's current stream, without the Stream object that
-# torch.cuda.current_stream builds around it (2 us of a call of 8)
+# torch.cuda.current_stream builds around it (2 us of a call of 8), and the current device
+# without the check that CUDA is initialised (an operator's buffers have done that)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 class _OnDevice:
@@ -46,7 +48,7 @@ class _OnDevice:
 
     def _call(self, func, stream, *args):
         s = _raw_stream(self._index) if stream is None else stream.cuda_stream
-        if torch.cuda.current_device() == self._index:
+        if _current_device() == self._index:
             func(*args, s)
         else:
             with torch.cuda.device(self._index):
