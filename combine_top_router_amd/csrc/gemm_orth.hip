@@ -682,6 +682,15 @@ __device__ __forceinline__ f16x8 tile_frag_mn(const bf16_t* s, int base, int kk,
   return out;
 }
 
+// dma16 to an LDS address that is a scalar already: a third of the instructions, which these
+// launches run cold
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)((MOE_LDS const void*)p));
+}
+__device__ __forceinline__ void dma16_to(const void* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
+}
+
 template <int OP, int TILE, int NS>
 __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_orth_tile(OrthArgs a, int tm, int tn, int items) {
   using C = TileCfg<TILE>;
@@ -725,12 +734,20 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     }
   }
   const size_t bstep = SYM ? (size_t)BK : (size_t)BK * a.lp;
+  const uint32_t l0 = lds_address(lds) + wv * 1024;
   auto issue = [&](int kt) {
-    bf16_t* const st = lds + (kt % NS) * STAGE;
+    const uint32_t st = l0 + (kt % NS) * STAGE * 2;
 #pragma unroll
     for (int q = 0; q < LP; ++q) {
-      dma16(la[q] + kt * BK, st + (q * C::WAVES + wv) * 512);
-      dma16(lb[q] + kt * bstep, st + OPER + (q * C::WAVES + wv) * 512);
+      // (eight waves' loads, 128 rows, come faster spread out by dma16's other instructions: 128 of
+      // 128 x 4096 536 us, 551 without; 64 rows: 8 of 768 x 2048 323 with dma16, 313 without)
+      if constexpr (TILE == 128) {
+        dma16(la[q] + kt * BK, lds + (kt % NS) * STAGE + (q * C::WAVES + wv) * 512);
+        dma16(lb[q] + kt * bstep, lds + (kt % NS) * STAGE + OPER + (q * C::WAVES + wv) * 512);
+      } else {
+        dma16_to(la[q] + kt * BK, st + q * C::WAVES * 1024);
+        dma16_to(lb[q] + kt * bstep, st + OPER * 2 + q * C::WAVES * 1024);
+      }
     }
   };
   const int wm = wv & 1, wn = wv >> 1, ib = wm * 32 * C::TMI, jb = wn * 32;   // the wave's first row and column
@@ -743,9 +760,9 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
   for (int mi = 0; mi < C::TMI; ++mi)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[mi][r] = 0.f;
-#pragma unroll
-  for (int kt = 0; kt < NS - 1; ++kt)
-    if (kt < nk) issue(kt);
+#pragma unroll 1
+  for (int kt = 0; kt < min(NS - 1, nk); ++kt) issue(kt);
+#pragma unroll 1
   for (int kt = 0; kt < nk; ++kt) {
     // step kt has landed when at most the NS - 2 later steps' loads are out
     if (NS > 2 && nk - 1 - kt >= NS - 2) {
@@ -754,17 +771,26 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     } else {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
-    if (kt + NS - 1 < nk) issue(kt + NS - 1);   // into the stage read one step ago
+    // in the deep ring the step's fragments are asked for before a later step's loads, whose issue
+    // (16 KB at 64 a clock) then passes while they come: 1 of 1024 x 1024 142 us, 136 so; several
+    // workgroups on a CU fill that time themselves, and lose by the longer loop
+    if (NS == 2 && kt + NS - 1 < nk) issue(kt + NS - 1);   // into the stage read one step ago
     const bf16_t* const as = lds + (kt % NS) * STAGE;
     const bf16_t* const bs = as + OPER;
     if (above) continue;
+    f16x8 fa[C::TMI][BK / 16], fb[BK / 16];
 #pragma unroll
     for (int kk = 0; kk < BK / 16; ++kk) {
-      const f16x8 bf = SYM ? as_f16(frag_kmaj(bs, jb, kk, lane)) : tile_frag_mn<TILE>(bs, jb, kk, lane);
+      fb[kk] = SYM ? as_f16(frag_kmaj(bs, jb, kk, lane)) : tile_frag_mn<TILE>(bs, jb, kk, lane);
+#pragma unroll
+      for (int mi = 0; mi < C::TMI; ++mi) fa[mi][kk] = as_f16(frag_kmaj(as, ib + mi * 32, kk, lane));
+    }
+    if (NS > 2 && kt + NS - 1 < nk) issue(kt + NS - 1);
+#pragma unroll
+    for (int kk = 0; kk < BK / 16; ++kk)
 #pragma unroll
       for (int mi = 0; mi < C::TMI; ++mi)
-        acc[mi] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf, as_f16(frag_kmaj(as, ib + mi * 32, kk, lane)), acc[mi], 0, 0, 0);
-    }
+        acc[mi] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[kk], fa[mi][kk], acc[mi], 0, 0, 0);
   }
   // lane l: row l % 32 of each block, columns 8q + 4 (l / 32) .. + 3
   if (j0 + jb >= ldn || above) return;
@@ -1040,10 +1066,11 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
     kmaj_slot((q * NW + wv) * 64 + lane, r, c);
     la[q] = reinterpret_cast<const bf16_t*>(a.x) + (z * MP + r) * K + c * 8;
   }
-  bf16_t* const ring = reinterpret_cast<bf16_t*>(lds);
+  const bf16_t* const ring = reinterpret_cast<const bf16_t*>(lds);
+  const uint32_t l0 = lds_address(lds) + wv * 1024;
   auto issue = [&](int kt) {
 #pragma unroll
-    for (int q = 0; q < LP; ++q) dma16(la[q] + kt * BK, ring + (kt % NS) * OPER + (q * NW + wv) * 512);
+    for (int q = 0; q < LP; ++q) dma16_to(la[q] + kt * BK, l0 + (kt % NS) * OPER * 2 + q * NW * 1024);
   };
   f32x16 acc[SB];
 #pragma unroll
@@ -1057,16 +1084,21 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
     // step kt has landed when at most the NS - 2 later steps' loads are out
     if (nk - 1 - kt >= NS - 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LP * (NS - 2)) : "memory");
     else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kt + NS - 1 < nk) issue(kt + NS - 1);   // into the stage read one step ago
     const bf16_t* const st = ring + (kt % NS) * OPER;
+    constexpr int KS = BK / 16 / SPLIT;
+    f16x8 pf[KS], qf[SB][KS];   // before the loads at 64 rows, as in k_orth_tile; at 128, LDS is busy all the time
+    if (MP == 128 && kt + NS - 1 < nk) issue(kt + NS - 1);   // into the stage read one step ago
 #pragma unroll
-    for (int k = 0; k < BK / 16 / SPLIT; ++k) {
-      const int kk = part * (BK / 16 / SPLIT) + k;
-      const f16x8 pf = as_f16(frag_kmaj(st, bi, kk, lane));
+    for (int k = 0; k < KS; ++k) {
+      pf[k] = as_f16(frag_kmaj(st, bi, part * KS + k, lane));
 #pragma unroll
-      for (int b = 0; b < SB; ++b)
-        acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_f16(frag_kmaj(st, bj0 + b * BSTEP, kk, lane)), pf, acc[b], 0, 0, 0);
+      for (int b = 0; b < SB; ++b) qf[b][k] = as_f16(frag_kmaj(st, bj0 + b * BSTEP, part * KS + k, lane));
     }
+    if (MP == 64 && kt + NS - 1 < nk) issue(kt + NS - 1);
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int b = 0; b < SB; ++b) acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[b][k], pf[k], acc[b], 0, 0, 0);
   }
   __syncthreads();   // the ring's space is the matrices' from here on
   if constexpr (SPLIT > 1) {
