@@ -877,7 +877,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
 // The tile of a product, M x N over K in n matrices (M x M by halves when symmetric): the one
 // of least estimated time, from what the four kernels were measured to take on one MI355X, in
 // us, for t tiles a CU and k steps of 64:
-//   64 rows, deep ring    3 + 0.27 k                        one tile a CU at most
+//   64 rows, deep ring    3 + 0.24 k                        one tile a CU at most
 //   64 rows               3 + max(0.40 k, t (0.8 + 0.18 k))  five workgroups share a CU
 //   128 rows              4 + max(0.58 k, t (1.9 + 0.70 k))  two share a CU
 //   256 rows              5 + ceil(t) (7 + c k)              c = 1.25 on few CUs, 2.15 on all
@@ -893,7 +893,7 @@ static OrthTileKind orth_tile_kind(bool sym, int n, int M, int N, int K, double*
     return n * (sym ? tm * (tm + 1) / 2 : tm * tn) / cus;
   };
   const double t64 = load(64), t128 = load(128), t256 = load(256);
-  const double us[4] = {t64 <= 1.0 ? 3.0 + 0.27 * k : 1e30, 3.0 + fmax(0.40 * k, t64 * (0.8 + 0.18 * k)),
+  const double us[4] = {t64 <= 1.0 ? 3.0 + 0.24 * k : 1e30, 3.0 + fmax(0.40 * k, t64 * (0.8 + 0.18 * k)),
                         4.0 + fmax(0.58 * k, t128 * (1.9 + 0.70 * k)),
                         5.0 + ceil(t256) * (7.0 + (1.25 + 0.9 * fmin(t256, 1.0)) * k)};
   int best = TILE_256;
@@ -1379,17 +1379,17 @@ static bool merge_pays(int n, int mp, int lp) {
 // Whether a step's squares are made by k_orth_square (mp <= 128).  A lone workgroup reads its
 // matrix at 40 to 80 GB/s, so the products by tiles win where K is long and matrices are few:
 // whole updates, squares in one launch / by tiles, 5 of 64 x 1024 48 / 79 us, 100 of them 74 /
-// 105, 1 of 64 x 4096 86 / 124, 2 of 128 x 512 56 / 75, 1 of 128 x 2048 99 / 99, 128 of 128 x
-// 4096 538 / 644, 300 of 128 x 600 234 / 246, 1 of 96 x 4096 156 / 137.  Estimated time of a
-// step's squares, in us, with two workgroups a CU for 64 rows and one for 128; the factor is
-// what the merged steps (1 launch for 6) add.
+// 105, 1 of 64 x 4096 86 / 124, 2 of 128 x 512 56 / 75, 1 of 128 x 1500 81 / 87, 1 of 128 x 2048
+// 91 / 92, 128 of 128 x 4096 538 / 644, 300 of 128 x 600 234 / 246, 1 of 96 x 4096 156 / 121.
+// Estimated time of a step's squares, in us, with two workgroups a CU for 64 rows and one for
+// 128; the factor is what the merged steps (1 launch for 6) add.
 static bool square_pays(int n, int mp, int lp) {
   if (mp > 128) return false;
   double gram, poly;
   orth_tile_kind(true, n, mp, mp, lp, &gram);
   orth_tile_kind(true, n, mp, mp, mp, &poly);
   const double k = lp / 64.0, rounds = ceil(n / ((mp == 64 ? 2.0 : 1.0) * num_cus()));
-  return rounds * (mp == 64 ? 4.0 + 0.20 * k : 6.0 + 0.42 * k) <= 1.3 * (gram + poly);
+  return rounds * (mp == 64 ? 4.0 + 0.20 * k : 6.0 + 0.42 * k) <= 1.4 * (gram + poly);
 }
 struct OrthLayout {
   int m, l, mp, lp, chunks;
