@@ -654,10 +654,14 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_stream(OrthArgs a, int n, int 
 }
 
 // ---- the products on 128 x 128 and 64 x 64 tiles: one tile a workgroup ----
-// For matrices whose 256-row tiles leave CUs idle or mostly padding.  Such launches wait for
-// loads, not for MFMAs.  The K steps ring through NS stages of LDS, so NS - 1 steps of
-// direct-to-LDS loads are in flight, with one barrier a step: eight stages where a CU gets one
-// tile, two where several workgroups on a CU cover each other's waits.
+// For matrices whose 256-row tiles leave CUs idle or mostly padding.  The K steps ring through
+// NS stages of LDS, so NS - 1 steps of direct-to-LDS loads are in flight, with one barrier a
+// step: four stages where a CU gets up to two tiles, two where several workgroups on a CU cover
+// each other's waits.  A step of a lone workgroup is LDS reads, the issue of the loads and the
+// products in turn (0.24 us for 64 rows, the same when its data are in the nearest cache, with
+// half the bytes on 32 rows, or with eight stages; three and five stages cost a division).
+// Eight stages, one workgroup a CU, took 113 us for 5 of 333 x 1000 where four take 107, and
+// with two tiles a CU on four stages instead of two 4 of 700 x 1500 take 180 instead of 200.
 template <int TILE> struct TileCfg;
 template <> struct TileCfg<64> { static constexpr int WAVES = 4, TMI = 1; };    // 2 x 2 waves of 32 x 32
 template <> struct TileCfg<128> { static constexpr int WAVES = 8, TMI = 2; };   // 2 x 4 waves of 64 x 32
@@ -751,9 +755,9 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     }
   };
   const int wm = wv & 1, wn = wv >> 1, ib = wm * 32 * C::TMI, jb = wn * 32;   // the wave's first row and column
-  // above the diagonal: mirrored from below.  Not in the deep ring, whose lone workgroups wait
-  // for loads: there the branch costs more than the products (5 of 333 x 1000 117 us, 128 with
-  // it; 128 of 320 x 640, in the short ring, 463 us without and 452 with)
+  // above the diagonal: mirrored from below.  Not in the deep ring: lone workgroups have nothing
+  // to do in the time, and the branch costs more than the products (5 of 333 x 1000 117 us, 128
+  // with it; 128 of 320 x 640, in the short ring, 463 us without and 452 with)
   const bool above = SYM && NS == 2 && i0 == j0 && jb >= ib + 32 * C::TMI;
   f32x16 acc[C::TMI];
 #pragma unroll
@@ -877,14 +881,14 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
 // The tile of a product, M x N over K in n matrices (M x M by halves when symmetric): the one
 // of least estimated time, from what the four kernels were measured to take on one MI355X, in
 // us, for t tiles a CU and k steps of 64:
-//   64 rows, deep ring    3 + 0.24 k                        one tile a CU at most
+//   64 rows, deep ring    3 + max(0.24 k, t (0.8 + 0.18 k))  two share a CU, for two tiles at most
 //   64 rows               3 + max(0.40 k, t (0.8 + 0.18 k))  five workgroups share a CU
 //   128 rows              4 + max(0.58 k, t (1.9 + 0.70 k))  two share a CU
 //   256 rows              5 + ceil(t) (7 + c k)              c = 1.25 on few CUs, 2.15 on all
-// Whole updates, bf16, with 64 deep / 64 / 128 / 256 rows throughout: 100 of 64 x 1024 148 /
-// 124 / 145 / 246 us; 11 of 362 x 362 113 / 103 / 131 / 264; 8 of 768 x 2048 576 / 384 / 351 /
-// 586; 128 of 320 x 640 783 / 486 / 478 / 625; the symmetric product of 20 of 256 over K =
-// 1024 7.4 / 9.4 / 12.5 / 27.5; 128 of 768 x 2048 take 4.1 ms with 256 rows.
+// Whole updates, bf16, by this rule and with 64 deep / 64 / 128 / 256 rows throughout: 11 of 362 x
+// 362 98 us and 98 / 105 / 135 / 239; 1 of 1024 x 1024 126 and 127 / 171 / 229 / 461; 4 of 700 x
+// 1500 174 and 176 / 198 / 249 / 448; 8 of 768 x 2048 290 and 343 / 313 / 321 / 523; 128 of 320 x
+// 640 404 and 454 / 412 / 444 / 528.
 enum OrthTileKind { TILE_64_DEEP, TILE_64, TILE_128, TILE_256 };
 static OrthTileKind orth_tile_kind(bool sym, int n, int M, int N, int K, double* time = nullptr) {
   const double k = K / 64.0, cus = num_cus();
@@ -893,7 +897,7 @@ static OrthTileKind orth_tile_kind(bool sym, int n, int M, int N, int K, double*
     return n * (sym ? tm * (tm + 1) / 2 : tm * tn) / cus;
   };
   const double t64 = load(64), t128 = load(128), t256 = load(256);
-  const double us[4] = {t64 <= 1.0 ? 3.0 + 0.24 * k : 1e30, 3.0 + fmax(0.40 * k, t64 * (0.8 + 0.18 * k)),
+  const double us[4] = {t64 <= 2.0 ? 3.0 + fmax(0.24 * k, t64 * (0.8 + 0.18 * k)) : 1e30, 3.0 + fmax(0.40 * k, t64 * (0.8 + 0.18 * k)),
                         4.0 + fmax(0.58 * k, t128 * (1.9 + 0.70 * k)),
                         5.0 + ceil(t256) * (7.0 + (1.25 + 0.9 * fmin(t256, 1.0)) * k)};
   int best = TILE_256;
@@ -934,7 +938,7 @@ template <int OP>
 static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t st) {
   constexpr bool SYM = orth_sym(OP);
   switch (orth_tile_kind(SYM, n, a.mp, SYM ? a.mp : a.lp, a.K)) {
-    case TILE_64_DEEP: return orth_tiles<OP, 64, 8>(name, a, n, st);
+    case TILE_64_DEEP: return orth_tiles<OP, 64, 4>(name, a, n, st);
     case TILE_64: return orth_tiles<OP, 64, 2>(name, a, n, st);
     case TILE_128: return orth_tiles<OP, 128, 2>(name, a, n, st);
     default: break;
@@ -1030,8 +1034,8 @@ __device__ __forceinline__ void small_put(f16* dst, int ld, const float (&v)[16]
 // With m at most 128 a matrix's squares fit in one CU's LDS, so one launch makes A of X, passed
 // through a ring of K steps that serves as both factors, and of it B; or, for the first two
 // steps as one, all of R, B_0, S, A_1, B_1 and P.  That is 2 launches a step in place of 3, and
-// 1 in place of 6 for the merged ones.  What is left is the read of X by a lone CU (0.2 us a K
-// step of 8 KB, 0.4 of 16 KB) and 4 to 6 us a launch.  A by the lower triangle alone, a wave a
+// 1 in place of 6 for the merged ones.  What is left is the K steps of a lone CU (0.2 us a step of
+// 64 rows, 0.4 of 128, most of it LDS reads) and 4 to 6 us a launch.  A by the lower triangle alone, a wave a
 // 16-deep slice of K (a third of the LDS reads, but shares to join), was slower up to K =
 // 4096 at 128 rows, and faster past 2048 at 64.
 struct SquareArgs {
@@ -1046,13 +1050,13 @@ struct SquareArgs {
 };
 template <int MP, bool MERGED>
 __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
-  constexpr int NS = 8, OPER = MP * BK, LP = OPER * 2 / 1024 / NW;   // 1 KB loads a wave and K step
+  constexpr int NS = 4, OPER = MP * BK, LP = OPER * 2 / 1024 / NW;   // 1 KB loads a wave and K step
   static_assert(LP * NW * 512 == OPER && LP * (NS - 2) < 64, "wave loads divide among the waves");
   constexpr int LDM = MP + 8, RB = MP / 32, BLOCKS = RB * RB;
   constexpr int SB = BLOCKS > NW ? BLOCKS / NW : 1;       // 32 x 32 blocks a wave
   constexpr int SPLIT = BLOCKS < NW ? NW / BLOCKS : 1;    // waves that share a block's K steps
-  constexpr int MAT = MP * LDM, ELEMS = NS * OPER > 4 * MAT ? NS * OPER : 4 * MAT;
-  static_assert(SPLIT == 1 || 4 * MAT + BLOCKS * 1024 * 2 * (SPLIT - 1) <= ELEMS, "shares behind the matrices");
+  constexpr int MAT = MP * LDM, SHARES = BLOCKS * 1024 * 2 * (SPLIT - 1);   // fp32, behind the matrices
+  constexpr int ELEMS = NS * OPER > 4 * MAT + SHARES ? NS * OPER : 4 * MAT + SHARES;
   __shared__ __attribute__((aligned(16))) f16 lds[ELEMS];
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), w = wv % BLOCKS, part = wv / BLOCKS;
   const int bi = w % RB * 32, bj0 = w / RB * 32;
@@ -1376,8 +1380,8 @@ static bool merge_pays(int n, int mp, int lp) {
 
 // Scratch: norm shares and factors, then X (two iterates, hi and lo), and the square matrices:
 // D and B of a step, or R, B_0, S, A_1 and B_1 of two merged ones, whose P takes S's place
-// Whether a step's squares are made by k_orth_square (mp <= 128).  A lone workgroup reads its
-// matrix at 40 to 80 GB/s, so the products by tiles win where K is long and matrices are few:
+// Whether a step's squares are made by k_orth_square (mp <= 128).  A lone workgroup takes
+// 0.2 or 0.42 us a K step, so the products by tiles win where K is long and matrices are few:
 // whole updates, squares in one launch / by tiles, 5 of 64 x 1024 48 / 79 us, 100 of them 74 /
 // 105, 1 of 64 x 4096 86 / 124, 2 of 128 x 512 56 / 75, 1 of 128 x 1500 81 / 87, 1 of 128 x 2048
 // 91 / 92, 128 of 128 x 4096 538 / 644, 300 of 128 x 600 234 / 246, 1 of 96 x 4096 156 / 121.
