@@ -97,17 +97,18 @@ __device__ __forceinline__ int load_slot(int q, int pw, int lane) { return load_
 // (or 4) bytes from their own global address into consecutive LDS slots starting at
 // the wave-uniform base held in M0.  The compiler does not see these as LDS writes, so
 // it adds no waits of its own; the stream orders them with explicit vmcnt waits.
-// M0 is restored after each load.
+// M0 is restored after each load.  A load right behind a scalar write of M0 takes the old
+// value: one wait state lies between (which nothing here would add by itself).
 __device__ __forceinline__ void dma16(const void* g, bf16_t* lds_wave_base) {
   const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)((MOE_LDS void*)lds_wave_base));
   uint32_t saved;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
                : "=&s"(saved) : "v"(g), "s"(m) : "memory");
 }
 __device__ __forceinline__ void dma4(const void* g, void* lds_wave_base) {
   const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)((MOE_LDS void*)lds_wave_base));
   uint32_t saved;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dword %1, off\n\ts_mov_b32 m0, %0"
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %1, off\n\ts_mov_b32 m0, %0"
                : "=&s"(saved) : "v"(g), "s"(m) : "memory");
 }
 // LDS address of wave load q of load wave pw in the A or B region of a stage
