@@ -35,11 +35,36 @@ _current_device = torch._C._cuda_getDevice
 class _OnDevice:
     """Checks and streams of the operators around the layer.  A call runs on `stream`, or on
     the current stream of the operator's own device; its buffers are reused from call to
-    call, so calls of one operator on several streams have to be ordered by the caller."""
+    call, so calls of one operator on several streams have to be ordered by the caller.  The
+    buffers' memory is that of the stream that is current when they are made, whose earlier
+    work may still use it: the first call on another stream waits for that work."""
+
+    _birth, _ordered = None, ()
 
     def _place(self, device):
         self.device = _device(device)
         self._index = self.device.index
+
+    def _allocated(self):
+        """Called behind every allocation of buffers."""
+        if self._index is None:
+            return
+        with torch.cuda.device(self._index):
+            home = torch.cuda.current_stream()
+            self._ordered = {home.cuda_stream}
+            # a graph's memory pool is its own, and an event inside a capture is no other stream's
+            self._birth = None if torch.cuda.is_current_stream_capturing() else home.record_event()
+
+    def _order(self, handle, stream):
+        """`stream` (None: the current one), of that handle, has not been used with the buffers."""
+        if self._birth is None:
+            return
+        s = torch.cuda.current_stream(self._index) if stream is None else stream
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                return   # takes no wait for work outside: that is the launch's to order, or the capture's start
+            s.wait_event(self._birth)
+        self._ordered.add(handle)
 
     def _check(self, t, shape, dtype, name):
         if t.dtype != dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
@@ -48,6 +73,8 @@ class _OnDevice:
 
     def _call(self, func, stream, *args):
         s = _raw_stream(self._index) if stream is None else stream.cuda_stream
+        if s not in self._ordered:
+            self._order(s, stream)
         if _current_device() == self._index:
             func(*args, s)
         else:
@@ -81,6 +108,7 @@ class MoeNorm(_OnDevice):
         self._p_dx, self._p_dw, self._p_scratch = _p(self.dx), _p(self.dw), _p(self.scratch)
         self.sum = None
         self.inputs = None
+        self._allocated()
 
     def forward(self, x, w, b=None, res=None, stream=None):
         self._check(x, self._row, self.dtype, "x")
@@ -127,6 +155,7 @@ class BalanceLoss(_OnDevice):
         self.scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
         self._p_fwd = (_p(self.loss), _p(self.counts), _p(self.prob), _p(self.scratch))
         self.inputs = None
+        self._allocated()
 
     def forward(self, logits, topk_idx, coef, mask=None, stream=None):
         self._check(logits, self._logits, torch.float32, "logits")
@@ -167,12 +196,14 @@ class Orthogonalizer(_OnDevice):
         self._size = torch.Size((n, rows, cols))
         self.o = None
         self.scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
+        self._allocated()
 
     def update(self, g, scale=1.0, out=None, stream=None):
         self._check(g, self._size, self.dtype, "g")
         if out is None:
             if self.o is None:
                 self.o = torch.empty(self._size, dtype=torch.bfloat16, device=self.device)
+                self._allocated()
             out = self.o
         else:
             self._check(out, self._size, torch.bfloat16, "out")
@@ -281,15 +312,17 @@ class MoeLayer:
         """Orthogonalised updates (bf16) of the last backward's dw_gate, dw_up and dw_down."""
         s, code = self.shape, self.shape.dtype
 
+        # before the operators, whose calls on another stream wait for what was queued before them
+        if not self._updates:
+            self._updates = {n: torch.empty(g.shape, dtype=torch.bfloat16, device=self.device)
+                             for n, g in (("gate", self.dw_gate), ("up", self.dw_up), ("down", self.dw_down))}
+
         def op(rows, cols):
             key = (rows, cols, steps)
             if key not in self._orth:
                 self._orth[key] = Orthogonalizer(s.e_local, rows, cols, code, steps, self.device)
             return self._orth[key]
 
-        if not self._updates:
-            self._updates = {n: torch.empty(g.shape, dtype=torch.bfloat16, device=self.device)
-                             for n, g in (("gate", self.dw_gate), ("up", self.dw_up), ("down", self.dw_down))}
         for n, g in (("gate", self.dw_gate), ("up", self.dw_up), ("down", self.dw_down)):
             op(g.shape[1], g.shape[2]).update(g, scale, out=self._updates[n], stream=stream)
         return dict(self._updates)
