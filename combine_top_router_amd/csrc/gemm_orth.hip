@@ -21,17 +21,22 @@
 // * from step 3 on, when the singular values are near 1, A is kept as D = A - I:
 //   b A + c A^2 = (b + c) I + (b + 2c) D + c D^2, so the diagonal's rounding enters times
 //   b + 2c = -0.71 instead of b = -4.8.
-// Against fp64 that is 0.7 to 2e-3 of the result's norm over spectra from flat to a
-// thousandfold spread, next to 1.7e-3 for the output's own rounding to bf16 (plain fp16
-// iterates: up to 4e-2, bf16 ones: up to 3e-1, on the same matrices).
+// Against fp64, five steps, that is 0.7 to 2e-3 of the result's norm over spectra from flat to
+// a thousandfold spread, next to 1.7e-3 for the output's own rounding (plain fp16 iterates: up
+// to 4e-2, bf16 ones: up to 3e-1, on the same matrices).  Gradients of few tokens, of rank 1 to
+// 64 with a few rows or columns 30 to 1000 times the others, usually cost 1 to 3e-3 and up to
+// 5e-3, most of it the rounding of b A + c A^2 where a few rows hold it all; of rank 1 in fp32,
+// which enters in 15 bits, up to 8e-3.
+// The first two steps as one, in the square matrices (A_1 = a^2 R + 2a B_0 R + B_0^2 R and so on),
+// would save 9% of the large updates below and up to a fifth of those of few rows, but its
+// roundings cost up to 2e-2 on such gradients.
 //
 // Cost.  A step is 3 m^2 l + m^3 multiply-adds (A and A^2 by halves), which binds from a few
 // matrices of some hundred rows on; below, launches and latencies do.  Measured on one MI355X,
-// five steps, bf16, one call after another: 128 of 2048 x 768 3.42 ms, 16 of 1536 x 4096 3.04
+// five steps, bf16, one call after another: 128 of 2048 x 768 3.72 ms, 16 of 1536 x 4096 3.28
 // (2.6 PFLOP of such work each, 2.4 ms at the 1.08 PFLOP/s of a large library fp16 product;
 // both run at the clock that their power leaves).  Of the former 0.23 read g twice and write X
-// (5.1 TB/s); the products with X run at 0.77 PFLOP/s (0.95 at 1536 rows), the symmetric ones
-// at 0.84 of what they execute, which is 5.25 of 9 tiles at 768 rows where 4.5 are needed.
+// (5.1 TB/s).
 #define MOE_GEMM_FW 256
 #include <math.h>
 
@@ -50,8 +55,6 @@ constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr double NS_EPS = 1e-7;
 constexpr int X_LOG2 = 15;
 constexpr float X_SCALE = 32768.f, D_SCALE = 16384.f, B_SCALE = 16384.f;
-// of two merged steps: |S| <= 2.8, and P's eigenvalues lie in [-11.5, 0]
-constexpr float S_SCALE = 16384.f, P_SCALE = 4096.f;
 constexpr float LO_SCALE = 16.f;  // |lo| <= 16, half a step of fp16 at its top: 256 of E4M3's 448
 constexpr int LO_STEPS = 2;      // the first iterates that are kept as hi + lo
 constexpr int SHIFT_STEP = 3;    // from this step on, D = A - I
@@ -180,21 +183,20 @@ __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int
 }
 
 // ---- the products ----
-// What a product is for.  SYM0..3: a symmetric one, of which the lower triangle of tiles is
-// computed and mirrored: C = c0 P Q^T - diag I; c0 P Q^T + c1 Q; + c2 P; + c2 R.  APPLY: X' =
-// c0 P X + c1 X; LAST: the same into the result.
-enum { ORTH_SYM0 = 0, ORTH_SYM1 = 1, ORTH_SYM2 = 2, ORTH_SYM3 = 3, ORTH_APPLY = 4, ORTH_LAST = 5 };
-constexpr bool orth_sym(int op) { return op <= ORTH_SYM3; }
+// What a product is for.  GRAM and POLY: a symmetric one, of which the lower triangle of tiles
+// is computed and mirrored: C = c0 P P^T - diag I, and c0 P P^T + c1 P.  APPLY: X' = c0 P X +
+// c1 X; LAST: the same into the result.
+enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_APPLY = 2, ORTH_LAST = 3 };
+constexpr bool orth_sym(int op) { return op <= ORTH_POLY; }
 
 struct OrthArgs {
   int mp, lp;             // padded sizes, multiples of 64
-  int K;                  // the contraction: rows of P (and Q) are K long
+  int K;                  // the contraction: rows of P are K long
   int m, l, rows, cols;
   const f16* p;           // [n, mp, K]
-  const f16* q;           // symmetric: [n, mp, K]; else X hi [n, mp, lp]
-  const f16* side;        // P or R of SYM2 and SYM3 [n, mp, mp]
-  float c0, c1, c2, diag;
-  f16 r1, r2;             // c1 / c0 and SYM2's c2 / c0, which the scales make fp16 numbers
+  const f16* q;           // symmetric: P; else X hi [n, mp, lp]
+  float c0, c1, diag;
+  f16 r1;                 // c1 / c0, which the scales make an fp16 number
   const float* factor;    // per matrix, stored X -> X, in every X (the first products); null: 1
   f16* c;                 // symmetric: C [n, mp, mp]
   const uint8_t* xlo;     // X lo, or null
@@ -340,7 +342,7 @@ struct JOrth {
   static constexpr bool SYM = orth_sym(OP);
   static constexpr bool A_KMAJ = true, B_KMAJ = SYM;
   static constexpr bool DYN = false, TRANS = !TALL, EPI_LDS = true, NSPLIT = false, SIDE = false;
-  static constexpr bool DIAG = OP != ORTH_SYM0;
+  static constexpr bool DIAG = OP != ORTH_GRAM;
   OrthArgs a;
   int n, tm, tn;   // matrices; tiles along the rows and columns of a product
   __device__ __forceinline__ static int ncol(int wn, int ni) { return wn * WCOLS + ni * 32; }
@@ -440,12 +442,11 @@ struct JOrth {
       }
     __builtin_amdgcn_sched_group_barrier(MFMA, MI * NI, 0);
   }
-  // c1 Q (of which X is one) and SYM2's c2 P are part of the products: the tile's own block of
-  // Q passes through LDS as the K steps of the tile's rows, where a fragment of r1 I multiplies
-  // it (Q is symmetric or X), the block of P at those of its columns.  r1 = c1 / c0 is fp16 and
-  // the sums are fp32, so nothing is rounded that an addition in the epilogue would not round.
-  // Read and added there, the blocks cost 8% of a product with X at K = 768 (433 and 405 us,
-  // 128 of 768 x 2048) and 3% at 1536, 6% of one with a Q, 20% of one with P and Q.
+  // c1 Q (P itself, or X) is part of the product: the tile's own block of Q passes through LDS
+  // as the K steps of the tile's rows, where a fragment of r1 I multiplies it (P is symmetric).
+  // r1 = c1 / c0 is fp16 and the sums are fp32, so nothing is rounded that an addition in the
+  // epilogue would not round.  Read and added there, the block costs 8% of a product with X at
+  // K = 768 (433 and 405 us, 128 of 768 x 2048) and 3% at 1536, 6% of a symmetric one.
   __device__ __forceinline__ static f16x8 scaled_identity(f16 r, int half, int lane) {   // 16 of 32 rows
     const int at = (lane & 31) - 16 * half - 8 * (lane >> 5);
     f16x8 v;
@@ -455,7 +456,6 @@ struct JOrth {
   }
   __device__ __forceinline__ void diagonal(const bf16_t* st, const Tile& p, int kc, Acc& acc, int lane, const WaveRows& w,
                                            int wn) const {
-    const bf16_t* As = st;
     const bf16_t* Bs = st + A_ELEMS;
     const int k0 = kc * BK;
 #pragma unroll
@@ -475,19 +475,6 @@ struct JOrth {
         }
       }
     }
-    if (OP == ORTH_SYM2 && k0 == p.j0 + wn * WCOLS) {
-      static_assert(WCOLS == BK, "a wave's columns are one K step");
-      int ln = lane;
-      asm volatile("" : "+v"(ln));
-#pragma unroll
-      for (int kk = 0; kk < BK / 16; ++kk) {
-        const f16x8 e = scaled_identity(a.r2, kk & 1, ln);
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
-          acc[mi][kk >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(e, as_f16(frag_kmaj(As, w.base + mi * 32, kk, ln)),
-                                                                    acc[mi][kk >> 1], 0, 0, 0);
-      }
-    }
   }
   __device__ __forceinline__ void epilogue(const Tile& p, const Acc& acc, float* stage) const {
     const int tid = threadIdx.x, wv = tid >> 6, wm = (int)((unsigned)wv % WM), wn = (int)((unsigned)wv / WM);
@@ -496,8 +483,8 @@ struct JOrth {
     if constexpr (TALL) out_tall(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
     else out_rows(p, acc, wreg, p.i0 + wm * WROWS, p.j0 + wn * WCOLS);
   }
-  // C^T accumulators: lane l holds row l % 32 of each band.  What the products do not hold (R,
-  // X lo) is loaded in that layout two bands ahead; finished bands leave through the wave's LDS
+  // C^T accumulators: lane l holds row l % 32 of each band.  What the products do not hold
+  // (X lo) is loaded in that layout two bands ahead; finished bands leave through the wave's LDS
   // region as whole row segments, and those of an off-diagonal tile of a symmetric product once
   // more as columns.
   __device__ __forceinline__ void out_rows(const Tile& p, const Acc& acc, bf16_t* wreg, int i0, int j0) const {
@@ -505,21 +492,16 @@ struct JOrth {
     const size_t xo = (size_t)p.z * a.mp * a.lp, so = (size_t)p.z * a.mp * a.mp;
     const int ld = SYM ? a.mp : a.lp;
     constexpr int AHEAD = 2;
-    i32x4 xl[AHEAD][NI], xr[AHEAD][NI][2];
+    i32x4 xl[AHEAD][NI];
     auto fetch = [&](int mi) {
       const size_t row = (size_t)min(i0 + mi * 32 + (lane & 31), a.mp - 1) * ld + j0;
 #pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        if constexpr (OP == ORTH_SYM3) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            xr[mi % AHEAD][ni][s] = *reinterpret_cast<const i32x4*>(a.side + so + row + ni * 32 + 16 * s + 8 * (lane >> 5));
-        }
-        if constexpr (LO) xl[mi % AHEAD][ni] = *reinterpret_cast<const i32x4*>(a.xlo + xo + row + ni * 32 + 16 * (lane >> 5));
-      }
+      for (int ni = 0; ni < NI; ++ni) xl[mi % AHEAD][ni] = *reinterpret_cast<const i32x4*>(a.xlo + xo + row + ni * 32 + 16 * (lane >> 5));
     };
-    fetch(0);
-    fetch(1);
+    if constexpr (LO) {
+      fetch(0);
+      fetch(1);
+    }
     const float c0 = SYM ? a.c0 * p.f * p.f : a.c0 * p.f, c1 = a.c1 * p.f;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
@@ -527,13 +509,12 @@ struct JOrth {
       if (rb >= p.i0 + p.cnt) {
         // the bands already on their way: a load that is never waited for here would be waited
         // for where its registers are next written, in the K loop
+        if constexpr (LO) {
 #pragma unroll
-        for (int k = 0; k < AHEAD && mi + k < MI; ++k)
+          for (int k = 0; k < AHEAD && mi + k < MI; ++k)
 #pragma unroll
-          for (int ni = 0; ni < NI; ++ni) {
-            if constexpr (OP == ORTH_SYM3) asm volatile("" ::"v"(xr[(mi + k) % AHEAD][ni][0]), "v"(xr[(mi + k) % AHEAD][ni][1]));
-            if constexpr (LO) asm volatile("" ::"v"(xl[(mi + k) % AHEAD][ni]));
-          }
+            for (int ni = 0; ni < NI; ++ni) asm volatile("" ::"v"(xl[(mi + k) % AHEAD][ni]));
+        }
         break;
       }
       i32x4 ch[NI][2], codes[NI];
@@ -542,16 +523,10 @@ struct JOrth {
         float v[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = acc[mi][ni][r] * c0;
-        if constexpr (OP == ORTH_SYM0) {
+        if constexpr (OP == ORTH_GRAM) {
 #pragma unroll
           for (int r = 0; r < 16; ++r)
             if (rb + (lane & 31) == j0 + ni * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= a.diag;
-        }
-        if constexpr (OP == ORTH_SYM3) {
-          float u[16];
-          untrans_chunks_f16(xr[mi % AHEAD][ni], u);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] += u[r] * a.c2;
         }
         if constexpr (LO) {
           float u[16] = {};
@@ -573,7 +548,7 @@ struct JOrth {
           codes[ni] = trans_codes(v);
         }
       }
-      if (mi + AHEAD < MI) fetch(mi + AHEAD);
+      if (LO && mi + AHEAD < MI) fetch(mi + AHEAD);
       if (OP == ORTH_APPLY && a.xnlo) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
@@ -806,29 +781,21 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     if (i0 + ib + mi * 32 >= a.mp) break;
     const size_t at = (size_t)i * ldn + j;
     float v[16];
-    auto side = [&](const f16* from, float (&u)[16]) {
-      i32x4 ch[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) ch[s] = *reinterpret_cast<const i32x4*>(from + at + 16 * s + 8 * (lane >> 5));
-      untrans_chunks_f16(ch, u);
-    };
-    if constexpr (OP == ORTH_SYM0) {
+    if constexpr (OP == ORTH_GRAM) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         v[r] = acc[mi][r] * c0;
         if (i == j + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= a.diag;
       }
     } else {
-      side(a.q + (SYM ? so : xo), v);
+      i32x4 ch[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        ch[s] = *reinterpret_cast<const i32x4*>(a.q + (SYM ? so : xo) + at + 16 * s + 8 * (lane >> 5));
+      untrans_chunks_f16(ch, v);
       if (!SYM && a.xlo) add_codes(*reinterpret_cast<const i32x4*>(a.xlo + xo + at + 16 * (lane >> 5)), v);
 #pragma unroll
       for (int r = 0; r < 16; ++r) v[r] = acc[mi][r] * c0 + v[r] * c1;
-      if constexpr (OP == ORTH_SYM2) {
-        float u[16];
-        side(a.side + so, u);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] += u[r] * a.c2;
-      }
     }
     if constexpr (OP == ORTH_LAST) {
       bf16_t* const out = a.out + (size_t)z * a.rows * a.cols;
@@ -945,12 +912,6 @@ static void orth_product(const char* name, const OrthArgs& a, int n, hipStream_t
   }
   orth_stream<OP>(name, a, n, st);
 }
-// SYM3 differs from SYM2 in the streamed kernel only
-template <>
-void orth_product<ORTH_SYM3>(const char* name, const OrthArgs& a, int n, hipStream_t st) {
-  if (orth_tile_kind(true, n, a.mp, a.mp, a.K) == TILE_256) orth_stream<ORTH_SYM3>(name, a, n, st);
-  else orth_product<ORTH_SYM2>(name, a, n, st);
-}
 // ---- small matrices: the whole iteration in one workgroup ----
 // X [MP, lp] (at most SMALL_ELEMS) stays in one CU: as fp32 in the accumulator layout of its
 // eight waves (so no iterate is rounded but for the products), and as fp16 in LDS beside D and
@@ -1032,31 +993,28 @@ __device__ __forceinline__ void small_put(f16* dst, int ld, const float (&v)[16]
 
 // ---- few rows: a step's square matrices in one workgroup ----
 // With m at most 128 a matrix's squares fit in one CU's LDS, so one launch makes A of X, passed
-// through a ring of K steps that serves as both factors, and of it B; or, for the first two
-// steps as one, all of R, B_0, S, A_1, B_1 and P.  That is 2 launches a step in place of 3, and
-// 1 in place of 6 for the merged ones.  What is left is the K steps of a lone CU (0.2 us a step of
-// 64 rows, 0.4 of 128, most of it LDS reads) and 4 to 6 us a launch.  A by the lower triangle alone, a wave a
-// 16-deep slice of K (a third of the LDS reads, but shares to join), was slower up to K =
-// 4096 at 128 rows, and faster past 2048 at 64.
+// through a ring of K steps that serves as both factors, and of it B: 2 launches a step in place
+// of 3.  What is left is the K steps of a lone CU (0.2 us a step of 64 rows, 0.4 of 128, most of
+// it LDS reads) and 4 to 6 us a launch.  A by the lower triangle alone, a wave a 16-deep slice of
+// K (a third of the LDS reads, but shares to join), was slower up to K = 4096 at 128 rows, and
+// faster past 2048 at 64.
 struct SquareArgs {
   const f16* x;          // [n, MP, K]
   int K;
   const float* factor;   // per matrix, stored X -> X; null: 1
   float c0, diag;        // D = c0 X X^T - diag I
-  float sq, lin;         // B = sq D^2 + lin D, and B_1 of A_1
-  float s, a0, as, ar;   // S = s B_0 R;  A_1 = a0 B_0 S + as S + ar R
-  float p0, p1;          // P = p0 B_1 B_0 + p1 (B_0 + B_1)
-  f16* out;              // B or P [n, MP, MP]
+  float sq, lin;         // B = sq D^2 + lin D
+  f16* out;              // B [n, MP, MP]
 };
-template <int MP, bool MERGED>
+template <int MP>
 __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
   constexpr int NS = 4, OPER = MP * BK, LP = OPER * 2 / 1024 / NW;   // 1 KB loads a wave and K step
   static_assert(LP * NW * 512 == OPER && LP * (NS - 2) < 64, "wave loads divide among the waves");
   constexpr int LDM = MP + 8, RB = MP / 32, BLOCKS = RB * RB;
   constexpr int SB = BLOCKS > NW ? BLOCKS / NW : 1;       // 32 x 32 blocks a wave
   constexpr int SPLIT = BLOCKS < NW ? NW / BLOCKS : 1;    // waves that share a block's K steps
-  constexpr int MAT = MP * LDM, SHARES = BLOCKS * 1024 * 2 * (SPLIT - 1);   // fp32, behind the matrices
-  constexpr int ELEMS = NS * OPER > 4 * MAT + SHARES ? NS * OPER : 4 * MAT + SHARES;
+  constexpr int MAT = MP * LDM, SHARES = BLOCKS * 1024 * 2 * (SPLIT - 1);   // fp32, behind D
+  constexpr int ELEMS = NS * OPER > MAT + SHARES ? NS * OPER : MAT + SHARES;
   __shared__ __attribute__((aligned(16))) f16 lds[ELEMS];
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), w = wv % BLOCKS, part = wv / BLOCKS;
   const int bi = w % RB * 32, bj0 = w / RB * 32;
@@ -1104,9 +1062,9 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
 #pragma unroll
       for (int b = 0; b < SB; ++b) acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[b][k], pf[k], acc[b], 0, 0, 0);
   }
-  __syncthreads();   // the ring's space is the matrices' from here on
+  __syncthreads();   // the ring's space is D's from here on
   if constexpr (SPLIT > 1) {
-    float* const share = reinterpret_cast<float*>(lds + 4 * MAT) + w * 1024 + lane;
+    float* const share = reinterpret_cast<float*>(lds + MAT) + w * 1024 + lane;
     static_assert(SPLIT == 2, "one share a block");
     if (part == 1) {
 #pragma unroll
@@ -1118,64 +1076,44 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
       for (int r = 0; r < 16; ++r) acc[0][r] += share[r * 64];
     }
   }
+  // blocks in this wave's layout: lane l holds row bi + l % 32, columns 8 q + 4 (l / 32) .. + 3 of
+  // each
   const bool on = part == 0;
-  // dst (the next matrix, or the result) = c acc + c1 S1 + c2 S2, blocks in this wave's layout:
-  // lane l holds row bi + l % 32, columns 8 q + 4 (l / 32) .. + 3 of each block
-  auto finish = [&](f16* dst, float c, float diag, const f16* s1, float c1, const f16* s2, float c2) {
-    if (!on) return;
+  f16* const d = lds;
+  const float f = a.factor ? a.factor[z] : 1.f, c0 = a.c0 * f * f;
+  if (on) {
 #pragma unroll
     for (int b = 0; b < SB; ++b) {
       const int bj = bj0 + b * BSTEP;
       float v[16];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) v[r] = acc[b][r] * c;
-      if (diag != 0.f && bi == bj) {
+      for (int r = 0; r < 16; ++r) v[r] = acc[b][r] * c0;
+      if (bi == bj) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if ((lane & 31) == 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= diag;
+          if ((lane & 31) == 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) v[r] -= a.diag;
       }
-      auto add = [&](const f16* side, float k) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f16x4 u = *reinterpret_cast<const f16x4*>(side + (bi + (lane & 31)) * LDM + bj + 8 * q + 4 * (lane >> 5));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * q + e] += (float)u[e] * k;
-        }
-      };
-      if (s1) add(s1, c1);
-      if (s2) add(s2, c2);
-      if (dst) {
-        small_put(dst + bi * LDM + bj, LDM, v, lane);
-      } else {
-        i32x4 ch[2];
-        trans_chunks_f16(v, ch);
-        f16* const o = a.out + (z * MP + bi + (lane & 31)) * MP + bj + 8 * (lane >> 5);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<i32x4*>(o + 16 * h) = ch[h];
-      }
+      small_put(d + bi * LDM + bj, LDM, v, lane);
     }
-  };
-  auto product = [&](const f16* p, const f16* q) {
-    __syncthreads();
-    if (on) small_blocks<SB>(p + bi * LDM, LDM, q + bj0 * LDM, LDM, BSTEP, MP, lane, acc);
-  };
-  f16 *const d = lds, *const b0 = lds + MAT, *const sm = lds + 2 * MAT, *const a1 = lds + 3 * MAT;
-  const float f = a.factor ? a.factor[z] : 1.f;
-  finish(d, a.c0 * f * f, a.diag, nullptr, 0.f, nullptr, 0.f);
-  product(d, d);
-  if constexpr (!MERGED) {
-    finish(nullptr, a.sq, 0.f, d, a.lin, nullptr, 0.f);
-  } else {
-    f16* const b1 = d;
-    finish(b0, a.sq, 0.f, d, a.lin, nullptr, 0.f);
-    product(b0, d);
-    finish(sm, a.s, 0.f, nullptr, 0.f, nullptr, 0.f);
-    product(b0, sm);
-    finish(a1, a.a0, 0.f, sm, a.as, d, a.ar);
-    product(a1, a1);   // its barrier also ends the reads of d, whose place B_1 takes
-    finish(b1, a.sq, 0.f, a1, a.lin, nullptr, 0.f);
-    product(b1, b0);
-    finish(nullptr, a.p0, 0.f, b0, a.p1, b1, a.p1);
+  }
+  __syncthreads();
+  if (!on) return;
+  small_blocks<SB>(d + bi * LDM, LDM, d + bj0 * LDM, LDM, BSTEP, MP, lane, acc);
+#pragma unroll
+  for (int b = 0; b < SB; ++b) {
+    const int bj = bj0 + b * BSTEP;
+    float v[16];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f16x4 u = *reinterpret_cast<const f16x4*>(d + (bi + (lane & 31)) * LDM + bj + 8 * q + 4 * (lane >> 5));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * q + e] = acc[b][4 * q + e] * a.sq + (float)u[e] * a.lin;
+    }
+    i32x4 ch[2];
+    trans_chunks_f16(v, ch);
+    f16* const o = a.out + (z * MP + bi + (lane & 31)) * MP + bj + 8 * (lane >> 5);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<i32x4*>(o + 16 * h) = ch[h];
   }
 }
 
@@ -1363,42 +1301,28 @@ inline int pad64(int v) { return (v + 63) & ~63; }
 
 }  // namespace
 
-// The first two steps as one: with R = A of the first step and B_i = b A_i + c A_i^2 of both,
-//   A_1 = (a I + B_0) R (a I + B_0) = a^2 R + 2a S + B_0 S,  S = B_0 R  (all commute),
-//   X_2 = (a^2 I + P) X_0,  P = a B_0 + a B_1 + B_1 B_0,
-// three symmetric m^3 products in place of X_1 (its product, its A, and its rounding: no lo of
-// it is kept either).  It pays where matrices are long: 128 of 768 x 2048 bf16 take 4.1 ms step
-// by step and 3.7 merged; at 1 : 1 the two are alike.  Merging further pairs in this way
-// costs precision (A_3 out of A_2 has its rounding multiplied by up to a^2: 3 to 4e-3 in all).
-static bool merge_pays(int n, int mp, int lp) {
-  double gram, apply, sym;
-  orth_tile_kind(true, n, mp, mp, lp, &gram);
-  orth_tile_kind(false, n, mp, lp, mp, &apply);
-  orth_tile_kind(true, n, mp, mp, mp, &sym);
-  return gram + apply > 3.0 * sym;
-}
-
-// Scratch: norm shares and factors, then X (two iterates, hi and lo), and the square matrices:
-// D and B of a step, or R, B_0, S, A_1 and B_1 of two merged ones, whose P takes S's place
 // Whether a step's squares are made by k_orth_square (mp <= 128).  A lone workgroup takes
 // 0.2 or 0.42 us a K step, so the products by tiles win where K is long and matrices are few:
-// whole updates, squares in one launch / by tiles, 5 of 64 x 1024 48 / 79 us, 100 of them 74 /
-// 105, 1 of 64 x 4096 86 / 124, 2 of 128 x 512 56 / 75, 1 of 128 x 1500 81 / 87, 1 of 128 x 2048
-// 91 / 92, 128 of 128 x 4096 538 / 644, 300 of 128 x 600 234 / 246, 1 of 96 x 4096 156 / 121.
-// Estimated time of a step's squares, in us, with two workgroups a CU for 64 rows and one for
-// 128; the factor is what the merged steps (1 launch for 6) add.
+// whole updates of five steps, squares in one launch / by tiles, 5 of 64 x 1024 51 / 64 us, 100
+// of them 89 / 105, 1 of 64 x 4096 93 / 112, 400 of 64 x 1024 212 / 228, 2 of 128 x 512 57 / 61,
+// 1 of 128 x 1500 89 / 81, 16 of 128 x 768 77 / 68, 128 of 96 x 1024 163 / 174, 300 of 128 x 600
+// 271 / 266, 520 of them 436 / 473, 1 of 96 x 4096 166 / 125; 128 of 128 x 4096, 687 / 729, is on
+// the wrong side.  Estimated time of a step's squares, in us, with two workgroups a CU for 64
+// rows and one for 128; the factor is the launch that the tiles need more.
 static bool square_pays(int n, int mp, int lp) {
   if (mp > 128) return false;
   double gram, poly;
   orth_tile_kind(true, n, mp, mp, lp, &gram);
   orth_tile_kind(true, n, mp, mp, mp, &poly);
   const double k = lp / 64.0, rounds = ceil(n / ((mp == 64 ? 2.0 : 1.0) * num_cus()));
-  return rounds * (mp == 64 ? 4.0 + 0.20 * k : 6.0 + 0.42 * k) <= 1.4 * (gram + poly);
+  return rounds * (mp == 64 ? 4.0 + 0.20 * k : 6.0 + 0.42 * k) <= 1.15 * (gram + poly);
 }
+// Scratch: norm shares and factors, then X (two iterates, hi and lo), and the square matrices, D
+// and B of a step
 struct OrthLayout {
   int m, l, mp, lp, chunks;
-  bool square, merge;   // k_orth_square; the first two steps as one
-  size_t off_part, off_factor, off_x[2], off_lo[2], off_s[5], bytes;
+  bool square;   // k_orth_square, whose D stays in LDS
+  size_t off_part, off_factor, off_x[2], off_lo[2], off_s[2], bytes;
 };
 static OrthLayout orth_layout(const moe_orth_shape& s) {
   OrthLayout L{};
@@ -1424,8 +1348,7 @@ static OrthLayout orth_layout(const moe_orth_shape& s) {
     L.off_lo[i] = take(xb / 2);
   }
   L.square = square_pays(s.n, L.mp, L.lp);
-  L.merge = s.steps >= 2 && (L.square || merge_pays(s.n, L.mp, L.lp));
-  for (int i = 0; i < (L.square ? 1 : L.merge ? 5 : 2); ++i) L.off_s[i] = take(db);
+  for (int i = 0; i < (L.square ? 1 : 2); ++i) L.off_s[i] = take(db);
   L.bytes = off;
   return L;
 }
@@ -1465,34 +1388,30 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   else orth_enter(s, L, (const float*)g, ws, st);
   f16* const x[2] = {reinterpret_cast<f16*>(ws + L.off_x[0]), reinterpret_cast<f16*>(ws + L.off_x[1])};
   uint8_t* const xlo[2] = {reinterpret_cast<uint8_t*>(ws + L.off_lo[0]), reinterpret_cast<uint8_t*>(ws + L.off_lo[1])};
-  f16* sq[5];
-  for (int i = 0; i < 5; ++i) sq[i] = reinterpret_cast<f16*>(ws + L.off_s[i]);
+  f16* const sq[2] = {reinterpret_cast<f16*>(ws + L.off_s[0]), reinterpret_cast<f16*>(ws + L.off_s[1])};
   OrthArgs base{};
   base.mp = L.mp; base.lp = L.lp; base.m = L.m; base.l = L.l; base.rows = s.rows; base.cols = s.cols;
   base.out = (bf16_t*)o;
   const float* factor = reinterpret_cast<const float*>(ws + L.off_factor);
   int cur = 0;                              // X's buffer
   bool has_lo = s.dtype == MOE_F32;
-  int los = L.merge ? LO_STEPS - 1 : LO_STEPS;   // iterates still to be kept with their lo
-  // C = c0 P Q^T + c1 Q + c2 side - diag I, side P or another
-  auto sym = [&](const char* name, const f16* p, const f16* q, int K, f16* c, float c0, float diag, const float* f,
-                 float c1 = 0.f, const f16* side = nullptr, float c2 = 0.f) {
-    OrthArgs a = base;
-    a.p = p; a.q = q; a.K = K; a.c = c; a.c0 = c0; a.diag = diag; a.c1 = c1; a.side = side; a.c2 = c2;
-    a.r1 = (f16)(c1 / c0);
-    a.r2 = (f16)(c2 / c0);
-    a.factor = f;
-    if (side && side == p) orth_product<ORTH_SYM2>(name, a, s.n, st);
-    else if (side) orth_product<ORTH_SYM3>(name, a, s.n, st);
-    else if (c1 != 0.f) orth_product<ORTH_SYM1>(name, a, s.n, st);
-    else orth_product<ORTH_SYM0>(name, a, s.n, st);
-  };
+  int los = LO_STEPS;                       // iterates still to be kept with their lo
   // D = A - t I of the current X, and B = beta D + c D^2
   auto gram = [&](f16* d, float ds, float t, const float* f) {
-    sym("orth_gram", x[cur], x[cur], L.lp, d, f ? ds : ds / (X_SCALE * X_SCALE), t * ds, f);
+    OrthArgs a = base;
+    a.p = a.q = x[cur]; a.K = L.lp; a.c = d;
+    a.c0 = f ? ds : ds / (X_SCALE * X_SCALE);
+    a.diag = t * ds;
+    a.factor = f;
+    orth_product<ORTH_GRAM>("orth_gram", a, s.n, st);
   };
-  auto poly = [&](f16* d, float ds, f16* b, float bs, float beta) {
-    sym("orth_poly", d, d, L.mp, b, NS_C * bs / (ds * ds), 0.f, nullptr, beta * bs / ds);
+  auto poly = [&](const f16* d, float ds, f16* b, float bs, float beta) {
+    OrthArgs a = base;
+    a.p = a.q = d; a.K = L.mp; a.c = b;
+    a.c0 = NS_C * bs / (ds * ds);
+    a.c1 = beta * bs / ds;
+    a.r1 = (f16)(a.c1 / a.c0);
+    orth_product<ORTH_POLY>("orth_poly", a, s.n, st);
   };
   // X <- alpha X + P X (P at p_scale); the last one into the result
   auto apply = [&](const f16* p, float p_scale, float alpha, const float* f, bool last) {
@@ -1511,55 +1430,27 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
     else orth_product<ORTH_APPLY>("orth_apply", a, s.n, st);
     cur ^= 1;
   };
-  auto square = [&](SquareArgs& a, bool merged, float ds, float bs, float beta, const float* f) {
-    a.x = x[cur]; a.K = L.lp; a.factor = f; a.out = sq[0];
+  auto square = [&](f16* b, float ds, float t, float bs, float beta, const float* f) {
+    SquareArgs a{};
+    a.x = x[cur]; a.K = L.lp; a.factor = f; a.out = b;
     a.c0 = f ? ds : ds / (X_SCALE * X_SCALE);
+    a.diag = t * ds;
     a.sq = NS_C * bs / (ds * ds);
     a.lin = beta * bs / ds;
     const dim3 grid((unsigned)s.n), block(NTHR);
-#define CALL(MP)                                                                               \
-  if (merged) MOE_LAUNCH("orth_square2", (k_orth_square<MP, true>), grid, block, 0, st, a);    \
-  else MOE_LAUNCH("orth_square", (k_orth_square<MP, false>), grid, block, 0, st, a)
     if (L.mp == 64) {
-      CALL(64);
+      MOE_LAUNCH("orth_square", k_orth_square<64>, grid, block, 0, st, a);
     } else {
-      CALL(128);
+      MOE_LAUNCH("orth_square", k_orth_square<128>, grid, block, 0, st, a);
     }
-#undef CALL
   };
-  int step = 0;
-  if (L.merge && L.square) {
-    const float ds = fit_scale(NS_B / NS_C, D_SCALE), bs = fit_scale(NS_A, 0.5f * B_SCALE);
-    const float ps = fit_scale(NS_A * NS_A, P_SCALE);
-    SquareArgs a{};
-    a.s = S_SCALE / (bs * ds);
-    a.a0 = ds / (bs * S_SCALE); a.as = 2.f * NS_A * ds / S_SCALE; a.ar = NS_A * NS_A;
-    a.p0 = ps / (bs * bs); a.p1 = NS_A * ps / bs;
-    square(a, true, ds, bs, NS_B, factor);
-    apply(sq[0], ps, NS_A * NS_A, factor, s.steps == 2);
-    step = 2;
-  } else if (L.merge) {
-    f16 *r = sq[0], *b0 = sq[1], *sp = sq[2], *a1 = sq[3], *b1 = sq[4];
-    const float ds = fit_scale(NS_B / NS_C, D_SCALE), bs = fit_scale(NS_A, 0.5f * B_SCALE);   // 2 a bs is fp16, too
-    const float ps = fit_scale(NS_A * NS_A, P_SCALE);
-    gram(r, ds, 0.f, factor);
-    poly(r, ds, b0, bs, NS_B);
-    sym("orth_s", b0, r, L.mp, sp, S_SCALE / (bs * ds), 0.f, nullptr);
-    sym("orth_a1", b0, sp, L.mp, a1, ds / (bs * S_SCALE), 0.f, nullptr, 2.f * NS_A * ds / S_SCALE, r, NS_A * NS_A);
-    poly(a1, ds, b1, bs, NS_B);
-    sym("orth_p", b1, b0, L.mp, sp, ps / (bs * bs), 0.f, nullptr, NS_A * ps / bs, b1, NS_A * ps / bs);
-    apply(sp, ps, NS_A * NS_A, factor, s.steps == 2);
-    step = 2;
-  }
-  for (; step < s.steps; ++step) {
+  for (int step = 0; step < s.steps; ++step) {
     const StepCoef co = step_coef(step);
     const float* f = step == 0 ? factor : nullptr;
     const float ds = fit_scale(co.beta / NS_C, D_SCALE), bs = fit_scale(co.alpha, B_SCALE);
     f16* const b = L.square ? sq[0] : sq[1];
     if (L.square) {
-      SquareArgs a{};
-      a.diag = co.t * ds;
-      square(a, false, ds, bs, co.beta, f);
+      square(b, ds, co.t, bs, co.beta, f);
     } else {
       gram(sq[0], ds, co.t, f);
       poly(sq[0], ds, b, bs, co.beta);

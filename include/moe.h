@@ -338,9 +338,12 @@ int moe_orth_scratch_bytes(const moe_orth_shape* shape, size_t* scratch_bytes);
  *   o = scale X, transposed back
  * g: [n, rows, cols] of shape.dtype; o: [n, rows, cols] bf16, which may be g when that is
  * bf16.  Inside, X and the products' factors are fp16 (the first iterates with a byte
- * more) and the sums fp32; the result is within about 2e-3 of its norm, besides o's
- * rounding, for five steps.  Directions far below a matrix's largest are multiplied by 3.4 a
- * step, g's own rounding errors with them.  A zero matrix gives zeros; one with a NaN or infinity gives
+ * more) and the sums fp32.  For five steps the result is within 2e-3 of its norm, besides o's
+ * rounding, where the singular values spread evenly or as a power law; gradients of few
+ * tokens (rank 1 to 64, a few rows or columns far above the rest) cost 1 to 3e-3 as a rule
+ * and up to 5e-3, in fp32, which enters in 15 bits, up to 8e-3; a sixth step doubles these.
+ * Directions far below a matrix's largest are multiplied by 3.4 a step, g's own rounding
+ * errors with them.  A zero matrix gives zeros; one with a NaN or infinity gives
  * NaN, and leaves the others alone.  scale must be finite.  Needs scratch. */
 int moe_orthogonalize(const moe_orth_shape* shape, const void* g, void* o, float scale, void* scratch, void* stream);
 

@@ -90,11 +90,14 @@ def orthogonalize(g, steps, scale=1.0):
     return scale * (x.T if tall else x)
 
 
-def orthogonalize_rounded(g, steps, merged=False):
+def orthogonalize_rounded(g, steps, merged=False, fp32=False):
     """The same with the iterates held in fp16: the first two as pairs hi + lo, lo in E4M3
     times 16 (hi in the products, both in a X), A - I in place of A from the fourth step on,
-    scales 2^15 (X) and 2^14; merged: the first two steps as one, in the square matrices.
-    What this is off is what such a precision costs."""
+    scales 2^15 (X) and 2^14.  fp32: g, too, enters as such a pair (bf16 values are fp16
+    numbers times a power of two).  What this is off is what such a precision costs.  merged:
+    the first two steps as one, in the square matrices, which saves products but costs more
+    on matrices of a few strong rows (up to 2e-2, where step by step stays below 5e-3); the
+    kernels go step by step."""
     def half(v, s):
         return (v * s).astype(np.float16).astype(np.float64) / s
 
@@ -110,6 +113,8 @@ def orthogonalize_rounded(g, steps, merged=False):
     if tall:
         x = x.T
     hi, first, los = x, 0, 2
+    if fp32:
+        hi, x = pair(x)
     if merged:
         r = half(hi @ hi.T, 2.0 ** 14)
         b0 = half(b * r + c * (r @ r), 2.0 ** 14)
