@@ -9,7 +9,8 @@
 //
 // Precision.  The products run on fp16 MFMAs with fp32 sums; fp16 has three more bits than
 // bf16 at the same rate, and the bounds above fix scales that keep it in range:
-//   X * 2^15 (<= 39400), A * 2^14 (<= 23700), (b A + c A^2) * 2^14 (<= 46000).
+//   X * 2^15 (<= 39400; times a power of two for each matrix whose norm is next to eps or below,
+//   so that its iterates, as small, keep their bits), A * 2^14 (<= 23700), (b A + c A^2) * 2^14 (<= 46000).
 // An early rounding is what hurts: a singular value far below the largest is multiplied by
 // a = 3.4 a step, and so is the rounding noise that lands beside it.  So
 // * the step's a X is added to the fp32 sums by itself (with a I inside the fp16 factor, the
@@ -98,6 +99,16 @@ __device__ __forceinline__ double wave_sum_f64(double a) {
   return a;
 }
 
+// Norms next to eps or below make iterates as small, X_i <= |X_0| a^i: stored times 2^-s besides
+// their usual scale, s <= 0 with 2^-s |X_0| grow in [1/2, 1) (grow = a^(steps - 1)), they stay in
+// range and keep their bits.  0 for all other norms.
+__device__ __forceinline__ int small_shift(double norm, double grow) {
+  const double most = norm / (norm + NS_EPS) * grow;
+  int s = 0;
+  if (most > 0.0 && most < 1.0) frexp(most, &s);
+  return s;
+}
+
 // sums of squares of chunk blockIdx.x of matrix blockIdx.y, in fp64: neither a gradient of
 // 1e-30 nor one of 1e30 leaves the range
 template <typename T>
@@ -122,12 +133,13 @@ __global__ __launch_bounds__(256) void k_orth_sumsq(const T* __restrict__ g, int
 
 // X0 (hi, and lo for fp32 input) [m_p, l_p] of each matrix, padded with zeros, from g
 // [rows, cols] (transposed when rows > cols) times 2^e, where 2^e brings the norm into
-// [2^14, 2^15); factor[matrix] = 2^-e / (norm + eps) turns stored values into X0.  One
-// workgroup makes 64 rows by `tiles` tiles of 64 columns.
+// [2^14, 2^15).  factor [3, n]: f0 = 2^-e / (norm + eps) turns stored values into X0, fi =
+// 2^(s - 15) the later iterates' into X, and fx = f0 / fi those of X0 into those (s: small_shift).
+// One workgroup makes 64 rows by `tiles` tiles of 64 columns.
 template <typename T, bool TR>
 __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int rows, int cols,
-                                                    const double* __restrict__ part, int chunks, int mp, int lp,
-                                                    int tiles, f16* __restrict__ hi, uint8_t* __restrict__ lo,
+                                                    const double* __restrict__ part, int chunks, double grow,
+                                                    int mp, int lp, int tiles, f16* __restrict__ hi, uint8_t* __restrict__ lo,
                                                     float* __restrict__ factor) {
   __shared__ float tile[TR ? 64 : 1][65];
   static_assert(NORM_CHUNKS <= 64, "one lane a share");
@@ -138,8 +150,13 @@ __global__ __launch_bounds__(256) void k_orth_enter(const T* __restrict__ g, int
     frexp(norm, &e);   // norm = f 2^e, f in [1/2, 1)
     e = X_LOG2 - e;
   }
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-    factor[blockIdx.z] = (float)(ldexp(1.0, -e) / (norm + NS_EPS));
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    const double f = ldexp(1.0, -e) / (norm + NS_EPS);
+    const int s = small_shift(norm, grow);
+    factor[blockIdx.z] = (float)f;
+    factor[gridDim.z + blockIdx.z] = (float)ldexp(f, X_LOG2 - s);
+    factor[2 * gridDim.z + blockIdx.z] = (float)ldexp(1.0, s - X_LOG2);
+  }
   const int tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;   // rows tr, tr + 32; 8 columns
   const int r0 = blockIdx.y * 64;   // of X
   const T* p = g + (size_t)blockIdx.z * rows * cols;
@@ -197,7 +214,7 @@ struct OrthArgs {
   const f16* q;           // symmetric: P; else X hi [n, mp, lp]
   float c0, c1, diag;
   f16 r1;                 // c1 / c0, which the scales make an fp16 number
-  const float* factor;    // per matrix, stored X -> X, in every X (the first products); null: 1
+  const float* factor;    // per matrix, times c0 and c1 (symmetric: its square times c0); null: 1
   f16* c;                 // symmetric: C [n, mp, mp]
   const uint8_t* xlo;     // X lo, or null
   f16* xn;                // X'
@@ -313,7 +330,7 @@ __device__ __forceinline__ void band_columns(const bf16_t* wreg, F&& store) {
 struct OrthTile {
   int z, i0, j0, nk;
   int cnt, ncols;   // rows and columns of the product in the tile
-  float f;          // stored X -> X
+  float f;          // the matrix's factor
 };
 
 struct OrthLd {
@@ -1001,7 +1018,7 @@ __device__ __forceinline__ void small_put(f16* dst, int ld, const float (&v)[16]
 struct SquareArgs {
   const f16* x;          // [n, MP, K]
   int K;
-  const float* factor;   // per matrix, stored X -> X; null: 1
+  const float* factor;   // per matrix, stored X -> X
   float c0, diag;        // D = c0 X X^T - diag I
   float sq, lin;         // B = sq D^2 + lin D
   f16* out;              // B [n, MP, MP]
@@ -1080,7 +1097,7 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
   // each
   const bool on = part == 0;
   f16* const d = lds;
-  const float f = a.factor ? a.factor[z] : 1.f, c0 = a.c0 * f * f;
+  const float f = a.factor[z], c0 = a.c0 * f * f;
   if (on) {
 #pragma unroll
     for (int b = 0; b < SB; ++b) {
@@ -1124,7 +1141,7 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_square(SquareArgs a) {
 // where 64 x 128 took 12.2).
 template <typename T, int MP, int XB, bool TALL>
 __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out, int rows, int cols, int lp,
-                                                        int steps, float scale) {
+                                                        int steps, double grow, float scale) {
   __shared__ __attribute__((aligned(16))) f16 small[small_lds(MP)];
   __shared__ double red[NW];
   constexpr int LDM = MP + 8, RB = MP / 32;
@@ -1174,11 +1191,15 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
     frexp(norm, &e);
     e = -e;
   }
-  const float f = (float)(ldexp(1.0, -e) / (norm + NS_EPS));   // through 2^e: no factor leaves fp32's range
+  // X 2^(15 - sh), as in LDS (sh: small norms, as in k_orth_enter); through 2^e: no factor leaves
+  // fp32's range
+  const int sh = small_shift(norm, grow);
+  const float f = (float)ldexp(1.0 / (norm + NS_EPS), X_LOG2 - sh - e);
+  const float dscale = ldexpf(D_SCALE, 2 * (sh - X_LOG2));
 #pragma unroll
   for (int b = 0; b < XB; ++b)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) x[b][r] = ldexpf(x[b][r], e) * (f * X_SCALE);   // X 2^15, as in LDS
+    for (int r = 0; r < 16; ++r) x[b][r] = ldexpf(x[b][r], e) * f;
   for (int step = 0; step < steps; ++step) {
     const StepCoef co = step_coef(step);
 #pragma unroll
@@ -1207,7 +1228,7 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
         const int bj = bj0 + b * (NW / RB) * 32;
         float v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = acc[b][r] * (D_SCALE / (X_SCALE * X_SCALE));
+        for (int r = 0; r < 16; ++r) v[r] = acc[b][r] * dscale;
         if (bi == bj) {
 #pragma unroll
           for (int r = 0; r < 16; ++r)
@@ -1250,7 +1271,7 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
     }
     __syncthreads();   // xs, ds and bs have been read
   }
-  scale *= 1.f / X_SCALE;
+  scale *= ldexpf(1.f, sh - X_LOG2);
 #pragma unroll
   for (int b = 0; b < XB; ++b) {
     const int blk = wv + NW * b, i = g_row(blk), j0 = g_col(blk);
@@ -1272,14 +1293,18 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_small(const T* g, bf16_t* out,
   }
 }
 
+// what the last stored iterate is of X_0 at most
+inline double growth(int steps) { return pow((double)NS_A, steps - 1); }
+
 inline bool orth_small(int mp, int lp) { return mp <= SMALL_MP && mp * lp <= SMALL_ELEMS; }
 
 template <typename T, int MP, bool TALL>
 static hipError_t launch_small(const moe_orth_shape& s, const T* g, bf16_t* o, int lp, float scale, hipStream_t st) {
   const dim3 grid((unsigned)s.n), block(NTHR);
   const int blocks = (int)ceil_div(MP / 32 * (lp / 32), NW);
+  const double grow = growth(s.steps);
 #define CALL(XB) \
-  MOE_LAUNCH("orth_small", (k_orth_small<T, MP, XB, TALL>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, scale)
+  MOE_LAUNCH("orth_small", (k_orth_small<T, MP, XB, TALL>), grid, block, 0, st, g, o, s.rows, s.cols, lp, s.steps, grow, scale)
   if (blocks == 1) CALL(1);
   else if (blocks == 2) CALL(2);
   else CALL(4);
@@ -1342,7 +1367,7 @@ static OrthLayout orth_layout(const moe_orth_shape& s) {
   const size_t xb = (size_t)s.n * L.mp * L.lp * 2, db = (size_t)s.n * L.mp * L.mp * 2;
   if (orth_small(L.mp, L.lp)) return L;   // no scratch
   L.off_part = take((size_t)s.n * L.chunks * 8);
-  L.off_factor = take((size_t)s.n * 4);
+  L.off_factor = take((size_t)s.n * 4 * 3);
   for (int i = 0; i < 2; ++i) {
     L.off_x[i] = take(xb);
     L.off_lo[i] = take(xb / 2);
@@ -1364,17 +1389,18 @@ static void orth_enter(const moe_orth_shape& s, const OrthLayout& L, const T* g,
   uint8_t* lo = s.dtype == MOE_F32 ? reinterpret_cast<uint8_t*>(ws + L.off_lo[0]) : nullptr;
   MOE_LAUNCH("orth_sumsq", k_orth_sumsq<T>, dim3((unsigned)L.chunks, (unsigned)s.n), dim3(256), 0, st, g, count, chunk,
              part);
+  const double grow = growth(s.steps);
   // up to 8 tiles a workgroup (the norm's shares are read once for them) where that leaves
   // 4096 workgroups
   const int64_t all = (int64_t)s.n * (L.lp / 64) * (L.mp / 64);
   const int tiles = (int)(all < 4096 ? 1 : all > 8 * 4096 ? 8 : all / 4096);
   const dim3 grid((unsigned)ceil_div(L.lp / 64, tiles), (unsigned)(L.mp / 64), (unsigned)s.n);
   if (s.rows > s.cols)
-    MOE_LAUNCH("orth_enter", (k_orth_enter<T, true>), grid, dim3(256), 0, st, g, s.rows, s.cols, part, L.chunks, L.mp,
-               L.lp, tiles, hi, lo, factor);
+    MOE_LAUNCH("orth_enter", (k_orth_enter<T, true>), grid, dim3(256), 0, st, g, s.rows, s.cols, part, L.chunks, grow,
+               L.mp, L.lp, tiles, hi, lo, factor);
   else
-    MOE_LAUNCH("orth_enter", (k_orth_enter<T, false>), grid, dim3(256), 0, st, g, s.rows, s.cols, part, L.chunks, L.mp,
-               L.lp, tiles, hi, lo, factor);
+    MOE_LAUNCH("orth_enter", (k_orth_enter<T, false>), grid, dim3(256), 0, st, g, s.rows, s.cols, part, L.chunks, grow,
+               L.mp, L.lp, tiles, hi, lo, factor);
 }
 
 hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o, float scale, void* scratch,
@@ -1392,7 +1418,7 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   OrthArgs base{};
   base.mp = L.mp; base.lp = L.lp; base.m = L.m; base.l = L.l; base.rows = s.rows; base.cols = s.cols;
   base.out = (bf16_t*)o;
-  const float* factor = reinterpret_cast<const float*>(ws + L.off_factor);
+  const float *f0 = reinterpret_cast<const float*>(ws + L.off_factor), *fx = f0 + s.n, *fi = fx + s.n;
   int cur = 0;                              // X's buffer
   bool has_lo = s.dtype == MOE_F32;
   int los = LO_STEPS;                       // iterates still to be kept with their lo
@@ -1400,7 +1426,7 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   auto gram = [&](f16* d, float ds, float t, const float* f) {
     OrthArgs a = base;
     a.p = a.q = x[cur]; a.K = L.lp; a.c = d;
-    a.c0 = f ? ds : ds / (X_SCALE * X_SCALE);
+    a.c0 = ds;
     a.diag = t * ds;
     a.factor = f;
     orth_product<ORTH_GRAM>("orth_gram", a, s.n, st);
@@ -1416,7 +1442,7 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   // X <- alpha X + P X (P at p_scale); the last one into the result
   auto apply = [&](const f16* p, float p_scale, float alpha, const float* f, bool last) {
     OrthArgs a = base;
-    const float out = (last ? scale : X_SCALE) * (f ? 1.f : 1.f / X_SCALE);
+    const float out = last ? scale : 1.f;
     a.p = p; a.q = x[cur]; a.K = L.mp;
     a.c0 = out / p_scale;
     a.c1 = out * alpha;
@@ -1433,7 +1459,7 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   auto square = [&](f16* b, float ds, float t, float bs, float beta, const float* f) {
     SquareArgs a{};
     a.x = x[cur]; a.K = L.lp; a.factor = f; a.out = b;
-    a.c0 = f ? ds : ds / (X_SCALE * X_SCALE);
+    a.c0 = ds;
     a.diag = t * ds;
     a.sq = NS_C * bs / (ds * ds);
     a.lin = beta * bs / ds;
@@ -1446,7 +1472,8 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
   };
   for (int step = 0; step < s.steps; ++step) {
     const StepCoef co = step_coef(step);
-    const float* f = step == 0 ? factor : nullptr;
+    const bool last = step == s.steps - 1;
+    const float* const f = step == 0 ? f0 : fi;   // the stored X -> X
     const float ds = fit_scale(co.beta / NS_C, D_SCALE), bs = fit_scale(co.alpha, B_SCALE);
     f16* const b = L.square ? sq[0] : sq[1];
     if (L.square) {
@@ -1455,7 +1482,7 @@ hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o,
       gram(sq[0], ds, co.t, f);
       poly(sq[0], ds, b, bs, co.beta);
     }
-    apply(b, bs, co.alpha, f, step == s.steps - 1);
+    apply(b, bs, co.alpha, last ? f : step == 0 ? fx : nullptr, last);
   }
   return hipGetLastError();
 }

@@ -342,6 +342,7 @@ int moe_orth_scratch_bytes(const moe_orth_shape* shape, size_t* scratch_bytes);
  * rounding, where the singular values spread evenly or as a power law; gradients of few
  * tokens (rank 1 to 64, a few rows or columns far above the rest) cost 1 to 3e-3 as a rule
  * and up to 5e-3, in fp32, which enters in 15 bits, up to 8e-3; a sixth step doubles these.
+ * All that holds at any norm, also far below the 1e-7.
  * Directions far below a matrix's largest are multiplied by 3.4 a step, g's own rounding
  * errors with them.  A zero matrix gives zeros; one with a NaN or infinity gives
  * NaN, and leaves the others alone.  scale must be finite.  Needs scratch. */

@@ -93,7 +93,8 @@ def orthogonalize(g, steps, scale=1.0):
 def orthogonalize_rounded(g, steps, merged=False, fp32=False):
     """The same with the iterates held in fp16: the first two as pairs hi + lo, lo in E4M3
     times 16 (hi in the products, both in a X), A - I in place of A from the fourth step on,
-    scales 2^15 (X) and 2^14.  fp32: g, too, enters as such a pair (bf16 values are fp16
+    scales 2^15 (X; times 2^s where the norm is so far below 1e-7 that the iterates stay below
+    2^-s) and 2^14.  fp32: g, too, enters as such a pair (bf16 values are fp16
     numbers times a power of two).  What this is off is what such a precision costs.  merged:
     the first two steps as one, in the square matrices, which saves products but costs more
     on matrices of a few strong rows (up to 2e-2, where step by step stays below 5e-3); the
@@ -102,19 +103,24 @@ def orthogonalize_rounded(g, steps, merged=False, fp32=False):
         return (v * s).astype(np.float16).astype(np.float64) / s
 
     def pair(v):
-        hi = half(v, 2.0 ** 15)
-        lo = mx.e4m3_decode(mx.e4m3_encode((v - hi) * 2.0 ** 19)) / 2.0 ** 19
+        hi = half(v, more * 2.0 ** 15)
+        lo = mx.e4m3_decode(mx.e4m3_encode((v - hi) * (more * 2.0 ** 19))) / (more * 2.0 ** 19)
         return hi, hi + lo
 
     a, b, c = NS
     x = np.asarray(g, np.float64)
-    x = x / (np.sqrt((x * x).sum()) + 1e-7)
+    norm = np.sqrt((x * x).sum())
+    hi = x
+    if fp32 and norm > 0:   # as it enters, its norm in [2^14, 2^15)
+        more = 2.0 ** -np.frexp(norm)[1]
+        hi, x = pair(x)
+    hi, x = hi / (norm + 1e-7), x / (norm + 1e-7)
+    most = norm / (norm + 1e-7) * a ** (steps - 1)
+    more = 2.0 ** max(0, -np.frexp(most)[1]) if most > 0 else 1.0
     tall = x.shape[0] > x.shape[1]
     if tall:
-        x = x.T
-    hi, first, los = x, 0, 2
-    if fp32:
-        hi, x = pair(x)
+        hi, x = hi.T, x.T
+    first, los = 0, 2
     if merged:
         r = half(hi @ hi.T, 2.0 ** 14)
         b0 = half(b * r + c * (r @ r), 2.0 ** 14)
@@ -135,5 +141,5 @@ def orthogonalize_rounded(g, steps, merged=False, fp32=False):
             if i - first < los - (1 if merged else 0):
                 hi, x = pair(x)
             else:
-                hi = x = half(x, 2.0 ** 15)
+                hi = x = half(x, more * 2.0 ** 15)
     return x.T if tall else x

@@ -44,6 +44,18 @@ def test_precision_of_few_tokens(m, l, kind, fp32):
         assert _off(ot.orthogonalize_rounded(g, steps, fp32=fp32), ot.orthogonalize(g, steps)) < (8e-3 if fp32 else 5e-3), steps
 
 
+@pytest.mark.parametrize("size", [1e-7, 1e-9, 1e-12, 1e-15, 1e-18, 1e-24, 1e-30])
+@pytest.mark.parametrize("m,l,steps", [(100, 200, 5), (200, 100, 3), (60, 90, 6)])
+def test_precision_of_small_norms(m, l, steps, size):
+    """Far below the 1e-7 in the divisor the iterates are as small, X_i = a^i X_0, and each
+    rounding is one to fp16, 2^-12 of a value at most; five stored iterates stay
+    below 5 * 2^-12 = 1.3e-3, and next to 1e-7 below the 2e-3 of ordinary norms."""
+    g = few_tokens(m, l, m // 3, 0, 0, 1, 0.1, 1, dt=torch.float32).double().numpy()
+    g *= size / np.linalg.norm(g)
+    assert _off(ot.orthogonalize_rounded(g, steps), ot.orthogonalize(g, steps)) < 2e-3
+    assert _off(ot.orthogonalize_rounded(g, steps, fp32=True), ot.orthogonalize(g, steps)) < 2e-3
+
+
 # in one CU; squares in one launch a step; small tiles; a tall one; the largest tiles, padded with
 # other matrices to the number that takes them there
 @pytest.mark.gpu
@@ -79,3 +91,25 @@ def test_orth_does_not_depend_on_the_others():
         g[n // 2] = a
         o = Orthogonalizer(n, 384, 1024).update(g.cuda())
         assert _off(o[n // 2].double().cpu().numpy(), want) < tol, n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols,n", [(96, 70, 8), (64, 1024, 8), (192, 500, 8), (500, 192, 8), (320, 600, 64)])
+@pytest.mark.parametrize("steps", [1, 2, 5])
+def test_orth_of_small_norms(rows, cols, n, steps, dt):
+    """Matrices of norms from 1e-6 to 1e-30 side by side."""
+    from combine_top_router_amd import Orthogonalizer
+    import combine_top_router_amd.lib as L
+    sizes = [1e-6, 1e-7, 1e-9, 1e-12, 1e-15, 1e-18, 1e-24, 1e-30]
+    g = torch.randn(n, rows, cols, generator=torch.Generator().manual_seed(steps)).to(dt)
+    for i, size in enumerate(sizes):
+        a = few_tokens(rows, cols, min(rows, cols) // 3, 0, 0, 1, 0.1, i, dt=torch.float64)
+        g[i] = (a * (size / a.norm())).to(dt)
+    op = Orthogonalizer(n, rows, cols, dtype=L.MOE_BF16 if dt == torch.bfloat16 else L.MOE_F32, steps=steps)
+    o = op.update(g.cuda()).double().cpu().numpy()
+    for i, size in enumerate(sizes):
+        a = g[i].double().numpy()
+        want = ot.orthogonalize(a, steps)
+        tol = 2.0 ** -8 + 2 ** 0.5 * _off(ot.orthogonalize_rounded(a, steps, fp32=dt == torch.float32), want)
+        assert np.isfinite(o[i]).all() and _off(o[i], want) < tol, size
