@@ -219,8 +219,12 @@ class MoeLayer:
     (activation checkpointing: the backward recomputes the gate/up GEMM).  With ``fuse_gather`` the token rows are
     read from x through row_src inside the GEMMs instead of a gathered copy xp.
 
-    ``balance`` gives the load-balance loss of the last forward's routing; the backward then
-    adds its gradient to d_logits.  ``orthogonalize`` turns the last backward's weight
+    The shares of an expert-parallel layer see the same T tokens and all E logits; y, dx and
+    d_logits of a share are its part of a sum over the shares.
+
+    ``balance`` gives the load-balance loss of the last forward's routing, whole on every share
+    (not to be summed over them); the backward then adds its gradient to d_logits, on the share
+    that holds expert 0 alone, so that the sum counts it once.  ``orthogonalize`` turns the last backward's weight
     gradients into orthogonalised updates.  Both allocate their buffers on first use.
     """
 
@@ -328,7 +332,8 @@ class MoeLayer:
         return dict(self._updates)
 
     def backward(self, dy, stream=None, d_balance=None):
-        """``d_balance`` [1]: the upstream gradient of ``balance``'s loss (None: 1)."""
+        """``d_balance`` [1]: the upstream gradient of ``balance``'s loss (None: 1), the same on
+        every share."""
         s = self.shape
         self._check(dy, (s.T, s.H), self.dtype, "dy")
         if d_balance is not None and not self._balanced:
@@ -340,7 +345,7 @@ class MoeLayer:
                   _p(self.dw_gate), _p(self.dw_up), _p(self.dw_down), _p(self.d_topk_w), _p(self.scratch), h)
         L.moe_route_topk_bwd(s, _p(logits), _p(self.topk_idx), _p(self.topk_w), _p(self.d_topk_w),
                              _p(self.d_logits), h)
-        if self._balanced:
+        if self._balanced and s.e_begin == 0:
             self._balance.backward(d_balance, d_logits_in=self.d_logits, out=self.d_logits, stream=stream)
         return {"dx": self.dx, "dw_gate": self.dw_gate, "dw_up": self.dw_up, "dw_down": self.dw_down,
                 "d_topk_w": self.d_topk_w, "d_logits": self.d_logits}

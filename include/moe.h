@@ -278,7 +278,9 @@ int moe_balance_fwd(const moe_shape* shape, const float* logits, const int32_t* 
  * with c = counts and N = counts[E] as moe_balance_fwd wrote them, and the second term 0
  * for tokens that do not count.  d_loss: device fp32 [1], the loss's upstream gradient;
  * NULL is 1.  d_logits_in may be NULL (taken as 0) or equal to d_logits: what
- * moe_route_topk_bwd wrote, so that d_logits goes on to moe_router_bwd whole. */
+ * moe_route_topk_bwd wrote, so that d_logits goes on to moe_router_bwd whole.  What that
+ * wrote on one share of an expert-parallel layer is its part of a sum over the shares: this
+ * gradient, of the whole loss, is added on one of them (MoeLayer: the one of expert 0). */
 int moe_balance_bwd(const moe_shape* shape, const float* logits, const int32_t* counts, const uint8_t* mask,
                     float coef, const float* d_loss, const float* d_logits_in, float* d_logits, void* stream);
 
