@@ -336,8 +336,10 @@ class MoeLayer:
         every share."""
         s = self.shape
         self._check(dy, (s.T, s.H), self.dtype, "dy")
-        if d_balance is not None and not self._balanced:
-            raise RuntimeError("d_balance without a balance loss in this pass")
+        if d_balance is not None:
+            if not self._balanced:
+                raise RuntimeError("d_balance without a balance loss in this pass")
+            self._check(d_balance, (1,), torch.float32, "d_balance")
         logits, x, w_gate, w_up, w_down = self.inputs
         h = stream_handle(stream)
         L.moe_bwd(s, _p(dy), _p(x), _p(self.xp), _p(self.offsets), _p(self.row_src), _p(self.row_of),

@@ -43,3 +43,17 @@ def test_the_loss_counts_once_over_the_shares(bounds, d_balance):
     # the kernel's fp32 gradient (softmax and counts, a few 2^-24 of the largest each) and one rounded
     # sum with the routing's: well below 1e-5 of the largest
     assert np.abs(total - want).max() <= 1e-5 * np.abs(want).max()
+
+
+def test_a_wrong_d_balance_is_refused_before_any_launch():
+    from combine_top_router_amd import MoeLayer
+    logits, x, wg, wu, wd, dy = _inputs()
+    lay = MoeLayer(T, H, I, E, K)
+    lay.forward(logits, x, wg, wu, wd)
+    lay.balance(COEF)
+    lay.dx.fill_(3.0)
+    for bad in (torch.ones(2, device="cuda"), torch.ones(1), torch.ones(1, device="cuda", dtype=torch.float64)):
+        with pytest.raises(ValueError):
+            lay.backward(dy, d_balance=bad)
+    torch.cuda.synchronize()
+    assert (lay.dx == 3).all()
