@@ -260,6 +260,7 @@ class MoeLayer:
         self.inputs = None
         self._balance, self._balanced = None, False
         self._orth, self._updates = {}, {}
+        self._has_grads = False
 
     def _check(self, t, shape, dtype, name):
         if t.device != self.device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
@@ -313,7 +314,10 @@ class MoeLayer:
         return None if self._balance is None else self._balance.counts
 
     def orthogonalize(self, steps=5, scale=1.0, stream=None):
-        """Orthogonalised updates (bf16) of the last backward's dw_gate, dw_up and dw_down."""
+        """Orthogonalised updates (bf16) of the last backward's dw_gate, dw_up and dw_down, in
+        buffers that the next call overwrites."""
+        if not self._has_grads:
+            raise RuntimeError("orthogonalize without a backward")
         s, code = self.shape, self.shape.dtype
 
         # before the operators, whose calls on another stream wait for what was queued before them
@@ -345,6 +349,7 @@ class MoeLayer:
         L.moe_bwd(s, _p(dy), _p(x), _p(self.xp), _p(self.offsets), _p(self.row_src), _p(self.row_of),
                   _p(self.topk_w), _p(w_gate), _p(w_up), _p(w_down), _p(self.saved), _p(self.dx),
                   _p(self.dw_gate), _p(self.dw_up), _p(self.dw_down), _p(self.d_topk_w), _p(self.scratch), h)
+        self._has_grads = True
         L.moe_route_topk_bwd(s, _p(logits), _p(self.topk_idx), _p(self.topk_w), _p(self.d_topk_w),
                              _p(self.d_logits), h)
         if self._balanced and s.e_begin == 0:
