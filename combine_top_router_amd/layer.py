@@ -27,9 +27,11 @@ def _device(device) -> torch.device:
 
 # the raw handle of a device's current stream, without the Stream object that
 # torch.cuda.current_stream builds around it (2 us of a call of 8), and the current device
-# without the check that CUDA is initialised (an operator's buffers have done that)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# without the check that CUDA is initialised (an operator's buffers have done that); a torch
+# that lacks them, as one built without a GPU does, has the public ones
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
 class _OnDevice:
