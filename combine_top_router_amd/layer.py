@@ -187,9 +187,13 @@ class BalanceLoss(_OnDevice):
 
 class Orthogonalizer(_OnDevice):
     """Orthogonalised updates of n weight matrices of one size (the experts' gradients, or
-    their momentum), by Newton-Schulz steps as in the Muon optimiser."""
+    their momentum), by Newton-Schulz steps as in the Muon optimiser.
 
-    def __init__(self, n, rows, cols, dtype=L.MOE_BF16, steps=5, device="cuda"):
+    ``scratch``: uint8 memory of at least ``moe_orth_scratch_bytes``, such as that of another
+    Orthogonalizer whose calls are ordered with this one's; by default it makes its own (about
+    three times a bf16 g, and 4 m^2 bytes a matrix of shorter side m)."""
+
+    def __init__(self, n, rows, cols, dtype=L.MOE_BF16, steps=5, device="cuda", scratch=None):
         self.shape = L.MoeOrthShape(n, rows, cols, dtype, steps)
         scratch_b = L.moe_orth_scratch_bytes(self.shape)
         self._place(device)
@@ -197,7 +201,14 @@ class Orthogonalizer(_OnDevice):
         self.dtype = _DT[dtype]
         self._size = torch.Size((n, rows, cols))
         self.o = None
-        self.scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
+        if scratch is None:
+            scratch = torch.empty(scratch_b, dtype=torch.uint8, device=dev)
+        else:
+            self._check(scratch, scratch.shape, torch.uint8, "scratch")
+            if scratch.numel() < scratch_b or scratch.data_ptr() % 256:
+                raise ValueError(f"scratch: expected {scratch_b} bytes at a multiple of 256, got {scratch.numel()} "
+                                 f"at {scratch.data_ptr():#x}")
+        self.scratch = scratch
         self._allocated()
 
     def update(self, g, scale=1.0, out=None, stream=None):
@@ -329,8 +340,10 @@ class MoeLayer:
 
         def op(rows, cols):
             key = (rows, cols, steps)
-            if key not in self._orth:
-                self._orth[key] = Orthogonalizer(s.e_local, rows, cols, code, steps, self.device)
+            if key not in self._orth:   # they run in turn: one scratch, as far as it suffices
+                need = L.moe_orth_scratch_bytes(L.MoeOrthShape(s.e_local, rows, cols, code, steps))
+                have = [o.scratch for o in self._orth.values() if o.scratch.numel() >= need]
+                self._orth[key] = Orthogonalizer(s.e_local, rows, cols, code, steps, self.device, *have[:1])
             return self._orth[key]
 
         for n, g in (("gate", self.dw_gate), ("up", self.dw_up), ("down", self.dw_down)):
