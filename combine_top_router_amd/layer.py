@@ -52,10 +52,12 @@ class _OnDevice:
         if self._index is None:
             return
         with torch.cuda.device(self._index):
+            if torch.cuda.is_current_stream_capturing():
+                return   # a graph's memory pool is its own, and an event inside a capture is no other stream's
             home = torch.cuda.current_stream()
-            self._ordered = {home.cuda_stream}
-            # a graph's memory pool is its own, and an event inside a capture is no other stream's
-            self._birth = None if torch.cuda.is_current_stream_capturing() else home.record_event()
+            if self._birth is not None and home.cuda_stream not in self._ordered:
+                home.wait_event(self._birth)   # the new event stands for the buffers before, too
+            self._birth, self._ordered = home.record_event(), {home.cuda_stream}
 
     def _order(self, handle, stream):
         """`stream` (None: the current one), of that handle, has not been used with the buffers."""

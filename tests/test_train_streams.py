@@ -29,20 +29,25 @@ class _Nothing:
         return False
 
 
-@pytest.mark.parametrize("capturing", [False, True])
-def test_the_first_call_on_another_stream_waits(monkeypatch, capturing):
+def _operator(monkeypatch, state):
     from combine_top_router_amd import layer
-    log = []
-    home, side = _Fake(1, log), _Fake(2, log)
-    state = {"capturing": False}
-    monkeypatch.setattr(layer.torch.cuda, "current_stream", lambda *a: home)
+    monkeypatch.setattr(layer.torch.cuda, "current_stream", lambda *a: state["current"])
     monkeypatch.setattr(layer.torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
     monkeypatch.setattr(layer.torch.cuda, "device", _Nothing)
     monkeypatch.setattr(layer.torch.cuda, "stream", _Nothing)
-    monkeypatch.setattr(layer, "_raw_stream", lambda i: home.cuda_stream)
+    monkeypatch.setattr(layer, "_raw_stream", lambda i: state["current"].cuda_stream)
     monkeypatch.setattr(layer, "_current_device", lambda: 0)
     op = layer._OnDevice()
     op.device, op._index = torch.device("cuda", 0), 0
+    return op
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_the_first_call_on_another_stream_waits(monkeypatch, capturing):
+    log = []
+    home, side = _Fake(1, log), _Fake(2, log)
+    state = {"capturing": False, "current": home}
+    op = _operator(monkeypatch, state)
     op._allocated()
     call = lambda stream: op._call(lambda s: log.append(("launch", s)), stream)  # noqa: E731
     call(None)
@@ -54,6 +59,23 @@ def test_the_first_call_on_another_stream_waits(monkeypatch, capturing):
     state["capturing"] = False
     call(side)
     assert log[-2:] == [("wait", 2, ("event", 1)) if capturing else ("launch", 2), ("launch", 2)]
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_buffers_made_on_two_streams(monkeypatch, capturing):
+    """A later buffer of another stream: what runs there, and elsewhere, waits for both."""
+    log = []
+    one, two, three = (_Fake(i, log) for i in (1, 2, 3))
+    state = {"capturing": False, "current": one}
+    op = _operator(monkeypatch, state)
+    op._allocated()
+    state.update(current=two, capturing=capturing)
+    op._allocated()
+    later = [] if capturing else [("wait", 2, ("event", 1)), ("record", 2)]
+    assert log == [("record", 1)] + later
+    state["capturing"] = False
+    op._call(lambda s: log.append(("launch", s)), three)
+    assert log[-2:] == [("wait", 3, ("event", 1 if capturing else 2)), ("launch", 3)]
 
 
 # ---- on the GPU: the blocks that the operators get are ones that the current stream has freed
