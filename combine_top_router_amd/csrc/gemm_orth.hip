@@ -34,7 +34,7 @@
 //
 // Cost.  A step is 3 m^2 l + m^3 multiply-adds (A and A^2 by halves), which binds from a few
 // matrices of some hundred rows on; below, launches and latencies do.  Measured on one MI355X,
-// five steps, bf16, one call after another: 128 of 2048 x 768 3.72 ms, 16 of 1536 x 4096 3.28
+// five steps, bf16, one call after another: 128 of 2048 x 768 3.65 ms, 16 of 1536 x 4096 3.22
 // (2.6 PFLOP of such work each, 2.4 ms at the 1.08 PFLOP/s of a large library fp16 product;
 // both run at the clock that their power leaves).  Of the former 0.23 read g twice and write X
 // (5.1 TB/s).
@@ -382,8 +382,8 @@ struct JOrth {
     p.f = a.factor ? sload(a.factor + p.z) : 1.f;
   }
   // A diagonal tile's waves that lie above the diagonal: mirrored from those below it, which
-  // leaves out two of eight (all of them computed: 3503 and 3060 us for the two batches above,
-  // 3423 and 3042 so)
+  // leaves out two of eight (all of them computed: 3740 and 3200 us for the two batches above,
+  // 3650 and 3220 so)
   __device__ __forceinline__ static bool above(const Tile& p, int wm, int wn) {
     return SYM && p.i0 == p.j0 && wn * WCOLS >= (wm + 1) * WROWS;
   }
@@ -425,8 +425,8 @@ struct JOrth {
     const bf16_t* Bs = st + A_ELEMS;
     // Each k-step's fragments are read while the step before multiplies, one read after one
     // product: the compiler's own order read a step's fragments together and waited, 2% of the
-    // whole update at 128 x 2048 x 768 and at 16 x 1536 x 4096 (3739 and 3062 us; 3677 and
-    // 2995 so). Raising the wave's priority around the products cost 2 to 4%.
+    // whole update at 128 x 2048 x 768 (3730 us, 3650 so) and up to 1% at 16 x 1536 x 4096. Raising
+    // the wave's priority around the products cost 2 to 4%.
     bf16x8 af[2][MI], bf[2][NI];
     auto frags = [&](int kk) {
 #pragma unroll
@@ -652,8 +652,8 @@ __global__ __launch_bounds__(NTHR, 1) void k_orth_stream(OrthArgs a, int n, int 
 // each other's waits.  A step of a lone workgroup is LDS reads, the issue of the loads and the
 // products in turn (0.24 us for 64 rows, the same when its data are in the nearest cache, with
 // half the bytes on 32 rows, or with eight stages; three and five stages cost a division).
-// Eight stages, one workgroup a CU, took 113 us for 5 of 333 x 1000 where four take 107, and
-// with two tiles a CU on four stages instead of two 4 of 700 x 1500 take 180 instead of 200.
+// Eight stages, one workgroup a CU, take 122 us for 5 of 333 x 1000 where four take 105, and
+// with two tiles a CU on four stages instead of two 4 of 700 x 1500 take 179 instead of 204.
 template <int TILE> struct TileCfg;
 template <> struct TileCfg<64> { static constexpr int WAVES = 4, TMI = 1; };    // 2 x 2 waves of 32 x 32
 template <> struct TileCfg<128> { static constexpr int WAVES = 8, TMI = 2; };   // 2 x 4 waves of 64 x 32
@@ -735,21 +735,14 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
     const uint32_t st = l0 + (kt % NS) * STAGE * 2;
 #pragma unroll
     for (int q = 0; q < LP; ++q) {
-      // (eight waves' loads, 128 rows, come faster spread out by dma16's other instructions: 128 of
-      // 128 x 4096 536 us, 551 without; 64 rows: 8 of 768 x 2048 323 with dma16, 313 without)
-      if constexpr (TILE == 128) {
-        dma16(la[q] + kt * BK, lds + (kt % NS) * STAGE + (q * C::WAVES + wv) * 512);
-        dma16(lb[q] + kt * bstep, lds + (kt % NS) * STAGE + OPER + (q * C::WAVES + wv) * 512);
-      } else {
-        dma16_to(la[q] + kt * BK, st + q * C::WAVES * 1024);
-        dma16_to(lb[q] + kt * bstep, st + OPER * 2 + q * C::WAVES * 1024);
-      }
+      dma16_to(la[q] + kt * BK, st + q * C::WAVES * 1024);
+      dma16_to(lb[q] + kt * bstep, st + OPER * 2 + q * C::WAVES * 1024);
     }
   };
   const int wm = wv & 1, wn = wv >> 1, ib = wm * 32 * C::TMI, jb = wn * 32;   // the wave's first row and column
   // above the diagonal: mirrored from below.  Not in the deep ring: lone workgroups have nothing
-  // to do in the time, and the branch costs more than the products (5 of 333 x 1000 117 us, 128
-  // with it; 128 of 320 x 640, in the short ring, 463 us without and 452 with)
+  // to do in the time, and the branch costs more than the products (5 of 333 x 1000 105 us, 120
+  // with it; in the short ring it saves 2% of 128 of 320 x 640)
   const bool above = SYM && NS == 2 && i0 == j0 && jb >= ib + 32 * C::TMI;
   f32x16 acc[C::TMI];
 #pragma unroll
@@ -768,7 +761,7 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
     // in the deep ring the step's fragments are asked for before a later step's loads, whose issue
-    // (16 KB at 64 a clock) then passes while they come: 1 of 1024 x 1024 142 us, 136 so; several
+    // (16 KB at 64 a clock) then passes while they come: 1 of 1024 x 1024 130 us, 125 so; several
     // workgroups on a CU fill that time themselves, and lose by the longer loop
     if (NS == 2 && kt + NS - 1 < nk) issue(kt + NS - 1);   // into the stage read one step ago
     const bf16_t* const as = lds + (kt % NS) * STAGE;
@@ -870,9 +863,9 @@ __global__ __launch_bounds__(64 * TileCfg<TILE>::WAVES, NS == 2 ? 4 : 1) void k_
 //   128 rows              4 + max(0.58 k, t (1.9 + 0.70 k))  two share a CU
 //   256 rows              5 + ceil(t) (7 + c k)              c = 1.25 on few CUs, 2.15 on all
 // Whole updates, bf16, by this rule and with 64 deep / 64 / 128 / 256 rows throughout: 11 of 362 x
-// 362 98 us and 98 / 105 / 135 / 239; 1 of 1024 x 1024 126 and 127 / 171 / 229 / 461; 4 of 700 x
-// 1500 174 and 176 / 198 / 249 / 448; 8 of 768 x 2048 290 and 343 / 313 / 321 / 523; 128 of 320 x
-// 640 404 and 454 / 412 / 444 / 528.
+// 362 93 us and 93 / 100 / 132 / 240; 1 of 1024 x 1024 125 and 125 / 171 / 226 / 465; 4 of 700 x
+// 1500 179 and 180 / 204 / 251 / 450; 8 of 768 x 2048 311 and 370 / 348 / 338 / 535; 128 of 320 x
+// 640 419 and 472 / 424 / 444 / 543.
 enum OrthTileKind { TILE_64_DEEP, TILE_64, TILE_128, TILE_256 };
 static OrthTileKind orth_tile_kind(bool sym, int n, int M, int N, int K, double* time = nullptr) {
   const double k = K / 64.0, cus = num_cus();

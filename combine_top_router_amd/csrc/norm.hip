@@ -11,10 +11,12 @@
 // EPT fp32 values in each of the threads that share it: the statistics are two passes
 // over registers (the variance about the mean itself, not E[s^2] - mu^2, which cancels),
 // and the backward keeps each thread's columns of dw and db in registers over all its rows.
-// Measured on one MI355X at 16384 x 4096 bf16 with a residual: forward 93 us for 537 MB,
-// backward 99 us for 671 MB (x, res, dy, ds_in, dx), 5.8 and 6.8 TB/s beside the 5.1 TB/s of a
-// large copy (part of each array is still in the 256 MB cache); 4096 x 2048 forward 13.4 us;
-// one row 2.5 us, a launch.
+// Measured on one MI355X, in a graph: 16384 x 4096 bf16 with a residual forward 94 us for 537 MB,
+// backward 134 us for 671 MB (x, res, dy, ds_in, dx), 5.7 and 5.0 TB/s beside the 5.1 TB/s of a
+// large copy, the same over four sets of tensors in turn; 4096 x 2048 forward 13.4 us; one row 2.5
+// us, a launch.  Rows past the registers (16384 columns) are read again for each pass: 8192 x
+// 20000 bf16 forward 181 us for 655 MB, backward 540 us for 983, of which dw and db, column by
+// column, are the larger part.
 #include "common.h"
 
 namespace moe {
@@ -544,16 +546,16 @@ inline unsigned row_grid(int64_t wgs) { return (unsigned)(wgs < (1 << 20) ? wgs 
 // Threads of a row.  One wave up to 1024 columns (8 or 16 values a thread); then a workgroup
 // of as many waves as 8 values a thread fill, to 8192 columns, and 1024 threads of 16 to
 // 16384.  More values in fewer threads, with fewer barriers, lose: 16384 x 4096 bf16 with 128
-// threads of 32 takes 109 us forward and 195 backward, with 512 of 8 95 and 136.
+// threads of 32 takes 107 us forward and 345 backward, with 512 of 8 94 and 134.
 inline int norm_threads(int H) {
   return H <= 1024 ? 256 : H > 8192 ? 1024 : (int)(ceil_div(ceil_div(H, 8), 64) * 64);
 }
 
-// Shares of dw: workgroups of the backward, or row slices of the long rows.  About four rows
-// each, as far as that leaves 256 workgroups and asks for at most 256 K threads (512
-// workgroups at least): at 16384 x 4096 bf16 with a residual, 256 threads, 256 / 512 / 1024 /
-// 2048 shares take 320 / 198 / 136 / 145 us, too few rows in flight on one side and more
-// shares than rows are worth on the other.
+// Shares of dw: workgroups of the backward, or row slices of the long rows.  One for every four
+// of the rows (groups of four up to 1024 columns) that a workgroup takes at a time, but 256 where
+// there are rows for them, and no more than 256 K threads hold, or 512: at 16384 x 4096 bf16 with
+// a residual, 512 threads, 256 / 512 / 1024 / 2048 shares take 212 / 135 / 153 / 142 us, too few
+// rows in flight on one side and more shares than rows are worth on the other.
 int norm_parts(const moe_norm_shape& s) {
   if (s.T == 0) return 0;
   const int rows = s.H <= 1024 ? 4 : 1;   // rows a workgroup holds at once
