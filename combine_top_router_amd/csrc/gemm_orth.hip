@@ -9,8 +9,9 @@
 //
 // Precision.  The products run on fp16 MFMAs with fp32 sums; fp16 has three more bits than
 // bf16 at the same rate, and the bounds above fix scales that keep it in range:
-//   X * 2^15 (<= 39400; times a power of two for each matrix whose norm is next to eps or below,
-//   so that its iterates, as small, keep their bits), A * 2^14 (<= 23700), (b A + c A^2) * 2^14 (<= 46000).
+//   X * 2^15 (<= 39400), A * 2^14 (<= 23700), (b A + c A^2) * 2^14 (<= 46000);
+// a matrix whose norm is next to eps or below, and its iterates as small, takes another power of
+// two on X, so that they keep their bits.
 // An early rounding is what hurts: a singular value far below the largest is multiplied by
 // a = 3.4 a step, and so is the rounding noise that lands beside it.  So
 // * the step's a X is added to the fp32 sums by itself (with a I inside the fp16 factor, the
@@ -29,7 +30,7 @@
 // 5e-3, most of it the rounding of b A + c A^2 where a few rows hold it all; of rank 1 in fp32,
 // which enters in 15 bits, up to 8e-3.
 // The first two steps as one, in the square matrices (A_1 = a^2 R + 2a B_0 R + B_0^2 R and so on),
-// would save 9% of the large updates below and up to a fifth of those of few rows, but its
+// would save 9% of the large updates below and up to a quarter of those of few rows, but its
 // roundings cost up to 2e-2 on such gradients.
 //
 // Cost.  A step is 3 m^2 l + m^3 multiply-adds (A and A^2 by halves), which binds from a few
