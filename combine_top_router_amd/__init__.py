@@ -7,7 +7,7 @@ been built (``python -m combine_top_router_amd.build``).  There is no fallback p
 from . import lib
 from .lib import *  # noqa: F401,F403
 
-_CLASSES = ("MoeLayer", "MoeNorm", "BalanceLoss", "Orthogonalizer")
+_CLASSES = ("MoeLayer", "MoeNorm", "BalanceLoss", "Orthogonalizer", "Gate", "Linear", "AdamW")
 __all__ = list(lib.__all__) + list(_CLASSES)
 
 

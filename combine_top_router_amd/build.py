@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 # gemm.hip is compiled twice, through gemm_fw256.hip and gemm_fw320.hip (one tile height each)
 SOURCES = ["api.hip", "route.hip", "index.hip", "gemm_fw256.hip", "gemm_fw320.hip", "gemm_f32.hip", "mx_quant.hip",
-           "router_gemm.hip", "norm.hip", "balance.hip", "gemm_orth.hip"]
+           "router_gemm.hip", "norm.hip", "balance.hip", "gemm_orth.hip",
+           "gate.hip", "linear.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,321 @@
+// One AdamW step over many tensors in one launch (per 40 tensors), moments in fp32 or 8 bits.
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+//   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+// in fp32, from the new m and v before they are rounded.
+//
+// 8 bits: m and sqrt(v) as E4M3 codes, 32 consecutive elements sharing a power of two (the
+// scale rule of mx_scale_exp).  sqrt(v) has half v's range in exponents, and its relative
+// step of 1/8 at most is what the update sees.  Rounded to nearest, a moment whose step
+// changes it by less than half a code stands still (at b2 = 0.95 every decay of v); rounded
+// stochastically it moves on average as it should.  A v above 0 keeps the smallest code at
+// least: as 0 it would leave m / eps.
+// Random bits: 32 per element, h = mix(lo(i) ^ mix(hi(i) + k)) with i the element's place
+// (moe_adamw_tensor::at), k = mix(t + mix(lo(seed) + mix(hi(seed)))) and mix the output
+// permutation of PCG (O'Neill 2014): m takes the low half, sqrt(v) the high one, and a
+// stochastically rounded bf16 parameter the low half of mix(h).
+#include "common.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int AT = 256;       // threads of a workgroup
+constexpr int VEC = 8;        // elements a thread takes at a time
+constexpr int CHUNK = AT * VEC;
+constexpr int kTensors = 40;  // tensors of a launch: their table travels with its arguments
+
+struct AdamwTable {
+  moe_adamw_tensor t[kTensors];
+  uint32_t first[kTensors];   // a tensor's first workgroup
+  int n;
+};
+static_assert(sizeof(AdamwTable) <= 3600, "the arguments of a launch hold 4 KB");
+
+struct AdamwHyper {
+  float b1, b1c, b2, b2c;     // beta and 1 - beta
+  float decay, rate, root;    // 1 - lr wd; lr / (1 - b1^t); 1 / sqrt(1 - b2^t)
+  float eps, wd;
+  float to_m;                 // 1 / (1 - b1^t)
+  uint32_t key;               // the step's random key
+  int state, stochastic;
+  const float* lr;            // device, or null
+  const float* grad_scale;    // device, or null
+  const AdamwClock* clock;    // device, or null
+};
+
+__host__ __device__ inline uint32_t mix(uint32_t v) {
+  const uint32_t s = v * 747796405u + 2891336453u;
+  const uint32_t w = ((s >> ((s >> 28) + 4)) ^ s) * 277803737u;
+  return (w >> 22) ^ w;
+}
+__host__ __device__ inline uint32_t step_key(uint64_t seed, int64_t t) {
+  return mix((uint32_t)t + mix((uint32_t)seed + mix((uint32_t)(seed >> 32))));
+}
+
+// y >= 0 (at most 448) on the grid of E4M3, up with r / 2^16 below the part that is cut off
+__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t r) {
+  const int e = max((int)(__float_as_uint(y) >> 23) - 127, -6);
+  const float n = ldexpf(y, 3 - e), low = floorf(n);
+  return ldexpf(low + ((float)r < (n - low) * 65536.f ? 1.f : 0.f), e - 3);
+}
+
+// The 8 values of a thread, 4 threads to a block of 32, as codes and the block's scale.
+// What is not finite becomes NaN and does not move the scale.
+template <bool ROOT>
+__device__ __forceinline__ void encode(const float (&x)[VEC], const uint32_t (&r)[VEC], bool stochastic, uint2& codes,
+                                       int& X) {
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const float a = fabsf(x[i]);
+    am = fmaxf(am, a < __builtin_inff() ? a : 0.f);
+  }
+  am = fmaxf(am, __shfl_xor(am, 1, 64));
+  am = fmaxf(am, __shfl_xor(am, 2, 64));
+  X = mx_scale_exp(am);
+  float y[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    float a = fabsf(x[i]);
+    const bool fin = a < __builtin_inff();
+    a = ldexpf(a, -X);
+    if (stochastic) a = e4m3_stochastic(fin ? a : 0.f, ROOT ? r[i] >> 16 : r[i] & 0xffffu);
+    if (ROOT && x[i] > 0.f && a < 0x1p-9f) a = 0x1p-9f;
+    y[i] = fin ? copysignf(a, x[i]) : __builtin_nanf("");
+  }
+  codes.x = e4m3_pack4(y[0], y[1], y[2], y[3], 0);
+  codes.y = e4m3_pack4(y[4], y[5], y[6], y[7], 0);
+}
+
+__device__ __forceinline__ void decode(uint2 c, int X, float (&x)[VEC]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int w = (int)(h ? c.y : c.x);
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    x[4 * h] = ldexpf(lo[0], X); x[4 * h + 1] = ldexpf(lo[1], X);
+    x[4 * h + 2] = ldexpf(hi[0], X); x[4 * h + 3] = ldexpf(hi[1], X);
+  }
+}
+
+// elements i .. i + 7 of a tensor of n; whole: all inside and the address at a multiple of 16
+__device__ __forceinline__ void load8(const void* p, int dtype, int64_t i, int64_t n, bool whole, float (&x)[VEC]) {
+  if (dtype == MOE_BF16) {
+    const bf16_t* q = (const bf16_t*)p + i;
+    if (whole) {
+      const i32x4 u = *reinterpret_cast<const i32x4*>(q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float((uint32_t)u[j] << 16);
+        x[2 * j + 1] = __uint_as_float((uint32_t)u[j] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[j] = i + j < n ? bf2f(q[j]) : 0.f;
+    }
+  } else {
+    const float* q = (const float*)p + i;
+    if (whole) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(q), b = *reinterpret_cast<const f32x4*>(q + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = a[j];
+        x[4 + j] = b[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[j] = i + j < n ? q[j] : 0.f;
+    }
+  }
+}
+__device__ __forceinline__ void store8_f32(float* q, int64_t left, bool whole, const float (&x)[VEC]) {
+  if (whole) {
+    *reinterpret_cast<f32x4*>(q) = f32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4*>(q + 4) = f32x4{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j < left) q[j] = x[j];
+  }
+}
+__device__ __forceinline__ void store8_bf16(bf16_t* q, int64_t left, bool whole, const uint32_t (&w)[VEC / 2]) {
+  if (whole) {
+    *reinterpret_cast<i32x4*>(q) = i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j < left) q[j] = (bf16_t)(w[j / 2] >> (16 * (j & 1)));
+  }
+}
+
+// bf16 bits of x: towards 0 after 16 random bits were added below; NaN stays, and what would
+// round past the largest number does not
+__device__ __forceinline__ uint32_t bf16_stochastic(float x, uint32_t r) {
+  const uint32_t u = __float_as_uint(x), a = u & 0x7fffffffu;
+  if (a >= 0x7f800000u) return (u >> 16) | (a > 0x7f800000u ? 0x40u : 0u);
+  const uint32_t up = (u + r) >> 16;
+  return (up & 0x7fffu) == 0x7f80u ? u >> 16 : up;
+}
+
+template <bool S8>
+__global__ __launch_bounds__(AT) void k_adamw(AdamwTable tab, AdamwHyper h) {
+  // the workgroup's tensor
+  int lo = 0, hi = tab.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab.first[mid] <= blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const moe_adamw_tensor& T = tab.t[lo];
+  const int64_t n = T.n, i = (int64_t)(blockIdx.x - tab.first[lo]) * CHUNK + (int64_t)threadIdx.x * VEC;
+  float rate = h.rate, root = h.root, decay = h.decay;
+  uint32_t key = h.key;
+  if (h.clock) {
+    rate = h.rate * h.clock->to_m;   // h.rate: the rate itself
+    root = h.clock->root;
+    key = h.clock->key;
+  }
+  if (h.lr) {
+    decay = 1.f - h.lr[0] * h.wd;
+    rate = h.lr[0] * (h.clock ? h.clock->to_m : h.to_m);
+  }
+  const float gs = h.grad_scale ? h.grad_scale[0] : 1.f;
+  const int64_t left = n - i;
+  const bool full = left >= VEC;
+  if ((i & ~(int64_t)31) >= n) return;   // a block of 32, four lanes, stays together
+  const bool p16 = ((uintptr_t)T.p & 15) == 0, g16 = ((uintptr_t)T.g & 15) == 0;
+  const void* pin = T.master ? (const void*)T.master : T.p;
+  const int pdt = T.master ? MOE_F32 : T.p_dtype;
+  const bool in16 = ((uintptr_t)pin & 15) == 0;
+  float p[VEC], g[VEC], m[VEC], v[VEC];
+  load8(T.g, T.g_dtype, i, n, full && g16, g);
+  load8(pin, pdt, i, n, full && in16, p);
+  if constexpr (S8) {
+    if (left > 0) {   // the states' room ends with a block
+      float s[VEC];
+      decode(*reinterpret_cast<const uint2*>((const uint8_t*)T.m + i), (int)T.m_scale[i >> 5] - 127, m);
+      decode(*reinterpret_cast<const uint2*>((const uint8_t*)T.v + i), (int)T.v_scale[i >> 5] - 127, s);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = s[j] * s[j];
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j >= left) m[j] = v[j] = 0.f;
+  } else {
+    load8(T.m, MOE_F32, i, n, full, m);
+    load8(T.v, MOE_F32, i, n, full, v);
+  }
+  float s[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    const float gj = g[j] * gs;
+    m[j] = h.b1 * m[j] + h.b1c * gj;
+    v[j] = h.b2 * v[j] + h.b2c * (gj * gj);
+    s[j] = sqrtf(v[j]);
+    p[j] = p[j] * decay - rate * m[j] / (s[j] * root + h.eps);
+  }
+  uint32_t r[VEC];
+  if (h.stochastic) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const uint64_t at = (uint64_t)T.at + (uint64_t)(i + j);
+      r[j] = mix((uint32_t)at ^ mix((uint32_t)(at >> 32) + key));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) r[j] = 0;
+  }
+  if constexpr (S8) {
+    uint2 cm, cv;
+    int Xm, Xv;
+    encode<false>(m, r, h.stochastic != 0, cm, Xm);
+    encode<true>(s, r, h.stochastic != 0, cv, Xv);
+    if (left > 0) {
+      *reinterpret_cast<uint2*>((uint8_t*)T.m + i) = cm;
+      *reinterpret_cast<uint2*>((uint8_t*)T.v + i) = cv;
+      if ((i & 31) == 0) {
+        T.m_scale[i >> 5] = (uint8_t)(Xm + 127);
+        T.v_scale[i >> 5] = (uint8_t)(Xv + 127);
+      }
+    }
+  } else {
+    store8_f32((float*)T.m + i, left, full, m);
+    store8_f32((float*)T.v + i, left, full, v);
+  }
+  if (T.master) store8_f32(T.master + i, left, full && in16, p);
+  if (T.p_dtype == MOE_F32) {
+    store8_f32((float*)T.p + i, left, full && p16, p);
+  } else {
+    uint32_t w[VEC / 2];
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+      if (h.stochastic && !T.master)
+        w[j] = bf16_stochastic(p[2 * j], mix(r[2 * j]) & 0xffffu) |
+               bf16_stochastic(p[2 * j + 1], mix(r[2 * j + 1]) & 0xffffu) << 16;
+      else
+        w[j] = pk_bf16(p[2 * j], p[2 * j + 1]);
+    }
+    store8_bf16((bf16_t*)T.p + i, left, full && p16, w);
+  }
+}
+
+// t + 1 and what follows from it
+__global__ void k_adamw_clock(AdamwClock* c, double b1, double b2, uint64_t seed) {
+  const int64_t t = c->t + 1;
+  c->t = t;
+  c->to_m = (float)(1.0 / (1.0 - pow(b1, (double)t)));
+  c->root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)t)));
+  c->key = step_key(seed, t);
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const moe_adamw_params& s, const moe_adamw_tensor* tensors, int count, const float* lr,
+                        const float* grad_scale, void* clock, hipStream_t st) {
+  if (clock)
+    MOE_LAUNCH("adamw_clock", k_adamw_clock, dim3(1), dim3(1), 0, st, (AdamwClock*)clock, s.beta1, s.beta2, s.seed);
+  AdamwHyper h{};
+  h.b1 = (float)s.beta1; h.b1c = (float)(1.0 - s.beta1);
+  h.b2 = (float)s.beta2; h.b2c = (float)(1.0 - s.beta2);
+  h.decay = (float)(1.0 - s.lr * s.weight_decay);
+  h.eps = (float)s.eps; h.wd = (float)s.weight_decay;
+  if (clock) {
+    h.rate = (float)s.lr;
+  } else {
+    const double to_m = 1.0 / (1.0 - pow(s.beta1, (double)s.step));
+    h.to_m = (float)to_m;
+    h.rate = (float)(s.lr * to_m);
+    h.root = (float)(1.0 / sqrt(1.0 - pow(s.beta2, (double)s.step)));
+    h.key = step_key(s.seed, s.step);
+  }
+  h.state = s.state; h.stochastic = s.stochastic;
+  h.lr = lr; h.grad_scale = grad_scale; h.clock = (const AdamwClock*)clock;
+  AdamwTable tab{};
+  int64_t wgs = 0;
+  auto go = [&]() -> hipError_t {
+    if (tab.n == 0) return hipSuccess;
+    if (s.state == MOE_STATE_8BIT)
+      MOE_LAUNCH("adamw_8bit", k_adamw<true>, dim3((unsigned)wgs), dim3(AT), 0, st, tab, h);
+    else
+      MOE_LAUNCH("adamw", k_adamw<false>, dim3((unsigned)wgs), dim3(AT), 0, st, tab, h);
+    tab.n = 0;
+    wgs = 0;
+    return hipGetLastError();
+  };
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (!t.g || t.n == 0) continue;
+    const int64_t need = ceil_div(t.n, CHUNK);
+    if (tab.n == kTensors || wgs + need > (1 << 30)) {
+      const hipError_t e = go();
+      if (e != hipSuccess) return e;
+    }
+    tab.t[tab.n] = t;
+    tab.first[tab.n] = (uint32_t)wgs;
+    ++tab.n;
+    wgs += need;
+  }
+  return go();
+}
+
+}  // namespace moe

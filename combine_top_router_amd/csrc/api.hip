@@ -832,4 +832,158 @@ int moe_orthogonalize(const moe_orth_shape* shape, const void* g, void* o, float
   return hip_status(launch_orthogonalize(*shape, g, o, scale, scratch, (hipStream_t)stream), __func__);
 }
 
+// ---- routing by scores, matrix product with an epilogue, AdamW ----
+static int check_gate(const moe_gate_shape* s) {
+  if (!s) return fail(MOE_EINVAL, "shape is NULL");
+  if (s->T < 0) return fail(MOE_EINVAL, "T = %d < 0", s->T);
+  if (s->E < 1 || s->E > 1024) return fail(MOE_EINVAL, "E = %d outside 1..1024", s->E);
+  if (s->score != MOE_SCORE_SOFTMAX && s->score != MOE_SCORE_SIGMOID) return fail(MOE_EINVAL, "score = %d", s->score);
+  if (s->groups < 1 || s->groups > 64 || s->E % s->groups != 0)
+    return fail(MOE_EINVAL, "groups = %d must be a divisor of E = %d in 1..64", s->groups, s->E);
+  if (s->topk_groups < 1 || s->topk_groups > s->groups)
+    return fail(MOE_EINVAL, "topk_groups = %d outside 1..%d", s->topk_groups, s->groups);
+  const int per = s->E / s->groups;
+  if (s->group_top < 1 || s->group_top > 2 || s->group_top > per)
+    return fail(MOE_EINVAL, "group_top = %d must be 1 or 2 and at most the %d experts of a group", s->group_top, per);
+  if (s->k < 1 || s->k > 16 || s->k > s->topk_groups * per)
+    return fail(MOE_EINVAL, "k = %d outside 1..min(%d, 16)", s->k, s->topk_groups * per);
+  if ((int64_t)s->T * s->k > 0x7fffffffLL) return fail(MOE_EINVAL, "T * k exceeds 2^31 - 1");
+  if (s->renorm != 0 && s->renorm != 1) return fail(MOE_EINVAL, "renorm = %d", s->renorm);
+  if (!isfinite(s->scale) || s->scale <= 0.f)
+    return fail(MOE_EINVAL, "scale = %g must be finite and > 0", (double)s->scale);
+  return MOE_OK;
+}
+
+int moe_gate_scratch_bytes(const moe_gate_shape* shape, size_t* scratch_bytes) {
+  REQUIRE(scratch_bytes);
+  int rc = check_gate(shape);
+  if (rc) return rc;
+  *scratch_bytes = align_up((size_t)gate_parts(shape->T, shape->E) * shape->E * 4);
+  return MOE_OK;
+}
+
+int moe_gate_fwd(const moe_gate_shape* shape, const float* logits, const float* bias, const uint8_t* mask,
+                 int32_t* topk_idx, float* topk_w, int32_t* counts, void* scratch, void* stream) {
+  int rc = check_gate(shape);
+  if (rc) return rc;
+  if (counts) REQUIRE_WS(scratch);
+  if (shape->T == 0 && !counts) return MOE_OK;
+  if (shape->T > 0) {
+    REQUIRE(logits);
+    REQUIRE(topk_idx);
+    REQUIRE(topk_w);
+  }
+  return hip_status(launch_gate_fwd(*shape, logits, bias, mask, topk_idx, topk_w, counts, (int32_t*)scratch,
+                                    (hipStream_t)stream),
+                    __func__);
+}
+
+int moe_gate_bwd(const moe_gate_shape* shape, const float* logits, const int32_t* topk_idx, const float* d_topk_w,
+                 float* d_logits, void* stream) {
+  int rc = check_gate(shape);
+  if (rc) return rc;
+  if (shape->T == 0) return MOE_OK;
+  REQUIRE(logits);
+  REQUIRE(topk_idx);
+  REQUIRE(d_topk_w);
+  REQUIRE(d_logits);
+  if (d_logits == logits) return fail(MOE_EINVAL, "%s: d_logits is logits", __func__);
+  return hip_status(launch_gate_bwd(*shape, logits, topk_idx, d_topk_w, d_logits, (hipStream_t)stream), __func__);
+}
+
+int moe_gate_update_bias(const moe_gate_shape* shape, const int32_t* counts, const float* bias, float rate,
+                         float* bias_out, void* stream) {
+  int rc = check_gate(shape);
+  if (rc) return rc;
+  if (!isfinite(rate)) return fail(MOE_EINVAL, "rate is not finite");
+  REQUIRE(counts);
+  REQUIRE(bias);
+  REQUIRE(bias_out);
+  return hip_status(launch_gate_bias(*shape, counts, bias, rate, bias_out, (hipStream_t)stream), __func__);
+}
+
+static int check_linear(const moe_linear_shape* s) {
+  if (!s) return fail(MOE_EINVAL, "shape is NULL");
+  if (s->T < 0) return fail(MOE_EINVAL, "T = %d < 0", s->T);
+  if (s->K < 1 || s->N < 1 || s->K > (1 << 20) || s->N > (1 << 20))
+    return fail(MOE_EINVAL, "K = %d and N = %d must lie in 1..2^20", s->K, s->N);
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) return fail(MOE_EINVAL, "dtype = %d", s->dtype);
+  if (s->act < MOE_ACT_NONE || s->act > MOE_ACT_GELU) return fail(MOE_EINVAL, "act = %d", s->act);
+  return MOE_OK;
+}
+
+int moe_linear_scratch_bytes(const moe_linear_shape* shape, size_t* scratch_bytes) {
+  REQUIRE(scratch_bytes);
+  int rc = check_linear(shape);
+  if (rc) return rc;
+  *scratch_bytes = align_up(linear_layout(*shape).bytes + 1);
+  return MOE_OK;
+}
+
+int moe_linear_fwd(const moe_linear_shape* shape, const void* x, const void* w, const void* b, const void* res,
+                   void* z, void* y, void* scratch, void* stream) {
+  int rc = check_linear(shape);
+  if (rc) return rc;
+  if (shape->T == 0) return MOE_OK;
+  REQUIRE(x);
+  REQUIRE(w);
+  REQUIRE(y);
+  REQUIRE_WS(scratch);
+  if (y == x || y == z || (z && (z == x || z == res)))
+    return fail(MOE_EINVAL, "%s: y may not be x or z, and z not x or res", __func__);
+  return hip_status(launch_linear_fwd(*shape, x, w, b, res, z, y, scratch, (hipStream_t)stream), __func__);
+}
+
+int moe_linear_bwd(const moe_linear_shape* shape, const void* dy, const void* x, const void* w, const void* z,
+                   const void* dx_in, void* dx, void* dw, void* db, void* scratch, void* stream) {
+  int rc = check_linear(shape);
+  if (rc) return rc;
+  REQUIRE(dw);
+  REQUIRE_WS(scratch);
+  if (dx_in && !dx) return fail(MOE_EINVAL, "%s: dx_in without dx", __func__);
+  if (shape->T > 0) {
+    REQUIRE(dy);
+    REQUIRE(x);
+    REQUIRE(w);
+    if (shape->act != MOE_ACT_NONE) REQUIRE(z);
+    if (dx && (dx == dy || dx == x || dx == z))
+      return fail(MOE_EINVAL, "%s: dx may be none of dy, x and z", __func__);
+  }
+  return hip_status(launch_linear_bwd(*shape, dy, x, w, z, dx_in, dx, dw, db, scratch, (hipStream_t)stream), __func__);
+}
+
+int moe_adamw(const moe_adamw_params* params, const moe_adamw_tensor* tensors, int32_t count, const float* lr,
+              const float* grad_scale, void* clock, void* stream) {
+  REQUIRE(params);
+  const moe_adamw_params& s = *params;
+  if (count < 0) return fail(MOE_EINVAL, "count = %d < 0", count);
+  if (!isfinite(s.lr) || !isfinite(s.weight_decay)) return fail(MOE_EINVAL, "lr and weight_decay must be finite");
+  if (!(s.beta1 >= 0.0 && s.beta1 < 1.0 && s.beta2 >= 0.0 && s.beta2 < 1.0))
+    return fail(MOE_EINVAL, "beta1 = %g and beta2 = %g must lie in [0, 1)", s.beta1, s.beta2);
+  // as the kernels take it: above 0 in fp32, too
+  if (!isfinite(s.eps) || !((float)s.eps > 0.f) || !isfinite((float)s.eps))
+    return fail(MOE_EINVAL, "eps = %g must be finite and > 0", s.eps);
+  if (s.state != MOE_STATE_F32 && s.state != MOE_STATE_8BIT) return fail(MOE_EINVAL, "state = %d", s.state);
+  if (s.stochastic != 0 && s.stochastic != 1) return fail(MOE_EINVAL, "stochastic = %d", s.stochastic);
+  if (!clock && s.step < 1) return fail(MOE_EINVAL, "step = %lld < 1", (long long)s.step);
+  if ((uintptr_t)clock % 8 != 0) return fail(MOE_EINVAL, "%s: clock is not at a multiple of 8", __func__);
+  if (count > 0) REQUIRE(tensors);
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.at < 0) return fail(MOE_EINVAL, "tensor %d: n and at must be >= 0", i);
+    if ((t.p_dtype != MOE_F32 && t.p_dtype != MOE_BF16) || (t.g_dtype != MOE_F32 && t.g_dtype != MOE_BF16))
+      return fail(MOE_EINVAL, "tensor %d: p_dtype = %d, g_dtype = %d", i, t.p_dtype, t.g_dtype);
+    if (!t.g || t.n == 0) continue;
+    if (!t.p || !t.m || !t.v) return fail(MOE_EINVAL, "tensor %d: p, m or v is NULL", i);
+    if (s.state == MOE_STATE_8BIT && (!t.m_scale || !t.v_scale))
+      return fail(MOE_EINVAL, "tensor %d: the 8-bit moments need m_scale and v_scale", i);
+    if ((uintptr_t)t.m % 32 != 0 || (uintptr_t)t.v % 32 != 0)
+      return fail(MOE_EINVAL, "tensor %d: m and v must lie at multiples of 32 bytes", i);
+    if ((uintptr_t)t.p % (t.p_dtype == MOE_BF16 ? 2 : 4) != 0 || (uintptr_t)t.g % (t.g_dtype == MOE_BF16 ? 2 : 4) != 0 ||
+        (uintptr_t)t.master % 4 != 0)
+      return fail(MOE_EINVAL, "tensor %d: p, g and master must lie at multiples of their element's size", i);
+  }
+  return hip_status(launch_adamw(s, tensors, count, lr, grad_scale, clock, (hipStream_t)stream), __func__);
+}
+
 }  // extern "C"

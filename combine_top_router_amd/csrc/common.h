@@ -150,6 +150,33 @@ hipError_t launch_norm_bwd(const moe_norm_shape& s, const void* dy, const void* 
 size_t orth_scratch_bytes(const moe_orth_shape& s);
 hipError_t launch_orthogonalize(const moe_orth_shape& s, const void* g, void* o, float scale, void* scratch,
                                 hipStream_t st);
+// routing by scores (gate.hip): part_c [gate_parts, E]
+int gate_parts(int T, int E);
+hipError_t launch_gate_fwd(const moe_gate_shape& s, const float* logits, const float* bias, const uint8_t* mask,
+                           int32_t* idx, float* w, int32_t* counts, int32_t* part_c, hipStream_t st);
+hipError_t launch_gate_bwd(const moe_gate_shape& s, const float* logits, const int32_t* idx, const float* dw,
+                           float* d_logits, hipStream_t st);
+hipError_t launch_gate_bias(const moe_gate_shape& s, const int32_t* counts, const float* bias, float rate, float* out,
+                            hipStream_t st);
+// AdamW (adamw.hip): what the clock of a step on the device holds
+struct AdamwClock {
+  int64_t t;      // steps taken
+  float to_m;     // 1 / (1 - beta1^t)
+  float root;     // 1 / sqrt(1 - beta2^t)
+  uint32_t key;   // of the step's random bits
+};
+static_assert(sizeof(AdamwClock) <= MOE_ADAMW_CLOCK_BYTES, "the clock");
+hipError_t launch_adamw(const moe_adamw_params& s, const moe_adamw_tensor* tensors, int count, const float* lr,
+                        const float* grad_scale, void* clock, hipStream_t st);
+// matrix product with an epilogue (linear.hip)
+struct LinearLayout {
+  size_t off_part, bytes;   // scratch: dz, then the shares of db
+};
+LinearLayout linear_layout(const moe_linear_shape& s);
+hipError_t launch_linear_fwd(const moe_linear_shape& s, const void* x, const void* w, const void* b, const void* res,
+                             void* z, void* y, void* scratch, hipStream_t st);
+hipError_t launch_linear_bwd(const moe_linear_shape& s, const void* dy, const void* x, const void* w, const void* z,
+                             const void* dx_in, void* dx, void* dw, void* db, void* scratch, hipStream_t st);
 hipError_t launch_dtopk(const moe_shape& s, const float* dw_part, int nparts, const int32_t* row_of,
                         float* d_topk_w, hipStream_t st);
 

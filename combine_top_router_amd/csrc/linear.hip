@@ -1,0 +1,198 @@
+// Matrix product with bias, activation and residual in its epilogue, and its backward.
+//
+//   z = x W + b,  y = act(z) + res
+//   dz = dy act'(z),  dx = dx_in + dz W^T,  dW = x^T dz,  db = sum_t dz
+// with x [T, K], W [K, N] as the layer's weights are stored, sums in fp32.  z is kept in the
+// data's type for the backward; y is formed from the fp32 sum.
+#include "linear.h"
+
+namespace moe {
+
+namespace {
+
+// ---------------- any size, any alignment ----------------
+// 64 x 64 tiles of four waves, K steps of 32 staged element by element.
+constexpr int GTILE = 64, GSTEP = 32;
+
+template <typename T> struct gstage;
+template <> struct gstage<bf16_t> { static constexpr int LD = GSTEP + 8; };
+template <> struct gstage<float> { static constexpr int LD = GSTEP + 1; };
+
+// C [M, N] = A B over K.  A element (m, k) at m * am + k * ak, B element (k, n) at k * bk + n * bn.
+template <typename T>
+struct GeneralArgs {
+  const T* a;
+  const T* b;
+  int64_t am, ak, bk, bn;
+  int64_t M, N, K;
+  Epilogue<T> e;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_linear_any(GeneralArgs<T> g) {
+  constexpr int LD = gstage<T>::LD;
+  __shared__ __attribute__((aligned(16))) T as[GTILE][LD];   // [m][k]
+  __shared__ __attribute__((aligned(16))) T bs[GTILE][LD];   // [n][k]
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int64_t m0 = (int64_t)blockIdx.x * GTILE, n0 = (int64_t)blockIdx.y * GTILE;
+  const int wm = (wv & 1) * 32, wn = (wv >> 1) * 32;
+  f32x16 acc;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+  for (int64_t k0 = 0; k0 < g.K; k0 += GSTEP) {
+    T ra[8], rb[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {   // neighbouring threads along the axis that is contiguous
+      const int s = tid + 256 * q;
+      const int am = g.ak == 1 ? s >> 5 : s & 63, ak = g.ak == 1 ? s & 31 : s >> 6;
+      const int bn = g.bk == 1 ? s >> 5 : s & 63, bk = g.bk == 1 ? s & 31 : s >> 6;
+      ra[q] = m0 + am < g.M && k0 + ak < g.K ? g.a[(m0 + am) * g.am + (k0 + ak) * g.ak] : (T)0;
+      rb[q] = n0 + bn < g.N && k0 + bk < g.K ? g.b[(k0 + bk) * g.bk + (n0 + bn) * g.bn] : (T)0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int s = tid + 256 * q;
+      const int am = g.ak == 1 ? s >> 5 : s & 63, ak = g.ak == 1 ? s & 31 : s >> 6;
+      const int bn = g.bk == 1 ? s >> 5 : s & 63, bk = g.bk == 1 ? s & 31 : s >> 6;
+      as[am][ak] = ra[q];
+      bs[bn][bk] = rb[q];
+    }
+    __syncthreads();
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int kk = 0; kk < GSTEP; kk += 16) {
+        const int k = kk + (lane >> 5) * 8;
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(&as[wm + (lane & 31)][k]),
+                                                      *reinterpret_cast<const bf16x8*>(&bs[wn + (lane & 31)][k]), acc,
+                                                      0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < GSTEP; kk += 2) {
+        const int k = kk + (lane >> 5);
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as[wm + (lane & 31)][k], bs[wn + (lane & 31)][k], acc, 0, 0, 0);
+      }
+    }
+  }
+  const int64_t n = n0 + wn + (lane & 31);
+  if (n >= g.N) return;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int64_t m = m0 + wm + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+    if (m < g.M) g.e.store(m, n, g.N, acc[j]);
+  }
+}
+
+template <typename T>
+hipError_t general(const char* name, const T* a, const T* b, int64_t am, int64_t ak, int64_t bk, int64_t bn, int64_t M,
+                   int64_t N, int64_t K, const Epilogue<T>& e, hipStream_t st) {
+  if (M == 0 || N == 0) return hipSuccess;
+  const GeneralArgs<T> g{a, b, am, ak, bk, bn, M, N, K, e};
+  MOE_LAUNCH(name, k_linear_any<T>, dim3((unsigned)ceil_div(M, GTILE), (unsigned)ceil_div(N, GTILE)), dim3(256), 0, st,
+             g);
+  return hipGetLastError();
+}
+
+// ---------------- dz and db ----------------
+// dz = dy act'(z) and the workgroup's share of db: 64 columns by ZR rows, 4 rows at a time.
+template <typename T>
+__global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dy, const T* __restrict__ z, int64_t rows,
+                                                   int N, int act, int slab, T* __restrict__ dz,
+                                                   float* __restrict__ part) {
+  __shared__ float red[4][64];
+  const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+  const int n = blockIdx.y * 64 + c;
+  const int64_t t0 = (int64_t)blockIdx.x * slab, t1 = min(rows, t0 + slab);
+  float s = 0.f;
+  if (n < N)
+    for (int64_t t = t0 + r; t < t1; t += 4) {
+      float d = elem<T>::load(dy + t * N + n);
+      if (dz) {
+        d *= act_slope(elem<T>::load(z + t * N + n), act);
+        elem<T>::store(dz + t * N + n, d);
+      }
+      s += d;
+    }
+  if (!part) return;
+  red[r][c] = s;
+  __syncthreads();
+  if (r == 0 && n < N) part[(size_t)blockIdx.x * N + n] = red[0][c] + red[1][c] + red[2][c] + red[3][c];
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_linear_db(const float* __restrict__ part, int W, int N, T* __restrict__ db) {
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float s = 0.f;
+  for (int w = 0; w < W; ++w) s += part[(size_t)w * N + n];
+  elem<T>::store(db + n, s);
+}
+
+constexpr int ZR = 64;   // rows of a share of db
+
+template <typename T>
+hipError_t fwd(const moe_linear_shape& s, const T* x, const T* w, const T* b, const T* res, T* z, T* y,
+               hipStream_t st) {
+  Epilogue<T> e{};
+  e.out = y; e.z = z; e.bias = b; e.add = res; e.act = s.act;
+  return general<T>("linear_fwd", x, w, s.K, 1, s.N, 1, s.T, s.N, s.K, e, st);
+}
+
+template <typename T>
+hipError_t bwd(const moe_linear_shape& s, const T* dy, const T* x, const T* w, const T* z, const T* dx_in, T* dx,
+               T* dw, T* db, void* scratch, hipStream_t st) {
+  const LinearLayout L = linear_layout(s);
+  T* const dzbuf = s.act == MOE_ACT_NONE ? nullptr : (T*)scratch;
+  float* const part = (float*)((char*)scratch + L.off_part);
+  const T* dz = dzbuf ? dzbuf : dy;
+  const int W = (int)ceil_div(s.T, ZR);
+  if ((dzbuf || db) && s.T > 0)
+    MOE_LAUNCH("linear_dz", k_linear_dz<T>, dim3((unsigned)W, (unsigned)ceil_div(s.N, 64)), dim3(256), 0, st, dy, z,
+               (int64_t)s.T, s.N, s.act, ZR, dzbuf, db ? part : nullptr);
+  if (db)
+    MOE_LAUNCH("linear_db", k_linear_db<T>, dim3((unsigned)ceil_div(s.N, 256)), dim3(256), 0, st, part, W, s.N, db);
+  hipError_t err = hipGetLastError();
+  if (err == hipSuccess && dx) {
+    Epilogue<T> e{};
+    e.out = dx; e.add = dx_in; e.act = MOE_ACT_NONE;
+    err = general<T>("linear_dx", dz, w, s.N, 1, 1, s.N, s.T, s.K, s.N, e, st);
+  }
+  if (err == hipSuccess) {
+    Epilogue<T> e{};
+    e.out = dw; e.act = MOE_ACT_NONE;
+    err = general<T>("linear_dw", x, dz, 1, s.K, s.N, 1, s.K, s.N, s.T, e, st);
+  }
+  return err;
+}
+
+}  // namespace
+
+LinearLayout linear_layout(const moe_linear_shape& s) {
+  const size_t es = s.dtype == MOE_BF16 ? 2 : 4;
+  LinearLayout L{};
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  L.off_part = s.act == MOE_ACT_NONE ? 0 : up((size_t)s.T * s.N * es);
+  L.bytes = L.off_part + up((size_t)ceil_div(s.T, ZR) * s.N * 4);
+  return L;
+}
+
+hipError_t launch_linear_fwd(const moe_linear_shape& s, const void* x, const void* w, const void* b, const void* res,
+                             void* z, void* y, void* scratch, hipStream_t st) {
+  (void)scratch;
+  if (s.dtype == MOE_BF16)
+    return fwd<bf16_t>(s, (const bf16_t*)x, (const bf16_t*)w, (const bf16_t*)b, (const bf16_t*)res, (bf16_t*)z,
+                       (bf16_t*)y, st);
+  return fwd<float>(s, (const float*)x, (const float*)w, (const float*)b, (const float*)res, (float*)z, (float*)y, st);
+}
+
+hipError_t launch_linear_bwd(const moe_linear_shape& s, const void* dy, const void* x, const void* w, const void* z,
+                             const void* dx_in, void* dx, void* dw, void* db, void* scratch, hipStream_t st) {
+  if (s.dtype == MOE_BF16)
+    return bwd<bf16_t>(s, (const bf16_t*)dy, (const bf16_t*)x, (const bf16_t*)w, (const bf16_t*)z,
+                       (const bf16_t*)dx_in, (bf16_t*)dx, (bf16_t*)dw, (bf16_t*)db, scratch, st);
+  return bwd<float>(s, (const float*)dy, (const float*)x, (const float*)w, (const float*)z, (const float*)dx_in,
+                    (float*)dx, (float*)dw, (float*)db, scratch, st);
+}
+
+}  // namespace moe

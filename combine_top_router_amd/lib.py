@@ -10,7 +10,10 @@ __all__ = [
     "MOE_OK", "MOE_EINVAL", "MOE_EUNSUPPORTED", "MOE_EWORKSPACE", "MOE_EHIP",
     "MOE_F32", "MOE_BF16", "MOE_BWD_SAME", "MOE_BWD_MXFP8", "MOE_FWD_SAME", "MOE_FWD_MXFP8",
     "MOE_NORM_LAYER", "MOE_NORM_RMS",
-    "MoeShape", "MoeNormShape", "MoeOrthShape", "MoeError", "load", "lib_path", "EXPORTS",
+    "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_ACT_NONE", "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU",
+    "MOE_STATE_F32", "MOE_STATE_8BIT", "MOE_ADAMW_CLOCK_BYTES",
+    "MoeShape", "MoeNormShape", "MoeOrthShape", "MoeGateShape", "MoeLinearShape", "MoeAdamwTensor", "MoeAdamwParams",
+    "MoeError", "load", "lib_path", "EXPORTS",
     "moe_abi_version", "moe_last_error", "moe_workspace_bytes", "moe_route_topk",
     "moe_dispatch", "moe_dispatch_noscratch", "moe_fwd", "moe_combine", "moe_bwd", "moe_route_topk_bwd",
     "moe_mx_quantize", "moe_mx_quantize_cols", "moe_timing_enable", "moe_timing_read",
@@ -18,6 +21,8 @@ __all__ = [
     "moe_balance_scratch_bytes", "moe_balance_fwd", "moe_balance_bwd",
     "moe_norm_scratch_bytes", "moe_norm_fwd", "moe_norm_bwd",
     "moe_orth_scratch_bytes", "moe_orthogonalize",
+    "moe_gate_scratch_bytes", "moe_gate_fwd", "moe_gate_bwd", "moe_gate_update_bias",
+    "moe_linear_scratch_bytes", "moe_linear_fwd", "moe_linear_bwd", "moe_adamw",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4
@@ -25,6 +30,10 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_BWD_SAME, MOE_BWD_MXFP8 = 0, 1
 MOE_FWD_SAME, MOE_FWD_MXFP8 = 0, 1
 MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU = 0, 1, 2, 3
+MOE_STATE_F32, MOE_STATE_8BIT = 0, 1
+MOE_ADAMW_CLOCK_BYTES = 32
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -50,6 +59,26 @@ class MoeOrthShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n", "rows", "cols", "dtype", "steps")]
 
 
+class MoeGateShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "E", "k", "score", "groups", "topk_groups", "group_top", "renorm")] + [("scale", ctypes.c_float)]
+
+
+class MoeLinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "dtype", "act")]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("p", "g", "master", "m", "v", "m_scale", "v_scale")]
+                + [(n, ctypes.c_int64) for n in ("n", "at")] + [(n, ctypes.c_int32) for n in ("p_dtype", "g_dtype")])
+
+
+class MoeAdamwParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")]
+                + [("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("state", ctypes.c_int32),
+                   ("stochastic", ctypes.c_int32)])
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, func: str, msg: str):
         super().__init__(f"{func} failed with status {code}: {msg}")
@@ -60,6 +89,8 @@ _P = ctypes.c_void_p
 _S = ctypes.POINTER(MoeShape)
 _NS = ctypes.POINTER(MoeNormShape)
 _OS = ctypes.POINTER(MoeOrthShape)
+_GS = ctypes.POINTER(MoeGateShape)
+_LS = ctypes.POINTER(MoeLinearShape)
 _SZ = ctypes.POINTER(ctypes.c_size_t)
 _F = ctypes.c_float
 _SIG = {
@@ -86,6 +117,15 @@ _SIG = {
     "moe_norm_bwd": (ctypes.c_int, [_NS] + [_P] * 12),
     "moe_orth_scratch_bytes": (ctypes.c_int, [_OS, _SZ]),
     "moe_orthogonalize": (ctypes.c_int, [_OS, _P, _P, _F, _P, _P]),
+    "moe_gate_scratch_bytes": (ctypes.c_int, [_GS, _SZ]),
+    "moe_gate_fwd": (ctypes.c_int, [_GS] + [_P] * 8),
+    "moe_gate_bwd": (ctypes.c_int, [_GS] + [_P] * 5),
+    "moe_gate_update_bias": (ctypes.c_int, [_GS, _P, _P, _F, _P, _P]),
+    "moe_linear_scratch_bytes": (ctypes.c_int, [_LS, _SZ]),
+    "moe_linear_fwd": (ctypes.c_int, [_LS] + [_P] * 8),
+    "moe_linear_bwd": (ctypes.c_int, [_LS] + [_P] * 10),
+    "moe_adamw": (ctypes.c_int, [ctypes.POINTER(MoeAdamwParams), ctypes.POINTER(MoeAdamwTensor), ctypes.c_int32]
+                  + [_P] * 4),
     "moe_timing_enable": (ctypes.c_int, [ctypes.c_int]),
     "moe_timing_read": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_char_p),
                                        ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int)]),
@@ -224,6 +264,42 @@ def moe_orth_scratch_bytes(shape: MoeOrthShape) -> int:
 
 def moe_orthogonalize(shape, g, o, scale, scratch, stream=0):
     _check(load().moe_orthogonalize(ctypes.byref(shape), g, o, scale, scratch, stream), "moe_orthogonalize")
+
+
+def moe_gate_scratch_bytes(shape: MoeGateShape) -> int:
+    return _scratch_bytes("moe_gate_scratch_bytes", shape)
+
+
+def moe_gate_fwd(shape, logits, bias, mask, topk_idx, topk_w, counts, scratch, stream=0):
+    _check(load().moe_gate_fwd(ctypes.byref(shape), logits, bias, mask, topk_idx, topk_w, counts, scratch, stream),
+           "moe_gate_fwd")
+
+
+def moe_gate_bwd(shape, logits, topk_idx, d_topk_w, d_logits, stream=0):
+    _check(load().moe_gate_bwd(ctypes.byref(shape), logits, topk_idx, d_topk_w, d_logits, stream), "moe_gate_bwd")
+
+
+def moe_gate_update_bias(shape, counts, bias, rate, bias_out, stream=0):
+    _check(load().moe_gate_update_bias(ctypes.byref(shape), counts, bias, rate, bias_out, stream),
+           "moe_gate_update_bias")
+
+
+def moe_linear_scratch_bytes(shape: MoeLinearShape) -> int:
+    return _scratch_bytes("moe_linear_scratch_bytes", shape)
+
+
+def moe_linear_fwd(shape, x, w, b, res, z, y, scratch, stream=0):
+    _check(load().moe_linear_fwd(ctypes.byref(shape), x, w, b, res, z, y, scratch, stream), "moe_linear_fwd")
+
+
+def moe_linear_bwd(shape, dy, x, w, z, dx_in, dx, dw, db, scratch, stream=0):
+    _check(load().moe_linear_bwd(ctypes.byref(shape), dy, x, w, z, dx_in, dx, dw, db, scratch, stream),
+           "moe_linear_bwd")
+
+
+def moe_adamw(params, tensors, count, lr, grad_scale, clock, stream=0):
+    """`tensors`: a ctypes array of MoeAdamwTensor, of which the first `count` are taken."""
+    _check(load().moe_adamw(ctypes.byref(params), tensors, count, lr, grad_scale, clock, stream), "moe_adamw")
 
 
 def moe_timing_enable(on: bool = True):

@@ -350,6 +350,135 @@ int moe_orth_scratch_bytes(const moe_orth_shape* shape, size_t* scratch_bytes);
  * NaN, and leaves the others alone.  scale must be finite.  Needs scratch. */
 int moe_orthogonalize(const moe_orth_shape* shape, const void* g, void* o, float scale, void* scratch, void* stream);
 
+/* ---- routing by scores ---- */
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_kind;
+
+typedef struct {
+  int32_t T;            /* tokens, >= 0 */
+  int32_t E;            /* routed experts, 1..1024 */
+  int32_t k;            /* experts per token, 1..16, at most topk_groups E / groups */
+  int32_t score;        /* moe_score_kind */
+  int32_t groups;       /* groups of E / groups consecutive experts, 1..64, a divisor of E */
+  int32_t topk_groups;  /* groups a token may choose from, 1..groups */
+  int32_t group_top;    /* experts whose sum is a group's score: 1 or 2, at most E / groups */
+  int32_t renorm;       /* 1: the weights of a token sum to scale; 0: scale times the scores */
+  float scale;          /* finite, > 0 */
+} moe_gate_shape;
+
+/* Bytes of scratch of moe_gate_fwd with counts.  Never 0. */
+int moe_gate_scratch_bytes(const moe_gate_shape* shape, size_t* scratch_bytes);
+
+/* Top-k routing by scores s = softmax(logits[t]) over all E, or sigmoid(logits[t]):
+ *   c_e = s_e + bias_e (bias: fp32 [E], e.g. one that evens the load; it chooses and does not
+ *         weigh), or with bias == NULL c_e = logits[t, e], which orders the experts alike;
+ *   a group's score is the sum of its group_top largest c (with bias == NULL and group_top = 2,
+ *   of s); the topk_groups best groups are open, and in them the k largest c are chosen,
+ *   ordered by c descending; ties to the lower group and the lower expert.
+ *   topk_w[t, j] = scale s_j / sum_i s_i over the chosen (renorm = 1) or scale s_j.
+ * c is compared in fp64.  A logit of -inf or NaN, or a c that is NaN, ranks behind every other
+ * expert of its group (a masked expert is chosen only where the open groups hold no k others,
+ * with weight 0); the k ids are always distinct and in range.  A NaN logit makes the weights
+ * of its row NaN where it is in their sum, as does +inf under the softmax.
+ * mask (uint8 [T], or NULL) = 0 marks a token that takes no expert, e.g. padding: its ids are
+ * -1 (which every call here takes as no expert), its weights 0, and its logits are not looked at.
+ * counts (int32 [E], or NULL): the chosen slots of each expert; needs scratch. */
+int moe_gate_fwd(const moe_gate_shape* shape, const float* logits, const float* bias, const uint8_t* mask,
+                 int32_t* topk_idx, float* topk_w, int32_t* counts, void* scratch, void* stream);
+
+/* Its backward for d_topk_w [T, k], the choice being piecewise constant: with s_j, q_j = s_j
+ * (renorm = 0) or s_j / sum_i s_i, and d = d_topk_w, d_logits [T, E] is, on the chosen experts,
+ *   scale q_j (d_j - sum_i q_i d_i)             softmax, renorm = 1
+ *   scale q_j (1 - s_j) (d_j - sum_i q_i d_i)   sigmoid, renorm = 1
+ *   scale s_j (1 - s_j) d_j                     sigmoid, renorm = 0
+ * and 0 elsewhere; for softmax with renorm = 0 scale s_e (g_e - sum_i s_i d_i) on every
+ * expert, g_e = d of the slot that chose e, else 0.  Slots with ids outside [0, E) add nothing
+ * (their d is not looked at); a token without any gets zeros.  d_logits may not be logits. */
+int moe_gate_bwd(const moe_gate_shape* shape, const float* logits, const int32_t* topk_idx, const float* d_topk_w,
+                 float* d_logits, void* stream);
+
+/* A step of the bias towards an even load: with counts (int32 [E], moe_gate_fwd's or their sum
+ * over GPUs) bias_out[e] = bias[e] + rate sign(sum_i counts[i] / E - counts[e]).  rate must be
+ * finite; bias_out may be bias.  Uses E of the shape. */
+int moe_gate_update_bias(const moe_gate_shape* shape, const int32_t* counts, const float* bias, float rate,
+                         float* bias_out, void* stream);
+
+/* ---- matrix product with bias, activation and residual ---- */
+
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act_kind;
+
+typedef struct {
+  int32_t T;      /* rows (tokens), >= 0 */
+  int32_t K;      /* columns of x, 1..2^20, any */
+  int32_t N;      /* columns of y, 1..2^20, any */
+  int32_t dtype;  /* moe_dtype of every matrix and vector */
+  int32_t act;    /* moe_act_kind; gelu is the one of the error function */
+} moe_linear_shape;
+
+/* Bytes of scratch of moe_linear_fwd and moe_linear_bwd.  Never 0. */
+int moe_linear_scratch_bytes(const moe_linear_shape* shape, size_t* scratch_bytes);
+
+/* z = x W + b, y = act(z) + res, with x [T, K], W [K, N], b [N] (NULL: none), res [T, N] (NULL:
+ * none).  The sums run in fp32 and y is rounded once.  z [T, N], rounded, is what moe_linear_bwd
+ * needs of an activation; NULL: not kept.  y may be res; it may not be x or z.  Needs scratch. */
+int moe_linear_fwd(const moe_linear_shape* shape, const void* x, const void* w, const void* b, const void* res,
+                   void* z, void* y, void* scratch, void* stream);
+
+/* Its backward for dy [T, N], z as the forward kept it (NULL for MOE_ACT_NONE):
+ *   dz = dy act'(z),  dx = dx_in + dz W^T,  dw = x^T dz,  db = sum_t dz
+ * (relu'(0) = 0; the gradient of res is dy).  dz enters the products in the data's type and db
+ * in fp32.  dx may be NULL (not wanted: x is an input), dx_in NULL (taken as 0) or dx; db may be
+ * NULL.  dx may be none of dy, x, z.  T = 0 gives dw = db = 0.  Results do not change from run to
+ * run.  Needs scratch. */
+int moe_linear_bwd(const moe_linear_shape* shape, const void* dy, const void* x, const void* w, const void* z,
+                   const void* dx_in, void* dx, void* dw, void* db, void* scratch, void* stream);
+
+/* ---- AdamW ---- */
+
+typedef enum { MOE_STATE_F32 = 0, MOE_STATE_8BIT = 1 } moe_state_kind;
+
+/* One parameter tensor of n elements.  p and g at multiples of their element's size; m and v at
+ * multiples of 32 bytes. */
+typedef struct {
+  void* p;           /* the parameter, updated */
+  const void* g;     /* its gradient; NULL: the tensor is left alone in this step */
+  float* master;     /* fp32 copy that is updated, p being its rounding; NULL: p itself */
+  void* m;           /* moments: fp32 [n], or with 8 bits uint8 codes [n rounded up to 32] */
+  void* v;
+  uint8_t* m_scale;  /* 8 bits: uint8 [n / 32, rounded up] each; else unused */
+  uint8_t* v_scale;
+  int64_t n;         /* >= 0 */
+  int64_t at;        /* >= 0: the first element's place in the numbering that the random bits go by */
+  int32_t p_dtype;   /* moe_dtype */
+  int32_t g_dtype;   /* moe_dtype */
+} moe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;  /* finite; betas in [0, 1), eps > 0 */
+  int64_t step;        /* the step's number, >= 1 (unused with a clock) */
+  uint64_t seed;       /* of the random bits */
+  int32_t state;       /* moe_state_kind */
+  int32_t stochastic;  /* 1: 8-bit moments, and bf16 parameters without a master, are rounded
+                          stochastically; 0: to nearest */
+} moe_adamw_params;
+
+#define MOE_ADAMW_CLOCK_BYTES 32
+
+/* One AdamW step of `count` tensors (a host array, read during the call) that do not overlap:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, from the new m and v before these are rounded.  With 8 bits a moment is held as E4M3
+ * codes with one e8m0 scale per 32 consecutive elements (the scale rule of moe_mx_quantize): m
+ * itself, and of v its square root, which stays above 0 where v is.  Zeroed codes are zero
+ * moments, with any scale.  What is not finite is held as NaN and touches its own element alone.
+ * lr (device fp32 [1]), NULL: params->lr.  grad_scale (device fp32 [1]), NULL: 1; g enters
+ * multiplied by it.  clock, NULL: the step is params->step.  Else device memory of
+ * MOE_ADAMW_CLOCK_BYTES at a multiple of 8, whose first 8 bytes hold the steps taken (int64):
+ * the call counts it up and the step is the new number, so that a captured call goes on at
+ * every replay. */
+int moe_adamw(const moe_adamw_params* params, const moe_adamw_tensor* tensors, int32_t count, const float* lr,
+              const float* grad_scale, void* clock, void* stream);
+
 /* Opt-in kernel timing for profilers and benchmarks (no effect on results).
  * moe_timing_enable(1) makes every kernel that this host thread launches through the
  * calls above carry two HIP events that the dispatch itself stamps at its start and end
