@@ -170,7 +170,7 @@ hipError_t launch_adamw(const moe_adamw_params& s, const moe_adamw_tensor* tenso
                         const float* grad_scale, void* clock, hipStream_t st);
 // matrix product with an epilogue (linear.hip)
 struct LinearLayout {
-  size_t off_part, bytes;   // scratch: dz, then the shares of db
+  size_t off_part, off_db, bytes;   // scratch: dz, the shares of a product split along its sum, those of db
 };
 LinearLayout linear_layout(const moe_linear_shape& s);
 hipError_t launch_linear_fwd(const moe_linear_shape& s, const void* x, const void* w, const void* b, const void* res,

@@ -6,22 +6,96 @@
 namespace moe {
 namespace {
 
-// 1 - sigmoid and sigmoid by the hardware reciprocal (1 ulp)
-__device__ __forceinline__ float act_value(float z, int act) {
-  if (act == MOE_ACT_RELU) return z < 0.f ? 0.f : z;   // NaN stays
-  if (act == MOE_ACT_SILU) return silu_f(z);
-  if (act == MOE_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.707106781f));
-  return z;
+// Of the normal law's distribution function at -|z|: 0.5 (1 - erf(|z| / sqrt 2)) as t (a1 + t (a2 + ...))
+// e^(-z^2 / 2) / 2 with t = 1 / (1 + p |z| / sqrt 2) (Abramowitz and Stegun 7.1.26, good to
+// 0.75e-7 here); e is that exponential.
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.707106781f, 1.f));
+  e = __expf(-0.5f * z * z);
+  const float p = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t, 0.254829592f);
+  return 0.5f * p * t * e;
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
-  if (act == MOE_ACT_RELU) return z > 0.f ? 1.f : z == z ? 0.f : z;
-  if (act == MOE_ACT_SILU) {
-    const float s = sigmoid_f(z);
-    return s * (1.f + z * (1.f - s));
+
+// act: one of moe_act_kind; uniform
+template <int N>
+__device__ __forceinline__ void act_values(float (&v)[N], int act) {
+  if (act == MOE_ACT_NONE) return;
+  if (act == MOE_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays
+  } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = silu_f(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float e;
+      const float t = normal_tail(v[i], e);
+      v[i] *= v[i] < 0.f ? t : 1.f - t;
+    }
   }
-  if (act == MOE_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.707106781f)) + z * 0.398942280f * __expf(-0.5f * z * z);
-  return 1.f;
+}
+__device__ __forceinline__ void act8(float (&v)[8], int act) { act_values<8>(v, act); }
+
+// d act'(z)
+__device__ __forceinline__ void slope8(float (&d)[8], const float (&z)[8], int act) {
+  if (act == MOE_ACT_NONE) return;
+  if (act == MOE_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] *= z[i] > 0.f ? 1.f : z[i] == z[i] ? 0.f : z[i];
+  } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sigmoid_f(z[i]);
+      d[i] *= s * (1.f + z[i] * (1.f - s));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float e;
+      const float t = normal_tail(z[i], e);
+      d[i] *= (z[i] < 0.f ? t : 1.f - t) + z[i] * 0.398942280f * e;
+    }
+  }
+}
+
+// 8 consecutive elements of a row with `left` to its end; WIDE: all there, at a multiple of 16 bytes
+template <typename T, bool WIDE>
+__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
+  if constexpr (!WIDE) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < left ? elem<T>::load(p + j) : 0.f;
+  } else if constexpr (sizeof(T) == 2) {
+    const i32x4 u = *reinterpret_cast<const i32x4*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float((uint32_t)u[j] << 16);
+      v[2 * j + 1] = __uint_as_float((uint32_t)u[j] & 0xffff0000u);
+    }
+  } else {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[4 + j] = b[j];
+    }
+  }
+}
+template <typename T, bool WIDE>
+__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
+  if constexpr (!WIDE) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) elem<T>::store(p + j, v[j]);
+  } else if constexpr (sizeof(T) == 2) {
+    i32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = (int)pk_bf16(v[2 * j], v[2 * j + 1]);
+    *reinterpret_cast<i32x4*>(p) = o;
+  } else {
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  }
 }
 
 // What becomes of an element of a product: bias, z kept, activation, a matrix added
@@ -35,11 +109,27 @@ struct Epilogue {
   __device__ __forceinline__ void store(int64_t m, int64_t n, int64_t N, float v) const {
     if (bias) v += elem<T>::load(bias + n);
     if (z) elem<T>::store(z + m * N + n, v);
-    v = act_value(v, act);
+    float w[1] = {v};
+    act_values<1>(w, act);
+    v = w[0];
     if (add) v += elem<T>::load(add + m * N + n);
     elem<T>::store(out + m * N + n, v);
   }
 };
 
 }  // namespace
+
+// linear_tiles.hip: C [M, N] = A B for bf16 matrices whose rows are whole 16-byte chunks, every
+// address at a multiple of 16.  A [M, K] of rows lda (a_k) or [K, M]; B [N, K] (b_k) or [K, N].
+struct LinearOut {
+  bf16_t* out;
+  bf16_t* z;
+  const bf16_t* bias;
+  const bf16_t* add;
+  int act;
+};
+size_t linear_part_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear_tiles(const char* name, const bf16_t* a, int64_t lda, bool a_k, const bf16_t* b, int64_t ldb,
+                               bool b_k, int64_t M, int64_t N, int64_t K, const LinearOut& o, float* part,
+                               hipStream_t st);
 }  // namespace moe

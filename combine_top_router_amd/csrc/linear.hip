@@ -95,45 +95,81 @@ hipError_t general(const char* name, const T* a, const T* b, int64_t am, int64_t
 }
 
 // ---------------- dz and db ----------------
-// dz = dy act'(z) and the workgroup's share of db: 64 columns by ZR rows, 4 rows at a time.
-template <typename T>
+// dz = dy act'(z) and the workgroup's share of db: 32 lanes of 8 columns by 8 rows at a time.
+constexpr int ZC = 256;   // columns of a workgroup
+template <typename T, bool WIDE>
 __global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dy, const T* __restrict__ z, int64_t rows,
                                                    int N, int act, int slab, T* __restrict__ dz,
                                                    float* __restrict__ part) {
-  __shared__ float red[4][64];
-  const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int n = blockIdx.y * 64 + c;
+  __shared__ float red[8][ZC];
+  const int c = (threadIdx.x & 31) * 8, r = threadIdx.x >> 5;
+  const int n = blockIdx.y * ZC + c;
   const int64_t t0 = (int64_t)blockIdx.x * slab, t1 = min(rows, t0 + slab);
-  float s = 0.f;
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = 0.f;
   if (n < N)
-    for (int64_t t = t0 + r; t < t1; t += 4) {
-      float d = elem<T>::load(dy + t * N + n);
+#pragma unroll 2
+    for (int64_t t = t0 + r; t < t1; t += 8) {
+      float d[8], v[8];
+      load8<T, WIDE>(dy + t * N + n, N - n, d);
       if (dz) {
-        d *= act_slope(elem<T>::load(z + t * N + n), act);
-        elem<T>::store(dz + t * N + n, d);
+        load8<T, WIDE>(z + t * N + n, N - n, v);
+        slope8(d, v, act);
+        store8<T, WIDE>(dz + t * N + n, N - n, d);
       }
-      s += d;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += d[j];
     }
   if (!part) return;
-  red[r][c] = s;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[r][c + j] = s[j];
   __syncthreads();
-  if (r == 0 && n < N) part[(size_t)blockIdx.x * N + n] = red[0][c] + red[1][c] + red[2][c] + red[3][c];
+  const int m = blockIdx.y * ZC + threadIdx.x;
+  if (m < N) {
+    float a = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) a += red[q][threadIdx.x];
+    part[(size_t)blockIdx.x * N + m] = a;
+  }
 }
 
+// db from its shares, added in a fixed order: 64 columns a workgroup, 16 slices of the shares
 template <typename T>
-__global__ __launch_bounds__(256) void k_linear_db(const float* __restrict__ part, int W, int N, T* __restrict__ db) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+__global__ __launch_bounds__(1024) void k_linear_db(const float* __restrict__ part, int W, int N, T* __restrict__ db) {
+  __shared__ float red[16][64];
+  const int c = threadIdx.x & 63, sl = threadIdx.x >> 6, n = blockIdx.x * 64 + c;
   float s = 0.f;
-  for (int w = 0; w < W; ++w) s += part[(size_t)w * N + n];
-  elem<T>::store(db + n, s);
+  if (n < N)
+    for (int w = sl; w < W; w += 16) s += part[(size_t)w * N + n];
+  red[sl][c] = s;
+  __syncthreads();
+  if (sl == 0 && n < N) {
+    for (int q = 1; q < 16; ++q) s += red[q][c];
+    elem<T>::store(db + n, s);
+  }
 }
 
-constexpr int ZR = 64;   // rows of a share of db
+// rows of a share of db: about 1024 workgroups, of at least 16 rows
+int dz_slab(const moe_linear_shape& s) {
+  const int64_t blocks = ceil_div(s.N, ZC), want = ceil_div((int64_t)s.T * blocks, 1024);
+  return (int)(ceil_div(want < 16 ? 16 : want > 65536 ? 65536 : want, 8) * 8);
+}
+
+inline bool at16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+// the tiles take bf16 rows of whole 16-byte chunks, the general kernel the rest
+template <typename T>
+bool tiled(const moe_linear_shape& s) { return sizeof(T) == 2 && s.K % 8 == 0 && s.N % 8 == 0; }
 
 template <typename T>
-hipError_t fwd(const moe_linear_shape& s, const T* x, const T* w, const T* b, const T* res, T* z, T* y,
+hipError_t fwd(const moe_linear_shape& s, const T* x, const T* w, const T* b, const T* res, T* z, T* y, void* scratch,
                hipStream_t st) {
+  if constexpr (sizeof(T) == 2)
+    if (tiled<T>(s) && at16(x) && at16(w) && at16(b) && at16(res) && at16(z) && at16(y)) {
+      const LinearLayout L = linear_layout(s);
+      return launch_linear_tiles("linear_fwd", x, s.K, true, w, s.N, false, s.T, s.N, s.K, {y, z, b, res, s.act},
+                                 (float*)((char*)scratch + L.off_part), st);
+    }
   Epilogue<T> e{};
   e.out = y; e.z = z; e.bias = b; e.add = res; e.act = s.act;
   return general<T>("linear_fwd", x, w, s.K, 1, s.N, 1, s.T, s.N, s.K, e, st);
@@ -144,15 +180,32 @@ hipError_t bwd(const moe_linear_shape& s, const T* dy, const T* x, const T* w, c
                T* dw, T* db, void* scratch, hipStream_t st) {
   const LinearLayout L = linear_layout(s);
   T* const dzbuf = s.act == MOE_ACT_NONE ? nullptr : (T*)scratch;
+  float* const dbp = (float*)((char*)scratch + L.off_db);
   float* const part = (float*)((char*)scratch + L.off_part);
   const T* dz = dzbuf ? dzbuf : dy;
-  const int W = (int)ceil_div(s.T, ZR);
-  if ((dzbuf || db) && s.T > 0)
-    MOE_LAUNCH("linear_dz", k_linear_dz<T>, dim3((unsigned)W, (unsigned)ceil_div(s.N, 64)), dim3(256), 0, st, dy, z,
-               (int64_t)s.T, s.N, s.act, ZR, dzbuf, db ? part : nullptr);
+  const int slab = dz_slab(s), W = (int)ceil_div(s.T, slab);
+  if ((dzbuf || db) && s.T > 0) {
+    const dim3 grid((unsigned)W, (unsigned)ceil_div(s.N, ZC));
+    if (s.N % 8 == 0 && at16(dy) && at16(z))
+      MOE_LAUNCH("linear_dz", (k_linear_dz<T, true>), grid, dim3(256), 0, st, dy, z, (int64_t)s.T, s.N, s.act, slab,
+                 dzbuf, db ? dbp : nullptr);
+    else
+      MOE_LAUNCH("linear_dz", (k_linear_dz<T, false>), grid, dim3(256), 0, st, dy, z, (int64_t)s.T, s.N, s.act, slab,
+                 dzbuf, db ? dbp : nullptr);
+  }
   if (db)
-    MOE_LAUNCH("linear_db", k_linear_db<T>, dim3((unsigned)ceil_div(s.N, 256)), dim3(256), 0, st, part, W, s.N, db);
+    MOE_LAUNCH("linear_db", k_linear_db<T>, dim3((unsigned)ceil_div(s.N, 64)), dim3(1024), 0, st, dbp, W, s.N, db);
   hipError_t err = hipGetLastError();
+  if constexpr (sizeof(T) == 2)
+    if (tiled<T>(s) && at16(dy) && at16(x) && at16(w) && at16(dx_in) && at16(dx) && at16(dw)) {
+      if (err == hipSuccess && dx && s.T > 0)
+        err = launch_linear_tiles("linear_dx", dz, s.N, true, w, s.N, true, s.T, s.K, s.N,
+                                  {dx, nullptr, nullptr, dx_in, MOE_ACT_NONE}, part, st);
+      if (err == hipSuccess)
+        err = launch_linear_tiles("linear_dw", x, s.K, false, dz, s.N, false, s.K, s.N, s.T,
+                                  {dw, nullptr, nullptr, nullptr, MOE_ACT_NONE}, part, st);
+      return err;
+    }
   if (err == hipSuccess && dx) {
     Epilogue<T> e{};
     e.out = dx; e.add = dx_in; e.act = MOE_ACT_NONE;
@@ -173,17 +226,24 @@ LinearLayout linear_layout(const moe_linear_shape& s) {
   LinearLayout L{};
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   L.off_part = s.act == MOE_ACT_NONE ? 0 : up((size_t)s.T * s.N * es);
-  L.bytes = L.off_part + up((size_t)ceil_div(s.T, ZR) * s.N * 4);
+  size_t part = 0;   // of the largest of the three products
+  if (s.dtype == MOE_BF16 && tiled<bf16_t>(s)) {
+    const size_t of[3] = {linear_part_bytes(s.T, s.N, s.K), linear_part_bytes(s.T, s.K, s.N),
+                          linear_part_bytes(s.K, s.N, s.T)};
+    for (size_t n : of) part = n > part ? n : part;
+  }
+  L.off_db = L.off_part + up(part);
+  L.bytes = L.off_db + up((size_t)ceil_div(s.T, dz_slab(s)) * s.N * 4);
   return L;
 }
 
 hipError_t launch_linear_fwd(const moe_linear_shape& s, const void* x, const void* w, const void* b, const void* res,
                              void* z, void* y, void* scratch, hipStream_t st) {
-  (void)scratch;
   if (s.dtype == MOE_BF16)
     return fwd<bf16_t>(s, (const bf16_t*)x, (const bf16_t*)w, (const bf16_t*)b, (const bf16_t*)res, (bf16_t*)z,
-                       (bf16_t*)y, st);
-  return fwd<float>(s, (const float*)x, (const float*)w, (const float*)b, (const float*)res, (float*)z, (float*)y, st);
+                       (bf16_t*)y, scratch, st);
+  return fwd<float>(s, (const float*)x, (const float*)w, (const float*)b, (const float*)res, (float*)z, (float*)y,
+                    scratch, st);
 }
 
 hipError_t launch_linear_bwd(const moe_linear_shape& s, const void* dy, const void* x, const void* w, const void* z,

@@ -199,3 +199,14 @@ def test_adamw_refuses_parameters():
         with pytest.raises(ValueError, match=r"grads\[0\]"):
             op.step([g, None, None], 0.1)
     assert op.t == 0
+
+
+@pytest.mark.parametrize("K,N", [(64, 128), (33, 7), (1 << 20, 1 << 20)])
+@pytest.mark.parametrize("T", [0, 1, 2 ** 31 - 1])
+@pytest.mark.parametrize("act", [0, 3])
+def test_linear_scratch_of_the_extremes(T, K, N, act):
+    """No division by what may be 0, no size that wraps."""
+    L = _lib()
+    for dtype in (L.MOE_BF16, L.MOE_F32):
+        n = L.moe_linear_scratch_bytes(_linear(L, T=T, K=K, N=N, dtype=dtype, act=act))
+        assert n >= (T * N * (2 if dtype else 4) if act else 1)
