@@ -5,8 +5,12 @@
 //   a group's score: the sum of its group_top largest c (of s where there is no bias)
 //   the topk_groups best groups, in them the k largest c, ties to the lower id
 //   q_j = s_j / sum_i s_i over the chosen (renorm), or s_j;  w_j = scale q_j
-// A choice is decided where two c differ in their last bits, so c is compared in fp64; the
-// weights and gradients are fp32.
+//
+// A choice is decided where two c differ in their last bits, so c is compared in fp64.  That
+// takes 5 times as long as fp32 (16384 x 256 in 8 groups: 56 us against FWD_US us), so a token is
+// routed in fp32 first, with a bound on what fp32 has got wrong; only where two neighbours of the
+// order, or the last open group and the first closed one, lie within it is the token routed
+// again in fp64 (one in some hundreds, on ordinary logits).
 #include "row_lanes.h"
 
 namespace moe {
@@ -45,6 +49,23 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
+// 1 / n!, n = 13 .. 2, then log2 e and ln 2 in two parts: read as scalars, so that they take no
+// vector registers from the code around
+__constant__ double kExp[15] = {1.0 / 6227020800.0, 1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+                                1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0, 0.5,
+                                1.44269504088896340736, 0x1.62e42fefap-1, 0x1.cf79abc9e3b3ap-40};
+// exp(d), d <= 0 or NaN, to about 1 unit in the last place: d = n ln 2 + r, |r| <= 0.35, and the
+// series of exp(r) to r^13 / 13! (the next term is below 2^-57)
+__device__ __forceinline__ double exp_d(double d) {
+  const double n = rint(d * kExp[12]);
+  const double r = fma(-n, kExp[14], fma(-n, kExp[13], d));
+  double p = kExp[0];
+#pragma unroll
+  for (int i = 1; i < 12; ++i) p = fma(p, r, kExp[i]);
+  p = fma(fma(p, r, 1.0), r, 1.0);
+  return d < -746.0 ? 0.0 : ldexp(p, (int)n);
+}
+
 // exp_neg down to the smallest numbers: the hardware's exponential makes 0 of what lies below
 // 2^-126, so the lower half is taken 2^64 higher (h + 64 is exact) and brought back
 __device__ __forceinline__ float exp_low(float d) {
@@ -57,10 +78,6 @@ __device__ __forceinline__ float exp_low(float d) {
   return d < -104.f ? 0.f : low ? q * 0x1p-64f : q;
 }
 
-__device__ __forceinline__ double sigmoid_d(double l) {
-  const double e = exp(-fabs(l));
-  return (l >= 0.0 ? 1.0 : e) / (1.0 + e);
-}
 // sigmoid(l) and 1 - sigmoid(l), each to its own last bits; NaN gives NaN
 __device__ __forceinline__ void sigmoid2(float l, float& s, float& r) {
   const float e = exp_low(-fabsf(l)), d = 1.f / (1.f + e);
@@ -68,12 +85,49 @@ __device__ __forceinline__ void sigmoid2(float l, float& s, float& r) {
   r = l >= 0.f ? e * d : d;
 }
 
+// Over the 16 lanes of a row by rotations (vector ALU alone), beyond them by exchanges; every
+// lane gets the same bits, as each step adds the same two values on both sides
+template <int N>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xf, 0xf, false);
+}
+template <int LPR, class F>
+__device__ __forceinline__ float fold(float v, F&& f) {
+  v = f(v, __uint_as_float(row_ror<8>(__float_as_uint(v))));
+  v = f(v, __uint_as_float(row_ror<4>(__float_as_uint(v))));
+  v = f(v, __uint_as_float(row_ror<2>(__float_as_uint(v))));
+  v = f(v, __uint_as_float(row_ror<1>(__float_as_uint(v))));
+  if constexpr (LPR == 64) {
+    v = f(v, __shfl_xor(v, 16, 64));
+    v = f(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ uint32_t fold_max(uint32_t v) {
+  v = max(v, row_ror<8>(v));
+  v = max(v, row_ror<4>(v));
+  v = max(v, row_ror<2>(v));
+  v = max(v, row_ror<1>(v));
+  if constexpr (LPR == 64) {
+    v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+    v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+  }
+  return v;
+}
+// the bits of a ballot that the lane's token has
+template <int LPR>
+__device__ __forceinline__ uint64_t token_bits(bool p) {
+  const uint64_t b = __ballot(p);
+  return LPR == 64 ? b : (b >> (threadIdx.x & 48)) & 0xffffull;
+}
+
 // The chosen experts' shares q of lanes sub < k (others 0) from their logits l: sigmoids over
 // their sum, scaled by exp(-min(max l, 0)) so that none of the largest underflows, or exp(l)
 // over its sum.  All of -inf: 0.
 template <int LPR>
 __device__ __forceinline__ float shares(float l, bool on, bool sigm) {
-  const float m = lanes_max<LPR>(on ? l : -__builtin_inff());
+  const float m = fold<LPR>(on ? l : -__builtin_inff(), [](float x, float y) { return fmaxf(x, y); });
   float z = 0.f;
   if (on && m != -__builtin_inff()) {
     if (sigm) {
@@ -84,151 +138,375 @@ __device__ __forceinline__ float shares(float l, bool on, bool sigm) {
     }
   }
   if (on && l != l) z = l;   // also where the row holds nothing but NaN
-  const float sum = group_sum<LPR>(z);
+  const float sum = fold<LPR>(z, [](float x, float y) { return x + y; });
   return sum == 0.f ? 0.f : z / sum;
 }
 
-template <int LPR, int NV>
-__global__ __launch_bounds__(GT) void k_gate_fwd(GateArgs a) {
-  constexpr int TOK = GT / LPR;
+// One token routed in fp64 by a whole wave (c and gscore: LDS of the wave); lane slot0 + j gets
+// the id of slot j.  Loops, not copies: it runs seldom, and its registers are everyone's.
+__device__ __forceinline__ void route_exact(const GateArgs& a, const float* row, int slot0, double* c, double* gscore,
+                                            int& my_id) {
+  const int lane = threadIdx.x & 63, E = a.E, per = E / a.groups;
+  const bool sigm = a.score == MOE_SCORE_SIGMOID, groups2 = a.groups > 1 && a.group_top > 1;
+  const bool scored = a.bias || groups2;
+  const double ninf = -__builtin_inf();
+  float m = 0.f;
+  double inv = 0.0;
+  if (scored && !sigm) {
+    m = -__builtin_inff();
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) m = fmaxf(m, row[e]);
+    m = lanes_max<64>(m);
+    if (m == -__builtin_inff()) m = 0.f;
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) sum += exp_d((double)row[e] - (double)m);
+    sum = lanes_sum<64>(sum);
+    inv = sum > 0.0 ? 1.0 / sum : sum;   // NaN stays
+  }
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) {
+    const float l = row[e];
+    double s = l;
+    if (scored) {
+      const double x = exp_d(sigm ? -fabs((double)l) : (double)l - (double)m);
+      s = sigm ? (l >= 0.f ? 1.0 : x) / (1.0 + x) : x * inv;
+      if (a.bias) s += (double)a.bias[e];
+    }
+    c[e] = l > -__builtin_inff() && s == s ? s : ninf;   // masked or not a number: behind every other
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  uint64_t open = ~0ull;
+  if (a.groups > 1) {
+    double s = ninf;
+    if (lane < a.groups) {
+      double b1 = ninf, b2 = ninf;
+#pragma unroll 1
+      for (int e = lane * per; e < (lane + 1) * per; ++e) {
+        b2 = fmax(b2, fmin(b1, c[e]));
+        b1 = fmax(b1, c[e]);
+      }
+      s = groups2 ? b1 + b2 : b1;
+      if (s != s) s = ninf;
+      gscore[lane] = s;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    int rank = 0;   // a group is open if fewer than topk_groups are better
+#pragma unroll 1
+    for (int o = 0; o < a.groups; ++o) rank += better(gscore[o], o, s, lane);
+    open = __ballot(lane < a.groups && rank < a.topk_groups);
+    if (!a.bias && groups2) {   // in the groups the logits order the experts
+#pragma unroll 1
+      for (int e = lane; e < E; e += 64) c[e] = row[e] == row[e] ? (double)row[e] : ninf;
+    }
+  }
+  uint32_t left = 0;   // which of the lane's experts can be chosen
+#pragma unroll 1
+  for (int e = lane, i = 0; e < E; e += 64, ++i)
+    if (a.groups == 1 || (open >> (e / per) & 1)) left |= 1u << i;
+#pragma unroll 1
+  for (int n = 0; n < a.k; ++n) {
+    double bv = ninf;
+    int bid = kPadId;
+#pragma unroll 1
+    for (int e = lane, i = 0; e < E; e += 64, ++i)
+      if ((left >> i & 1) && better(c[e], e, bv, bid)) {
+        bv = c[e];
+        bid = e;
+      }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      const double ov = __shfl_xor(bv, off, 64);
+      const int oid = __shfl_xor(bid, off, 64);
+      if (better(ov, oid, bv, bid)) {
+        bv = ov;
+        bid = oid;
+      }
+    }
+    if ((bid & 63) == lane) left &= ~(1u << (bid >> 6));
+    if (lane == slot0 + n) my_id = bid;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// fp32 numbers as whole ones in the same order, above 0; the low bits give way to a slot's place
+__device__ __forceinline__ uint32_t sortable(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unsorted(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+// What orders an expert, in fp64; NaN and masked ones as -inf
+struct Exact {
+  const float* row;
+  const float* bias;   // or null
+  bool scored, sigm;
+  float m;             // softmax: the row's largest, and 1 / sum exp(l - m)
+  double inv;
+  __device__ __forceinline__ double operator()(int e) const {
+    const float l = row[e];
+    double s = l;
+    if (scored) {
+      const double x = exp_d(sigm ? -fabs((double)l) : (double)l - (double)m);
+      s = sigm ? (l >= 0.f ? 1.0 : x) / (1.0 + x) : x * inv;
+      if (bias) s += (double)bias[e];
+    }
+    return l > -__builtin_inff() && s == s ? s : -__builtin_inf();
+  }
+};
+
+// A lane's 4 NV columns are kept as keys: the sortable c with its low 4 bits replaced by the
+// column's place in the lane, 0 for what cannot be chosen.  A maximum of keys then needs no
+// ids: the place is in the key, the lane from a ballot.  What the cut costs (16 units in the last
+// place) is counted with fp32's own errors, u = 2^-24:
+//   sigmoid: 4 u;  softmax: s (|l - m| + 12) u with s |l - m| <= 0.37 and s at most the row's largest,
+//   taken as 2^-19 of that (|l - m| < 20: what is smaller is below any of it);  the sum with b: u |c|
+// Two c that differ by more than the two bounds together are in order.  k + 2 rounds give the
+// order of the first k + 2: where the k-th and the next, or that one and the next, are apart, the
+// first k or k + 1 are the right set, and they are put in order in fp64, a lane each.  Else (ties)
+// the whole token is routed again.
+template <int LPR, int NV, bool GROUPS>
+__global__ __launch_bounds__(GT, 4) void k_gate_fwd(GateArgs a) {
+  constexpr int TOK = GT / LPR, COLS = 4 * LPR * NV;
   __shared__ int hist[1024];
-  __shared__ double gscore[TOK][kMaxGroups];
-  const int sub = threadIdx.x % LPR, group = threadIdx.x / LPR;
+  __shared__ float cs[GROUPS ? TOK : 1][GROUPS ? COLS + 4 : 1];     // the c of a token's experts
+  __shared__ double gscore[GROUPS ? TOK : 1][GROUPS ? kMaxGroups : 1];
+  __shared__ double ce[GT / 64][COLS], ge[GT / 64][GROUPS ? kMaxGroups : 1];
+  __shared__ int order[TOK][17];
+  const int group = threadIdx.x / LPR;
   const int E = a.E, k = a.k;
   const bool sigm = a.score == MOE_SCORE_SIGMOID, count = a.part_c != nullptr;
-  const double ninf = -__builtin_inf();
+  const float inf = __builtin_inff();
+  const bool groups2 = GROUPS && a.group_top > 1, scored = a.bias || groups2;
+  const int per = GROUPS ? E / a.groups : E;
   if (count) {
     for (int e = threadIdx.x; e < E; e += GT) hist[e] = 0;
     __syncthreads();
   }
-  for (int64_t t = (int64_t)blockIdx.x * TOK + group; t < a.T; t += (int64_t)gridDim.x * TOK) {
-    if (a.mask && a.mask[t] == 0) {
-      if (sub < k) {
-        a.idx[t * k + sub] = -1;
-        a.w[t * k + sub] = 0.f;
-      }
-      continue;
-    }
+  for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < a.T; t0 += (int64_t)gridDim.x * TOK) {
+    // what follows from the lane's place is worked out anew, not kept in registers over the loop
+    int sub = threadIdx.x % LPR;
+    asm volatile("" : "+v"(sub));
+    const int64_t t = t0 + group < a.T ? t0 + group : a.T - 1;   // all lanes stay
+    const bool there = t0 + group < a.T, live = there && (!a.mask || a.mask[t] != 0);
     const float* row = a.logits + (size_t)t * E;
-    float v[NV][4];
-    load_row<LPR, NV>(row, sub, E, -__builtin_inff(), v);
-    double c[NV][4];
-    float m = -__builtin_inff();
-    double sum = 0.0;
-    const bool scored = a.bias || (a.groups > 1 && a.group_top > 1);
+    float c[NV][4];
+    float m = -inf, sum = 0.f, err = 0.f;
+    load_row<LPR, NV>(row, sub, E, -inf, c);
     if (!sigm && (scored || !a.renorm)) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i][j]);
-      m = lanes_max<LPR>(m);
-      if (m == -__builtin_inff()) m = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          c[i][j] = exp((double)v[i][j] - (double)m);
-          sum += c[i][j];
-        }
-      sum = lanes_sum<LPR>(sum);
+        for (int j = 0; j < 4; ++j) m = fmaxf(m, c[i][j]);
+      m = fold<LPR>(m, [](float x, float y) { return fmaxf(x, y); });
+      if (m == -inf) m = 0.f;
     }
-    if (scored) {
-      const double inv = sum > 0.0 ? 1.0 / sum : sum;   // NaN stays
+    const float m0 = m;
+    // the scores; bit p of `out`: the lane's p-th expert is masked or not a number
+    uint32_t out = 0;
+    float p[NV][4];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int e = 4 * (sub + LPR * i) + j;
-          double s = sigm ? sigmoid_d((double)v[i][j]) : c[i][j] * inv;
-          if (a.bias && e < E) s += (double)a.bias[e];
-          // masked or not a number: behind every other
-          c[i][j] = v[i][j] > -__builtin_inff() && s == s ? s : ninf;
+      for (int j = 0; j < 4; ++j) {
+        const float l = c[i][j];
+        if (!(l > -inf)) out |= 1u << (4 * i + j);
+        if (sigm) {
+          const float e = exp_neg(-fabsf(l)), d = 1.f / (1.f + e);
+          p[i][j] = l >= 0.f ? d : e * d;
+        } else {
+          p[i][j] = exp_neg(l - m0);
+          sum += p[i][j];
         }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] = v[i][j] == v[i][j] ? (double)v[i][j] : ninf;
+      }
+      __builtin_amdgcn_sched_barrier(0);   // a few at a time: registers
     }
+    if (!sigm && (scored || !a.renorm)) sum = fold<LPR>(sum, [](float x, float y) { return x + y; });
+    const bool by_logit = !a.bias;   // in the groups, too
+    const float inv = sigm ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+    if (scored) err = sigm ? 0x1p-22f : 0x1p-19f * inv;   // (the row's largest score is inv)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {   // c: what orders the experts; what the groups go by to LDS
+      f32x4 u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool no = out >> (4 * i + j) & 1;
+        float s = 0.f;
+        if (scored) {
+          s = fmaf(p[i][j], inv, a.bias ? a.bias[min(4 * (sub + LPR * i) + j, E - 1)] : 0.f);
+          s = no || s != s ? -inf : s;
+        }
+        if (by_logit) c[i][j] = no ? -inf : c[i][j];
+        else c[i][j] = s;
+        u[j] = scored ? s : c[i][j];
+      }
+      if constexpr (GROUPS) *reinterpret_cast<f32x4*>(&cs[group][4 * (sub + LPR * i)]) = u;
+    }
+    const Exact exact0{row, a.bias, scored, sigm, m0, 0.0};
+    // 1 / sum exp(l - m) of the lanes' tokens in fp64 (softmax alone has one)
+    auto exact_of = [&]() {
+      Exact x = exact0;
+      if (scored && !sigm) {
+        double z = 0.0;
+#pragma unroll 1
+        for (int e = sub; e < E; e += LPR) z += exp_d((double)row[e] - (double)m0);
+        z = lanes_sum<LPR>(z);
+        x.inv = z > 0.0 ? 1.0 / z : z;   // NaN stays
+      }
+      return x;
+    };
+    bool whole = false;   // the token has to be routed again as a whole
     uint64_t open = ~0ull;
-    if (a.groups > 1) {
-      const int per = E / a.groups;
-      for (int g = 0; g < a.groups; ++g) {
-        double b1 = ninf, b2 = ninf;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 4 * (sub + LPR * i) + j;
-            if (e >= g * per && e < (g + 1) * per) {
-              b2 = fmax(b2, fmin(b1, c[i][j]));
-              b1 = fmax(b1, c[i][j]);
-            }
-          }
-#pragma unroll
-        for (int off = LPR / 2; off >= 1; off >>= 1) {
-          const double o1 = __shfl_xor(b1, off, 64), o2 = __shfl_xor(b2, off, 64);
-          b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-          b1 = fmax(b1, o1);
-        }
-        double s = a.group_top > 1 ? b1 + b2 : b1;
-        if (s != s) s = ninf;
-        if (sub == 0) gscore[group][g] = s;
-      }
+    if constexpr (GROUPS) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      // a group is open if fewer than topk_groups are better
+      // 2^h lanes to a group, so many groups at a time; low, high: the lowest open score and the
+      // highest closed one
+      int h = 0;
+      while ((a.groups << (h + 1)) <= LPR) ++h;
+      const int gl = 1 << h;
       uint64_t mine = 0;
-      for (int g = sub; g < a.groups; g += LPR) {
-        const double s = gscore[group][g];
-        int rank = 0;
-        for (int o = 0; o < a.groups; ++o) rank += better(gscore[group][o], o, s, g);
-        if (rank < a.topk_groups) mine |= 1ull << g;
-      }
+      double low = 0.0, high = 0.0, top = 0.0;
+      auto score_groups = [&](auto&& value) {
+        for (int g0 = 0; g0 < a.groups; g0 += LPR >> h) {
+          const int g = g0 + (sub >> h);
+          double b1 = -inf, b2 = -inf;
+          value(g, sub & (gl - 1), gl, b1, b2);
+#pragma unroll 1
+          for (int off = 1; off < gl; off <<= 1) {
+            const double o1 = __shfl_xor(b1, off, 64), o2 = __shfl_xor(b2, off, 64);
+            b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+            b1 = fmax(b1, o1);
+          }
+          if (g < a.groups && (sub & (gl - 1)) == 0) {
+            const double s = groups2 ? b1 + b2 : b1;
+            gscore[group][g] = s == s ? s : -inf;
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        mine = 0;
+        low = inf, high = -inf, top = 0.0;
+        for (int g = sub; g < a.groups; g += LPR) {   // open if fewer than topk_groups are better
+          const double s = gscore[group][g];
+          int rank = 0;
+#pragma unroll 4
+          for (int o = 0; o < a.groups; ++o) rank += better(gscore[group][o], o, s, g);
+          if (rank < a.topk_groups) {
+            mine |= 1ull << g;
+            low = fmin(low, s);
+          } else {
+            high = fmax(high, s);
+          }
+          top = fmax(top, fabs(s));
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int off = LPR / 2; off >= 1; off >>= 1) mine |= (uint64_t)__shfl_xor((unsigned long long)mine, off, 64);
+        for (int off = LPR / 2; off >= 1; off >>= 1) mine |= (uint64_t)__shfl_xor((unsigned long long)mine, off, 64);
+      };
+      score_groups([&](int g, int e0, int step, double& b1, double& b2) {
+        float x1 = -inf, x2 = -inf;
+        if (g < a.groups)
+#pragma unroll 4
+          for (int e = e0; e < per; e += step) {
+            const float x = cs[group][g * per + e];
+            x2 = fmaxf(x2, fminf(x1, x));
+            x1 = fmaxf(x1, x);
+          }
+        b1 = x1, b2 = x2;
+      });
       open = mine;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (!a.bias && a.group_top > 1) {   // in the groups the logits order the experts
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) c[i][j] = v[i][j] == v[i][j] ? (double)v[i][j] : ninf;
+      if (scored && a.topk_groups < a.groups) {   // logits alone have no error
+        const float lo = fold<LPR>((float)low, [](float x, float y) { return fminf(x, y); });
+        const float hi = fold<LPR>((float)high, [](float x, float y) { return fmaxf(x, y); });
+        const float tp = fold<LPR>((float)top, [](float x, float y) { return fmaxf(x, y); });
+        // two scores of two c each, and the roundings of the scores and sums here
+        const bool unsure = !(lo - hi > 4.f * err + tp * 0x1p-21f);
+        if (__ballot(unsure && live) != 0) {
+          const Exact x = exact_of();
+          score_groups([&](int g, int e0, int step, double& b1, double& b2) {
+            if (g < a.groups)
+#pragma unroll 1
+              for (int e = e0; e < per; e += step) {
+                const double y = x(g * per + e);
+                b2 = fmax(b2, fmin(b1, y));
+                b1 = fmax(b1, y);
+              }
+          });
+          if (unsure) open = mine;
+        }
       }
     }
-    bool taken[NV][4];
-    const int per = E / a.groups;
+    if (by_logit) err = 0.f;
+    uint32_t key[NV][4];
+    const float inv_per = 1.f / (float)per;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = 4 * (sub + LPR * i) + j;
-        taken[i][j] = e >= E || (a.groups > 1 && !(open >> (e / per) & 1));
+        bool in = e < E;
+        // e / per: (e + 1/2) / per lies 1 / (2 per) >= 2^-11 from a whole number, past its rounding
+        if constexpr (GROUPS) in = in && (open >> (int)(((float)e + 0.5f) * inv_per) & 1);
+        key[i][j] = in ? (sortable(c[i][j]) & ~15u) | (uint32_t)(4 * i + j) : 0u;
       }
     int my_id = 0;
-    for (int n = 0; n < k; ++n) {
-      double bv = ninf;
-      int bid = kPadId;
+    float last = 0.f;
+    bool near = false, at_k = false;   // neighbours among the first k, and the k-th and the next
+    for (int n = 0; n < k + 2; ++n) {
+      uint32_t best = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int e = 4 * (sub + LPR * i) + j;
-          if (!taken[i][j] && better(c[i][j], e, bv, bid)) { bv = c[i][j]; bid = e; }
-        }
-#pragma unroll
-      for (int off = LPR / 2; off >= 1; off >>= 1) {
-        const double ov = __shfl_xor(bv, off, 64);
-        const int oid = __shfl_xor(bid, off, 64);
-        if (better(ov, oid, bv, bid)) { bv = ov; bid = oid; }
+      for (int i = 0; i < NV; ++i) best = max(best, max(max(key[i][0], key[i][1]), max(key[i][2], key[i][3])));
+      const uint32_t all = fold_max<LPR>(best);
+      const float f = unsorted(all & ~15u);
+      // the cut takes at most 15 units of 2^-23 off, downwards as the order goes
+      if (n > 0 && all != 0) {
+        const bool close = !(last - f > 2.f * err + fmaxf(fabsf(last), fabsf(f)) * 0x1p-18f);
+        if (n < k) near |= close;
+        else if (n == k) at_k = close;
+        else whole |= at_k && close;
       }
+      last = f;
+      if (n == k + 1) break;
+      const uint64_t who = token_bits<LPR>(best == all);
+      if (n < k) near |= (who & (who - 1)) != 0;   // two lanes' keys alike
+      else at_k |= all != 0 && (who & (who - 1)) != 0;
+      whole |= all != 0 && (who & (who - 1)) != 0;
+      const int lane = LPR == 64 ? __builtin_ctzll(who) : __builtin_ctz((uint32_t)who);
+      const int place = (int)(all & 15u);
+      if (sub == n) my_id = all != 0 ? 4 * (lane + LPR * (place >> 2)) + (place & 3) : kPadId;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * (sub + LPR * i) + j == bid) taken[i][j] = true;
-      if (sub == n) my_id = bid;
+        for (int j = 0; j < 4; ++j) key[i][j] = key[i][j] == all ? 0u : key[i][j];
     }
-    const bool on = sub < k;
+    if (LPR == 16 && k == 16) whole |= at_k;   // no lane for the seventeenth
+    if (__ballot((near || at_k) && !whole && live) != 0) {
+      const Exact x = exact_of();
+      const int most = at_k && k < LPR ? k + 1 : k;   // the right set
+      const bool cand = sub < most && my_id != kPadId;
+      const double y = cand ? x(my_id) : 0.0;
+      int rank = 0;
+#pragma unroll 1
+      for (int n = 0; n <= k && n < LPR; ++n) {
+        const int src = (threadIdx.x & 63) - sub + n;
+        const double o = __shfl(y, src, 64);
+        const int oid = __shfl(cand ? my_id : kPadId, src, 64);
+        rank += oid != kPadId && better(o, oid, y, my_id);
+      }
+      if (cand) order[group][rank] = my_id;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if ((near || at_k) && sub < k) my_id = order[group][sub];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    for (uint64_t todo = __ballot(whole && live); todo != 0;) {   // token by token
+      const int slot0 = __builtin_ctzll(todo) / LPR * LPR;
+      todo &= LPR == 64 ? 0 : ~(0xffffull << slot0);
+      route_exact(a, a.logits + (size_t)__shfl(t, slot0, 64) * E, slot0, ce[threadIdx.x >> 6], ge[threadIdx.x >> 6],
+                  my_id);
+    }
+    // what is not live has not been routed again: its ids may be none
+    const bool on = sub < k && live;
     const float l = on ? row[my_id] : 0.f;
     float q;
     if (a.renorm) {
@@ -237,13 +515,12 @@ __global__ __launch_bounds__(GT) void k_gate_fwd(GateArgs a) {
       float r;
       sigmoid2(l, q, r);
     } else {
-      q = (float)(exp((double)l - (double)m) / sum);
-      if (sum == 0.0) q = 0.f;
+      q = sum == 0.f ? 0.f : exp_low(l - m0) / sum;
     }
-    if (on) {
-      a.idx[t * k + sub] = my_id;
-      a.w[t * k + sub] = a.scale * q;
-      if (count) atomicAdd(&hist[my_id], 1);
+    if (sub < k && there) {
+      a.idx[t * k + sub] = live ? my_id : -1;
+      a.w[t * k + sub] = live ? a.scale * q : 0.f;
+      if (count && live) atomicAdd(&hist[my_id], 1);
     }
   }
   if (count) {
@@ -260,6 +537,7 @@ __global__ __launch_bounds__(CT) void k_gate_counts(const int32_t* __restrict__ 
   const int e = blockIdx.x * 64 + (threadIdx.x & 63);
   int c = 0;
   if (e < E)
+    #pragma unroll 8
     for (int w = threadIdx.x >> 6; w < W; w += CT / 64) c += part_c[(size_t)w * E + e];
   red[threadIdx.x] = c;
   __syncthreads();
@@ -414,7 +692,9 @@ hipError_t launch_gate_fwd(const moe_gate_shape& s, const float* logits, const f
   a.part_c = counts ? part_c : nullptr;
   const unsigned W = counts ? (unsigned)gate_parts(s.T, s.E) : (unsigned)ceil_div(s.T, tokens_of(s.E));
   if (W > 0) {
-#define CALL(LPR, NV) MOE_LAUNCH("gate_fwd", (k_gate_fwd<LPR, NV>), dim3(W), dim3(GT), 0, st, a)
+#define CALL(LPR, NV)                                                                              \
+  if (s.groups > 1) MOE_LAUNCH("gate_fwd", (k_gate_fwd<LPR, NV, true>), dim3(W), dim3(GT), 0, st, a); \
+  else MOE_LAUNCH("gate_fwd", (k_gate_fwd<LPR, NV, false>), dim3(W), dim3(GT), 0, st, a)
     GATE_DISPATCH(s.E, CALL);
 #undef CALL
   }

@@ -114,6 +114,25 @@ def test_gate_near_ties():
                 assert np.array_equal(_n(op.counts), counts)
 
 
+@pytest.mark.parametrize("T", [1, 5, 16, 37])
+@pytest.mark.parametrize("E,k,groups,top,gt", [(16, 16, 1, 1, 1), (24, 8, 3, 1, 2), (256, 16, 8, 2, 2), (600, 9, 1, 1, 1),
+                                               (64, 4, 16, 1, 2), (8, 8, 2, 2, 1)])
+def test_gate_of_equal_rows(T, E, k, groups, top, gt):
+    """Nothing but ties, also in tokens that the mask leaves out and in a workgroup's places
+    past the last token; and tokens of which the open groups are taken whole."""
+    mask = (torch.arange(T) % 3 != 1).to(torch.uint8)
+    for logits in (torch.zeros(T, E), torch.full((T, E), -float("inf")), torch.full((T, E), float("nan"))):
+        for score in (0, 1):
+            for biased in (False, True):
+                op = _gate(T, E, k, groups, top, gt, score, 1, 1.0)
+                bias = torch.zeros(E) if biased else None
+                op.forward(logits.cuda(), bias=_c(bias), mask=mask.cuda(), count=True)
+                torch.cuda.synchronize()
+                idx, _, counts = os_.gate_forward(logits.double().numpy(), _n(bias), _n(mask), k, score, groups=groups,
+                                                  topk_groups=top, group_top=gt)
+                assert np.array_equal(_n(op.topk_idx), idx) and np.array_equal(_n(op.counts), counts)
+
+
 @pytest.mark.parametrize("score", [0, 1])
 @pytest.mark.parametrize("spread", [30.0, 300.0])
 def test_gate_of_wide_logits(score, spread):
