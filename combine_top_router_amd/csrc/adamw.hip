@@ -53,49 +53,79 @@ __host__ __device__ inline uint32_t step_key(uint64_t seed, int64_t t) {
   return mix((uint32_t)t + mix((uint32_t)seed + mix((uint32_t)(seed >> 32))));
 }
 
-// y >= 0 (at most 448) on the grid of E4M3, up with r / 2^16 below the part that is cut off
-__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t r) {
-  const int e = max((int)(__float_as_uint(y) >> 23) - 127, -6);
-  const float n = ldexpf(y, 3 - e), low = floorf(n);
-  return ldexpf(low + ((float)r < (n - low) * 65536.f ? 1.f : 0.f), e - 3);
+// The E4M3 code of y >= 0 (at most 448), up with r16 / 2^16 below the part that is cut off.  From
+// 2^-6 on the code is the fp32 number's exponent and upper 3 bits, less 960 for the bias; 20
+// bits are cut.  Below, the grid is that of 2^-9: y 2^29 cuts the same 20 bits (rounded up to
+// a whole number, which leaves every comparison with 16 r16 as it is).  Adding 2^20 - 1 - 16 r16
+// carries where the cut part is above 16 r16.
+__device__ __forceinline__ uint32_t e4m3_stochastic(float y, uint32_t room) {   // room = 2^20 - 1 - 16 r16
+  const uint32_t norm = __float_as_uint(y) - (960u << 20), sub = (uint32_t)ceilf(y * 0x1p29f);
+  return ((y < 0x1p-6f ? sub : norm) + room) >> 20;
 }
 
+// 2^X, X in -127 .. 127
+__device__ __forceinline__ float power(int X) { return __uint_as_float(X > -127 ? (uint32_t)(X + 127) << 23 : 0x400000u); }
+
 // The 8 values of a thread, 4 threads to a block of 32, as codes and the block's scale.
-// What is not finite becomes NaN and does not move the scale.
-template <bool ROOT>
-__device__ __forceinline__ void encode(const float (&x)[VEC], const uint32_t (&r)[VEC], bool stochastic, uint2& codes,
+// What is not finite becomes NaN and does not move the scale; FINITE: nothing is.
+template <bool ROOT, bool FINITE>
+__device__ __forceinline__ void encode(const float (&x)[VEC], const uint32_t (&h)[VEC], bool stochastic, uint2& codes,
                                        int& X) {
   float am = 0.f;
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     const float a = fabsf(x[i]);
-    am = fmaxf(am, a < __builtin_inff() ? a : 0.f);
+    am = fmaxf(am, FINITE || a < __builtin_inff() ? a : 0.f);
   }
   am = fmaxf(am, __shfl_xor(am, 1, 64));
   am = fmaxf(am, __shfl_xor(am, 2, 64));
   X = mx_scale_exp(am);
-  float y[VEC];
+  const float inv = power(-X);
+  uint32_t c[VEC];
+  if (stochastic) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const uint32_t r = ROOT ? h[i] >> 16 : h[i] & 0xffffu;
+      float a = fabsf(x[i]);
+      if (!FINITE) a = a < __builtin_inff() ? a : 0.f;
+      c[i] = e4m3_stochastic(a * inv, ((r ^ 0xffffu) << 4) | 15u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      const float a = FINITE || fabsf(x[i]) < __builtin_inff() ? fabsf(x[i]) : 0.f;
+      const float b = FINITE || fabsf(x[i + 1]) < __builtin_inff() ? fabsf(x[i + 1]) : 0.f;
+      const uint32_t w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+      c[i] = w & 0xffu;
+      c[i + 1] = w >> 8 & 0xffu;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    float a = fabsf(x[i]);
-    const bool fin = a < __builtin_inff();
-    a = ldexpf(a, -X);
-    if (stochastic) a = e4m3_stochastic(fin ? a : 0.f, ROOT ? r[i] >> 16 : r[i] & 0xffffu);
-    if (ROOT && x[i] > 0.f && a < 0x1p-9f) a = 0x1p-9f;
-    y[i] = fin ? copysignf(a, x[i]) : __builtin_nanf("");
+    if (ROOT) c[i] = max(c[i], min(__float_as_uint(x[i]), 1u));   // what is above 0 stays above 0
+    else c[i] |= __float_as_uint(x[i]) >> 24 & 0x80u;
+    if (!FINITE && !(fabsf(x[i]) < __builtin_inff())) c[i] = 0x7fu;
   }
-  codes.x = e4m3_pack4(y[0], y[1], y[2], y[3], 0);
-  codes.y = e4m3_pack4(y[4], y[5], y[6], y[7], 0);
+  codes.x = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+  codes.y = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
 }
 
 __device__ __forceinline__ void decode(uint2 c, int X, float (&x)[VEC]) {
+  const float f = power(X);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int w = (int)(h ? c.y : c.x);
     const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
-    x[4 * h] = ldexpf(lo[0], X); x[4 * h + 1] = ldexpf(lo[1], X);
-    x[4 * h + 2] = ldexpf(hi[0], X); x[4 * h + 3] = ldexpf(hi[1], X);
+    x[4 * h] = lo[0] * f; x[4 * h + 1] = lo[1] * f;
+    x[4 * h + 2] = hi[0] * f; x[4 * h + 3] = hi[1] * f;
   }
+}
+
+// the root by the hardware's (1 ulp), of numbers below 2^-96 by that of 2^64 times them
+__device__ __forceinline__ float root(float v) {
+  const bool low = v < 0x1p-96f;
+  const float s = __builtin_amdgcn_sqrtf(low ? v * 0x1p64f : v);
+  return low ? s * 0x1p-32f : s;
 }
 
 // elements i .. i + 7 of a tensor of n; whole: all inside and the address at a multiple of 16
@@ -148,13 +178,13 @@ __device__ __forceinline__ void store8_bf16(bf16_t* q, int64_t left, bool whole,
   }
 }
 
-// bf16 bits of x: towards 0 after 16 random bits were added below; NaN stays, and what would
+// bf16 bits of x: towards 0 after 16 random bits were added below; NaN stays, and what could
 // round past the largest number does not
 __device__ __forceinline__ uint32_t bf16_stochastic(float x, uint32_t r) {
-  const uint32_t u = __float_as_uint(x), a = u & 0x7fffffffu;
-  if (a >= 0x7f800000u) return (u >> 16) | (a > 0x7f800000u ? 0x40u : 0u);
-  const uint32_t up = (u + r) >> 16;
-  return (up & 0x7fffu) == 0x7f80u ? u >> 16 : up;
+  const uint32_t u = __float_as_uint(x);
+  const bool top = (u & 0x7fffffffu) >= 0x7f7f0001u;
+  if (top && x != x) return u >> 16 | 0x40u;
+  return (top ? u : u + r) >> 16;
 }
 
 template <bool S8>
@@ -168,11 +198,11 @@ __global__ __launch_bounds__(AT) void k_adamw(AdamwTable tab, AdamwHyper h) {
   }
   const moe_adamw_tensor& T = tab.t[lo];
   const int64_t n = T.n, i = (int64_t)(blockIdx.x - tab.first[lo]) * CHUNK + (int64_t)threadIdx.x * VEC;
-  float rate = h.rate, root = h.root, decay = h.decay;
+  float rate = h.rate, unbias = h.root, decay = h.decay;
   uint32_t key = h.key;
   if (h.clock) {
     rate = h.rate * h.clock->to_m;   // h.rate: the rate itself
-    root = h.clock->root;
+    unbias = h.clock->root;
     key = h.clock->key;
   }
   if (h.lr) {
@@ -206,21 +236,23 @@ __global__ __launch_bounds__(AT) void k_adamw(AdamwTable tab, AdamwHyper h) {
     load8(T.v, MOE_F32, i, n, full, v);
   }
   float s[VEC];
+  float probe = 0.f;   // stays 0 where every root and parameter is finite, and with them m
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
     const float gj = g[j] * gs;
     m[j] = h.b1 * m[j] + h.b1c * gj;
     v[j] = h.b2 * v[j] + h.b2c * (gj * gj);
-    s[j] = sqrtf(v[j]);
-    p[j] = p[j] * decay - rate * m[j] / (s[j] * root + h.eps);
+    s[j] = root(v[j]);
+    p[j] = p[j] * decay - rate * m[j] * __builtin_amdgcn_rcpf(fmaf(s[j], unbias, h.eps));
+    if constexpr (S8) probe = fmaf(s[j], 0.f, fmaf(m[j], 0.f, probe));
   }
   uint32_t r[VEC];
   if (h.stochastic) {
+    // the upper half of the place changes once in the thread's 8 at most
+    const uint64_t at = (uint64_t)T.at + (uint64_t)i;
+    const uint32_t lo = (uint32_t)at, k0 = mix((uint32_t)(at >> 32) + key), k1 = mix((uint32_t)(at >> 32) + 1u + key);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const uint64_t at = (uint64_t)T.at + (uint64_t)(i + j);
-      r[j] = mix((uint32_t)at ^ mix((uint32_t)(at >> 32) + key));
-    }
+    for (int j = 0; j < VEC; ++j) r[j] = mix((lo + j) ^ (lo + j >= lo ? k0 : k1));
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) r[j] = 0;
@@ -228,8 +260,13 @@ __global__ __launch_bounds__(AT) void k_adamw(AdamwTable tab, AdamwHyper h) {
   if constexpr (S8) {
     uint2 cm, cv;
     int Xm, Xv;
-    encode<false>(m, r, h.stochastic != 0, cm, Xm);
-    encode<true>(s, r, h.stochastic != 0, cv, Xv);
+    if (__ballot(probe != 0.f) == 0) {
+      encode<false, true>(m, r, h.stochastic != 0, cm, Xm);
+      encode<true, true>(s, r, h.stochastic != 0, cv, Xv);
+    } else {
+      encode<false, false>(m, r, h.stochastic != 0, cm, Xm);
+      encode<true, false>(s, r, h.stochastic != 0, cv, Xv);
+    }
     if (left > 0) {
       *reinterpret_cast<uint2*>((uint8_t*)T.m + i) = cm;
       *reinterpret_cast<uint2*>((uint8_t*)T.v + i) = cv;

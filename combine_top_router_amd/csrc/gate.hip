@@ -682,7 +682,7 @@ GateArgs gate_args(const moe_gate_shape& s, const float* logits) {
 // Workgroups of a counting forward, each with a share of the counts
 int gate_parts(int T, int E) {
   const int64_t w = ceil_div(T, tokens_of(E));
-  return (int)(w < 1 ? 1 : w > 512 ? 512 : w);
+  return (int)(w < 1 ? 1 : w > 1024 ? 1024 : w);
 }
 
 hipError_t launch_gate_fwd(const moe_gate_shape& s, const float* logits, const float* bias, const uint8_t* mask,

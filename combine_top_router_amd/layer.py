@@ -390,8 +390,9 @@ class AdamW(_OnDevice):
         self._ptrs = [p.data_ptr() for p in params]
         self._shapes = [p.shape for p in params]
         self._table = (L.MoeAdamwTensor * len(params))()
+        self._entries = list(self._table)   # views of it
         width = 1 if eight else 4
-        for i, (p, at, e) in enumerate(zip(params, self._at, self._table)):
+        for i, (p, at, e) in enumerate(zip(params, self._at, self._entries)):
             e.p, e.m, e.v = self._ptrs[i], self.m.data_ptr() + at * width, self.v.data_ptr() + at * width
             if eight:
                 e.m_scale, e.v_scale = self.m_scale.data_ptr() + at // 32, self.v_scale.data_ptr() + at // 32
@@ -434,9 +435,9 @@ class AdamW(_OnDevice):
         if len(grads) != len(self.params):
             raise ValueError(f"grads: expected {len(self.params)}, got {len(grads)}")
         index, codes = self._index, self._codes
-        for i, (g, e, p, ptr, shape) in enumerate(zip(grads, self._table, self.params, self._ptrs, self._shapes)):
-            if p.data_ptr() != ptr or p.shape != shape:
-                raise ValueError(f"params[{i}] has been given other memory or another shape")
+        for i, (g, e, p, ptr, shape) in enumerate(zip(grads, self._entries, self.params, self._ptrs, self._shapes)):
+            if p.data_ptr() != ptr:
+                raise ValueError(f"params[{i}] has been given other memory")
             if g is None:
                 e.g = 0
                 continue
