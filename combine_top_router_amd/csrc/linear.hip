@@ -11,67 +11,80 @@ namespace moe {
 namespace {
 
 // ---------------- any size, any alignment ----------------
-// 64 x 64 tiles of four waves, K steps of 32 staged element by element.
+// 64 x 64 tiles of four waves, K steps of 32 staged element by element: the next step's loads are
+// under way while one is multiplied, one barrier a step.  With few tiles K is split, and the
+// shares, fp32 [share, M, N], are added in order by a second launch with the epilogue.
 constexpr int GTILE = 64, GSTEP = 32;
 
 template <typename T> struct gstage;
 template <> struct gstage<bf16_t> { static constexpr int LD = GSTEP + 8; };
 template <> struct gstage<float> { static constexpr int LD = GSTEP + 1; };
 
-// C [M, N] = A B over K.  A element (m, k) at m * am + k * ak, B element (k, n) at k * bk + n * bn.
+// C [M, N] = A B over K.  A element (m, k) at m * am + k * ak, B element (k, n) at k * bk + n * bn;
+// of each pair of strides one is 1.
 template <typename T>
 struct GeneralArgs {
   const T* a;
   const T* b;
   int64_t am, ak, bk, bn;
   int64_t M, N, K;
+  int64_t ks;     // of K a share, a multiple of GSTEP
+  float* part;    // or null: one share
   Epilogue<T> e;
 };
 
 template <typename T>
 __global__ __launch_bounds__(256) void k_linear_any(GeneralArgs<T> g) {
   constexpr int LD = gstage<T>::LD;
-  __shared__ __attribute__((aligned(16))) T as[GTILE][LD];   // [m][k]
-  __shared__ __attribute__((aligned(16))) T bs[GTILE][LD];   // [n][k]
+  __shared__ __attribute__((aligned(16))) T as[2][GTILE][LD];   // [m][k]
+  __shared__ __attribute__((aligned(16))) T bs[2][GTILE][LD];   // [n][k]
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int64_t m0 = (int64_t)blockIdx.x * GTILE, n0 = (int64_t)blockIdx.y * GTILE;
+  const int64_t m0 = (int64_t)blockIdx.x * GTILE, n0 = (int64_t)blockIdx.y * GTILE, k0 = blockIdx.z * g.ks;
+  const int64_t k1 = min(g.K, k0 + g.ks);
   const int wm = (wv & 1) * 32, wn = (wv >> 1) * 32;
+  // neighbouring threads along the axis that is contiguous: the thread's first place, and what
+  // each of its eight further ones adds
+  const bool ka = g.ak == 1, kb = g.bk == 1;
+  const int am = ka ? tid >> 5 : tid & 63, ak = ka ? tid & 31 : tid >> 6, dam = ka ? 8 : 0, dak = ka ? 0 : 4;
+  const int bn = kb ? tid >> 5 : tid & 63, bk = kb ? tid & 31 : tid >> 6, dbn = kb ? 8 : 0, dbk = kb ? 0 : 4;
+  const T* pa = g.a + (m0 + am) * g.am + (k0 + ak) * g.ak;
+  const T* pb = g.b + (k0 + bk) * g.bk + (n0 + bn) * g.bn;
+  const int64_t sa = dam * g.am + dak * g.ak, sb = dbk * g.bk + dbn * g.bn;
   f32x16 acc;
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-  for (int64_t k0 = 0; k0 < g.K; k0 += GSTEP) {
-    T ra[8], rb[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {   // neighbouring threads along the axis that is contiguous
-      const int s = tid + 256 * q;
-      const int am = g.ak == 1 ? s >> 5 : s & 63, ak = g.ak == 1 ? s & 31 : s >> 6;
-      const int bn = g.bk == 1 ? s >> 5 : s & 63, bk = g.bk == 1 ? s & 31 : s >> 6;
-      ra[q] = m0 + am < g.M && k0 + ak < g.K ? g.a[(m0 + am) * g.am + (k0 + ak) * g.ak] : (T)0;
-      rb[q] = n0 + bn < g.N && k0 + bk < g.K ? g.b[(k0 + bk) * g.bk + (n0 + bn) * g.bn] : (T)0;
-    }
-    __syncthreads();
+  T ra[8], rb[8];
+  auto load = [&](int64_t k) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int s = tid + 256 * q;
-      const int am = g.ak == 1 ? s >> 5 : s & 63, ak = g.ak == 1 ? s & 31 : s >> 6;
-      const int bn = g.bk == 1 ? s >> 5 : s & 63, bk = g.bk == 1 ? s & 31 : s >> 6;
-      as[am][ak] = ra[q];
-      bs[bn][bk] = rb[q];
+      ra[q] = m0 + am + q * dam < g.M && k + ak + q * dak < k1 ? pa[(k - k0) * g.ak + q * sa] : (T)0;
+      rb[q] = n0 + bn + q * dbn < g.N && k + bk + q * dbk < k1 ? pb[(k - k0) * g.bk + q * sb] : (T)0;
     }
-    __syncthreads();
+  };
+  if (k0 < k1) load(k0);
+  int st = 0;
+  for (int64_t k = k0; k < k1; k += GSTEP, st ^= 1) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      as[st][am + q * dam][ak + q * dak] = ra[q];
+      bs[st][bn + q * dbn][bk + q * dbk] = rb[q];
+    }
+    __syncthreads();   // the other stage's readers are past it: they have met this barrier since
+    if (k + GSTEP < k1) load(k + GSTEP);
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int kk = 0; kk < GSTEP; kk += 16) {
-        const int k = kk + (lane >> 5) * 8;
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(&as[wm + (lane & 31)][k]),
-                                                      *reinterpret_cast<const bf16x8*>(&bs[wn + (lane & 31)][k]), acc,
-                                                      0, 0, 0);
+        const int c = kk + (lane >> 5) * 8;
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(&as[st][wm + (lane & 31)][c]),
+                                                      *reinterpret_cast<const bf16x8*>(&bs[st][wn + (lane & 31)][c]),
+                                                      acc, 0, 0, 0);
       }
     } else {
 #pragma unroll
       for (int kk = 0; kk < GSTEP; kk += 2) {
-        const int k = kk + (lane >> 5);
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as[wm + (lane & 31)][k], bs[wn + (lane & 31)][k], acc, 0, 0, 0);
+        const int c = kk + (lane >> 5);
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as[st][wm + (lane & 31)][c], bs[st][wn + (lane & 31)][c], acc, 0, 0,
+                                                   0);
       }
     }
   }
@@ -80,18 +93,109 @@ __global__ __launch_bounds__(256) void k_linear_any(GeneralArgs<T> g) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const int64_t m = m0 + wm + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
-    if (m < g.M) g.e.store(m, n, g.N, acc[j]);
+    if (m >= g.M) continue;
+    if (g.part) g.part[(blockIdx.z * g.M + m) * g.N + n] = acc[j];
+    else g.e.store(m, n, g.N, acc[j]);
   }
 }
 
 template <typename T>
+__global__ __launch_bounds__(256) void k_linear_any_join(GeneralArgs<T> g, int splits) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, size = g.M * g.N;
+  if (i >= size) return;
+  float s = 0.f;
+#pragma unroll 4
+  for (int sp = 0; sp < splits; ++sp) s += g.part[sp * size + i];
+  g.e.store(i / g.N, i % g.N, g.N, s);
+}
+
+// shares of K: two workgroups for each CU, of four steps at least
+int general_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ceil_div(M, GTILE) * ceil_div(N, GTILE);
+  if (tiles == 0) return 1;
+  int64_t s = 2 * gemm_cus() / tiles;
+  s = s < K / (4 * GSTEP) ? s : K / (4 * GSTEP);
+  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+}
+size_t general_part_bytes(int64_t M, int64_t N, int64_t K) {
+  const int s = general_splits(M, N, K);
+  return s == 1 ? 0 : (size_t)s * M * N * 4;
+}
+
+template <typename T>
 hipError_t general(const char* name, const T* a, const T* b, int64_t am, int64_t ak, int64_t bk, int64_t bn, int64_t M,
-                   int64_t N, int64_t K, const Epilogue<T>& e, hipStream_t st) {
+                   int64_t N, int64_t K, const Epilogue<T>& e, float* part, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
-  const GeneralArgs<T> g{a, b, am, ak, bk, bn, M, N, K, e};
-  MOE_LAUNCH(name, k_linear_any<T>, dim3((unsigned)ceil_div(M, GTILE), (unsigned)ceil_div(N, GTILE)), dim3(256), 0, st,
-             g);
+  int splits = general_splits(M, N, K);
+  const int64_t ks = ceil_div(ceil_div(K, splits), GSTEP) * GSTEP;
+  splits = ks > 0 ? (int)ceil_div(K, ks) : 1;
+  const GeneralArgs<T> g{a, b, am, ak, bk, bn, M, N, K, ks, splits > 1 ? part : nullptr, e};
+  MOE_LAUNCH(name, k_linear_any<T>,
+             dim3((unsigned)ceil_div(M, GTILE), (unsigned)ceil_div(N, GTILE), (unsigned)splits), dim3(256), 0, st, g);
+  if (splits > 1)
+    MOE_LAUNCH("linear_join", k_linear_any_join<T>, dim3((unsigned)ceil_div(M * N, 256)), dim3(256), 0, st, g, splits);
   return hipGetLastError();
+}
+
+// ---------------- few rows ----------------
+// Up to FEW rows (the tokens of a decode step): W is read once, and that is what counts.  A
+// workgroup takes 16 columns, two lanes of 8, and all of K, 256 of its rows at a time; its sums
+// meet by lane exchanges and through LDS, so one launch does, without shares in memory.
+constexpr int FEW = 4, FT = 512, FC = 16;
+
+template <typename T, bool WIDE, int ROWS>
+__global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, const T* __restrict__ w, int rows, int K, int N,
+                                                   Epilogue<T> e) {
+  __shared__ float red[FT / 64][ROWS][FC];
+  // neighbouring column blocks, which share lines of memory, on one XCD
+  const int blocks = (N + FC - 1) / FC, xcd = blockIdx.x & 7;
+  const int lo = (int)((int64_t)blocks * xcd >> 3), hi = (int)((int64_t)blocks * (xcd + 1) >> 3);
+  const int block = lo + (int)(blockIdx.x >> 3);
+  if (block >= hi) return;
+  const int n0 = block * FC, c = (threadIdx.x & 1) * 8, n = n0 + c, kl = threadIdx.x >> 1;
+  float acc[ROWS][8];
+#pragma unroll
+  for (int t = 0; t < ROWS; ++t)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[t][j] = 0.f;
+  if (n < N)
+#pragma unroll 8
+    for (int k = kl; k < K; k += FT / 2) {
+      float v[8];
+      load8<T, WIDE>(w + (int64_t)k * N + n, N - n, v);
+#pragma unroll
+      for (int t = 0; t < ROWS; ++t) {
+        const float xv = elem<T>::load(x + (int64_t)min(t, rows - 1) * K + k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xv, v[j], acc[t][j]);
+      }
+    }
+#pragma unroll
+  for (int t = 0; t < ROWS; ++t)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int off = 2; off < 64; off <<= 1) acc[t][j] += __shfl_xor(acc[t][j], off, 64);
+      if ((threadIdx.x & 63) < 2) red[threadIdx.x >> 6][t][c + j] = acc[t][j];
+    }
+  __syncthreads();
+  const int t = threadIdx.x / FC, m = n0 + (int)threadIdx.x % FC;
+  if (t < rows && t < ROWS && m < N) {
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < FT / 64; ++q) s += red[q][t][threadIdx.x % FC];
+    e.store(t, m, N, s);
+  }
+}
+
+template <typename T, bool WIDE>
+void launch_few(const T* x, const T* w, int rows, int K, int N, const Epilogue<T>& e, hipStream_t st) {
+  const dim3 grid((unsigned)(ceil_div(ceil_div(N, FC), 8) * 8));
+#define CALL(R) MOE_LAUNCH("linear_fwd", (k_linear_few<T, WIDE, R>), grid, dim3(FT), 0, st, x, w, rows, K, N, e)
+  if (rows == 1) CALL(1);
+  else if (rows == 2) CALL(2);
+  else CALL(4);
+#undef CALL
 }
 
 // ---------------- dz and db ----------------
@@ -141,6 +245,7 @@ __global__ __launch_bounds__(1024) void k_linear_db(const float* __restrict__ pa
   const int c = threadIdx.x & 63, sl = threadIdx.x >> 6, n = blockIdx.x * 64 + c;
   float s = 0.f;
   if (n < N)
+  #pragma unroll 8
     for (int w = sl; w < W; w += 16) s += part[(size_t)w * N + n];
   red[sl][c] = s;
   __syncthreads();
@@ -164,15 +269,19 @@ bool tiled(const moe_linear_shape& s) { return sizeof(T) == 2 && s.K % 8 == 0 &&
 template <typename T>
 hipError_t fwd(const moe_linear_shape& s, const T* x, const T* w, const T* b, const T* res, T* z, T* y, void* scratch,
                hipStream_t st) {
-  if constexpr (sizeof(T) == 2)
-    if (tiled<T>(s) && at16(x) && at16(w) && at16(b) && at16(res) && at16(z) && at16(y)) {
-      const LinearLayout L = linear_layout(s);
-      return launch_linear_tiles("linear_fwd", x, s.K, true, w, s.N, false, s.T, s.N, s.K, {y, z, b, res, s.act},
-                                 (float*)((char*)scratch + L.off_part), st);
-    }
+  float* const part = (float*)((char*)scratch + linear_layout(s).off_part);
   Epilogue<T> e{};
   e.out = y; e.z = z; e.bias = b; e.add = res; e.act = s.act;
-  return general<T>("linear_fwd", x, w, s.K, 1, s.N, 1, s.T, s.N, s.K, e, st);
+  if (s.T <= FEW) {
+    if (s.N % 8 == 0 && at16(w)) launch_few<T, true>(x, w, s.T, s.K, s.N, e, st);
+    else launch_few<T, false>(x, w, s.T, s.K, s.N, e, st);
+    return hipGetLastError();
+  }
+  if constexpr (sizeof(T) == 2)
+    if (tiled<T>(s) && at16(x) && at16(w) && at16(b) && at16(res) && at16(z) && at16(y))
+      return launch_linear_tiles("linear_fwd", x, s.K, true, w, s.N, false, s.T, s.N, s.K, {y, z, b, res, s.act}, part,
+                                 st);
+  return general<T>("linear_fwd", x, w, s.K, 1, s.N, 1, s.T, s.N, s.K, e, part, st);
 }
 
 template <typename T>
@@ -209,12 +318,12 @@ hipError_t bwd(const moe_linear_shape& s, const T* dy, const T* x, const T* w, c
   if (err == hipSuccess && dx) {
     Epilogue<T> e{};
     e.out = dx; e.add = dx_in; e.act = MOE_ACT_NONE;
-    err = general<T>("linear_dx", dz, w, s.N, 1, 1, s.N, s.T, s.K, s.N, e, st);
+    err = general<T>("linear_dx", dz, w, s.N, 1, 1, s.N, s.T, s.K, s.N, e, part, st);
   }
   if (err == hipSuccess) {
     Epilogue<T> e{};
     e.out = dw; e.act = MOE_ACT_NONE;
-    err = general<T>("linear_dw", x, dz, 1, s.K, s.N, 1, s.K, s.N, s.T, e, st);
+    err = general<T>("linear_dw", x, dz, 1, s.K, s.N, 1, s.K, s.N, s.T, e, part, st);
   }
   return err;
 }
@@ -226,11 +335,13 @@ LinearLayout linear_layout(const moe_linear_shape& s) {
   LinearLayout L{};
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   L.off_part = s.act == MOE_ACT_NONE ? 0 : up((size_t)s.T * s.N * es);
-  size_t part = 0;   // of the largest of the three products
-  if (s.dtype == MOE_BF16 && tiled<bf16_t>(s)) {
-    const size_t of[3] = {linear_part_bytes(s.T, s.N, s.K), linear_part_bytes(s.T, s.K, s.N),
-                          linear_part_bytes(s.K, s.N, s.T)};
-    for (size_t n : of) part = n > part ? n : part;
+  size_t part = 0;   // of the largest of the three products, on the tiles or on the general kernel
+  const bool tiles = s.dtype == MOE_BF16 && tiled<bf16_t>(s);
+  const int64_t of[3][3] = {{s.T, s.N, s.K}, {s.T, s.K, s.N}, {s.K, s.N, s.T}};
+  for (const auto& d : of) {
+    const size_t a = tiles ? linear_part_bytes(d[0], d[1], d[2]) : 0, b = general_part_bytes(d[0], d[1], d[2]);
+    part = a > part ? a : part;
+    part = b > part ? b : part;
   }
   L.off_db = L.off_part + up(part);
   L.bytes = L.off_db + up((size_t)ceil_div(s.T, dz_slab(s)) * s.N * 4);

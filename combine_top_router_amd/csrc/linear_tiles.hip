@@ -186,8 +186,8 @@ __device__ __forceinline__ void load_add(const bf16_t* add, int64_t r0, int64_t 
 // A band of 32 rows and 32 NB columns of C^T accumulators through the epilogue: lanes l and
 // l + 32 trade halves so that each has 8 columns of its row in fp32, and the rounded results
 // leave through the wave's LDS region as whole row segments.  add: load_add's, if e.add is there;
-// after(): what to issue ahead of the stores.
-template <int NB, class F>
+// after(): what to issue ahead of the stores.  FULL: with bias, activation and z.
+template <bool FULL, int NB, class F>
 __device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f32x16* acc, const i32x4 (&add)[NB][2],
                                               int64_t r0, int64_t c0, int64_t M, int64_t N, bf16_t* wreg, int lane,
                                               F&& after) {
@@ -205,14 +205,16 @@ __device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f
         v[4 + i] = __uint_as_float(r[1]);
       }
       float u[8];
-      if (e.bias) {
-        const int64_t col = c0 + 32 * b + 16 * s + 8 * (lane >> 5);
-        unpack8(*reinterpret_cast<const i32x4*>(e.bias + min(col, N - 8)), u);
+      if constexpr (FULL) {
+        if (e.bias) {
+          const int64_t col = c0 + 32 * b + 16 * s + 8 * (lane >> 5);
+          unpack8(*reinterpret_cast<const i32x4*>(e.bias + min(col, N - 8)), u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += u[i];
+          for (int i = 0; i < 8; ++i) v[i] += u[i];
+        }
+        if (e.z) chz[b][s] = pack8(v);
+        act8(v, e.act);
       }
-      if (e.z) chz[b][s] = pack8(v);
-      act8(v, e.act);
       if (e.add) {
         unpack8(add[b][s], u);
 #pragma unroll
@@ -227,7 +229,8 @@ __device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f
       if (r < M && c < N) *reinterpret_cast<i32x4*>(to + r * N + c) = v;
     });
   };
-  if (e.z) put(e.z, chz);
+  if constexpr (FULL)
+    if (e.z) put(e.z, chz);
   put(e.out, chy);
 }
 
@@ -323,13 +326,13 @@ __global__ __launch_bounds__(S::THR, (S::OCC * S::TW + 3) / 4) void k_linear_til
   fetch(0);
 #pragma unroll
   for (int i = 0; i < S::MI; ++i)
-    band_epilogue<S::NB>(g.e, acc[i], add[i & 1], m0 + wm + i * 32, n0 + wn, g.M, g.N, wreg, lane, [&] {
+    band_epilogue<AK && !BKM, S::NB>(g.e, acc[i], add[i & 1], m0 + wm + i * 32, n0 + wn, g.M, g.N, wreg, lane, [&] {
       if (i + 1 < S::MI) fetch(i + 1);
     });
 }
 
 // The shares of a tile's bands added in order, and the epilogue: a workgroup for a band of each wave
-template <class S>
+template <class S, bool FULL>
 __global__ __launch_bounds__(S::THR) void k_linear_join(TileArgs g) {
   constexpr int TW = S::TW;
   __shared__ __attribute__((aligned(16))) bf16_t lds[TW * S::BAND];
@@ -347,7 +350,7 @@ __global__ __launch_bounds__(S::THR) void k_linear_join(TileArgs g) {
     for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
   const size_t share = (size_t)g.tm * g.tn * S::MI * TW * S::NI * 1024;
   const float* p = g.part + ((((size_t)tile * S::MI + i) * TW + wv) * S::NI) * 1024 + lane * 4;
-#pragma unroll 2
+#pragma unroll S::NB == 1 ? 8 : 4
   for (int sp = 0; sp < g.splits; ++sp, p += share) {
     f32x4 v[S::NB][4];
 #pragma unroll
@@ -361,7 +364,7 @@ __global__ __launch_bounds__(S::THR) void k_linear_join(TileArgs g) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[j][4 * q + r] += v[j][q][r];
   }
-  band_epilogue<S::NB>(g.e, acc, add, r0, c0, g.M, g.N, lds + wv * S::BAND, lane, [] {});
+  band_epilogue<FULL, S::NB>(g.e, acc, add, r0, c0, g.M, g.N, lds + wv * S::BAND, lane, [] {});
 }
 
 typedef Shape<256, 256, 4, 2, 64, 2, 1> Big;     // 8 waves of 128 x 64
@@ -422,8 +425,9 @@ hipError_t run(const char* name, bool a_k, bool b_k, const TileArgs& g, hipStrea
   if (a_k && !b_k) MOE_LAUNCH(name, (k_linear_tile<S, true, false>), grid, dim3(S::THR), 0, st, g);
   else if (a_k) MOE_LAUNCH(name, (k_linear_tile<S, true, true>), grid, dim3(S::THR), 0, st, g);
   else MOE_LAUNCH(name, (k_linear_tile<S, false, false>), grid, dim3(S::THR), 0, st, g);
-  if (g.part)
-    MOE_LAUNCH("linear_join", k_linear_join<S>, dim3((unsigned)(g.tm * g.tn * S::MI)), dim3(S::THR), 0, st, g);
+  const dim3 bands((unsigned)(g.tm * g.tn * S::MI));
+  if (g.part && a_k && !b_k) MOE_LAUNCH("linear_join", (k_linear_join<S, true>), bands, dim3(S::THR), 0, st, g);
+  else if (g.part) MOE_LAUNCH("linear_join", (k_linear_join<S, false>), bands, dim3(S::THR), 0, st, g);
   return hipGetLastError();
 }
 
