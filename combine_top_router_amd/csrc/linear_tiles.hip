@@ -1,8 +1,8 @@
 // The matrix product with an epilogue on matrix-core tiles: bf16, rows of whole 16-byte chunks.
 //
 // Workgroups of four waves, several to a CU, so that one's barriers, first loads and epilogue
-// hide behind the others' products.  K steps move global -> LDS by the direct loads into a ring
-// of NS stages, NS - 1 steps ahead, one barrier a step.  The operands keep their own layouts (an
+// hide behind the others' products (for the largest products eight waves alone).  K steps of 64
+// move global -> LDS by the direct loads into two stages, one barrier a step.  The operands keep their own layouts (an
 // axis of K is read in 16-byte pieces, one of M or N by the transposing LDS reads), so nothing
 // is transposed in memory.  Chunks past the end of K come from a zeroed area.  A product with
 // few tiles is split along K: the shares of a tile, in the accumulators' own order, are added by
@@ -17,45 +17,32 @@ namespace {
 
 __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
 
-// A tile shape: TM x TN outputs, waves of 32 MI x 32 NI, K steps of BKT in NS stages, OCC
+// A tile shape: TM x TN outputs, waves of 32 MI x 32 NI, K steps of BK in two stages, OCC
 // workgroups on a CU
-template <int TM_, int TN_, int MI_, int NI_, int BKT_, int NS_, int OCC_>
+template <int TM_, int TN_, int MI_, int NI_, int OCC_>
 struct Shape {
-  static constexpr int TM = TM_, TN = TN_, MI = MI_, NI = NI_, BKT = BKT_, NS = NS_, OCC = OCC_;
+  static constexpr int TM = TM_, TN = TN_, MI = MI_, NI = NI_, OCC = OCC_;
   static constexpr int WMS = TM / (32 * MI), WNS = TN / (32 * NI);   // waves along M and N
   static constexpr int TW = WMS * WNS, THR = 64 * TW;
-  static constexpr int A = TM * BKT, STAGE = (TM + TN) * BKT;
-  static constexpr int LA = TM * BKT * 2 / 1024 / TW, LB = TN * BKT * 2 / 1024 / TW;   // loads of a wave a stage
+  static constexpr int A = TM * BK, STAGE = (TM + TN) * BK;
+  static constexpr int LA = TM * BK * 2 / 1024 / TW, LB = TN * BK * 2 / 1024 / TW;   // loads of a wave a stage
   static constexpr int NB = NI;   // 32-column blocks of an epilogue band
   static constexpr int BAND = 32 * 32 * NB;
   static_assert(LA >= 1 && LB >= 1 && LA * TW * 512 == A, "whole loads");
-  static_assert(OCC * NS * STAGE * 2 <= 160 * 1024 && OCC * TW <= 16, "LDS");
+  static_assert(OCC * 2 * STAGE * 2 <= 160 * 1024 && OCC * TW <= 16, "LDS");
   static_assert(TW * BAND <= STAGE, "the epilogue's bands fit in a stage");
 };
 
-// K-major [rows][BKT]: chunk c of row r at c ^ (r / (128 / BKT)), so that 16 rows of one chunk
-// lie on distinct banks.  MN-major [BKT][W]: the four k-rows that a transposing read takes lie 64
-// bytes apart in the 256 of the banks.
-template <int BKT>
-__device__ __forceinline__ int km_chunk(int r, int c) { return c ^ ((r / (128 / BKT)) & (BKT / 8 - 1)); }
+// (K-major tiles as in gemm_engine.h.)  MN-major [BK][W]: the four k-rows that a transposing read
+// takes lie 64 bytes apart in the 256 of the banks.
 template <int W>
 __device__ __forceinline__ int mn_chunk(int r, int c) {
   return W >= 128 ? c ^ ((r & 3) << 2) : c ^ ((r & 2) << 1);
-}
-template <int BKT>
-__device__ __forceinline__ void km_slot(int s, int& r, int& c) {
-  r = s / (BKT / 8);
-  c = km_chunk<BKT>(r, s % (BKT / 8));
 }
 template <int W>
 __device__ __forceinline__ void mn_slot(int s, int& r, int& c) {
   r = s / (W / 8);
   c = mn_chunk<W>(r, s % (W / 8));
-}
-template <int BKT>
-__device__ __forceinline__ bf16x8 km_frag(const bf16_t* s, int base, int kk, int lane) {
-  const int r = base + (lane & 31);
-  return *reinterpret_cast<const bf16x8*>(s + r * BKT + (km_chunk<BKT>(r, kk * 2 + (lane >> 5)) << 3));
 }
 // (see frag_mnmaj)
 template <int W>
@@ -102,20 +89,20 @@ __device__ __forceinline__ void dma_lds(const char* base, const uint32_t (&off)[
 }
 
 // Where a lane's loads of one operand come from
-template <bool KM, int W, int BKT, int LP>
+template <bool KM, int W, int LP>
 struct TileLd {
   const char* base;    // of the next step to load (uniform)
   int64_t step;        // bytes a step
   uint32_t off[LP];    // the lane's places
   __device__ __forceinline__ static void slot(int q, int wv, int lane, int& r, int& c) {
     const int s = (wv * LP + q) * 64 + lane;
-    if constexpr (KM) km_slot<BKT>(s, r, c);
+    if constexpr (KM) kmaj_slot(s, r, c);
     else mn_slot<W>(s, r, c);
   }
   // rows (KM: of ld elements along K) or columns (of a [K, ld] matrix) x0 .. x0 + W - 1 of X
   __device__ __forceinline__ void setup(const bf16_t* m, int64_t ld, int64_t x0, int64_t X, int64_t k0, int wv, int lane) {
     base = (const char*)(m + (KM ? x0 * ld + k0 : k0 * ld + x0));
-    step = 2 * (KM ? (int64_t)BKT : BKT * ld);
+    step = 2 * (KM ? (int64_t)BK : BK * ld);
     const int most = (int)min(X - x0, (int64_t)W) - 1;   // the last row or column there is
 #pragma unroll
     for (int q = 0; q < LP; ++q) {
@@ -128,7 +115,7 @@ struct TileLd {
   // the step that has `left` elements of K to its end
   __device__ __forceinline__ void issue(int64_t left, bf16_t* dst, int wv, int lane) {
     dst += wv * LP * 512;
-    if (left >= BKT) {
+    if (left >= BK) {
       dma_lds<LP>(base, off, dst);
     } else {
 #pragma unroll
@@ -234,45 +221,38 @@ __device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f
   put(e.out, chy);
 }
 
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// The products of the stage at st: the fragments of a sub-step are read while the one before
-// multiplies
+// The products of the stage at st
 template <class S, bool AK, bool BKM>
 __device__ __forceinline__ void stage_products(const bf16_t* st, f32x16 (&acc)[S::MI][S::NI], int wm, int wn, int lane) {
 #pragma unroll
-  for (int kk = 0; kk < S::BKT / 16; ++kk) {
+  for (int kk = 0; kk < BK / 16; ++kk) {
     bf16x8 af[S::MI], bf[S::NI];
 #pragma unroll
     for (int i = 0; i < S::MI; ++i)
-      af[i] = AK ? km_frag<S::BKT>(st, wm + i * 32, kk, lane) : mn_frag<S::TM>(st, wm + i * 32, kk, lane);
+      af[i] = AK ? frag_kmaj(st, wm + i * 32, kk, lane) : mn_frag<S::TM>(st, wm + i * 32, kk, lane);
 #pragma unroll
     for (int j = 0; j < S::NI; ++j)
-      bf[j] = BKM ? km_frag<S::BKT>(st + S::A, wn + j * 32, kk, lane) : mn_frag<S::TN>(st + S::A, wn + j * 32, kk, lane);
+      bf[j] = BKM ? frag_kmaj(st + S::A, wn + j * 32, kk, lane) : mn_frag<S::TN>(st + S::A, wn + j * 32, kk, lane);
 #pragma unroll
     for (int i = 0; i < S::MI; ++i)
 #pragma unroll
-      for (int j = 0; j < S::NI; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < S::NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
   }
 }
 
 template <class S, bool AK, bool BKM>
 __global__ __launch_bounds__(S::THR, (S::OCC * S::TW + 3) / 4) void k_linear_tile(TileArgs g) {
-  constexpr int BKT = S::BKT, AHEAD = S::NS - 1, LPS = S::LA + S::LB, TW = S::TW;
-  __shared__ __attribute__((aligned(16))) bf16_t lds[S::NS * S::STAGE];
+  constexpr int TW = S::TW;
+  __shared__ __attribute__((aligned(16))) bf16_t lds[2 * S::STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wv = uni(tid >> 6);
   int mt, nt, sp;
   if (!tile_item(g, mt, nt, sp)) return;
   const int64_t m0 = (int64_t)mt * S::TM, n0 = (int64_t)nt * S::TN, k0 = sp * g.ks;
   const int64_t kn = min(g.ks, g.K - k0);   // this share's part of K
-  const int nk = (int)ceil_div(kn, BKT);
+  const int nk = (int)ceil_div(kn, BK);
   const int wm = wv % S::WMS * (32 * S::MI), wn = wv / S::WMS * (32 * S::NI);
-  TileLd<AK, S::TM, BKT, S::LA> la;
-  TileLd<BKM, S::TN, BKT, S::LB> lb;
+  TileLd<AK, S::TM, S::LA> la;
+  TileLd<BKM, S::TN, S::LB> lb;
   la.setup(g.a, g.lda, m0, g.M, k0, wv, lane);
   lb.setup(g.b, g.ldb, n0, g.N, k0, wv, lane);
   f32x16 acc[S::MI][S::NI];
@@ -282,24 +262,21 @@ __global__ __launch_bounds__(S::THR, (S::OCC * S::TW + 3) / 4) void k_linear_til
     for (int j = 0; j < S::NI; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  auto issue = [&](int kt, bf16_t* st) {
-    la.issue(kn - (int64_t)kt * BKT, st, wv, lane);
-    lb.issue(kn - (int64_t)kt * BKT, st + S::A, wv, lane);
+  auto issue = [&](int kt) {
+    bf16_t* const st = lds + (kt & 1) * S::STAGE;
+    la.issue(kn - (int64_t)kt * BK, st, wv, lane);
+    lb.issue(kn - (int64_t)kt * BK, st + S::A, wv, lane);
   };
+  if (nk > 0) issue(0);
+  // a copy of the step for each stage, whose addresses are constants of the code
+  for (int k = 0; k < nk; k += 2)
 #pragma unroll
-  for (int kt = 0; kt < AHEAD; ++kt)
-    if (kt < nk) issue(kt, lds + kt * S::STAGE);
-  // the stages' addresses are constants of the code: a copy of the step for each
-  for (int k = 0; k < nk; k += S::NS)
-#pragma unroll
-    for (int c = 0; c < S::NS; ++c) {
+    for (int c = 0; c < 2; ++c) {
       const int kt = k + c;
       if (kt < nk) {
-        // this step's loads have landed (the later steps' may be on their way), and every wave
-        // is done with the stage that the next loads fill
-        if (AHEAD == 1 || kt + AHEAD > nk) wait_loads<0>();
-        else wait_loads<(AHEAD - 1) * LPS>();
-        if (kt + AHEAD < nk) issue(kt + AHEAD, lds + (c + AHEAD) % S::NS * S::STAGE);
+        // this step's loads have landed, and every wave is done with the stage that the next fill
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (kt + 1 < nk) issue(kt + 1);
         stage_products<S, AK, BKM>(lds + c * S::STAGE, acc, wm, wn, lane);
       }
     }
@@ -317,7 +294,7 @@ __global__ __launch_bounds__(S::THR, (S::OCC * S::TW + 3) / 4) void k_linear_til
         }
     return;
   }
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave is done with the stages
   bf16_t* const wreg = lds + wv * S::BAND;
   i32x4 add[2][S::NB][2];   // of a band and the next
   auto fetch = [&](int i) {
@@ -367,10 +344,10 @@ __global__ __launch_bounds__(S::THR) void k_linear_join(TileArgs g) {
   band_epilogue<FULL, S::NB>(g.e, acc, add, r0, c0, g.M, g.N, lds + wv * S::BAND, lane, [] {});
 }
 
-typedef Shape<256, 256, 4, 2, 64, 2, 1> Big;     // 8 waves of 128 x 64
-typedef Shape<128, 128, 2, 2, 64, 2, 2> Mid;     // waves of 64 x 64
-typedef Shape<64, 128, 1, 2, 64, 2, 3> Low;      // waves of 32 x 64
-typedef Shape<64, 64, 1, 1, 64, 2, 4> Small;     // waves of 32 x 32
+typedef Shape<256, 256, 4, 2, 1> Big;     // 8 waves of 128 x 64
+typedef Shape<128, 128, 2, 2, 2> Mid;     // waves of 64 x 64
+typedef Shape<64, 128, 1, 2, 3> Low;      // waves of 32 x 64
+typedef Shape<64, 64, 1, 1, 4> Small;     // waves of 32 x 32
 
 // Which tiles, and into how many shares a product is split along K: by the estimated time.  A
 // step of 64 of K takes a workgroup alone on its CU `alone` us (barrier, LDS and load latency) and r
