@@ -11,8 +11,8 @@ namespace moe {
 namespace {
 
 // ---------------- any size, any alignment ----------------
-// 64 x 64 tiles of four waves, K steps of 32 staged element by element: the next step's loads are
-// under way while one is multiplied, one barrier a step.  With few tiles K is split, and the
+// 64 x 64 tiles of four waves, K steps of 32 staged element by element through registers: two
+// steps' loads are under way while one is multiplied, one barrier a step.  With few tiles K is split, and the
 // shares, fp32 [share, M, N], are added in order by a second launch with the epilogue.
 constexpr int GTILE = 64, GSTEP = 32;
 
@@ -47,47 +47,70 @@ __global__ __launch_bounds__(256) void k_linear_any(GeneralArgs<T> g) {
   const bool ka = g.ak == 1, kb = g.bk == 1;
   const int am = ka ? tid >> 5 : tid & 63, ak = ka ? tid & 31 : tid >> 6, dam = ka ? 8 : 0, dak = ka ? 0 : 4;
   const int bn = kb ? tid >> 5 : tid & 63, bk = kb ? tid & 31 : tid >> 6, dbn = kb ? 8 : 0, dbk = kb ? 0 : 4;
-  const T* pa = g.a + (m0 + am) * g.am + (k0 + ak) * g.ak;
-  const T* pb = g.b + (k0 + bk) * g.bk + (n0 + bn) * g.bn;
-  const int64_t sa = dam * g.am + dak * g.ak, sb = dbk * g.bk + dbn * g.bn;
+  // offsets within a step from its (uniform) first element; rows past the end give way to the
+  // last one, their results are discarded
+  const int mm = (int)min(g.M - 1 - m0, (int64_t)GTILE), nm = (int)min(g.N - 1 - n0, (int64_t)GTILE);
+  uint32_t oa[8], ob[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    oa[q] = (uint32_t)min(am + q * dam, mm) * (uint32_t)g.am + (uint32_t)(ak + q * dak) * (uint32_t)g.ak;
+    ob[q] = (uint32_t)min(bn + q * dbn, nm) * (uint32_t)g.bn + (uint32_t)(bk + q * dbk) * (uint32_t)g.bk;
+  }
+  const T* pa = g.a + m0 * g.am + k0 * g.ak;
+  const T* pb = g.b + k0 * g.bk + n0 * g.bn;
   f32x16 acc;
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-  T ra[8], rb[8];
-  auto load = [&](int64_t k) {
+  T ra[2][8], rb[2][8];   // of two steps ahead
+  auto load = [&](int left, T (&a)[8], T (&b)[8]) {   // left: of K from the step on
+    if (left >= GSTEP) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      ra[q] = m0 + am + q * dam < g.M && k + ak + q * dak < k1 ? pa[(k - k0) * g.ak + q * sa] : (T)0;
-      rb[q] = n0 + bn + q * dbn < g.N && k + bk + q * dbk < k1 ? pb[(k - k0) * g.bk + q * sb] : (T)0;
-    }
-  };
-  if (k0 < k1) load(k0);
-  int st = 0;
-  for (int64_t k = k0; k < k1; k += GSTEP, st ^= 1) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      as[st][am + q * dam][ak + q * dak] = ra[q];
-      bs[st][bn + q * dbn][bk + q * dbk] = rb[q];
-    }
-    __syncthreads();   // the other stage's readers are past it: they have met this barrier since
-    if (k + GSTEP < k1) load(k + GSTEP);
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int kk = 0; kk < GSTEP; kk += 16) {
-        const int c = kk + (lane >> 5) * 8;
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(&as[st][wm + (lane & 31)][c]),
-                                                      *reinterpret_cast<const bf16x8*>(&bs[st][wn + (lane & 31)][c]),
-                                                      acc, 0, 0, 0);
+      for (int q = 0; q < 8; ++q) {
+        a[q] = pa[oa[q]];
+        b[q] = pb[ob[q]];
       }
     } else {
 #pragma unroll
-      for (int kk = 0; kk < GSTEP; kk += 2) {
-        const int c = kk + (lane >> 5);
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as[st][wm + (lane & 31)][c], bs[st][wn + (lane & 31)][c], acc, 0, 0,
-                                                   0);
+      for (int q = 0; q < 8; ++q) {
+        a[q] = ak + q * dak < left ? pa[oa[q]] : (T)0;
+        b[q] = bk + q * dbk < left ? pb[ob[q]] : (T)0;
       }
     }
-  }
+    pa += GSTEP * g.ak;
+    pb += GSTEP * g.bk;
+  };
+  const int len = (int)(k1 - k0);
+  if (len > 0) load(len, ra[0], rb[0]);
+  if (len > GSTEP) load(len - GSTEP, ra[1], rb[1]);
+  for (int k2 = 0; k2 < len; k2 += 2 * GSTEP)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int k = k2 + c * GSTEP;
+      if (k >= len) break;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        as[c][am + q * dam][ak + q * dak] = ra[c][q];
+        bs[c][bn + q * dbn][bk + q * dbk] = rb[c][q];
+      }
+      __syncthreads();   // the other stage's readers are past it: they have met this barrier since
+      if (k + 2 * GSTEP < len) load(len - k - 2 * GSTEP, ra[c], rb[c]);
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int kk = 0; kk < GSTEP; kk += 16) {
+          const int i = kk + (lane >> 5) * 8;
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(&as[c][wm + (lane & 31)][i]),
+                                                        *reinterpret_cast<const bf16x8*>(&bs[c][wn + (lane & 31)][i]),
+                                                        acc, 0, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < GSTEP; kk += 2) {
+          const int i = kk + (lane >> 5);
+          acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as[c][wm + (lane & 31)][i], bs[c][wn + (lane & 31)][i], acc, 0, 0,
+                                                     0);
+        }
+      }
+    }
   const int64_t n = n0 + wn + (lane & 31);
   if (n >= g.N) return;
 #pragma unroll
@@ -199,42 +222,64 @@ void launch_few(const T* x, const T* w, int rows, int K, int N, const Epilogue<T
 }
 
 // ---------------- dz and db ----------------
-// dz = dy act'(z) and the workgroup's share of db: 32 lanes of 8 columns by 8 rows at a time.
+// dz = dy act'(z) and the workgroup's share of db.  WIDE: 32 lanes of 8 columns by 8 rows at a time;
+// else a lane for each column, row by row.
 constexpr int ZC = 256;   // columns of a workgroup
 template <typename T, bool WIDE>
 __global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dy, const T* __restrict__ z, int64_t rows,
                                                    int N, int act, int slab, T* __restrict__ dz,
                                                    float* __restrict__ part) {
-  __shared__ float red[8][ZC];
-  const int c = (threadIdx.x & 31) * 8, r = threadIdx.x >> 5;
-  const int n = blockIdx.y * ZC + c;
   const int64_t t0 = (int64_t)blockIdx.x * slab, t1 = min(rows, t0 + slab);
-  float s[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = 0.f;
-  if (n < N)
-#pragma unroll 2
-    for (int64_t t = t0 + r; t < t1; t += 8) {
-      float d[8], v[8];
-      load8<T, WIDE>(dy + t * N + n, N - n, d);
-      if (dz) {
-        load8<T, WIDE>(z + t * N + n, N - n, v);
-        slope8(d, v, act);
-        store8<T, WIDE>(dz + t * N + n, N - n, d);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += d[j];
-    }
-  if (!part) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) red[r][c + j] = s[j];
-  __syncthreads();
   const int m = blockIdx.y * ZC + threadIdx.x;
-  if (m < N) {
-    float a = 0.f;
+  if constexpr (WIDE) {
+    __shared__ float red[8][ZC];
+    const int c = (threadIdx.x & 31) * 8, r = threadIdx.x >> 5, n = blockIdx.y * ZC + c;
+    float s[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) a += red[q][threadIdx.x];
-    part[(size_t)blockIdx.x * N + m] = a;
+    for (int j = 0; j < 8; ++j) s[j] = 0.f;
+    if (n < N)
+#pragma unroll 2
+      for (int64_t t = t0 + r; t < t1; t += 8) {
+        float d[8], v[8];
+        load8<T, true>(dy + t * N + n, 8, d);
+        if (dz) {
+          load8<T, true>(z + t * N + n, 8, v);
+          slope8(d, v, act);
+          store8<T, true>(dz + t * N + n, 8, d);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += d[j];
+      }
+    if (!part) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[r][c + j] = s[j];
+    __syncthreads();
+    if (m < N) {
+      float a = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) a += red[q][threadIdx.x];
+      part[(size_t)blockIdx.x * N + m] = a;
+    }
+  } else {
+    if (m >= N) return;
+    float s = 0.f;
+    for (int64_t t = t0; t < t1; t += 8) {   // 8 rows in flight; past the end the last one, for nothing
+      float d[8], v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t at = min(t + j, t1 - 1) * N + m;
+        d[j] = elem<T>::load(dy + at);
+        v[j] = dz ? elem<T>::load(z + at) : 0.f;
+      }
+      if (dz) slope8(d, v, act);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (t + j < t1) {
+          if (dz) elem<T>::store(dz + (t + j) * N + m, d[j]);
+          s += d[j];
+        }
+    }
+    if (part) part[(size_t)blockIdx.x * N + m] = s;
   }
 }
 

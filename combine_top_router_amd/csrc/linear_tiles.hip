@@ -346,7 +346,6 @@ __global__ __launch_bounds__(S::THR) void k_linear_join(TileArgs g) {
 
 typedef Shape<256, 256, 4, 2, 1> Big;     // 8 waves of 128 x 64
 typedef Shape<128, 128, 2, 2, 2> Mid;     // waves of 64 x 64
-typedef Shape<64, 128, 1, 2, 3> Low;      // waves of 32 x 64
 typedef Shape<64, 64, 1, 1, 4> Small;     // waves of 32 x 32
 
 // Which tiles, and into how many shares a product is split along K: by the estimated time.  A
@@ -361,8 +360,7 @@ struct Cost {
   int tm, tn, occ;
   double alone, share;
 };
-constexpr Cost kCost[4] = {{256, 256, 1, 1.45, 1.45}, {128, 128, 2, 0.65, 0.54}, {64, 128, 3, 0.50, 0.305},
-                           {64, 64, 4, 0.45, 0.182}};
+constexpr Cost kCost[3] = {{256, 256, 1, 1.45, 1.45}, {128, 128, 2, 0.65, 0.54}, {64, 64, 4, 0.45, 0.182}};
 
 double plan_us(const Cost& c, int64_t M, int64_t N, int64_t ks, int splits) {
   const double cus = num_cus();
@@ -377,9 +375,9 @@ double plan_us(const Cost& c, int64_t M, int64_t N, int64_t ks, int splits) {
 }
 
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  Plan best{3, 1, ceil_div(K, BK) * BK};
+  Plan best{2, 1, ceil_div(K, BK) * BK};
   double least = 1e30;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 3; ++i) {
     int64_t last = -1;
     for (int s = 1; s <= 16; ++s) {
       const int64_t ks = ceil_div(ceil_div(K, s), BK) * BK;
@@ -430,7 +428,6 @@ hipError_t launch_linear_tiles(const char* name, const bf16_t* a, int64_t lda, b
   switch (p.shape) {
     case 0: return run<Big>(name, a_k, b_k, g, st);
     case 1: return run<Mid>(name, a_k, b_k, g, st);
-    case 2: return run<Low>(name, a_k, b_k, g, st);
     default: return run<Small>(name, a_k, b_k, g, st);
   }
 }
