@@ -38,7 +38,7 @@ struct AdamwHyper {
   float eps, wd;
   float to_m;                 // 1 / (1 - b1^t)
   uint32_t key;               // the step's random key
-  int state, stochastic;
+  int stochastic;
   const float* lr;            // device, or null
   const float* grad_scale;    // device, or null
   const AdamwClock* clock;    // device, or null
@@ -325,7 +325,7 @@ hipError_t launch_adamw(const moe_adamw_params& s, const moe_adamw_tensor* tenso
     h.root = (float)(1.0 / sqrt(1.0 - pow(s.beta2, (double)s.step)));
     h.key = step_key(s.seed, s.step);
   }
-  h.state = s.state; h.stochastic = s.stochastic;
+  h.stochastic = s.stochastic;
   h.lr = lr; h.grad_scale = grad_scale; h.clock = (const AdamwClock*)clock;
   AdamwTable tab{};
   int64_t wgs = 0;

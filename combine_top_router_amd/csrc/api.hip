@@ -929,8 +929,8 @@ int moe_linear_fwd(const moe_linear_shape* shape, const void* x, const void* w, 
   REQUIRE(w);
   REQUIRE(y);
   REQUIRE_WS(scratch);
-  if (y == x || y == z || (z && (z == x || z == res)))
-    return fail(MOE_EINVAL, "%s: y may not be x or z, and z not x or res", __func__);
+  if (y == x || y == w || y == z || (z && (z == x || z == w || z == res)))
+    return fail(MOE_EINVAL, "%s: y may not be x, w or z, and z not x, w or res", __func__);
   return hip_status(launch_linear_fwd(*shape, x, w, b, res, z, y, scratch, (hipStream_t)stream), __func__);
 }
 
@@ -946,8 +946,10 @@ int moe_linear_bwd(const moe_linear_shape* shape, const void* dy, const void* x,
     REQUIRE(x);
     REQUIRE(w);
     if (shape->act != MOE_ACT_NONE) REQUIRE(z);
-    if (dx && (dx == dy || dx == x || dx == z))
-      return fail(MOE_EINVAL, "%s: dx may be none of dy, x and z", __func__);
+    if (dx && (dx == dy || dx == x || dx == w || dx == z))
+      return fail(MOE_EINVAL, "%s: dx may be none of dy, x, w and z", __func__);
+    if (dw == dy || dw == x || dw == w || dw == z || dw == dx)
+      return fail(MOE_EINVAL, "%s: dw may be none of dy, x, w, z and dx", __func__);
   }
   return hip_status(launch_linear_bwd(*shape, dy, x, w, z, dx_in, dx, dw, db, scratch, (hipStream_t)stream), __func__);
 }

@@ -2,6 +2,8 @@
 the C ABI.  Every step runs in libmoe; torch only provides memory and the stream."""
 from __future__ import annotations
 
+import weakref
+
 import torch
 
 from . import lib as L
@@ -250,6 +252,7 @@ class Gate(_OnDevice):
         self._p_idx, self._p_w, self._p_counts = _p(self.topk_idx), _p(self.topk_w), _p(self.counts)
         self._p_scratch = _p(self.scratch)
         self.inputs, self._counted = None, False
+        self.layer = None   # weak, the MoeLayer that routes by it
         self._allocated()
 
     def forward(self, logits, bias=None, mask=None, count=False, stream=None):
@@ -432,6 +435,8 @@ class AdamW(_OnDevice):
         """One step with a gradient for each parameter (bf16 or fp32; None: that one is left
         alone).  lr: a number, or a device fp32 tensor [1], such as a captured step reads anew at
         every replay; grad_scale: a device fp32 tensor [1] that the gradients are multiplied by."""
+        if self._clock is None and self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a captured step needs capturable=True: its number would be the same at every replay")
         if len(grads) != len(self.params):
             raise ValueError(f"grads: expected {len(self.params)}, got {len(grads)}")
         index, codes = self._index, self._codes
@@ -478,7 +483,7 @@ class MoeLayer:
 
     ``gate``: a ``Gate`` of the same T, E and k routes in place of the softmax of the logits (and
     of ``renorm``); ``forward`` then takes its bias, its mask and ``count``, and tokens that the
-    mask leaves out get y = 0.
+    mask leaves out get y = 0.  A gate is one layer's: the backward reads what it holds.
     """
 
     def __init__(self, T, H, I, E, k, e_begin=0, e_local=None, dtype=L.MOE_BF16, bwd=L.MOE_BWD_SAME,
@@ -492,6 +497,10 @@ class MoeLayer:
         if gate is not None and ((gate.shape.T, gate.shape.E, gate.shape.k) != (T, E, k) or gate.device != self.device):
             raise ValueError(f"gate: expected T = {T}, E = {E}, k = {k} on {self.device}, got T = {gate.shape.T}, "
                              f"E = {gate.shape.E}, k = {gate.shape.k} on {gate.device}")
+        if gate is not None:
+            if gate.layer is not None and gate.layer() is not None:
+                raise ValueError("gate: another layer has it, whose backward would find this one's routing")
+            gate.layer = weakref.ref(self)
         self.gate = gate
         saved_b, scratch_b = L.moe_workspace_bytes(self.shape)
         self.R_cap = T * min(k, e_local)

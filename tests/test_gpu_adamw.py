@@ -320,3 +320,19 @@ def test_adamw_refuses_other_tensors():
     with pytest.raises(ValueError, match="other memory"):
         op.step([g], 0.1)
     assert op.t == 0
+
+
+def test_adamw_captured_needs_its_clock():
+    """A step number from the host would be the same at every replay."""
+    from combine_top_router_amd import AdamW
+    p = torch.zeros(64, device="cuda")
+    op = AdamW([p])
+    x = torch.ones(8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.mul_(2.0)
+        with pytest.raises(RuntimeError, match="capturable"):
+            op.step([p], 0.1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert op.t == 0 and not p.any() and (x == 2.0).all()

@@ -8,6 +8,8 @@ functions of 1 to 2 ulp, and the argument's rounding); y is rounded once.  The b
 reads z with h and keeps dz with h: z h times the slope's own slope (at most 0.8), and dz h, enter
 the products as errors of dz.  At relu's corner the sign of z is that of its rounding: where z is
 within its error dz may be off by all of dy."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -309,3 +311,27 @@ def test_linear_refuses_other_tensors():
     for kw in (dict(dy=dy.float()), dict(dy=dy[:7]), dict(dy=dy, dx_in=dy)):
         with pytest.raises(ValueError):
             op.backward(**kw)
+
+
+@pytest.mark.parametrize("T", [2, 193])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gelu_far_out(dtype, T):
+    """gelu and its slope relative to their own values, down the negative side: z itself is exact (one product
+    with 1, of multiples of 1/16 below 2^8 of them).  The value is good to 1.1e-5 (the polynomial's fit), z^2 u
+    (the exponent's two roundings, times it) and 16 u (reciprocal, exponential, eight steps); the slope is
+    Q + z phi, each of them so.  Roundings to the type: y once, dx twice."""
+    z = torch.arange(-192, 1).double()[:T] / 16 if T > 4 else torch.tensor([-9.0, -5.5]).double()
+    x, w = torch.zeros(T, 8, dtype=DT[dtype], device="cuda"), torch.zeros(8, 8, dtype=DT[dtype], device="cuda")
+    x[:, 0], w[0, 0] = z.to(DT[dtype]).cuda(), 1.0
+    dy = torch.zeros(T, 8, dtype=DT[dtype], device="cuda")
+    dy[:, 0] = 1.0
+    op = _op(T, 8, 8, "gelu", dtype)
+    y = _f(op.forward(x, w))[:, 0]
+    dx = _f(op.backward(dy)["dx"])[:, 0]
+    z = z.numpy()
+    q = 0.5 * np.array([math.erfc(-v / math.sqrt(2.0)) for v in z])
+    phi = z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    rel = 1.1e-5 + (z * z + 16) * U
+    assert (np.abs(y - z * q) <= (rel * (1 + HALF[dtype]) + HALF[dtype]) * np.abs(z * q)).all()
+    err = rel * (q + np.abs(phi))
+    assert (np.abs(dx - (q + phi)) <= 2.1 * HALF[dtype] * np.abs(q + phi) + (1 + HALF[dtype]) ** 2 * err).all()

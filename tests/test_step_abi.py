@@ -210,3 +210,27 @@ def test_linear_scratch_of_the_extremes(T, K, N, act):
     for dtype in (L.MOE_BF16, L.MOE_F32):
         n = L.moe_linear_scratch_bytes(_linear(L, T=T, K=K, N=N, dtype=dtype, act=act))
         assert n >= (T * N * (2 if dtype else 4) if act else 1)
+
+
+def test_linear_outputs_apart():
+    """What is written lies apart from what the call reads after it."""
+    L = _lib()
+    s = _linear(L)
+    fwd = dict(x=P, w=2 * P, b=0, res=0, z=0, y=3 * P, scratch=P)
+    for same in (dict(y=2 * P), dict(z=2 * P)):
+        assert _code(lambda: L.moe_linear_fwd(s, *dict(fwd, **same).values())) == L.MOE_EINVAL, same
+    bwd = dict(dy=P, x=2 * P, w=3 * P, z=4 * P, dx_in=0, dx=5 * P, dw=6 * P, db=0, scratch=P)
+    assert _code(lambda: L.moe_linear_bwd(s, *dict(bwd, dx=3 * P).values())) == L.MOE_EINVAL
+    for name in ("dy", "x", "w", "z", "dx"):
+        assert _code(lambda: L.moe_linear_bwd(s, *dict(bwd, dw=bwd[name]).values())) == L.MOE_EINVAL, name
+
+
+def test_a_gate_is_one_layers():
+    _lib()
+    from combine_top_router_amd import Gate, MoeLayer
+    g = Gate(4, 8, 2, device="cpu")
+    lay = MoeLayer(4, 64, 64, 8, 2, device="cpu", gate=g)
+    with pytest.raises(ValueError, match="another layer"):
+        MoeLayer(4, 64, 64, 8, 2, device="cpu", gate=g)
+    del lay
+    MoeLayer(4, 64, 64, 8, 2, device="cpu", gate=g)
