@@ -60,43 +60,72 @@ __device__ __forceinline__ void slope8(float (&d)[8], const float (&z)[8], int a
   }
 }
 
-// 8 consecutive elements of a row with `left` to its end; WIDE: all there, at a multiple of 16 bytes
-template <typename T, bool WIDE>
-__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
-  if constexpr (!WIDE) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < left ? elem<T>::load(p + j) : 0.f;
-  } else if constexpr (sizeof(T) == 2) {
-    const i32x4 u = *reinterpret_cast<const i32x4*>(p);
+// 16 bytes at a multiple of an element's size (the hardware takes them from anywhere)
+typedef i32x4 i32x4_a2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_e4 __attribute__((aligned(4)));
+
+// 8 consecutive elements as loaded, and as fp32
+template <typename T> struct raw8;
+template <> struct raw8<bf16_t> {
+  i32x4 u;
+  __device__ __forceinline__ void load(const bf16_t* p) { u = *reinterpret_cast<const i32x4_a2*>(p); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float((uint32_t)u[j] << 16);
       v[2 * j + 1] = __uint_as_float((uint32_t)u[j] & 0xffff0000u);
     }
-  } else {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  }
+};
+template <> struct raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f32x4_e4*>(p);
+    b = *reinterpret_cast<const f32x4_e4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[j] = a[j];
       v[4 + j] = b[j];
     }
   }
+};
+__device__ __forceinline__ void load8(const bf16_t* p, bf16_t (&v)[8]) {
+  const i32x4 u = *reinterpret_cast<const i32x4_a2*>(p);
+  __builtin_memcpy(v, &u, 16);
 }
-template <typename T, bool WIDE>
-__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
-  if constexpr (!WIDE) {
+__device__ __forceinline__ void load8(const bf16_t* p, float (&v)[8]) {
+  raw8<bf16_t> r;
+  r.load(p);
+  r.get(v);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  raw8<float> r;
+  r.load(p);
+  r.get(v);
+}
+// the first `left` of them, 0 behind
+template <typename T>
+__device__ __forceinline__ void load_some(const T* p, int left, float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < left) elem<T>::store(p + j, v[j]);
-  } else if constexpr (sizeof(T) == 2) {
-    i32x4 o;
+  for (int j = 0; j < 8; ++j) v[j] = j < left ? elem<T>::load(p + j) : 0.f;
+}
+__device__ __forceinline__ void store8(bf16_t* p, const float (&v)[8]) {
+  i32x4 o;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = (int)pk_bf16(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<i32x4*>(p) = o;
-  } else {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-  }
+  for (int j = 0; j < 4; ++j) o[j] = (int)pk_bf16(v[2 * j], v[2 * j + 1]);
+  *reinterpret_cast<i32x4_a2*>(p) = o;
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<f32x4_e4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4_e4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, int left, const float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < left) elem<T>::store(p + j, v[j]);
 }
 
 // What becomes of an element of a product: bias, z kept, activation, a matrix added
@@ -118,16 +147,61 @@ struct Epilogue {
   }
 };
 
+// Which tiles, and into how many shares a product is split along K: by the estimated time.  A
+// step of K takes a workgroup alone on its CU `alone` us (barrier, LDS and load latency) and r of
+// them r `share` us together, and a round of workgroups `over` us (first loads, epilogue), as
+// measured on one MI355X; the shares' sums cost a launch and the shares' bytes.
+struct Plan {
+  int shape, splits;
+  int64_t ks;       // of K a share, whole steps
+};
+struct PlanCost {
+  int tm, tn, occ;  // outputs of a tile, workgroups on a CU
+  double alone, share, over;
+  double join;      // of the second launch
+  double bytes;     // of an output's share, at 4 TB/s
+};
+inline double plan_us(const PlanCost& c, int step, int cus, int64_t M, int64_t N, int64_t ks, int splits) {
+  const int64_t wgs = ceil_div(M, c.tm) * ceil_div(N, c.tn) * splits, slots = (int64_t)cus * c.occ;
+  auto of = [&](double r) { return r * c.share > c.alone ? r * c.share : c.alone; };
+  const int64_t full = wgs / slots, rest = wgs - full * slots;
+  const double r = 0.5 * ((double)rest / cus + (double)ceil_div(rest, (int64_t)cus));   // some CUs have one more
+  const double steps = (double)ceil_div(ks, step);
+  double us = full * (steps * of(c.occ) + c.over) + (rest > 0 ? steps * of(r) + c.over : 0.0);
+  if (splits > 1) us += c.join + (double)splits * M * N * c.bytes / 4e6;
+  return us;
+}
+inline Plan plan_product(const PlanCost* costs, int shapes, int step, int cus, int64_t M, int64_t N, int64_t K) {
+  Plan best{shapes - 1, 1, ceil_div(K, step) * step};
+  double least = 1e30;
+  for (int i = 0; i < shapes; ++i) {
+    int64_t last = -1;
+    for (int s = 1; s <= 64; s += s < 16 ? 1 : s < 32 ? 8 : 16) {
+      const int64_t ks = ceil_div(ceil_div(K, s), step) * step;
+      const int n = ks > 0 ? (int)ceil_div(K, ks) : 1;   // shares that are not empty
+      if (ks == last) continue;
+      last = ks;
+      const double us = plan_us(costs[i], step, cus, M, N, ks, n);
+      if (us < least) {
+        least = us;
+        best = {i, n, ks};
+      }
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
-// linear_tiles.hip: C [M, N] = A B for bf16 matrices whose rows are whole 16-byte chunks, every
-// address at a multiple of 16.  A [M, K] of rows lda (a_k) or [K, M]; B [N, K] (b_k) or [K, N].
+// linear_tiles.hip: C [M, N] = A B for bf16 matrices A and B whose rows are whole 16-byte chunks
+// (zeros past the end of K in them), at multiples of 16.  A [M, K] of rows lda (a_k) or [K, M]; B [N, K] (b_k) or [K, N].
 struct LinearOut {
   bf16_t* out;
   bf16_t* z;
   const bf16_t* bias;
   const bf16_t* add;
   int act;
+  bool wide;   // N a multiple of 8 and every pointer at one of 16
 };
 size_t linear_part_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_tiles(const char* name, const bf16_t* a, int64_t lda, bool a_k, const bf16_t* b, int64_t ldb,

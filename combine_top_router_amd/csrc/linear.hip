@@ -4,6 +4,8 @@
 //   dz = dy act'(z),  dx = dx_in + dz W^T,  dW = x^T dz,  db = sum_t dz
 // with x [T, K], W [K, N] as the layer's weights are stored, sums in fp32.  z is kept in the
 // data's type for the backward; y is formed from the fp32 sum.
+#include <type_traits>
+
 #include "linear.h"
 
 namespace moe {
@@ -11,14 +13,16 @@ namespace moe {
 namespace {
 
 // ---------------- any size, any alignment ----------------
-// 64 x 64 tiles of four waves, K steps of 32 staged element by element through registers: two
-// steps' loads are under way while one is multiplied, one barrier a step.  With few tiles K is split, and the
-// shares, fp32 [share, M, N], are added in order by a second launch with the epilogue.
-constexpr int GTILE = 64, GSTEP = 32;
+// Tiles of 64 or 128 square, four waves, K steps of 32 staged through registers, 8 consecutive elements a
+// thread, several steps' loads under way while one is multiplied, one barrier a step.  With few
+// tiles K is split, and the shares, fp32 [share, M, N], are added in order by a second launch with
+// the epilogue.
+constexpr int GSTEP = 32;
 
+// rows of K in LDS, whole 16-byte pieces that 16 rows spread over all the banks
 template <typename T> struct gstage;
 template <> struct gstage<bf16_t> { static constexpr int LD = GSTEP + 8; };
-template <> struct gstage<float> { static constexpr int LD = GSTEP + 1; };
+template <> struct gstage<float> { static constexpr int LD = GSTEP + 4; };
 
 // C [M, N] = A B over K.  A element (m, k) at m * am + k * ak, B element (k, n) at k * bk + n * bn;
 // of each pair of strides one is 1.
@@ -33,92 +37,157 @@ struct GeneralArgs {
   Epilogue<T> e;
 };
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_linear_any(GeneralArgs<T> g) {
-  constexpr int LD = gstage<T>::LD;
-  __shared__ __attribute__((aligned(16))) T as[2][GTILE][LD];   // [m][k]
-  __shared__ __attribute__((aligned(16))) T bs[2][GTILE][LD];   // [n][k]
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int64_t m0 = (int64_t)blockIdx.x * GTILE, n0 = (int64_t)blockIdx.y * GTILE, k0 = blockIdx.z * g.ks;
-  const int64_t k1 = min(g.K, k0 + g.ks);
-  const int wm = (wv & 1) * 32, wn = (wv >> 1) * 32;
-  // neighbouring threads along the axis that is contiguous: the thread's first place, and what
-  // each of its eight further ones adds
-  const bool ka = g.ak == 1, kb = g.bk == 1;
-  const int am = ka ? tid >> 5 : tid & 63, ak = ka ? tid & 31 : tid >> 6, dam = ka ? 8 : 0, dak = ka ? 0 : 4;
-  const int bn = kb ? tid >> 5 : tid & 63, bk = kb ? tid & 31 : tid >> 6, dbn = kb ? 8 : 0, dbk = kb ? 0 : 4;
-  // offsets within a step from its (uniform) first element; rows past the end give way to the
-  // last one, their results are discarded
-  const int mm = (int)min(g.M - 1 - m0, (int64_t)GTILE), nm = (int)min(g.N - 1 - n0, (int64_t)GTILE);
-  uint32_t oa[8], ob[8];
+// One operand's part of a thread: H times 8 elements along the axis that is contiguous, 64 rows or
+// columns apart
+template <typename T, int H>
+struct GeneralLd {
+  const T* p;        // the step's first element (uniform)
+  int64_t step;
+  uint32_t off[H];   // the thread's places from there
+  int row[H], k;     // the first in the tile: row of LDS, and in the step
+  int some;          // of the 8 (uniform)
+  bool km;           // K is contiguous
+  __device__ __forceinline__ void setup(const T* m, int64_t xs, int64_t ks, int64_t x0, int64_t X, int64_t k0, int tid) {
+    km = ks == 1;
+    // K contiguous: 4 threads a row.  Else 4 threads of 8 columns by 16 of K in a wave, whose
+    // writes into LDS then meet in no bank more than twice.
+    const int x = km ? tid >> 2 : ((tid & 3) | (tid >> 6 & 1) << 2) * 8;
+    k = km ? (tid & 3) * 8 : (tid >> 2 & 15) | (tid >> 7) << 4;
+    p = m + x0 * xs + k0 * ks;
+    step = GSTEP * ks;
+    const int left = (int)min(X - x0, (int64_t)(64 * H));   // rows or columns there are
+    some = km ? 8 : min(8, left);
+    // past the end: the last row, or the last 8 columns, loaded again; what stays unwritten in LDS
+    // goes into results that are discarded
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    oa[q] = (uint32_t)min(am + q * dam, mm) * (uint32_t)g.am + (uint32_t)(ak + q * dak) * (uint32_t)g.ak;
-    ob[q] = (uint32_t)min(bn + q * dbn, nm) * (uint32_t)g.bn + (uint32_t)(bk + q * dbk) * (uint32_t)g.bk;
+    for (int h = 0; h < H; ++h) {
+      const int y = min(x + 64 * h, km ? left - 1 : max(0, left - 8));
+      row[h] = km ? x + 64 * h : y;
+      off[h] = (uint32_t)y * (uint32_t)xs + (uint32_t)k * (uint32_t)ks;
+    }
   }
-  const T* pa = g.a + m0 * g.am + k0 * g.ak;
-  const T* pb = g.b + k0 * g.bk + n0 * g.bn;
-  f32x16 acc;
+  // The step with `left` of K to its end.  What lies past it is loaded from the last place there
+  // is and made 0 by put: a selection here would wait for the loads.
+  __device__ __forceinline__ void load(int left, T (&v)[H][8]) {
+    const int past = max(0, k - (left - 1));
+    if (left >= GSTEP && some == 8) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-  T ra[2][8], rb[2][8];   // of two steps ahead
-  auto load = [&](int left, T (&a)[8], T (&b)[8]) {   // left: of K from the step on
-    if (left >= GSTEP) {
+      for (int h = 0; h < H; ++h) load8(p + off[h], v[h]);
+    } else if (!km && some == 8) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        a[q] = pa[oa[q]];
-        b[q] = pb[ob[q]];
-      }
+      for (int h = 0; h < H; ++h) load8(p + (off[h] - (uint32_t)past * (uint32_t)(step / GSTEP)), v[h]);
     } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        a[q] = ak + q * dak < left ? pa[oa[q]] : (T)0;
-        b[q] = bk + q * dbk < left ? pb[ob[q]] : (T)0;
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[h][j] = p[km ? off[h] - (uint32_t)k + (uint32_t)min(k + j, left - 1)
+                         : off[h] - (uint32_t)past * (uint32_t)(step / GSTEP) + (uint32_t)min(j, some - 1)];
+    }
+    p += step;
+  }
+  __device__ __forceinline__ void put(T (*s)[gstage<T>::LD], int left, T (&v)[H][8]) const {
+    if (left < GSTEP)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[h][j] = (km ? k + j : k) < left ? v[h][j] : (T)0;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      if (km) {
+        __builtin_memcpy(__builtin_assume_aligned(&s[row[h]][k], 16), v[h], sizeof(v[h]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[row[h] + j][k] = v[h][j];
       }
     }
-    pa += GSTEP * g.ak;
-    pb += GSTEP * g.bk;
-  };
-  const int len = (int)(k1 - k0);
-  if (len > 0) load(len, ra[0], rb[0]);
-  if (len > GSTEP) load(len - GSTEP, ra[1], rb[1]);
-  for (int k2 = 0; k2 < len; k2 += 2 * GSTEP)
+  }
+};
+
+// H: tiles of 64 H, waves of 32 H; DEPTH steps' loads are under way
+template <typename T, int H>
+__global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<T> g) {
+  constexpr int LD = gstage<T>::LD, TILE = 64 * H, DEPTH = H == 1 && sizeof(T) == 2 ? 4 : 2;
+  __shared__ __attribute__((aligned(16))) T as[2][TILE][LD];   // [m][k]
+  __shared__ __attribute__((aligned(16))) T bs[2][TILE][LD];   // [n][k]
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int64_t m0 = (int64_t)blockIdx.x * TILE, n0 = (int64_t)blockIdx.y * TILE, k0 = blockIdx.z * g.ks;
+  const int64_t k1 = min(g.K, k0 + g.ks);
+  const int wm = (wv & 1) * 32 * H, wn = (wv >> 1) * 32 * H;
+  GeneralLd<T, H> la, lb;
+  la.setup(g.a, g.am, g.ak, m0, g.M, k0, tid);
+  lb.setup(g.b, g.bn, g.bk, n0, g.N, k0, tid);
+  f32x16 acc[H][H];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+  for (int i = 0; i < H * H; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[i / H][i % H][j] = 0.f;
+  T ra[DEPTH][H][8], rb[DEPTH][H][8];
+  const int len = (int)(k1 - k0);
+#pragma unroll
+  for (int c = 0; c < DEPTH; ++c)
+    if (c * GSTEP < len) {
+      la.load(len - c * GSTEP, ra[c]);
+      lb.load(len - c * GSTEP, rb[c]);
+    }
+  for (int k2 = 0; k2 < len; k2 += DEPTH * GSTEP)
+#pragma unroll
+    for (int c = 0; c < DEPTH; ++c) {
       const int k = k2 + c * GSTEP;
       if (k >= len) break;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        as[c][am + q * dam][ak + q * dak] = ra[c][q];
-        bs[c][bn + q * dbn][bk + q * dbk] = rb[c][q];
-      }
+      la.put(as[c & 1], len - k, ra[c]);
+      lb.put(bs[c & 1], len - k, rb[c]);
       __syncthreads();   // the other stage's readers are past it: they have met this barrier since
-      if (k + 2 * GSTEP < len) load(len - k - 2 * GSTEP, ra[c], rb[c]);
+      if (k + DEPTH * GSTEP < len) {
+        la.load(len - k - DEPTH * GSTEP, ra[c]);
+        lb.load(len - k - DEPTH * GSTEP, rb[c]);
+      }
+      const T* const pa = &as[c & 1][wm + (lane & 31)][0];
+      const T* const pb = &bs[c & 1][wn + (lane & 31)][0];
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int kk = 0; kk < GSTEP; kk += 16) {
-          const int i = kk + (lane >> 5) * 8;
-          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(&as[c][wm + (lane & 31)][i]),
-                                                        *reinterpret_cast<const bf16x8*>(&bs[c][wn + (lane & 31)][i]),
-                                                        acc, 0, 0, 0);
+          bf16x8 va[H], vb[H];
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            va[h] = *reinterpret_cast<const bf16x8*>(pa + 32 * h * LD + kk + (lane >> 5) * 8);
+            vb[h] = *reinterpret_cast<const bf16x8*>(pb + 32 * h * LD + kk + (lane >> 5) * 8);
+          }
+#pragma unroll
+          for (int i = 0; i < H * H; ++i)
+            acc[i / H][i % H] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[i / H], vb[i % H], acc[i / H][i % H], 0, 0, 0);
         }
       } else {
+        // the instruction sums k of its lower and of its upper lanes: here k and k + 4
 #pragma unroll
-        for (int kk = 0; kk < GSTEP; kk += 2) {
-          const int i = kk + (lane >> 5);
-          acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as[c][wm + (lane & 31)][i], bs[c][wn + (lane & 31)][i], acc, 0, 0,
-                                                     0);
+        for (int kk = 0; kk < GSTEP; kk += 8) {
+          f32x4 va[H], vb[H];
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            va[h] = *reinterpret_cast<const f32x4*>(pa + 32 * h * LD + kk + (lane >> 5) * 4);
+            vb[h] = *reinterpret_cast<const f32x4*>(pb + 32 * h * LD + kk + (lane >> 5) * 4);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < H * H; ++i)
+              acc[i / H][i % H] =
+                  __builtin_amdgcn_mfma_f32_32x32x2f32(va[i / H][j], vb[i % H][j], acc[i / H][i % H], 0, 0, 0);
         }
       }
     }
-  const int64_t n = n0 + wn + (lane & 31);
-  if (n >= g.N) return;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const int64_t m = m0 + wm + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
-    if (m >= g.M) continue;
-    if (g.part) g.part[(blockIdx.z * g.M + m) * g.N + n] = acc[j];
-    else g.e.store(m, n, g.N, acc[j]);
+  for (int i = 0; i < H * H; ++i) {
+    const int64_t n = n0 + wn + 32 * (i % H) + (lane & 31);
+    if (n >= g.N) continue;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int64_t m = m0 + wm + 32 * (i / H) + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+      if (m >= g.M) continue;
+      const float v = acc[i / H][i % H][j];
+      if (g.part) g.part[(blockIdx.z * g.M + m) * g.N + n] = v;
+      else g.e.store(m, n, g.N, v);
+    }
   }
 }
 
@@ -132,16 +201,15 @@ __global__ __launch_bounds__(256) void k_linear_any_join(GeneralArgs<T> g, int s
   g.e.store(i / g.N, i % g.N, g.N, s);
 }
 
-// shares of K: two workgroups for each CU, of four steps at least
-int general_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = ceil_div(M, GTILE) * ceil_div(N, GTILE);
-  if (tiles == 0) return 1;
-  int64_t s = 2 * gemm_cus() / tiles;
-  s = s < K / (4 * GSTEP) ? s : K / (4 * GSTEP);
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+constexpr PlanCost kAny16[2] = {{128, 128, 2, 1.1, 0.6, 6.0, 5.0, 6.0}, {64, 64, 4, 0.8, 0.26, 3.0, 5.0, 6.0}};
+constexpr PlanCost kAny32[2] = {{128, 128, 2, 2.8, 2.4, 7.0, 5.0, 6.0}, {64, 64, 4, 1.1, 0.66, 3.0, 5.0, 6.0}};
+template <typename T>
+Plan general_plan(int64_t M, int64_t N, int64_t K) {
+  return plan_product(sizeof(T) == 2 ? kAny16 : kAny32, 2, GSTEP, gemm_cus(), M, N, K);
 }
+template <typename T>
 size_t general_part_bytes(int64_t M, int64_t N, int64_t K) {
-  const int s = general_splits(M, N, K);
+  const int s = general_plan<T>(M, N, K).splits;
   return s == 1 ? 0 : (size_t)s * M * N * 4;
 }
 
@@ -149,24 +217,25 @@ template <typename T>
 hipError_t general(const char* name, const T* a, const T* b, int64_t am, int64_t ak, int64_t bk, int64_t bn, int64_t M,
                    int64_t N, int64_t K, const Epilogue<T>& e, float* part, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
-  int splits = general_splits(M, N, K);
-  const int64_t ks = ceil_div(ceil_div(K, splits), GSTEP) * GSTEP;
-  splits = ks > 0 ? (int)ceil_div(K, ks) : 1;
-  const GeneralArgs<T> g{a, b, am, ak, bk, bn, M, N, K, ks, splits > 1 ? part : nullptr, e};
-  MOE_LAUNCH(name, k_linear_any<T>,
-             dim3((unsigned)ceil_div(M, GTILE), (unsigned)ceil_div(N, GTILE), (unsigned)splits), dim3(256), 0, st, g);
-  if (splits > 1)
-    MOE_LAUNCH("linear_join", k_linear_any_join<T>, dim3((unsigned)ceil_div(M * N, 256)), dim3(256), 0, st, g, splits);
+  const Plan p = general_plan<T>(M, N, K);
+  const GeneralArgs<T> g{a, b, am, ak, bk, bn, M, N, K, p.ks, p.splits > 1 ? part : nullptr, e};
+  const int tile = p.shape == 0 ? 128 : 64;
+  const dim3 grid((unsigned)ceil_div(M, tile), (unsigned)ceil_div(N, tile), (unsigned)p.splits);
+  if (tile == 128) MOE_LAUNCH(name, (k_linear_any<T, 2>), grid, dim3(256), 0, st, g);
+  else MOE_LAUNCH(name, (k_linear_any<T, 1>), grid, dim3(256), 0, st, g);
+  if (p.splits > 1)
+    MOE_LAUNCH("linear_join", k_linear_any_join<T>, dim3((unsigned)ceil_div(M * N, 256)), dim3(256), 0, st, g, p.splits);
   return hipGetLastError();
 }
 
 // ---------------- few rows ----------------
-// Up to FEW rows (the tokens of a decode step): W is read once, and that is what counts.  A
+// Up to FEW rows (the tokens of a decode step) of 8 columns or more: W is read once, and that is what counts.  A
 // workgroup takes 16 columns, two lanes of 8, and all of K, 256 of its rows at a time; its sums
 // meet by lane exchanges and through LDS, so one launch does, without shares in memory.
 constexpr int FEW = 4, FT = 512, FC = 16;
 
-template <typename T, bool WIDE, int ROWS>
+// U: rows of W under way
+template <typename T, int ROWS, int U = (sizeof(T) == 2 ? 8 : 4) * (ROWS == 1 ? 2 : 1)>
 __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, const T* __restrict__ w, int rows, int K, int N,
                                                    Epilogue<T> e) {
   __shared__ float red[FT / 64][ROWS][FC];
@@ -175,32 +244,63 @@ __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, cons
   const int lo = (int)((int64_t)blocks * xcd >> 3), hi = (int)((int64_t)blocks * (xcd + 1) >> 3);
   const int block = lo + (int)(blockIdx.x >> 3);
   if (block >= hi) return;
-  const int n0 = block * FC, c = (threadIdx.x & 1) * 8, n = n0 + c, kl = threadIdx.x >> 1;
+  const int n0 = block * FC, n = n0 + (threadIdx.x & 1) * 8, kl = threadIdx.x >> 1;
+  const int at = min(n, N - 8);   // the last columns: the last 8 there are, of which it keeps its own
   float acc[ROWS][8];
 #pragma unroll
   for (int t = 0; t < ROWS; ++t)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[t][j] = 0.f;
-  if (n < N)
-#pragma unroll 8
-    for (int k = kl; k < K; k += FT / 2) {
-      float v[8];
-      load8<T, WIDE>(w + (int64_t)k * N + n, N - n, v);
+  const int64_t step = (int64_t)(FT / 2) * N;
+  const T* wp = w + (int64_t)kl * N + at;
+  // U rows of W: all loads before the first product; TAIL: past the end the first one again, for nothing
+  auto rows_of_w = [&](auto tail, int k) {
+    constexpr bool TAIL = decltype(tail)::value;
+    raw8<T> v[U];
+    T xv[U][ROWS];
 #pragma unroll
-      for (int t = 0; t < ROWS; ++t) {
-        const float xv = elem<T>::load(x + (int64_t)min(t, rows - 1) * K + k);
+    for (int u = 0; u < U; ++u) {
+      const bool in = !TAIL || k + u * (FT / 2) < K;
+      v[u].load(in ? wp + u * step : wp);
+      const T* const xp = x + (in ? k + u * (FT / 2) : k);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xv, v[j], acc[t][j]);
-      }
+      for (int t = 0; t < ROWS; ++t) xv[u][t] = xp[(int64_t)min(t, rows - 1) * K];
     }
 #pragma unroll
-  for (int t = 0; t < ROWS; ++t)
+    for (int u = 0; u < U; ++u) {
+      float f[8];
+      v[u].get(f);
+      const bool in = !TAIL || k + u * (FT / 2) < K;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+      for (int t = 0; t < ROWS; ++t)
 #pragma unroll
-      for (int off = 2; off < 64; off <<= 1) acc[t][j] += __shfl_xor(acc[t][j], off, 64);
-      if ((threadIdx.x & 63) < 2) red[threadIdx.x >> 6][t][c + j] = acc[t][j];
+        for (int j = 0; j < 8; ++j) {
+          const float s = fmaf(elem<T>::load(&xv[u][t]), f[j], acc[t][j]);
+          acc[t][j] = in ? s : acc[t][j];
+        }
     }
+    wp += U * step;
+  };
+  int k = kl;
+  for (; k + (U - 1) * (FT / 2) < K; k += U * (FT / 2)) rows_of_w(std::false_type{}, k);
+  if (k < K) rows_of_w(std::true_type{}, k);
+  // over the 32 lanes of a column block: half of the 8 values goes to the other lane of a pair,
+  // then half of the 4 left, then of the 2
+  const int lane = threadIdx.x & 63;
+  const bool b1 = lane & 2, b2 = lane & 4, b3 = lane & 8;
+  const int col = (b1 ? 4 : 0) + (b2 ? 2 : 0) + (b3 ? 1 : 0);
+#pragma unroll
+  for (int t = 0; t < ROWS; ++t) {
+    float h[4], q[2], s;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = (b1 ? acc[t][4 + j] : acc[t][j]) + __shfl_xor(b1 ? acc[t][j] : acc[t][4 + j], 2, 64);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) q[j] = (b2 ? h[2 + j] : h[j]) + __shfl_xor(b2 ? h[j] : h[2 + j], 4, 64);
+    s = (b3 ? q[1] : q[0]) + __shfl_xor(b3 ? q[0] : q[1], 8, 64);
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (lane < 16 && at + col >= n) red[threadIdx.x >> 6][t][at + col - n0] = s;
+  }
   __syncthreads();
   const int t = threadIdx.x / FC, m = n0 + (int)threadIdx.x % FC;
   if (t < rows && t < ROWS && m < N) {
@@ -211,75 +311,108 @@ __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, cons
   }
 }
 
-template <typename T, bool WIDE>
+template <typename T>
 void launch_few(const T* x, const T* w, int rows, int K, int N, const Epilogue<T>& e, hipStream_t st) {
   const dim3 grid((unsigned)(ceil_div(ceil_div(N, FC), 8) * 8));
-#define CALL(R) MOE_LAUNCH("linear_fwd", (k_linear_few<T, WIDE, R>), grid, dim3(FT), 0, st, x, w, rows, K, N, e)
+#define CALL(R) MOE_LAUNCH("linear_fwd", (k_linear_few<T, R>), grid, dim3(FT), 0, st, x, w, rows, K, N, e)
   if (rows == 1) CALL(1);
   else if (rows == 2) CALL(2);
   else CALL(4);
 #undef CALL
 }
 
+// ---------------- rows laid out for the tiles ----------------
+// Two bf16 matrices copied with rows of whole 16-byte chunks, zeros behind: a row takes 2^sh
+// lanes, a chunk each.
+struct Pad {
+  const bf16_t* from;
+  bf16_t* to;
+  int64_t rows, wgs;
+  int cols, sh;
+};
+__global__ __launch_bounds__(256) void k_linear_pad(Pad p0, Pad p1) {
+  const bool second = blockIdx.x >= p0.wgs;
+  const Pad p = second ? p1 : p0;
+  const int64_t row = ((int64_t)blockIdx.x - (second ? p0.wgs : 0)) * (256 >> p.sh) + (threadIdx.x >> p.sh);
+  if (row >= p.rows) return;
+  const int chunks = (p.cols + 7) / 8;
+  const bf16_t* const from = p.from + row * p.cols;
+  i32x4* const to = reinterpret_cast<i32x4*>(p.to) + row * chunks;
+  for (int c = threadIdx.x & ((1 << p.sh) - 1); c < chunks; c += 1 << p.sh) {
+    i32x4 u;
+    if (8 * c + 8 <= p.cols) {
+      u = *reinterpret_cast<const i32x4_a2*>(from + 8 * c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = 8 * c + 2 * j;
+        u[j] = (int)((uint32_t)(n < p.cols ? from[n] : 0) | (uint32_t)(n + 1 < p.cols ? from[n + 1] : 0) << 16);
+      }
+    }
+    to[c] = u;
+  }
+}
+
+Pad pad_of(const bf16_t* from, bf16_t* to, int64_t rows, int cols) {
+  int sh = 2;
+  while (sh < 6 && (8 << sh) < cols) ++sh;
+  return {from, to, rows, ceil_div(rows, 256 >> sh), cols, sh};
+}
+
 // ---------------- dz and db ----------------
-// dz = dy act'(z) and the workgroup's share of db.  WIDE: 32 lanes of 8 columns by 8 rows at a time;
-// else a lane for each column, row by row.
+// dz = dy act'(z) and the workgroup's share of db: 32 lanes of 8 columns by 8 rows at a time.  dz
+// (or null) has rows of ldz, zeros past N; z may be null: no activation, dz a copy.
 constexpr int ZC = 256;   // columns of a workgroup
-template <typename T, bool WIDE>
+template <typename T>
 __global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dy, const T* __restrict__ z, int64_t rows,
-                                                   int N, int act, int slab, T* __restrict__ dz,
+                                                   int N, int act, int slab, T* __restrict__ dz, int ldz,
                                                    float* __restrict__ part) {
+  __shared__ float red[8][ZC];
   const int64_t t0 = (int64_t)blockIdx.x * slab, t1 = min(rows, t0 + slab);
-  const int m = blockIdx.y * ZC + threadIdx.x;
-  if constexpr (WIDE) {
-    __shared__ float red[8][ZC];
-    const int c = (threadIdx.x & 31) * 8, r = threadIdx.x >> 5, n = blockIdx.y * ZC + c;
-    float s[8];
+  const int c = (threadIdx.x & 31) * 8, r = threadIdx.x >> 5, n = blockIdx.y * ZC + c;
+  float s[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = 0.f;
-    if (n < N)
+  for (int j = 0; j < 8; ++j) s[j] = 0.f;
+  if (n + 8 <= N) {
 #pragma unroll 2
-      for (int64_t t = t0 + r; t < t1; t += 8) {
-        float d[8], v[8];
-        load8<T, true>(dy + t * N + n, 8, d);
-        if (dz) {
-          load8<T, true>(z + t * N + n, 8, v);
-          slope8(d, v, act);
-          store8<T, true>(dz + t * N + n, 8, d);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] += d[j];
-      }
-    if (!part) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) red[r][c + j] = s[j];
-    __syncthreads();
-    if (m < N) {
-      float a = 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) a += red[q][threadIdx.x];
-      part[(size_t)blockIdx.x * N + m] = a;
-    }
-  } else {
-    if (m >= N) return;
-    float s = 0.f;
-    for (int64_t t = t0; t < t1; t += 8) {   // 8 rows in flight; past the end the last one, for nothing
+    for (int64_t t = t0 + r; t < t1; t += 8) {
       float d[8], v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t at = min(t + j, t1 - 1) * N + m;
-        d[j] = elem<T>::load(dy + at);
-        v[j] = dz ? elem<T>::load(z + at) : 0.f;
-      }
-      if (dz) slope8(d, v, act);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (t + j < t1) {
-          if (dz) elem<T>::store(dz + (t + j) * N + m, d[j]);
-          s += d[j];
+      load8(dy + t * N + n, d);
+      if (dz) {
+        if (z) {
+          load8(z + t * N + n, v);
+          slope8(d, v, act);
         }
+        store8(dz + t * ldz + n, d);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += d[j];
     }
-    if (part) part[(size_t)blockIdx.x * N + m] = s;
+  } else if (n < N) {
+    for (int64_t t = t0 + r; t < t1; t += 8) {
+      float d[8], v[8];
+      load_some(dy + t * N + n, N - n, d);
+      if (dz) {
+        if (z) {
+          load_some(z + t * N + n, N - n, v);
+          slope8(d, v, act);
+        }
+        store_some(dz + t * ldz + n, ldz - n, d);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += d[j];
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[r][c + j] = s[j];
+  __syncthreads();
+  const int m = blockIdx.y * ZC + threadIdx.x;
+  if (m < N) {
+    float a = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) a += red[q][threadIdx.x];
+    part[(size_t)blockIdx.x * N + m] = a;
   }
 }
 
@@ -307,25 +440,66 @@ int dz_slab(const moe_linear_shape& s) {
 }
 
 inline bool at16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+constexpr double kPadFrom = 2e8;
 // the tiles take bf16 rows of whole 16-byte chunks, the general kernel the rest
 template <typename T>
 bool tiled(const moe_linear_shape& s) { return sizeof(T) == 2 && s.K % 8 == 0 && s.N % 8 == 0; }
+// or, where that is worth the copies, the tiles after x and W were laid out anew
+bool padded(const moe_linear_shape& s) {
+  return s.dtype == MOE_BF16 && s.T > FEW && (s.K % 8 != 0 || s.N % 8 != 0) && (double)s.T * s.K * s.N >= kPadFrom;
+}
+inline int up8(int n) { return (n + 7) / 8 * 8; }
+
+struct LinearLayout {
+  // scratch: dz, x and W laid out anew, the shares of db, those of a product split along its sum
+  size_t off_x, off_w, off_db, off_part;
+};
+// (the shares come last: their room takes the plans of all three products, which a call need not know)
+LinearLayout linear_layout(const moe_linear_shape& s) {
+  const size_t es = s.dtype == MOE_BF16 ? 2 : 4;
+  LinearLayout L{};
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const bool pad = padded(s);
+  L.off_x = s.act == MOE_ACT_NONE && !(pad && s.N % 8 != 0) ? 0 : up((size_t)s.T * (pad ? up8(s.N) : s.N) * es);
+  L.off_w = L.off_x + (pad && s.K % 8 != 0 ? up((size_t)s.T * up8(s.K) * es) : 0);
+  L.off_db = L.off_w + (pad && s.N % 8 != 0 ? up((size_t)s.K * up8(s.N) * es) : 0);
+  L.off_part = L.off_db + up((size_t)ceil_div(s.T, dz_slab(s)) * s.N * 4);
+  return L;
+}
+
+// the operands as the tiles take them; false: one is out of place
+bool pad_operands(const moe_linear_shape& s, const LinearLayout& L, void* scratch, const bf16_t*& x, const bf16_t*& w,
+                  hipStream_t st) {
+  const bool px = s.K % 8 != 0, pw = s.N % 8 != 0;
+  if ((!px && !at16(x)) || (!pw && !at16(w))) return false;
+  Pad p[2];
+  int n = 0;
+  if (px) p[n++] = pad_of(x, (bf16_t*)((char*)scratch + L.off_x), s.T, s.K);
+  if (pw) p[n++] = pad_of(w, (bf16_t*)((char*)scratch + L.off_w), s.K, s.N);
+  if (n == 1) p[1] = Pad{};
+  MOE_LAUNCH("linear_pad", k_linear_pad, dim3((unsigned)(p[0].wgs + p[1].wgs)), dim3(256), 0, st, p[0], p[1]);
+  if (px) x = (const bf16_t*)((char*)scratch + L.off_x);
+  if (pw) w = (const bf16_t*)((char*)scratch + L.off_w);
+  return true;
+}
 
 template <typename T>
 hipError_t fwd(const moe_linear_shape& s, const T* x, const T* w, const T* b, const T* res, T* z, T* y, void* scratch,
                hipStream_t st) {
-  float* const part = (float*)((char*)scratch + linear_layout(s).off_part);
   Epilogue<T> e{};
   e.out = y; e.z = z; e.bias = b; e.add = res; e.act = s.act;
-  if (s.T <= FEW) {
-    if (s.N % 8 == 0 && at16(w)) launch_few<T, true>(x, w, s.T, s.K, s.N, e, st);
-    else launch_few<T, false>(x, w, s.T, s.K, s.N, e, st);
+  if (s.T <= FEW && s.N >= 8) {
+    launch_few<T>(x, w, s.T, s.K, s.N, e, st);
     return hipGetLastError();
   }
-  if constexpr (sizeof(T) == 2)
-    if (tiled<T>(s) && at16(x) && at16(w) && at16(b) && at16(res) && at16(z) && at16(y))
-      return launch_linear_tiles("linear_fwd", x, s.K, true, w, s.N, false, s.T, s.N, s.K, {y, z, b, res, s.act}, part,
-                                 st);
+  const LinearLayout L = linear_layout(s);
+  float* const part = (float*)((char*)scratch + L.off_part);
+  if constexpr (sizeof(T) == 2) {
+    const bool wide = s.N % 8 == 0 && at16(b) && at16(res) && at16(z) && at16(y);
+    if ((tiled<T>(s) && wide && at16(x) && at16(w)) || (padded(s) && pad_operands(s, L, scratch, x, w, st)))
+      return launch_linear_tiles("linear_fwd", x, up8(s.K), true, w, up8(s.N), false, s.T, s.N, s.K,
+                                 {y, z, b, res, s.act, wide}, part, st);
+  }
   return general<T>("linear_fwd", x, w, s.K, 1, s.N, 1, s.T, s.N, s.K, e, part, st);
 }
 
@@ -333,31 +507,34 @@ template <typename T>
 hipError_t bwd(const moe_linear_shape& s, const T* dy, const T* x, const T* w, const T* z, const T* dx_in, T* dx,
                T* dw, T* db, void* scratch, hipStream_t st) {
   const LinearLayout L = linear_layout(s);
-  T* const dzbuf = s.act == MOE_ACT_NONE ? nullptr : (T*)scratch;
+  bool tiles = tiled<T>(s) && at16(dy) && at16(x) && at16(w) && at16(dx_in) && at16(dx) && at16(dw);
+  if constexpr (sizeof(T) == 2)
+    if (padded(s) && (s.N % 8 != 0 || at16(dy))) tiles = pad_operands(s, L, scratch, x, w, st);
+  const bool pad_dz = tiles && s.N % 8 != 0;
+  const int ldz = pad_dz ? up8(s.N) : s.N;
+  T* const dzbuf = s.act == MOE_ACT_NONE && !pad_dz ? nullptr : (T*)scratch;
   float* const dbp = (float*)((char*)scratch + L.off_db);
   float* const part = (float*)((char*)scratch + L.off_part);
   const T* dz = dzbuf ? dzbuf : dy;
   const int slab = dz_slab(s), W = (int)ceil_div(s.T, slab);
   if ((dzbuf || db) && s.T > 0) {
     const dim3 grid((unsigned)W, (unsigned)ceil_div(s.N, ZC));
-    if (s.N % 8 == 0 && at16(dy) && at16(z))
-      MOE_LAUNCH("linear_dz", (k_linear_dz<T, true>), grid, dim3(256), 0, st, dy, z, (int64_t)s.T, s.N, s.act, slab,
-                 dzbuf, db ? dbp : nullptr);
-    else
-      MOE_LAUNCH("linear_dz", (k_linear_dz<T, false>), grid, dim3(256), 0, st, dy, z, (int64_t)s.T, s.N, s.act, slab,
-                 dzbuf, db ? dbp : nullptr);
+    MOE_LAUNCH("linear_dz", k_linear_dz<T>, grid, dim3(256), 0, st, dy, z, (int64_t)s.T, s.N, s.act, slab, dzbuf, ldz,
+               db ? dbp : nullptr);
   }
   if (db)
     MOE_LAUNCH("linear_db", k_linear_db<T>, dim3((unsigned)ceil_div(s.N, 64)), dim3(1024), 0, st, dbp, W, s.N, db);
   hipError_t err = hipGetLastError();
   if constexpr (sizeof(T) == 2)
-    if (tiled<T>(s) && at16(dy) && at16(x) && at16(w) && at16(dx_in) && at16(dx) && at16(dw)) {
+    if (tiles) {
+      const int ldx = up8(s.K), ldw = up8(s.N);
       if (err == hipSuccess && dx && s.T > 0)
-        err = launch_linear_tiles("linear_dx", dz, s.N, true, w, s.N, true, s.T, s.K, s.N,
-                                  {dx, nullptr, nullptr, dx_in, MOE_ACT_NONE}, part, st);
+        err = launch_linear_tiles("linear_dx", dz, ldw, true, w, ldw, true, s.T, s.K, s.N,
+                                  {dx, nullptr, nullptr, dx_in, MOE_ACT_NONE, s.K % 8 == 0 && at16(dx) && at16(dx_in)}, part,
+                                  st);
       if (err == hipSuccess)
-        err = launch_linear_tiles("linear_dw", x, s.K, false, dz, s.N, false, s.K, s.N, s.T,
-                                  {dw, nullptr, nullptr, nullptr, MOE_ACT_NONE}, part, st);
+        err = launch_linear_tiles("linear_dw", x, ldx, false, dz, ldw, false, s.K, s.N, s.T,
+                                  {dw, nullptr, nullptr, nullptr, MOE_ACT_NONE, s.N % 8 == 0 && at16(dw)}, part, st);
       return err;
     }
   if (err == hipSuccess && dx) {
@@ -375,22 +552,18 @@ hipError_t bwd(const moe_linear_shape& s, const T* dy, const T* x, const T* w, c
 
 }  // namespace
 
-LinearLayout linear_layout(const moe_linear_shape& s) {
-  const size_t es = s.dtype == MOE_BF16 ? 2 : 4;
-  LinearLayout L{};
-  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  L.off_part = s.act == MOE_ACT_NONE ? 0 : up((size_t)s.T * s.N * es);
+size_t linear_scratch_bytes(const moe_linear_shape& s) {
   size_t part = 0;   // of the largest of the three products, on the tiles or on the general kernel
-  const bool tiles = s.dtype == MOE_BF16 && tiled<bf16_t>(s);
+  const bool tiles = padded(s) || (s.dtype == MOE_BF16 && tiled<bf16_t>(s));
   const int64_t of[3][3] = {{s.T, s.N, s.K}, {s.T, s.K, s.N}, {s.K, s.N, s.T}};
   for (const auto& d : of) {
-    const size_t a = tiles ? linear_part_bytes(d[0], d[1], d[2]) : 0, b = general_part_bytes(d[0], d[1], d[2]);
+    const size_t a = tiles ? linear_part_bytes(d[0], d[1], d[2]) : 0;
+    const size_t b = s.dtype == MOE_BF16 ? general_part_bytes<bf16_t>(d[0], d[1], d[2])
+                                         : general_part_bytes<float>(d[0], d[1], d[2]);
     part = a > part ? a : part;
     part = b > part ? b : part;
   }
-  L.off_db = L.off_part + up(part);
-  L.bytes = L.off_db + up((size_t)ceil_div(s.T, dz_slab(s)) * s.N * 4);
-  return L;
+  return linear_layout(s).off_part + part;
 }
 
 hipError_t launch_linear_fwd(const moe_linear_shape& s, const void* x, const void* w, const void* b, const void* res,

@@ -158,24 +158,47 @@ __device__ __forceinline__ bool tile_item(const TileArgs& g, int& mt, int& nt, i
   return true;
 }
 
-// The added matrix's pieces of a band, as band_epilogue takes them; outside of it any valid one
-template <int NB>
-__device__ __forceinline__ void load_add(const bf16_t* add, int64_t r0, int64_t c0, int64_t M, int64_t N, int lane,
-                                         i32x4 (&u)[NB][2]) {
-  const bf16_t* const row = add + min(r0 + (lane & 31), M - 1) * N;
+// 8 elements from column c of a row of N on; past its end any there are.  WIDE: the row is whole chunks
+template <bool WIDE>
+__device__ __forceinline__ i32x4 row_piece(const bf16_t* row, int64_t c, int64_t N) {
+  if constexpr (WIDE) return *reinterpret_cast<const i32x4*>(row + min(c, N - 8));
+  if (c + 8 <= N) return *reinterpret_cast<const i32x4_a2*>(row + c);
+  i32x4 u;
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      u[b][s] = *reinterpret_cast<const i32x4*>(row + min(c0 + 32 * b + 16 * s + 8 * (lane >> 5), N - 8));
+  for (int j = 0; j < 4; ++j)
+    u[j] = (int)((uint32_t)row[min(c + 2 * j, N - 1)] | (uint32_t)row[min(c + 2 * j + 1, N - 1)] << 16);
+  return u;
 }
+
+// The added matrix's pieces of a band, as band_epilogue takes them; outside of it any valid one.
+// Elements one by one take registers that the tile needs: they are loaded where they are added.
+template <bool WIDE, int NB>
+struct AddBand {
+  const bf16_t* row;
+  int64_t c, N;
+  i32x4 u[WIDE ? NB : 1][2];
+  __device__ __forceinline__ void load(const bf16_t* add, int64_t r0, int64_t c0, int64_t M, int64_t N_, int lane) {
+    row = add + min(r0 + (lane & 31), M - 1) * N_;
+    c = c0 + 8 * (lane >> 5);
+    N = N_;
+    if constexpr (WIDE)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) u[b][s] = row_piece<true>(row, c + 32 * b + 16 * s, N);
+  }
+  __device__ __forceinline__ i32x4 piece(int b, int s) const {
+    if constexpr (WIDE) return u[b][s];
+    else return row_piece<false>(row, c + 32 * b + 16 * s, N);
+  }
+};
 
 // A band of 32 rows and 32 NB columns of C^T accumulators through the epilogue: lanes l and
 // l + 32 trade halves so that each has 8 columns of its row in fp32, and the rounded results
-// leave through the wave's LDS region as whole row segments.  add: load_add's, if e.add is there;
+// leave through the wave's LDS region as whole row segments.  add: loaded, if e.add is there;
 // after(): what to issue ahead of the stores.  FULL: with bias, activation and z.
-template <bool FULL, int NB, class F>
-__device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f32x16* acc, const i32x4 (&add)[NB][2],
+template <bool FULL, bool WIDE, int NB, class F>
+__device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f32x16* acc, const AddBand<WIDE, NB>& add,
                                               int64_t r0, int64_t c0, int64_t M, int64_t N, bf16_t* wreg, int lane,
                                               F&& after) {
   i32x4 chz[NB][2], chy[NB][2];
@@ -195,7 +218,7 @@ __device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f
       if constexpr (FULL) {
         if (e.bias) {
           const int64_t col = c0 + 32 * b + 16 * s + 8 * (lane >> 5);
-          unpack8(*reinterpret_cast<const i32x4*>(e.bias + min(col, N - 8)), u);
+          unpack8(row_piece<WIDE>(e.bias, col, N), u);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] += u[i];
         }
@@ -203,7 +226,7 @@ __device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f
         act8(v, e.act);
       }
       if (e.add) {
-        unpack8(add[b][s], u);
+        unpack8(add.piece(b, s), u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += u[i];
       }
@@ -213,7 +236,15 @@ __device__ __forceinline__ void band_epilogue(const Epilogue<bf16_t>& e, const f
   auto put = [&](bf16_t* to, const i32x4 (&ch)[NB][2]) {
     band_store(wreg, ch, [&](int rr, int cb, i32x4 v) {
       const int64_t r = r0 + rr, c = c0 + cb;
-      if (r < M && c < N) *reinterpret_cast<i32x4*>(to + r * N + c) = v;
+      if constexpr (WIDE) {
+        if (r < M && c < N) *reinterpret_cast<i32x4*>(to + r * N + c) = v;
+      } else if (r < M && c + 8 <= N) {
+        *reinterpret_cast<i32x4_a2*>(to + r * N + c) = v;
+      } else if (r < M) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < N) to[r * N + c + j] = (bf16_t)((uint32_t)v[j / 2] >> (16 * (j & 1)));
+      }
     });
   };
   if constexpr (FULL)
@@ -240,7 +271,8 @@ __device__ __forceinline__ void stage_products(const bf16_t* st, f32x16 (&acc)[S
   }
 }
 
-template <class S, bool AK, bool BKM>
+// WIDE: the epilogue's rows are whole 16-byte chunks at multiples of 16
+template <class S, bool AK, bool BKM, bool WIDE>
 __global__ __launch_bounds__(S::THR, (S::OCC * S::TW + 3) / 4) void k_linear_tile(TileArgs g) {
   constexpr int TW = S::TW;
   __shared__ __attribute__((aligned(16))) bf16_t lds[2 * S::STAGE];
@@ -296,20 +328,20 @@ __global__ __launch_bounds__(S::THR, (S::OCC * S::TW + 3) / 4) void k_linear_til
   }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave is done with the stages
   bf16_t* const wreg = lds + wv * S::BAND;
-  i32x4 add[2][S::NB][2];   // of a band and the next
+  AddBand<WIDE, S::NB> add[2];   // of a band and the next
   auto fetch = [&](int i) {
-    if (g.e.add) load_add<S::NB>(g.e.add, m0 + wm + i * 32, n0 + wn, g.M, g.N, lane, add[i & 1]);
+    if (g.e.add) add[i & 1].load(g.e.add, m0 + wm + i * 32, n0 + wn, g.M, g.N, lane);
   };
   fetch(0);
 #pragma unroll
   for (int i = 0; i < S::MI; ++i)
-    band_epilogue<AK && !BKM, S::NB>(g.e, acc[i], add[i & 1], m0 + wm + i * 32, n0 + wn, g.M, g.N, wreg, lane, [&] {
+    band_epilogue<AK && !BKM, WIDE, S::NB>(g.e, acc[i], add[i & 1], m0 + wm + i * 32, n0 + wn, g.M, g.N, wreg, lane, [&] {
       if (i + 1 < S::MI) fetch(i + 1);
     });
 }
 
 // The shares of a tile's bands added in order, and the epilogue: a workgroup for a band of each wave
-template <class S, bool FULL>
+template <class S, bool FULL, bool WIDE>
 __global__ __launch_bounds__(S::THR) void k_linear_join(TileArgs g) {
   constexpr int TW = S::TW;
   __shared__ __attribute__((aligned(16))) bf16_t lds[TW * S::BAND];
@@ -318,8 +350,8 @@ __global__ __launch_bounds__(S::THR) void k_linear_join(TileArgs g) {
   const int mt = tile / g.tn, nt = tile % g.tn;
   const int wm = wv % S::WMS * (32 * S::MI), wn = wv / S::WMS * (32 * S::NI);
   const int64_t r0 = (int64_t)mt * S::TM + wm + i * 32, c0 = (int64_t)nt * S::TN + wn;
-  i32x4 add[S::NB][2];
-  if (g.e.add) load_add<S::NB>(g.e.add, r0, c0, g.M, g.N, lane, add);
+  AddBand<WIDE, S::NB> add;
+  if (g.e.add) add.load(g.e.add, r0, c0, g.M, g.N, lane);
   f32x16 acc[S::NB];
 #pragma unroll
   for (int j = 0; j < S::NB; ++j)
@@ -341,84 +373,52 @@ __global__ __launch_bounds__(S::THR) void k_linear_join(TileArgs g) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[j][4 * q + r] += v[j][q][r];
   }
-  band_epilogue<FULL, S::NB>(g.e, acc, add, r0, c0, g.M, g.N, lds + wv * S::BAND, lane, [] {});
+  band_epilogue<FULL, WIDE, S::NB>(g.e, acc, add, r0, c0, g.M, g.N, lds + wv * S::BAND, lane, [] {});
 }
 
 typedef Shape<256, 256, 4, 2, 1> Big;     // 8 waves of 128 x 64
 typedef Shape<128, 128, 2, 2, 2> Mid;     // waves of 64 x 64
 typedef Shape<64, 64, 1, 1, 4> Small;     // waves of 32 x 32
 
-// Which tiles, and into how many shares a product is split along K: by the estimated time.  A
-// step of 64 of K takes a workgroup alone on its CU `alone` us (barrier, LDS and load latency) and r
-// of them r `share` us together, as measured on one MI355X; the shares' sums cost a launch and
-// their bytes.
-struct Plan {
-  int shape, splits;
-  int64_t ks;
-};
-struct Cost {
-  int tm, tn, occ;
-  double alone, share;
-};
-constexpr Cost kCost[3] = {{256, 256, 1, 1.45, 1.45}, {128, 128, 2, 0.65, 0.54}, {64, 64, 4, 0.45, 0.182}};
-
-double plan_us(const Cost& c, int64_t M, int64_t N, int64_t ks, int splits) {
-  const double cus = num_cus();
-  const int64_t wgs = ceil_div(M, c.tm) * ceil_div(N, c.tn) * splits, slots = (int64_t)cus * c.occ;
-  auto step = [&](double r) { return r * c.share > c.alone ? r * c.share : c.alone; };
-  const int64_t full = wgs / slots, rest = wgs - full * slots;
-  const double r = 0.5 * (rest / cus + (double)ceil_div(rest, (int64_t)cus));   // some CUs have one more
-  const double steps = (double)ceil_div(ks, BK);
-  double us = full * (steps * step(c.occ) + 2.0) + (rest > 0 ? steps * step(r) + 2.0 : 0.0);
-  if (splits > 1) us += 5.0 + (double)splits * M * N * 4 / 4e6;
-  return us;
+constexpr PlanCost kCost[3] = {{256, 256, 1, 1.45, 1.45, 2.0, 5.0, 4.0}, {128, 128, 2, 0.65, 0.54, 2.0, 5.0, 4.0},
+                                {64, 64, 4, 0.45, 0.182, 2.0, 5.0, 4.0}};
+// (wide: the largest tiles have no registers for an epilogue element by element)
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool wide) {
+  const int first = wide ? 0 : 1;
+  Plan p = plan_product(kCost + first, 3 - first, BK, num_cus(), M, N, K);
+  p.shape += first;
+  return p;
 }
 
-Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  Plan best{2, 1, ceil_div(K, BK) * BK};
-  double least = 1e30;
-  for (int i = 0; i < 3; ++i) {
-    int64_t last = -1;
-    for (int s = 1; s <= 16; ++s) {
-      const int64_t ks = ceil_div(ceil_div(K, s), BK) * BK;
-      const int n = ks > 0 ? (int)ceil_div(K, ks) : 1;   // shares that are not empty
-      if (ks == last) continue;
-      last = ks;
-      const double us = plan_us(kCost[i], M, N, ks, n);
-      if (us < least) {
-        least = us;
-        best = {i, n, ks};
-      }
-    }
-  }
-  return best;
-}
-
-template <class S>
+template <class S, bool WIDE>
 hipError_t run(const char* name, bool a_k, bool b_k, const TileArgs& g, hipStream_t st) {
   const dim3 grid((unsigned)(ceil_div((int64_t)g.tm * g.tn * g.splits, 8) * 8));
-  if (a_k && !b_k) MOE_LAUNCH(name, (k_linear_tile<S, true, false>), grid, dim3(S::THR), 0, st, g);
-  else if (a_k) MOE_LAUNCH(name, (k_linear_tile<S, true, true>), grid, dim3(S::THR), 0, st, g);
-  else MOE_LAUNCH(name, (k_linear_tile<S, false, false>), grid, dim3(S::THR), 0, st, g);
+  if (a_k && !b_k) MOE_LAUNCH(name, (k_linear_tile<S, true, false, WIDE>), grid, dim3(S::THR), 0, st, g);
+  else if (a_k) MOE_LAUNCH(name, (k_linear_tile<S, true, true, WIDE>), grid, dim3(S::THR), 0, st, g);
+  else MOE_LAUNCH(name, (k_linear_tile<S, false, false, WIDE>), grid, dim3(S::THR), 0, st, g);
   const dim3 bands((unsigned)(g.tm * g.tn * S::MI));
-  if (g.part && a_k && !b_k) MOE_LAUNCH("linear_join", (k_linear_join<S, true>), bands, dim3(S::THR), 0, st, g);
-  else if (g.part) MOE_LAUNCH("linear_join", (k_linear_join<S, false>), bands, dim3(S::THR), 0, st, g);
+  if (g.part && a_k && !b_k) MOE_LAUNCH("linear_join", (k_linear_join<S, true, WIDE>), bands, dim3(S::THR), 0, st, g);
+  else if (g.part) MOE_LAUNCH("linear_join", (k_linear_join<S, false, WIDE>), bands, dim3(S::THR), 0, st, g);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t linear_part_bytes(int64_t M, int64_t N, int64_t K) {
-  const Plan p = plan_of(M, N, K);
-  if (p.splits == 1) return 0;
-  const Cost& c = kCost[p.shape];
-  return (size_t)p.splits * ceil_div(M, c.tm) * ceil_div(N, c.tn) * c.tm * c.tn * 4;
+  size_t most = 0;
+  for (int wide = 0; wide < 2; ++wide) {
+    const Plan p = plan_of(M, N, K, wide != 0);
+    const PlanCost& c = kCost[p.shape];
+    const size_t b = p.splits == 1 ? 0 : (size_t)p.splits * ceil_div(M, c.tm) * ceil_div(N, c.tn) * c.tm * c.tn * 4;
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 hipError_t launch_linear_tiles(const char* name, const bf16_t* a, int64_t lda, bool a_k, const bf16_t* b, int64_t ldb,
                                bool b_k, int64_t M, int64_t N, int64_t K, const LinearOut& o, float* part,
                                hipStream_t st) {
-  const Plan p = plan_of(M, N, K);
+  const Plan p = plan_of(M, N, K, o.wide);
   TileArgs g{};
   g.a = a; g.b = b; g.lda = lda; g.ldb = ldb; g.M = M; g.N = N; g.K = K;
   g.tm = (int)ceil_div(M, kCost[p.shape].tm); g.tn = (int)ceil_div(N, kCost[p.shape].tn);
@@ -426,9 +426,9 @@ hipError_t launch_linear_tiles(const char* name, const bf16_t* a, int64_t lda, b
   g.part = p.splits > 1 ? part : nullptr;
   g.e.out = o.out; g.e.z = o.z; g.e.bias = o.bias; g.e.add = o.add; g.e.act = o.act;
   switch (p.shape) {
-    case 0: return run<Big>(name, a_k, b_k, g, st);
-    case 1: return run<Mid>(name, a_k, b_k, g, st);
-    default: return run<Small>(name, a_k, b_k, g, st);
+    case 0: return run<Big, true>(name, a_k, b_k, g, st);
+    case 1: return o.wide ? run<Mid, true>(name, a_k, b_k, g, st) : run<Mid, false>(name, a_k, b_k, g, st);
+    default: return o.wide ? run<Small, true>(name, a_k, b_k, g, st) : run<Small, false>(name, a_k, b_k, g, st);
   }
 }
 

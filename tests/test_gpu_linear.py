@@ -335,3 +335,57 @@ def test_gelu_far_out(dtype, T):
     assert (np.abs(y - z * q) <= (rel * (1 + HALF[dtype]) + HALF[dtype]) * np.abs(z * q)).all()
     err = rel * (q + np.abs(phi))
     assert (np.abs(dx - (q + phi)) <= 2.1 * HALF[dtype] * np.abs(q + phi) + (1 + HALF[dtype]) ** 2 * err).all()
+
+
+# widths that no 16 bytes divide, large enough for the copies with padded rows, of one operand or of both;
+# 8185 rows: the general kernel's larger tiles; one and three rows of 7, 8 and 9 columns
+ODD = [(300, 777, 1555), (1000, 1001, 520), (1000, 520, 1001), (4100, 1001, 100), (8185, 261, 1021), (1, 300, 9), (3, 70, 7),
+       (3, 4100, 17), (4, 1, 8)]
+
+
+@pytest.mark.parametrize("act,bias,res", [("none", False, False), ("silu", True, True)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", ODD, ids=lambda s: "x".join(map(str, s)))
+def test_linear_of_odd_widths(size, dtype, act, bias, res):
+    T, K, N = size
+    t = _inputs(T, K, N, dtype, T + K, bias, res)
+    x, w, b, r, dy = t
+    op = _op(T, K, N, act, dtype)
+    op.scratch.fill_(0xFF)   # NaN wherever it is read before it is written
+    y = op.forward(x, w, b, res=r)
+    op.scratch.fill_(0xFF)
+    dx_in = torch.randn(T, K, generator=torch.Generator().manual_seed(1)).to(x.dtype).cuda()
+    grads = op.backward(dy, dx_in=dx_in)
+    torch.cuda.synchronize()
+    _verify(op, t, y, grads, dx_in)
+
+
+@pytest.mark.parametrize("size", [(300, 777, 1555), (1000, 1001, 520), (1000, 520, 1001)])
+@pytest.mark.parametrize("off", [1, 8])
+def test_linear_of_odd_widths_anywhere(size, off):
+    """The same from any address, and nothing around the results is written."""
+    from combine_top_router_amd import lib as L
+    T, K, N = size
+    t = _inputs(T, K, N, "bf16", 4)
+
+    def moved(v):
+        buf = torch.full((v.numel() + 16,), float("nan"), dtype=v.dtype, device="cuda")
+        buf[off:off + v.numel()] = v.reshape(-1)
+        return buf[off:off + v.numel()].view(v.shape)
+
+    x, w, b, r, dy = t = tuple(moved(v) for v in t)
+    op = _op(T, K, N, "silu", "bf16")
+    bufs = {n: torch.full((s + 16,), 7.0, dtype=x.dtype, device="cuda") for n, s in
+            (("y", T * N), ("z", T * N), ("dx", T * K), ("dw", K * N), ("db", N))}
+    at = {n: v[off:].data_ptr() for n, v in bufs.items()}
+    st = torch.cuda.current_stream().cuda_stream
+    L.moe_linear_fwd(op.shape, x.data_ptr(), w.data_ptr(), b.data_ptr(), r.data_ptr(), at["z"], at["y"],
+                     op.scratch.data_ptr(), st)
+    L.moe_linear_bwd(op.shape, dy.data_ptr(), x.data_ptr(), w.data_ptr(), at["z"], 0, at["dx"], at["dw"], at["db"],
+                     op.scratch.data_ptr(), st)
+    torch.cuda.synchronize()
+    size_of = {"y": (T, N), "z": (T, N), "dx": (T, K), "dw": (K, N), "db": (N,)}
+    for n, s in size_of.items():
+        assert (bufs[n][:off] == 7).all() and (bufs[n][off + math.prod(s):] == 7).all(), n
+    got = {n: bufs[n][off:off + math.prod(s)].view(s) for n, s in size_of.items()}
+    _verify(op, t, got["y"], got)
