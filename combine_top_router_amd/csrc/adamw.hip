@@ -121,6 +121,13 @@ __device__ __forceinline__ void decode(uint2 c, int X, float (&x)[VEC]) {
   }
 }
 
+// a x + b y, each product and the sum rounded by itself: with gradients of few bits b1 m + (1 - b1) g
+// often lies halfway between two codes in fp32, and a fused product would take the other one
+__device__ __forceinline__ float blend(float a, float x, float b, float y) {
+#pragma clang fp contract(off)
+  return a * x + b * y;
+}
+
 // the root by the hardware's (1 ulp), of numbers below 2^-96 by that of 2^64 times them
 __device__ __forceinline__ float root(float v) {
   const bool low = v < 0x1p-96f;
@@ -240,8 +247,8 @@ __global__ __launch_bounds__(AT) void k_adamw(AdamwTable tab, AdamwHyper h) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
     const float gj = g[j] * gs;
-    m[j] = h.b1 * m[j] + h.b1c * gj;
-    v[j] = h.b2 * v[j] + h.b2c * (gj * gj);
+    m[j] = blend(h.b1, m[j], h.b1c, gj);
+    v[j] = blend(h.b2, v[j], h.b2c, gj * gj);
     s[j] = root(v[j]);
     p[j] = p[j] * decay - rate * m[j] * __builtin_amdgcn_rcpf(fmaf(s[j], unbias, h.eps));
     if constexpr (S8) probe = fmaf(s[j], 0.f, fmaf(m[j], 0.f, probe));

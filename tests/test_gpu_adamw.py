@@ -336,3 +336,26 @@ def test_adamw_captured_needs_its_clock():
     graph.replay()
     torch.cuda.synchronize()
     assert op.t == 0 and not p.any() and (x == 2.0).all()
+
+
+def test_adamw_of_few_bits_goes_by_the_formula_in_fp32():
+    """Gradients of few bits put 0.9 m + 0.1 g halfway between two codes in fp32, each product and the sum
+    rounded: the codes are those of that number, to the bit (a fused product would move it off)."""
+    from combine_top_router_amd import AdamW, lib as L
+    g = torch.Generator().manual_seed(6)
+    n = 32 * 4096
+    p = torch.zeros(n, device="cuda")
+    op = AdamW([p], state=L.MOE_STATE_8BIT)
+    m = torch.zeros(n)
+    b, c = torch.tensor(0.9), torch.tensor(1.0 - 0.9)
+    for _ in range(4):
+        grad = (torch.randint(-64, 65, (n,), generator=g) / 16.0).bfloat16()
+        op.step([grad.cuda()], 1e-3)
+        m = b * m + c * grad.float()
+        blocks = m.view(-1, 32)
+        mant, e = torch.frexp(blocks.abs().amax(1))
+        e = e - 9 + (mant > 0.875).to(e.dtype)
+        codes = torch.ldexp(blocks, -e[:, None]).to(torch.float8_e4m3fn)
+        assert torch.equal(op.m.cpu(), codes.view(torch.uint8).view(-1))
+        assert torch.equal(op.m_scale.cpu(), (e + 127).to(torch.uint8))
+        m = torch.ldexp(codes.float(), e[:, None]).view(-1)
