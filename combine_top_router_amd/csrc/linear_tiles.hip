@@ -7,6 +7,12 @@
 // is transposed in memory.  Chunks past the end of K come from a zeroed area.  A product with
 // few tiles is split along K: the shares of a tile, in the accumulators' own order, are added by
 // a second launch in a fixed order, with the epilogue.
+//
+// The loads (127 to 170 us of 16384 x 1536 x 4096's 210) and the products (140 to 165) each come near
+// the whole time: what is left is their overlap.  4096^3 takes 113 us, 1.22 PFLOP/s (a library's
+// product of 8192^3: 1.27); 16384 x 1536 x 4096 forward 208 us with y alone, 264 with bias, silu,
+// residual and z (the epilogue's 400 MB, unhidden with one workgroup on a CU), dx 211, dw 187 + 25
+// for the shares.
 #define MOE_GEMM_FW 256
 #include "gemm_engine.h"
 #include "linear.h"
@@ -380,12 +386,15 @@ typedef Shape<256, 256, 4, 2, 1> Big;     // 8 waves of 128 x 64
 typedef Shape<128, 128, 2, 2, 2> Mid;     // waves of 64 x 64
 typedef Shape<64, 64, 1, 1, 4> Small;     // waves of 32 x 32
 
-constexpr PlanCost kCost[3] = {{256, 256, 1, 1.45, 1.45, 2.0, 5.0, 4.0}, {128, 128, 2, 0.65, 0.54, 2.0, 5.0, 4.0},
-                                {64, 64, 4, 0.45, 0.182, 2.0, 5.0, 4.0}};
-// (wide: the largest tiles have no registers for an epilogue element by element)
-Plan plan_of(int64_t M, int64_t N, int64_t K, bool wide) {
+constexpr PlanCost kCost[3] = {{256, 256, 1, 1.35, 1.6, 7.0, 5.0, 4.0}, {128, 128, 2, 0.65, 0.5, 6.0, 5.0, 4.0},
+                                {64, 64, 4, 0.45, 0.182, 4.0, 5.0, 4.0}};
+// wide: the largest tiles have no registers for an epilogue element by element.  arrays: 1 and how
+// many more the epilogue reads or writes; alone on its CU, a largest tile hides none of them.
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool wide, int arrays) {
+  PlanCost c[3] = {kCost[0], kCost[1], kCost[2]};
+  c[0].over += 4.0 * (arrays - 1);
   const int first = wide ? 0 : 1;
-  Plan p = plan_product(kCost + first, 3 - first, BK, num_cus(), M, N, K);
+  Plan p = plan_product(c + first, 3 - first, BK, num_cus(), M, N, K);
   p.shape += first;
   return p;
 }
@@ -406,8 +415,8 @@ hipError_t run(const char* name, bool a_k, bool b_k, const TileArgs& g, hipStrea
 
 size_t linear_part_bytes(int64_t M, int64_t N, int64_t K) {
   size_t most = 0;
-  for (int wide = 0; wide < 2; ++wide) {
-    const Plan p = plan_of(M, N, K, wide != 0);
+  for (int i = 0; i < 4; ++i) {   // element by element, or wide with 1, 2 or 3 arrays
+    const Plan p = plan_of(M, N, K, i > 0, i);
     const PlanCost& c = kCost[p.shape];
     const size_t b = p.splits == 1 ? 0 : (size_t)p.splits * ceil_div(M, c.tm) * ceil_div(N, c.tn) * c.tm * c.tn * 4;
     most = b > most ? b : most;
@@ -418,7 +427,7 @@ size_t linear_part_bytes(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_linear_tiles(const char* name, const bf16_t* a, int64_t lda, bool a_k, const bf16_t* b, int64_t ldb,
                                bool b_k, int64_t M, int64_t N, int64_t K, const LinearOut& o, float* part,
                                hipStream_t st) {
-  const Plan p = plan_of(M, N, K, o.wide);
+  const Plan p = plan_of(M, N, K, o.wide, 1 + (o.z ? 1 : 0) + (o.add ? 1 : 0));
   TileArgs g{};
   g.a = a; g.b = b; g.lda = lda; g.ldb = ldb; g.M = M; g.N = N; g.K = K;
   g.tm = (int)ceil_div(M, kCost[p.shape].tm); g.tn = (int)ceil_div(N, kCost[p.shape].tn);
