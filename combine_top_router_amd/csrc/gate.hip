@@ -7,15 +7,15 @@
 //   q_j = s_j / sum_i s_i over the chosen (renorm), or s_j;  w_j = scale q_j
 //
 // A choice is decided where two c differ in their last bits, so c is compared in fp64.  That
-// takes longer than fp32 (16384 x 256 in 8 groups: 56 us against 22), so a token is
+// takes longer than fp32 (16384 x 256 in 8 groups: 56 us against 21), so a token is
 // routed in fp32 first, with a bound on what fp32 has got wrong; only where two neighbours of the
 // order, or the last open group and the first closed one, lie within it is the token routed
 // again in fp64 (one in some hundreds, on ordinary logits).
 //
 // A token takes 16 lanes (up to 256 experts) or 64, its row in their registers: one read of the
 // logits, no barrier.  The k + 2 rounds of the selection, each a maximum over the lanes by
-// rotations, bound it, not memory: 16384 x 256 (16.8 MB) 22 us, 4096 x 128 without groups 8.  The
-// counts go through LDS and are joined by a second launch (4 us); fewer workgroups than 1024 would
+// rotations, bound it, not memory: 16384 x 256 (16.8 MB) 21 us, 4096 x 128 without groups 9.  The
+// counts go through LDS and are joined by a second launch (3 to 4 us); fewer workgroups than 1024 would
 // shorten that and lengthen the forward (30 us at 512).  The backward writes its row once:
 // 16384 x 256 in 7 us, 2.7 TB/s.
 #include "row_lanes.h"

@@ -193,7 +193,7 @@ inline Plan plan_product(const PlanCost* costs, int shapes, int step, int cus, i
 
 }  // namespace
 
-// linear_tiles.hip: C [M, N] = A B for bf16 matrices A and B whose rows are whole 16-byte chunks
+// gemm_linear.hip: C [M, N] = A B for bf16 matrices A and B whose rows are whole 16-byte chunks
 // (zeros past the end of K in them), at multiples of 16.  A [M, K] of rows lda (a_k) or [K, M]; B [N, K] (b_k) or [K, N].
 struct LinearOut {
   bf16_t* out;

@@ -6,7 +6,7 @@
 // data's type for the backward; y is formed from the fp32 sum.
 //
 // Three ways to a product: up to four rows by k_linear_few, bf16 by matrix-core tiles
-// (linear_tiles.hip), fp32 and what is left by k_linear_any.
+// (gemm_linear.hip), fp32 and what is left by k_linear_any.
 #include <type_traits>
 
 #include "linear.h"
