@@ -1,12 +1,12 @@
 // The matrix product with an epilogue on matrix-core tiles: bf16, rows of whole 16-byte chunks.
 //
-// Workgroups of four waves, several to a CU, so that one's barriers, first loads and epilogue
-// hide behind the others' products (for the largest products eight waves alone).  K steps of 64
-// move global -> LDS by the direct loads into two stages, one barrier a step.  The operands keep their own layouts (an
-// axis of K is read in 16-byte pieces, one of M or N by the transposing LDS reads), so nothing
-// is transposed in memory.  Chunks past the end of K come from a zeroed area.  A product with
-// few tiles is split along K: the shares of a tile, in the accumulators' own order, are added by
-// a second launch in a fixed order, with the epilogue.
+// Workgroups of four waves, several to a CU, so that one's barriers, first loads and epilogue hide
+// behind the others' products (for the largest products eight waves alone).  K steps of 64 move
+// global -> LDS by the direct loads into two stages, one barrier a step.  The operands keep their own
+// layouts (an axis of K is read in 16-byte pieces, one of M or N by the transposing LDS reads), so
+// nothing is transposed in memory.  Chunks past the end of K come from a zeroed area.  A product
+// with few tiles is split along K: the shares of a tile, in the accumulators' own order, are added
+// by a second launch in a fixed order, with the epilogue.
 //
 // The loads (127 to 170 us of 16384 x 1536 x 4096's 210) and the products (140 to 165) each come near
 // the whole time: what is left is their overlap.  4096^3 takes 113 us, 1.22 PFLOP/s (a library's

@@ -16,9 +16,9 @@ namespace moe {
 namespace {
 
 // ---------------- any size, any alignment ----------------
-// Tiles of 64 or 128 square, four waves, K steps of 32 staged through registers, 8 consecutive elements a
-// thread, several steps' loads under way while one is multiplied, one barrier a step.  With few
-// tiles K is split, and the shares, fp32 [share, M, N], are added in order by a second launch with
+// Tiles of 64 or 128 square, four waves, K steps of 32 staged through registers, 8 consecutive
+// elements a thread, several steps' loads under way while one is multiplied, one barrier a step.
+// With few tiles K is split, and the shares, fp32 [share, M, N], are added in order by a second launch with
 // the epilogue.  In fp32 the matrix cores bound it (busy 77 % of the time: 8192 x 1024 x 2048 dx 290
 // us, 118 TFLOP/s with tiles of 128, 98 with tiles of 64); for small products, the loads' latency.
 constexpr int GSTEP = 32;
@@ -108,7 +108,8 @@ struct GeneralLd {
   }
 };
 
-// H: tiles of 64 H, waves of 32 H; DEPTH steps' loads are under way
+// H: tiles of 64 H, waves of 32 H; DEPTH steps' loads are under way (four where the registers of four
+// workgroups on a CU hold them: in fp32 three workgroups with four steps were no faster)
 template <typename T, int H>
 __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<T> g) {
   constexpr int LD = gstage<T>::LD, TILE = 64 * H, DEPTH = H == 1 && sizeof(T) == 2 ? 4 : 2;
