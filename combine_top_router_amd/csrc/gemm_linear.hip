@@ -11,8 +11,8 @@
 // The loads (127 to 170 us of 16384 x 1536 x 4096's 210) and the products (140 to 165) each come near
 // the whole time: what is left is their overlap.  4096^3 takes 113 us, 1.22 PFLOP/s (a library's
 // product of 8192^3: 1.27); 16384 x 1536 x 4096 forward 208 us with y alone, 264 with bias, silu,
-// residual and z (the epilogue's 400 MB, unhidden with one workgroup on a CU), dx 211, dw 187 + 25
-// for the shares.
+// residual and z (the epilogue's 400 MB, unhidden with one workgroup on a CU), dx 211, dw
+// about 230 with the sum of its shares.
 #define MOE_GEMM_FW 256
 #include "gemm_engine.h"
 #include "linear.h"
