@@ -18,8 +18,9 @@
 // Every tensor's pieces of 2048 elements are workgroups of one grid, found by a search in a table
 // that travels with the arguments (no memory to fill ahead of a launch): 24 small tensors take 7 us.
 // Large ones are bound by memory: bf16 parameters with fp32 states and copies (28 bytes an element,
-// 100 M elements) 518 us, 5.4 TB/s; 8-bit states, stochastic (10 bytes, 201 M) 470, 4.3 TB/s, where
-// the random bits and codes, about 60 whole-number instructions an element, run nearly as long.
+// 100 M elements) 517 us, 5.4 TB/s; 8-bit states, stochastic (10 bytes, 201 M) 506, 4.0 TB/s, where
+// the random bits, codes and roots, about 70 instructions an element, run nearly as long (481 with the
+// hardware's root, which is off by 1 ulp at most and so takes another code for some in a million).
 #include "common.h"
 
 namespace moe {
@@ -132,13 +133,6 @@ __device__ __forceinline__ void decode(uint2 c, int X, float (&x)[VEC]) {
 __device__ __forceinline__ float blend(float a, float x, float b, float y) {
 #pragma clang fp contract(off)
   return a * x + b * y;
-}
-
-// the root by the hardware's (1 ulp), of numbers below 2^-96 by that of 2^64 times them
-__device__ __forceinline__ float root(float v) {
-  const bool low = v < 0x1p-96f;
-  const float s = __builtin_amdgcn_sqrtf(low ? v * 0x1p64f : v);
-  return low ? s * 0x1p-32f : s;
 }
 
 // elements i .. i + 7 of a tensor of n; whole: all inside and the address at a multiple of 16
@@ -255,7 +249,7 @@ __global__ __launch_bounds__(AT) void k_adamw(AdamwTable tab, AdamwHyper h) {
     const float gj = g[j] * gs;
     m[j] = blend(h.b1, m[j], h.b1c, gj);
     v[j] = blend(h.b2, v[j], h.b2c, gj * gj);
-    s[j] = root(v[j]);
+    s[j] = sqrtf(v[j]);   // rounded to nearest: with 8 bits its last bits decide a code (the hardware's is off by 1 ulp)
     p[j] = p[j] * decay - rate * m[j] * __builtin_amdgcn_rcpf(fmaf(s[j], unbias, h.eps));
     if constexpr (S8) probe = fmaf(s[j], 0.f, fmaf(m[j], 0.f, probe));
   }
