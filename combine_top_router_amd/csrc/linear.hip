@@ -15,6 +15,73 @@ namespace moe {
 
 namespace {
 
+// ---------------- relu's corner ----------------
+// Where z is within its sum's rounding of 0, that rounding takes the side, and dz is off by all of dy: one
+// in 10^7 elements of fp32's products, which in a matrix of 1003 x 333 leaves 2.7e-3 of a gradient's norm where
+// all other roundings leave 3e-7.  So in fp32 (in bf16 it stays below the type's own steps) such a z is
+// formed again in fp64 before it is kept; y, off by |z| at most, stays.  Which: a rounding is 2^-24 of a partial sum at
+// most.  One over the first k of K is at most |x_1..k| |W_1..k|, and as the sum is near -b, at most
+// |b| + |x_k+1..K| |W_k+1..K| too; the two products together are |x| |W| at most, so the smaller is
+// (|x| |W| + |b|) / 2.  With K such roundings, taken as independent, 3 sqrt(K) of them are five standard deviations.
+// The squares of both norms are added up beside the products.  Ordinary data have one such z in ten thousand
+// or so; with all of it the forward of 1003 x 769 x 333 takes 18.8 us (16.5 without), of 8192 x 1024 x 2048 340 (313), of
+// one row of 2048 x 768 4.6 (4.1).
+struct Corner {
+  const float* a;
+  const float* b;
+  const float* bias;   // or null
+  float* z;
+  int64_t am, ak, bk, bn, N, K;
+};
+
+// whether that z has to be formed again; b: its bias, sq: the product of the squared norms (3 2^-24 / 2 and 1 %
+// for the norms' own rounding)
+__device__ __forceinline__ bool corner_near(const Corner& c, float z, float b, float sq) {
+  const float bound = 0x1.84p-24f * sqrtf((float)c.K + 64.f) * (sqrtf(sq) + fabsf(b));
+  return fabsf(z) < bound && bound < __builtin_inff();
+}
+// A whole wave forms them, one at a time; near: a bit for each of a lane's elements, of which place gives
+// row and column; zero: those whose z came out as 0.  Where these are over a third of all `count` elements, the
+// products themselves are 0 (one-hot rows, pruned weights): their sums are exact and stay.
+template <int U, class F>   // U: products under way
+__device__ __forceinline__ void settle(const Corner& c, uint64_t near, uint64_t zero, int count, F&& place) {
+  uint64_t lanes = __ballot(near != 0);
+  if (lanes == 0) return;
+  int zeros = __popcll(zero);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) zeros += __shfl_xor(zeros, off, 64);
+  if (3 * zeros > count) {
+    near &= ~zero;
+    lanes = __ballot(near != 0);
+  }
+  const int lane = threadIdx.x & 63;
+  for (; lanes != 0; lanes &= lanes - 1) {
+    const int src = __builtin_ctzll(lanes);
+#pragma unroll 1
+    for (uint64_t bits = __shfl((unsigned long long)near, src, 64); bits != 0; bits &= bits - 1) {
+      int m, n;
+      place(__builtin_ctzll(bits), src, m, n);
+      const float *const pa = c.a + m * c.am, *const pb = c.b + n * c.bn;
+      const int K = (int)c.K;
+      double s = 0.0;
+      for (int k = lane; k - lane < K; k += 64 * U) {
+        float u[U], v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {   // past the end the last again, for nothing
+          const int at = min(k + 64 * j, K - 1);
+          u[j] = pa[at * c.ak];
+          v[j] = pb[at * c.bk];
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) s = fma((double)(k + 64 * j < K ? u[j] : 0.f), (double)v[j], s);
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
+      if (lane == src) c.z[m * c.N + n] = (float)(c.bias ? s + (double)c.bias[n] : s);
+    }
+  }
+}
+
 // ---------------- any size, any alignment ----------------
 // Tiles of 64 or 128 square, four waves, K steps of 32 staged through registers, 8 consecutive
 // elements a thread, several steps' loads under way while one is multiplied, one barrier a step.
@@ -38,8 +105,12 @@ struct GeneralArgs {
   int64_t M, N, K;
   int64_t ks;     // of K a share, a multiple of GSTEP
   float* part;    // or null: one share
+  float* squares; // with shares and relu's corner: [share, M + N], the squares of A's rows and of B's columns
   Epilogue<T> e;
 };
+inline __device__ Corner corner_of(const GeneralArgs<float>& g) {
+  return {g.a, g.b, g.e.bias, g.e.z, g.am, g.ak, g.bk, g.bn, g.N, g.K};
+}
 
 // One operand's part of a thread: H times 8 elements along the axis that is contiguous, 64 rows or
 // columns apart
@@ -109,8 +180,8 @@ struct GeneralLd {
 };
 
 // H: tiles of 64 H, waves of 32 H; DEPTH steps' loads are under way (four where the registers of four
-// workgroups on a CU hold them: in fp32 three workgroups with four steps were no faster)
-template <typename T, int H>
+// workgroups on a CU hold them: in fp32 three workgroups with four steps were no faster); CORNER: see settle
+template <typename T, int H, bool CORNER = false>
 __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<T> g) {
   constexpr int LD = gstage<T>::LD, TILE = 64 * H, DEPTH = H == 1 && sizeof(T) == 2 ? 4 : 2;
   __shared__ __attribute__((aligned(16))) T as[2][TILE][LD];   // [m][k]
@@ -128,6 +199,7 @@ __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[i / H][i % H][j] = 0.f;
   T ra[DEPTH][H][8], rb[DEPTH][H][8];
+  float qa = 0.f, qb = 0.f;   // CORNER: squares of a part of a row of each stage
   const int len = (int)(k1 - k0);
 #pragma unroll
   for (int c = 0; c < DEPTH; ++c)
@@ -180,6 +252,15 @@ __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<
                   __builtin_amdgcn_mfma_f32_32x32x2f32(va[i / H][j], vb[i % H][j], acc[i / H][i % H], 0, 0, 0);
         }
       }
+      if constexpr (CORNER) {
+#pragma unroll
+        for (int j = 0; j < 8 * H; j += 4) {
+          const f32x4 u = *reinterpret_cast<const f32x4*>(&as[c & 1][tid % TILE][tid / TILE * 8 * H + j]);
+          const f32x4 v = *reinterpret_cast<const f32x4*>(&bs[c & 1][tid % TILE][tid / TILE * 8 * H + j]);
+          qa += fmaf(u[0], u[0], u[1] * u[1]) + fmaf(u[2], u[2], u[3] * u[3]);
+          qb += fmaf(v[0], v[0], v[1] * v[1]) + fmaf(v[2], v[2], v[3] * v[3]);
+        }
+      }
     }
 #pragma unroll
   for (int i = 0; i < H * H; ++i) {
@@ -194,6 +275,50 @@ __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<
       else g.e.store(m, n, g.N, v);
     }
   }
+  if constexpr (CORNER) {
+    __shared__ float an[256], bn[256];
+    an[tid] = qa;
+    bn[tid] = qb;
+    __syncthreads();
+    if (tid < TILE) {
+#pragma unroll
+      for (int p = 1; p < 4 / H; ++p) {
+        qa += an[tid + p * TILE];
+        qb += bn[tid + p * TILE];
+      }
+      an[tid] = qa;
+      bn[tid] = qb;
+    }
+    if (g.part) {   // rows by the first workgroup along N, columns by the first along M
+      float* const to = g.squares + blockIdx.z * (g.M + g.N);
+      if (tid < TILE && blockIdx.y == 0 && m0 + tid < g.M) to[m0 + tid] = qa;
+      if (tid < TILE && blockIdx.x == 0 && n0 + tid < g.N) to[g.M + n0 + tid] = qb;
+      return;
+    }
+    __syncthreads();
+    const Corner c = corner_of(g);
+    uint64_t near = 0, zero = 0;
+#pragma unroll
+    for (int i = 0; i < H * H; ++i) {
+      const int nl = wn + 32 * (i % H) + (lane & 31);
+      if (n0 + nl >= g.N) continue;
+      const float b = c.bias ? c.bias[n0 + nl] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int ml = wm + 32 * (i / H) + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+        const float z = acc[i / H][i % H][j] + b;
+        if (m0 + ml < g.M && corner_near(c, z, b, an[ml] * bn[nl])) {
+          near |= 1ull << (16 * i + j);
+          if (z == 0.f) zero |= 1ull << (16 * i + j);
+        }
+      }
+    }
+    settle<4>(c, near, zero, 64 * 16 * H * H, [&](int bit, int src, int& m, int& n) {
+      const int i = bit >> 4, j = bit & 15;
+      m = (int)m0 + wm + 32 * (i / H) + 8 * (j >> 2) + 4 * (src >> 5) + (j & 3);
+      n = (int)n0 + wn + 32 * (i % H) + (src & 31);
+    });
+  }
 }
 
 template <typename T>
@@ -206,6 +331,42 @@ __global__ __launch_bounds__(256) void k_linear_any_join(GeneralArgs<T> g, int s
   g.e.store(i / g.N, i % g.N, g.N, s);
 }
 
+// The same with relu's corner; eight shares' numbers are loaded before they are added, in the same order
+__global__ __launch_bounds__(256) void k_linear_corner_join(GeneralArgs<float> g, int splits) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, size = g.M * g.N;
+  const bool in = i < size;
+  const int64_t at = in ? i : size - 1;   // every lane stays
+  const int m = (int)(at / g.N), n = (int)(at - m * g.N);
+  const float *p = g.part + at, *pa = g.squares + m, *pb = g.squares + g.M + n;
+  float s = 0.f, qa = 0.f, qb = 0.f;
+  for (int sp = 0; sp < splits; sp += 8) {
+    float u[8], a[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t k = min(sp + j, splits - 1);
+      u[j] = p[k * size];
+      a[j] = pa[k * (g.M + g.N)];
+      b[j] = pb[k * (g.M + g.N)];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (sp + j < splits) {
+        s += u[j];
+        qa += a[j];
+        qb += b[j];
+      }
+  }
+  if (in) g.e.store(m, n, g.N, s);
+  const Corner c = corner_of(g);
+  const float b = c.bias ? c.bias[n] : 0.f, z = s + b;
+  const bool near = in && corner_near(c, z, b, qa * qb);
+  settle<16>(c, near, near && z == 0.f, 64, [&](int, int src, int& row, int& col) {
+    row = __shfl(m, src, 64);
+    col = __shfl(n, src, 64);
+  });
+}
+
 constexpr PlanCost kAny16[2] = {{128, 128, 2, 1.1, 0.6, 6.0, 5.0, 6.0}, {64, 64, 4, 0.8, 0.26, 3.0, 5.0, 6.0}};
 constexpr PlanCost kAny32[2] = {{128, 128, 2, 2.8, 2.4, 7.0, 5.0, 6.0}, {64, 64, 4, 1.1, 0.66, 3.0, 5.0, 6.0}};
 template <typename T>
@@ -213,23 +374,34 @@ Plan general_plan(int64_t M, int64_t N, int64_t K) {
   return plan_product(sizeof(T) == 2 ? kAny16 : kAny32, 2, GSTEP, gemm_cus(), M, N, K);
 }
 template <typename T>
-size_t general_part_bytes(int64_t M, int64_t N, int64_t K) {
+size_t general_part_bytes(int64_t M, int64_t N, int64_t K, bool corner) {
   const int s = general_plan<T>(M, N, K).splits;
-  return s == 1 ? 0 : (size_t)s * M * N * 4;
+  return s == 1 ? 0 : (size_t)s * (M * N + (corner ? M + N : 0)) * 4;
 }
+// what settle is for
+template <typename T>
+bool has_corner(const Epilogue<T>& e) { return sizeof(T) == 4 && e.act == MOE_ACT_RELU && e.z; }
 
 template <typename T>
 hipError_t general(const char* name, const T* a, const T* b, int64_t am, int64_t ak, int64_t bk, int64_t bn, int64_t M,
                    int64_t N, int64_t K, const Epilogue<T>& e, float* part, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
   const Plan p = general_plan<T>(M, N, K);
-  const GeneralArgs<T> g{a, b, am, ak, bk, bn, M, N, K, p.ks, p.splits > 1 ? part : nullptr, e};
+  const GeneralArgs<T> g{a, b, am, ak, bk, bn, M, N, K, p.ks, p.splits > 1 ? part : nullptr, part + p.splits * M * N, e};
   const int tile = p.shape == 0 ? 128 : 64;
   const dim3 grid((unsigned)ceil_div(M, tile), (unsigned)ceil_div(N, tile), (unsigned)p.splits);
+  const dim3 join((unsigned)ceil_div(M * N, 256));
+  if constexpr (sizeof(T) == 4)
+    if (has_corner(e)) {
+      if (tile == 128) MOE_LAUNCH(name, (k_linear_any<T, 2, true>), grid, dim3(256), 0, st, g);
+      else MOE_LAUNCH(name, (k_linear_any<T, 1, true>), grid, dim3(256), 0, st, g);
+      if (p.splits > 1) MOE_LAUNCH("linear_join", k_linear_corner_join, join, dim3(256), 0, st, g, p.splits);
+      return hipGetLastError();
+    }
   if (tile == 128) MOE_LAUNCH(name, (k_linear_any<T, 2>), grid, dim3(256), 0, st, g);
   else MOE_LAUNCH(name, (k_linear_any<T, 1>), grid, dim3(256), 0, st, g);
   if (p.splits > 1)
-    MOE_LAUNCH("linear_join", k_linear_any_join<T>, dim3((unsigned)ceil_div(M * N, 256)), dim3(256), 0, st, g, p.splits);
+    MOE_LAUNCH("linear_join", k_linear_any_join<T>, join, dim3(256), 0, st, g, p.splits);
   return hipGetLastError();
 }
 
@@ -241,11 +413,12 @@ hipError_t general(const char* name, const T* a, const T* b, int64_t am, int64_t
 // MB) takes 4.9 us, one after another 7.0; 4 x 4096 x 4096 (33.6 MB) 10.1 and 25.5.
 constexpr int FEW = 4, FT = 512, FC = 16;
 
-// U: rows of W under way
-template <typename T, int ROWS, int U = (sizeof(T) == 2 ? 8 : 4) * (ROWS == 1 ? 2 : 1)>
+// U: rows of W under way; CORNER: see settle
+template <typename T, int ROWS, bool CORNER = false, int U = (sizeof(T) == 2 ? 8 : 4) * (ROWS == 1 ? 2 : 1)>
 __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, const T* __restrict__ w, int rows, int K, int N,
                                                    Epilogue<T> e) {
-  __shared__ float red[FT / 64][ROWS][FC];
+  constexpr int SUMS = ROWS + CORNER;   // the last: the squares of W's columns
+  __shared__ float red[FT / 64][SUMS][FC], xred[FT / 64][ROWS];
   // neighbouring column blocks, which share lines of memory, on one XCD
   const int blocks = (N + FC - 1) / FC, xcd = blockIdx.x & 7;
   const int lo = (int)((int64_t)blocks * xcd >> 3), hi = (int)((int64_t)blocks * (xcd + 1) >> 3);
@@ -253,11 +426,13 @@ __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, cons
   if (block >= hi) return;
   const int n0 = block * FC, n = n0 + (threadIdx.x & 1) * 8, kl = threadIdx.x >> 1;
   const int at = min(n, N - 8);   // the last columns: the last 8 there are, of which it keeps its own
-  float acc[ROWS][8];
+  float acc[SUMS][8], xq[ROWS];   // xq: the squares of x's rows
 #pragma unroll
-  for (int t = 0; t < ROWS; ++t)
+  for (int t = 0; t < SUMS; ++t)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[t][j] = 0.f;
+#pragma unroll
+  for (int t = 0; t < ROWS; ++t) xq[t] = 0.f;
   const int64_t step = (int64_t)(FT / 2) * N;
   const T* wp = w + (int64_t)kl * N + at;
   // U rows of W: all loads before the first product; TAIL: past the end the first one again, for nothing
@@ -285,6 +460,13 @@ __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, cons
           const float s = fmaf(elem<T>::load(&xv[u][t]), f[j], acc[t][j]);
           acc[t][j] = in ? s : acc[t][j];
         }
+      if constexpr (CORNER)
+        if (in) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[ROWS][j] = fmaf(f[j], f[j], acc[ROWS][j]);
+#pragma unroll
+          for (int t = 0; t < ROWS; ++t) xq[t] = fmaf(xv[u][t], xv[u][t], xq[t]);
+        }
     }
     wp += U * step;
   };
@@ -297,7 +479,7 @@ __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, cons
   const bool b1 = lane & 2, b2 = lane & 4, b3 = lane & 8;
   const int col = (b1 ? 4 : 0) + (b2 ? 2 : 0) + (b3 ? 1 : 0);
 #pragma unroll
-  for (int t = 0; t < ROWS; ++t) {
+  for (int t = 0; t < SUMS; ++t) {
     float h[4], q[2], s;
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = (b1 ? acc[t][4 + j] : acc[t][j]) + __shfl_xor(b1 ? acc[t][j] : acc[t][4 + j], 2, 64);
@@ -308,20 +490,53 @@ __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, cons
     s += __shfl_xor(s, 32, 64);
     if (lane < 16 && at + col >= n) red[threadIdx.x >> 6][t][at + col - n0] = s;
   }
+  if constexpr (CORNER) {
+#pragma unroll
+    for (int t = 0; t < ROWS; ++t) {
+#pragma unroll
+      for (int off = 2; off < 64; off <<= 1) xq[t] += __shfl_xor(xq[t], off, 64);   // a pair of lanes has the same of x
+      if (lane == 0) xred[threadIdx.x >> 6][t] = xq[t];
+    }
+  }
   __syncthreads();
   const int t = threadIdx.x / FC, m = n0 + (int)threadIdx.x % FC;
-  if (t < rows && t < ROWS && m < N) {
-    float s = 0.f;
+  const bool in = t < rows && t < ROWS && m < N;
+  float s = 0.f;
+  if (in) {
 #pragma unroll
     for (int q = 0; q < FT / 64; ++q) s += red[q][t][threadIdx.x % FC];
     e.store(t, m, N, s);
   }
+  if constexpr (CORNER)
+    if (threadIdx.x < 64) {   // rows and columns of a block: one wave
+      static_assert(FEW * FC <= 64, "one wave");
+      float qa = 0.f, qb = 0.f;
+#pragma unroll
+      for (int q = 0; q < FT / 64; ++q) {
+        qa += xred[q][min(t, ROWS - 1)];
+        qb += red[q][ROWS][threadIdx.x % FC];
+      }
+      const Corner c{x, w, e.bias, e.z, K, 1, N, 1, N, K};
+      const float b = in && e.bias ? e.bias[m] : 0.f, z = s + b;
+      const bool near = in && corner_near(c, z, b, qa * qb);
+      settle<16>(c, near, near && z == 0.f, 64, [&](int, int src, int& row, int& col) {
+        row = src / FC;
+        col = n0 + src % FC;
+      });
+    }
 }
 
 template <typename T>
 void launch_few(const T* x, const T* w, int rows, int K, int N, const Epilogue<T>& e, hipStream_t st) {
   const dim3 grid((unsigned)(ceil_div(ceil_div(N, FC), 8) * 8));
-#define CALL(R) MOE_LAUNCH("linear_fwd", (k_linear_few<T, R>), grid, dim3(FT), 0, st, x, w, rows, K, N, e)
+#define CALL(...) MOE_LAUNCH("linear_fwd", (k_linear_few<T, __VA_ARGS__>), grid, dim3(FT), 0, st, x, w, rows, K, N, e)
+  if constexpr (sizeof(T) == 4)
+    if (has_corner(e)) {
+      if (rows == 1) CALL(1, true);
+      else if (rows == 2) CALL(2, true);
+      else CALL(4, true);
+      return;
+    }
   if (rows == 1) CALL(1);
   else if (rows == 2) CALL(2);
   else CALL(4);
@@ -568,8 +783,8 @@ size_t linear_scratch_bytes(const moe_linear_shape& s) {
   const int64_t of[3][3] = {{s.T, s.N, s.K}, {s.T, s.K, s.N}, {s.K, s.N, s.T}};
   for (const auto& d : of) {
     const size_t a = tiles ? linear_part_bytes(d[0], d[1], d[2]) : 0;
-    const size_t b = s.dtype == MOE_BF16 ? general_part_bytes<bf16_t>(d[0], d[1], d[2])
-                                         : general_part_bytes<float>(d[0], d[1], d[2]);
+    const size_t b = s.dtype == MOE_BF16 ? general_part_bytes<bf16_t>(d[0], d[1], d[2], false)
+                                         : general_part_bytes<float>(d[0], d[1], d[2], s.act == MOE_ACT_RELU);
     part = a > part ? a : part;
     part = b > part ? b : part;
   }

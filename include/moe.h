@@ -420,7 +420,8 @@ int moe_linear_scratch_bytes(const moe_linear_shape* shape, size_t* scratch_byte
 
 /* z = x W + b, y = act(z) + res, with x [T, K], W [K, N], b [N] (NULL: none), res [T, N] (NULL:
  * none).  The sums run in fp32 and y is rounded once.  z [T, N], rounded, is what moe_linear_bwd
- * needs of an activation; NULL: not kept.  y may be res; it may not be x, w or z, nor z x, w or res.  Needs scratch. */
+ * needs of an activation; NULL: not kept.  In fp32 with relu a z that lies within its sum's rounding of
+ * 0 is kept as summed in fp64, so that the gradient goes by its sign.  y may be res; it may not be x, w or z, nor z x, w or res.  Needs scratch. */
 int moe_linear_fwd(const moe_linear_shape* shape, const void* x, const void* w, const void* b, const void* res,
                    void* z, void* y, void* scratch, void* stream);
 
