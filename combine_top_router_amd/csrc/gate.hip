@@ -489,7 +489,10 @@ __global__ __launch_bounds__(GT, 4) void k_gate_fwd(GateArgs a) {
     }
     if (LPR == 16 && k == 16) whole |= at_k;   // no lane for the seventeenth
     if (__ballot((near || at_k) && !whole && live) != 0) {
-      const Exact x = exact_of();
+      // without a bias by the logits, as the keys: their scores may be equal
+      Exact x = exact0;
+      if (!by_logit) x = exact_of();
+      x.scored = !by_logit;
       const int most = at_k && k < LPR ? k + 1 : k;   // the right set
       const bool cand = sub < most && my_id != kPadId;
       const double y = cand ? x(my_id) : 0.0;
