@@ -369,12 +369,13 @@ __global__ __launch_bounds__(GT, 4) void k_gate_fwd(GateArgs a) {
     if constexpr (GROUPS) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       // 2^h lanes to a group, so many groups at a time; low, high: the lowest open score and the
-      // highest closed one
+      // highest closed one; size: the largest sum of the sizes of a score's terms, that are not infinite
       int h = 0;
       while ((a.groups << (h + 1)) <= LPR) ++h;
       const int gl = 1 << h;
       uint64_t mine = 0;
-      double low = 0.0, high = 0.0, top = 0.0;
+      double low = 0.0, high = 0.0;
+      float size = 0.f;
       auto score_groups = [&](auto&& value) {
         for (int g0 = 0; g0 < a.groups; g0 += LPR >> h) {
           const int g = g0 + (sub >> h);
@@ -389,11 +390,13 @@ __global__ __launch_bounds__(GT, 4) void k_gate_fwd(GateArgs a) {
           if (g < a.groups && (sub & (gl - 1)) == 0) {
             const double s = groups2 ? b1 + b2 : b1;
             gscore[group][g] = s == s ? s : -inf;
+            const float z1 = fabsf((float)b1), z2 = groups2 ? fabsf((float)b2) : 0.f;
+            size = fmaxf(size, (z1 < inf ? z1 : 0.f) + (z2 < inf ? z2 : 0.f));
           }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         mine = 0;
-        low = inf, high = -inf, top = 0.0;
+        low = inf, high = -inf;
         for (int g = sub; g < a.groups; g += LPR) {   // open if fewer than topk_groups are better
           const double s = gscore[group][g];
           int rank = 0;
@@ -405,7 +408,6 @@ __global__ __launch_bounds__(GT, 4) void k_gate_fwd(GateArgs a) {
           } else {
             high = fmax(high, s);
           }
-          top = fmax(top, fabs(s));
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
@@ -426,9 +428,10 @@ __global__ __launch_bounds__(GT, 4) void k_gate_fwd(GateArgs a) {
       if (scored && a.topk_groups < a.groups) {   // logits alone have no error
         const float lo = fold<LPR>((float)low, [](float x, float y) { return fminf(x, y); });
         const float hi = fold<LPR>((float)high, [](float x, float y) { return fmaxf(x, y); });
-        const float tp = fold<LPR>((float)top, [](float x, float y) { return fmaxf(x, y); });
-        // two scores of two c each, and the roundings of the scores and sums here
-        const bool unsure = !(lo - hi > 4.f * err + tp * 0x1p-21f);
+        const float sz = fold<LPR>(size, [](float x, float y) { return fmaxf(x, y); });
+        // two scores of two c each: their errors, and the roundings of c = s + b, u of each (a sum may be far
+        // smaller than its terms), of the scores to fp32 and of this difference: 8 u of the terms in all
+        const bool unsure = !(lo - hi > 4.f * err + sz * 0x1p-21f);
         if (__ballot(unsure && live) != 0) {
           const Exact x = exact_of();
           score_groups([&](int g, int e0, int step, double& b1, double& b2) {
