@@ -345,7 +345,7 @@ __global__ __launch_bounds__(GT, 4) void k_gate_fwd(GateArgs a) {
           s = fmaf(p[i][j], inv, a.bias ? a.bias[min(4 * (sub + LPR * i) + j, E - 1)] : 0.f);
           s = no || s != s ? -inf : s;
         }
-        if (by_logit) c[i][j] = no ? -inf : c[i][j];
+        if (by_logit) c[i][j] = no ? -inf : c[i][j] + 0.f;   // -0 as 0: keys tell them apart
         else c[i][j] = s;
         u[j] = scored ? s : c[i][j];
       }
