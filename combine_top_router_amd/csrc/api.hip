@@ -962,9 +962,9 @@ int moe_adamw(const moe_adamw_params* params, const moe_adamw_tensor* tensors, i
   if (!isfinite(s.lr) || !isfinite(s.weight_decay)) return fail(MOE_EINVAL, "lr and weight_decay must be finite");
   if (!(s.beta1 >= 0.0 && s.beta1 < 1.0 && s.beta2 >= 0.0 && s.beta2 < 1.0))
     return fail(MOE_EINVAL, "beta1 = %g and beta2 = %g must lie in [0, 1)", s.beta1, s.beta2);
-  // as the kernels take it: above 0 in fp32, too
-  if (!isfinite(s.eps) || !((float)s.eps > 0.f) || !isfinite((float)s.eps))
-    return fail(MOE_EINVAL, "eps = %g must be finite and > 0", s.eps);
+  // as the kernels take it, in fp32; 1 / eps has to be finite there: 0 / eps is 0
+  if (!((float)s.eps >= 0x1p-126f) || !isfinite((float)s.eps))
+    return fail(MOE_EINVAL, "eps = %g must be finite and at least 2^-126", s.eps);
   if (s.state != MOE_STATE_F32 && s.state != MOE_STATE_8BIT) return fail(MOE_EINVAL, "state = %d", s.state);
   if (s.stochastic != 0 && s.stochastic != 1) return fail(MOE_EINVAL, "stochastic = %d", s.stochastic);
   if (!clock && s.step < 1) return fail(MOE_EINVAL, "step = %lld < 1", (long long)s.step);

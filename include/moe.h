@@ -455,7 +455,7 @@ typedef struct {
 } moe_adamw_tensor;
 
 typedef struct {
-  double lr, beta1, beta2, eps, weight_decay;  /* finite; betas in [0, 1), eps > 0 */
+  double lr, beta1, beta2, eps, weight_decay;  /* finite; betas in [0, 1), eps at least 2^-126 (1.2e-38) */
   int64_t step;        /* the step's number, >= 1 (unused with a clock) */
   uint64_t seed;       /* of the random bits */
   int32_t state;       /* moe_state_kind */
