@@ -681,6 +681,8 @@ __global__ __launch_bounds__(GT) void k_gate_bwd(GateArgs a, const int32_t* __re
   } while (0)
 
 inline int tokens_of(int E) { return GT / (E <= 256 ? 16 : 64); }
+// workgroups of a launch, far below what a launch takes (2^32 threads: beyond, the runtime cuts it off in silence)
+constexpr int64_t kMostGroups = 1 << 22;
 
 GateArgs gate_args(const moe_gate_shape& s, const float* logits) {
   GateArgs a{};
@@ -703,7 +705,8 @@ hipError_t launch_gate_fwd(const moe_gate_shape& s, const float* logits, const f
   GateArgs a = gate_args(s, logits);
   a.bias = bias; a.mask = mask; a.idx = idx; a.w = w;
   a.part_c = counts ? part_c : nullptr;
-  const unsigned W = counts ? (unsigned)gate_parts(s.T, s.E) : (unsigned)ceil_div(s.T, tokens_of(s.E));
+  const int64_t all = ceil_div(s.T, tokens_of(s.E));
+  const unsigned W = counts ? (unsigned)gate_parts(s.T, s.E) : (unsigned)(all < kMostGroups ? all : kMostGroups);
   if (W > 0) {
 #define CALL(LPR, NV)                                                                              \
   if (s.groups > 1) MOE_LAUNCH("gate_fwd", (k_gate_fwd<LPR, NV, true>), dim3(W), dim3(GT), 0, st, a); \
@@ -719,11 +722,17 @@ hipError_t launch_gate_fwd(const moe_gate_shape& s, const float* logits, const f
 
 hipError_t launch_gate_bwd(const moe_gate_shape& s, const float* logits, const int32_t* idx, const float* dw,
                            float* d_logits, hipStream_t st) {
-  const GateArgs a = gate_args(s, logits);
-  const dim3 grid((unsigned)ceil_div(s.T, tokens_of(s.E)));
-#define CALL(LPR, NV) MOE_LAUNCH("gate_bwd", (k_gate_bwd<LPR, NV>), grid, dim3(GT), 0, st, a, idx, dw, d_logits)
-  GATE_DISPATCH(s.E, CALL);
+  GateArgs a = gate_args(s, logits);
+  const int64_t most = kMostGroups * tokens_of(s.E);   // tokens of a launch
+  for (int64_t t = 0; t < s.T; t += most) {
+    a.T = (int)(s.T - t < most ? s.T - t : most);
+    a.logits = logits + t * s.E;
+    const dim3 grid((unsigned)ceil_div(a.T, tokens_of(s.E)));
+#define CALL(LPR, NV) \
+  MOE_LAUNCH("gate_bwd", (k_gate_bwd<LPR, NV>), grid, dim3(GT), 0, st, a, idx + t * s.k, dw + t * s.k, d_logits + t * s.E)
+    GATE_DISPATCH(s.E, CALL);
 #undef CALL
+  }
   return hipGetLastError();
 }
 
