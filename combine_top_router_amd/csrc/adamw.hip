@@ -31,6 +31,8 @@ constexpr int AT = 256;       // threads of a workgroup
 constexpr int VEC = 8;        // elements a thread takes at a time
 constexpr int CHUNK = AT * VEC;
 constexpr int kTensors = 40;  // tensors of a launch: their table travels with its arguments
+// workgroups of a launch: 2^31 threads (from 2^32 on the runtime cuts a launch off in silence)
+constexpr int64_t kMostGroups = (1LL << 31) / AT;
 
 struct AdamwTable {
   moe_adamw_tensor t[kTensors];
@@ -334,11 +336,12 @@ hipError_t launch_adamw(const moe_adamw_params& s, const moe_adamw_tensor* tenso
   }
   h.stochastic = s.stochastic;
   h.lr = lr; h.grad_scale = grad_scale; h.clock = (const AdamwClock*)clock;
+  const bool eight = s.state == MOE_STATE_8BIT;
   AdamwTable tab{};
   int64_t wgs = 0;
   auto go = [&]() -> hipError_t {
     if (tab.n == 0) return hipSuccess;
-    if (s.state == MOE_STATE_8BIT)
+    if (eight)
       MOE_LAUNCH("adamw_8bit", k_adamw<true>, dim3((unsigned)wgs), dim3(AT), 0, st, tab, h);
     else
       MOE_LAUNCH("adamw", k_adamw<false>, dim3((unsigned)wgs), dim3(AT), 0, st, tab, h);
@@ -347,17 +350,34 @@ hipError_t launch_adamw(const moe_adamw_params& s, const moe_adamw_tensor* tenso
     return hipGetLastError();
   };
   for (int i = 0; i < count; ++i) {
-    const moe_adamw_tensor& t = tensors[i];
-    if (!t.g || t.n == 0) continue;
-    const int64_t need = ceil_div(t.n, CHUNK);
-    if (tab.n == kTensors || wgs + need > (1 << 30)) {
-      const hipError_t e = go();
-      if (e != hipSuccess) return e;
+    moe_adamw_tensor t = tensors[i];   // what is left of it
+    if (!t.g) continue;
+    while (t.n > 0) {
+      if (tab.n == kTensors || wgs == kMostGroups) {
+        const hipError_t e = go();
+        if (e != hipSuccess) return e;
+      }
+      const int64_t need = ceil_div(t.n, CHUNK), take = need < kMostGroups - wgs ? need : kMostGroups - wgs;
+      const int64_t n = take < need ? take * CHUNK : t.n;
+      tab.t[tab.n] = t;
+      tab.t[tab.n].n = n;
+      tab.first[tab.n] = (uint32_t)wgs;
+      ++tab.n;
+      wgs += take;
+      t.n -= n;
+      if (t.n == 0) break;
+      // whole chunks are whole blocks of 32: the rest is a tensor of its own
+      t.p = (char*)t.p + n * (t.p_dtype == MOE_BF16 ? 2 : 4);
+      t.g = (const char*)t.g + n * (t.g_dtype == MOE_BF16 ? 2 : 4);
+      if (t.master) t.master += n;
+      t.m = (char*)t.m + n * (eight ? 1 : 4);
+      t.v = (char*)t.v + n * (eight ? 1 : 4);
+      if (eight) {
+        t.m_scale += n / 32;
+        t.v_scale += n / 32;
+      }
+      t.at += n;
     }
-    tab.t[tab.n] = t;
-    tab.first[tab.n] = (uint32_t)wgs;
-    ++tab.n;
-    wgs += need;
   }
   return go();
 }
