@@ -30,7 +30,13 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
+thread_local bool g_too_many = false;   // launch_fits has refused one
+
 int hip_status(hipError_t e, const char* where) {
+  if (g_too_many) {
+    g_too_many = false;
+    return fail(MOE_EUNSUPPORTED, "%s: more than a launch takes (2^32 threads along an axis)", where);
+  }
   if (e == hipSuccess) return MOE_OK;
   return fail(MOE_EHIP, "%s: %s", where, hipGetErrorString(e));
 }
@@ -269,6 +275,11 @@ thread_local Timing g_timing;
 }  // namespace
 
 namespace moe {
+bool launch_fits(const dim3& grid, const dim3& block) {
+  // once one is refused, neither are those behind it in the call, which would read what it has not written
+  if (((uint64_t)grid.x * block.x | (uint64_t)grid.y * block.y | (uint64_t)grid.z * block.z) >> 32 != 0) g_too_many = true;
+  return !g_too_many;
+}
 bool ktimer_pair(const char* name, hipStream_t st, hipEvent_t* start, hipEvent_t* stop) {
   Timing& T = g_timing;
   if (!T.on || T.used + 2 > (int)T.pool.size()) return false;

@@ -100,13 +100,18 @@ hipError_t static_hist_scratch(int32_t** out);
 // HIP events handed to hipExtLaunchKernel, which stamps them with the dispatch's own
 // start and end; with timing off (and always under graph capture) the plain launch.
 bool ktimer_pair(const char* name, hipStream_t st, hipEvent_t* start, hipEvent_t* stop);
+// 2^32 threads or more along an axis, which the runtime would cut off without an error, are not launched: the
+// call that hip_status ends returns MOE_EUNSUPPORTED.
+bool launch_fits(const dim3& grid, const dim3& block);
 #define MOE_LAUNCH(name, kernel, grid, block, shmem, st, ...)                               \
   do {                                                                                      \
+    const dim3 moe_grid_ = grid, moe_block_ = block;                                        \
+    if (!::moe::launch_fits(moe_grid_, moe_block_)) break;                                  \
     hipEvent_t moe_e0_, moe_e1_;                                                            \
     if (::moe::ktimer_pair(name, st, &moe_e0_, &moe_e1_))                                   \
-      hipExtLaunchKernelGGL(kernel, grid, block, shmem, st, moe_e0_, moe_e1_, 0, __VA_ARGS__); \
+      hipExtLaunchKernelGGL(kernel, moe_grid_, moe_block_, shmem, st, moe_e0_, moe_e1_, 0, __VA_ARGS__); \
     else                                                                                    \
-      hipLaunchKernelGGL(kernel, grid, block, shmem, st, __VA_ARGS__);                      \
+      hipLaunchKernelGGL(kernel, moe_grid_, moe_block_, shmem, st, __VA_ARGS__);            \
   } while (0)
 
 // ---- launch wrappers (defined in the .hip files) ----

@@ -58,7 +58,8 @@ typedef enum {
   MOE_EINVAL = -1,       /* a size, range or enum value is invalid, or a required pointer is NULL */
   MOE_EUNSUPPORTED = -2, /* a valid but unsupported combination: H or I not a multiple of 64 in
                             bf16 (H of 4 in fp32), MXFP8 with fp32 data or H, I not multiples of
-                            128, an MXFP8 padded row space past 2^31 - 1 rows */
+                            128, an MXFP8 padded row space past 2^31 - 1 rows, a launch of 2^32
+                            threads along an axis */
   MOE_EWORKSPACE = -3,   /* a required workspace pointer (saved / scratch) is NULL */
   MOE_EHIP = -4          /* the HIP runtime reported an error at launch */
 } moe_status;
