@@ -423,8 +423,10 @@ class AdamW(_OnDevice):
             if self._eight:
                 end = at + -(-n // 32) * 32
                 x = x[at:end].view(torch.float8_e4m3fn).float().view(-1, 32)
-                e = scale[at // 32:end // 32].to(torch.int32)[:, None] - 127
-                x = torch.ldexp(x, e).view(-1)[:n]
+                # 2^(scale - 127) from its bits (a power function is not exact on the GPU), as the kernel has it
+                e = scale[at // 32:end // 32].to(torch.int32).clamp(max=254)
+                e = torch.where(e > 0, e << 23, 0x400000).to(torch.int32).view(torch.float32)
+                x = (x * e[:, None]).view(-1)[:n]
                 x = torch.square(x) if scale is self.v_scale else x
             else:
                 x = x[at:at + n].clone()

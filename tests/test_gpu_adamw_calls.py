@@ -1,0 +1,25 @@
+"""AdamW called in ways of a user's program: states from elsewhere, a clock read beside other streams, captured
+steps on a given stream."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _op(p, state="8bit", **kw):
+    from combine_top_router_amd import AdamW, lib as L
+    return AdamW([p], state=L.MOE_STATE_8BIT if state == "8bit" else L.MOE_STATE_F32, **kw)
+
+
+def test_moments_are_what_the_codes_stand_for():
+    """moments() to the bit over fp32's exponents, against fp64 on the CPU (codes of 4 bits, squares of 8: exact)."""
+    n = 32 * 120
+    g = (torch.randn(n, generator=torch.Generator().manual_seed(2)).view(-1, 32) * torch.exp2(torch.arange(-60, 60.0))[:, None]).view(-1)
+    op = _op(torch.zeros(n, device="cuda"))
+    op.step([g.cuda()], 0.0)
+    for x, codes, scale, square in zip(op.moments(0), (op.m, op.v), (op.m_scale, op.v_scale), (False, True)):
+        want = codes.cpu().view(torch.float8_e4m3fn).double().view(-1, 32).numpy()
+        want = np.ldexp(want, scale.cpu().numpy().astype(np.int64)[:, None] - 127).reshape(-1)
+        want = want * want if square else want
+        assert np.array_equal(x.double().cpu().numpy(), want.astype(np.float32).astype(np.float64))
