@@ -72,8 +72,10 @@ __device__ __forceinline__ uint32_t e4m3_stochastic(float y, uint32_t room) {   
   return ((y < 0x1p-6f ? sub : norm) + room) >> 20;
 }
 
-// 2^X, X in -127 .. 127
-__device__ __forceinline__ float power(int X) { return __uint_as_float(X > -127 ? (uint32_t)(X + 127) << 23 : 0x400000u); }
+// 2^X, X in -127 .. 127; 128 (a scale of 255, that no code written here has) as 127: its zeros stay zeros
+__device__ __forceinline__ float power(int X) {
+  return __uint_as_float(X > -127 ? (uint32_t)(min(X, 127) + 127) << 23 : 0x400000u);
+}
 
 // The 8 values of a thread, 4 threads to a block of 32, as codes and the block's scale.
 // What is not finite becomes NaN and does not move the scale; FINITE: nothing is.

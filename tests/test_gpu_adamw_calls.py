@@ -12,6 +12,22 @@ def _op(p, state="8bit", **kw):
     return AdamW([p], state=L.MOE_STATE_8BIT if state == "8bit" else L.MOE_STATE_F32, **kw)
 
 
+@pytest.mark.parametrize("scale", [0, 1, 127, 254, 255])
+def test_zeroed_codes_with_any_scale(scale):
+    """Zeroed codes are zero moments, with any scale."""
+    g = torch.randn(1000, generator=torch.Generator().manual_seed(1)).cuda()
+    a, b = (_op(torch.ones(1000, device="cuda")) for _ in range(2))
+    for s in (b.m_scale, b.v_scale):
+        s.fill_(scale)
+    for x in b.moments(0):
+        assert not x.any() and torch.isfinite(x).all()
+    for _ in range(2):
+        a.step([g], 1e-2)
+        b.step([g], 1e-2)
+    for x, y in ((a.params[0], b.params[0]), (a.m, b.m), (a.v, b.v), (a.m_scale, b.m_scale), (a.v_scale, b.v_scale)):
+        assert torch.equal(x, y)
+
+
 def test_moments_are_what_the_codes_stand_for():
     """moments() to the bit over fp32's exponents, against fp64 on the CPU (codes of 4 bits, squares of 8: exact)."""
     n = 32 * 120
