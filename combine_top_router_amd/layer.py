@@ -354,7 +354,7 @@ class AdamW(_OnDevice):
     ``stochastic`` rounds 8-bit moments, and bf16 parameters without a copy, stochastically, by
     random bits from ``seed``, the step and the element's place.  ``t`` is the number of steps taken.  With
     ``capturable`` it is held on the device and counted there, so that a captured step goes on
-    at every replay; reading it then waits for the device."""
+    at every replay; reading and setting it then wait for the device."""
 
     def __init__(self, params, state=L.MOE_STATE_F32, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, master=False,
                  stochastic=False, seed=0, capturable=False):
@@ -406,14 +406,24 @@ class AdamW(_OnDevice):
 
     @property
     def t(self):
-        return self._t if self._clock is None else int(self._clock[0])
+        if self._clock is None:
+            return self._t
+        self._finish()
+        return int(self._clock[0])
 
     @t.setter
     def t(self, value):
         if self._clock is None:
             self._t = int(value)
         else:
+            self._finish()
             self._clock[0] = int(value)
+            self._finish()
+
+    def _finish(self):
+        """The clock is counted on the steps' streams, which may be others than the current one."""
+        if self.device.type == "cuda":
+            torch.cuda.synchronize(self.device)
 
     def moments(self, i):
         """(m, v) of tensor i as fp32 copies of its shape."""

@@ -39,3 +39,34 @@ def test_moments_are_what_the_codes_stand_for():
         want = np.ldexp(want, scale.cpu().numpy().astype(np.int64)[:, None] - 127).reshape(-1)
         want = want * want if square else want
         assert np.array_equal(x.double().cpu().numpy(), want.astype(np.float32).astype(np.float64))
+
+
+def test_steps_taken_on_another_stream_are_counted():
+    """`t` read while the step's stream is still at work."""
+    op, side = _op(torch.ones(64, device="cuda"), capturable=True), torch.cuda.Stream()
+    g = torch.ones(64, device="cuda")
+    rate = torch.ones(1, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            big = (big @ big) * 1e-4
+    op.step([g], rate, stream=side)
+    assert op.t == 1
+    side.synchronize()
+
+
+def test_clock_set_beside_another_stream():
+    """`t` set while the step's stream is still at work: the step before it counts from the old number, the next
+    from the new one."""
+    op, side = _op(torch.ones(64, device="cuda"), capturable=True), torch.cuda.Stream()
+    g, rate = torch.ones(64, device="cuda"), torch.ones(1, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            big = (big @ big) * 1e-4
+    op.step([g], rate, stream=side)
+    op.t = 10
+    op.step([g], rate, stream=side)
+    assert op.t == 11
