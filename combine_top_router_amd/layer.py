@@ -72,6 +72,13 @@ class _OnDevice:
             s.wait_event(self._birth)
         self._ordered.add(handle)
 
+    def _capturing(self, stream):
+        """Whether a call on `stream` (None: the current one of the operator's device) is captured."""
+        if stream is None and _current_device() == self._index:
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(torch.cuda.current_stream(self._index) if stream is None else stream):
+            return torch.cuda.is_current_stream_capturing()
+
     def _check(self, t, shape, dtype, name):
         if t.dtype != dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, got "
@@ -447,7 +454,7 @@ class AdamW(_OnDevice):
         """One step with a gradient for each parameter (bf16 or fp32; None: that one is left
         alone).  lr: a number, or a device fp32 tensor [1], such as a captured step reads anew at
         every replay; grad_scale: a device fp32 tensor [1] that the gradients are multiplied by."""
-        if self._clock is None and self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        if self._clock is None and self.device.type == "cuda" and self._capturing(stream):
             raise RuntimeError("a captured step needs capturable=True: its number would be the same at every replay")
         if len(grads) != len(self.params):
             raise ValueError(f"grads: expected {len(self.params)}, got {len(grads)}")

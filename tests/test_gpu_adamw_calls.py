@@ -70,3 +70,27 @@ def test_clock_set_beside_another_stream():
     op.t = 10
     op.step([g], rate, stream=side)
     assert op.t == 11
+
+
+def test_captured_on_a_given_stream_needs_the_clock():
+    """The step's own stream decides, not the current one."""
+    op = _op(torch.ones(64, device="cuda"))
+    g = torch.ones(64, device="cuda")
+    with_clock = _op(torch.ones(64, device="cuda"), capturable=True)
+    rate = torch.full((1,), 1e-2, device="cuda")
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = torch.cuda.current_stream()
+        with torch.cuda.stream(other):
+            with pytest.raises(RuntimeError, match="capturable"):
+                op.step([g], 1e-2, stream=captured)
+            with_clock.step([g], rate, stream=captured)
+    assert op.t == 0
+    for n in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        op.step([g], 1e-2)
+        assert op.t == n + 1 == with_clock.t
+        assert torch.equal(op.params[0], with_clock.params[0])
