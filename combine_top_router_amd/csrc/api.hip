@@ -942,6 +942,7 @@ int moe_linear_fwd(const moe_linear_shape* shape, const void* x, const void* w, 
   REQUIRE_WS(scratch);
   if (y == x || y == w || y == z || (z && (z == x || z == w || z == res)))
     return fail(MOE_EINVAL, "%s: y may not be x, w or z, and z not x, w or res", __func__);
+  if (b && (b == y || b == z)) return fail(MOE_EINVAL, "%s: b may be neither y nor z", __func__);
   return hip_status(launch_linear_fwd(*shape, x, w, b, res, z, y, scratch, (hipStream_t)stream), __func__);
 }
 
@@ -961,6 +962,8 @@ int moe_linear_bwd(const moe_linear_shape* shape, const void* dy, const void* x,
       return fail(MOE_EINVAL, "%s: dx may be none of dy, x, w and z", __func__);
     if (dw == dy || dw == x || dw == w || dw == z || dw == dx)
       return fail(MOE_EINVAL, "%s: dw may be none of dy, x, w, z and dx", __func__);
+    if (db && (db == dy || db == x || db == w || db == z || db == dx_in || db == dx || db == dw))
+      return fail(MOE_EINVAL, "%s: db may be none of the other matrices", __func__);
   }
   return hip_status(launch_linear_bwd(*shape, dy, x, w, z, dx_in, dx, dw, db, scratch, (hipStream_t)stream), __func__);
 }

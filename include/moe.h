@@ -422,7 +422,8 @@ int moe_linear_scratch_bytes(const moe_linear_shape* shape, size_t* scratch_byte
 /* z = x W + b, y = act(z) + res, with x [T, K], W [K, N], b [N] (NULL: none), res [T, N] (NULL:
  * none).  The sums run in fp32 and y is rounded once.  z [T, N], rounded, is what moe_linear_bwd
  * needs of an activation; NULL: not kept.  In fp32 with relu a z that lies within its sum's rounding of
- * 0 is kept as summed in fp64, so that the gradient goes by its sign.  y may be res; it may not be x, w or z, nor z x, w or res.  Needs scratch. */
+ * 0 is kept as summed in fp64, so that the gradient goes by its sign.  y may be res; it may not be x, w, b
+ * or z, nor z x, w, b or res.  Needs scratch. */
 int moe_linear_fwd(const moe_linear_shape* shape, const void* x, const void* w, const void* b, const void* res,
                    void* z, void* y, void* scratch, void* stream);
 
@@ -430,7 +431,8 @@ int moe_linear_fwd(const moe_linear_shape* shape, const void* x, const void* w, 
  *   dz = dy act'(z),  dx = dx_in + dz W^T,  dw = x^T dz,  db = sum_t dz
  * (relu'(0) = 0; the gradient of res is dy).  dz enters the products in the data's type and db
  * in fp32.  dx may be NULL (not wanted: x is an input), dx_in NULL (taken as 0) or dx; db may be
- * NULL.  dx may be none of dy, x, w, z, and dw none of these and dx.  T = 0 gives dw = db = 0.
+ * NULL.  dx may be none of dy, x, w, z, dw none of these and dx, and db, which is written first, none
+ * of all the others.  T = 0 gives dw = db = 0.
  * Results do not change from run to run.  Needs scratch. */
 int moe_linear_bwd(const moe_linear_shape* shape, const void* dy, const void* x, const void* w, const void* z,
                    const void* dx_in, void* dx, void* dw, void* db, void* scratch, void* stream);
