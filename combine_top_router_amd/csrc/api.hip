@@ -927,7 +927,15 @@ int moe_linear_scratch_bytes(const moe_linear_shape* shape, size_t* scratch_byte
   REQUIRE(scratch_bytes);
   int rc = check_linear(shape);
   if (rc) return rc;
-  *scratch_bytes = align_up(linear_scratch_bytes(*shape) + 1);
+  *scratch_bytes = align_up(linear_scratch_bytes(*shape, false) + 1);
+  return MOE_OK;
+}
+
+int moe_linear_fwd_scratch_bytes(const moe_linear_shape* shape, size_t* scratch_bytes) {
+  REQUIRE(scratch_bytes);
+  int rc = check_linear(shape);
+  if (rc) return rc;
+  *scratch_bytes = align_up(linear_scratch_bytes(*shape, true) + 1);
   return MOE_OK;
 }
 

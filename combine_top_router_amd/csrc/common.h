@@ -174,7 +174,7 @@ static_assert(sizeof(AdamwClock) <= MOE_ADAMW_CLOCK_BYTES, "the clock");
 hipError_t launch_adamw(const moe_adamw_params& s, const moe_adamw_tensor* tensors, int count, const float* lr,
                         const float* grad_scale, void* clock, hipStream_t st);
 // matrix product with an epilogue (linear.hip)
-size_t linear_scratch_bytes(const moe_linear_shape& s);
+size_t linear_scratch_bytes(const moe_linear_shape& s, bool forward);
 hipError_t launch_linear_fwd(const moe_linear_shape& s, const void* x, const void* w, const void* b, const void* res,
                              void* z, void* y, void* scratch, hipStream_t st);
 hipError_t launch_linear_bwd(const moe_linear_shape& s, const void* dy, const void* x, const void* w, const void* z,

@@ -679,16 +679,17 @@ struct LinearLayout {
   // scratch: dz, x and W laid out anew, the shares of db, those of a product split along its sum
   size_t off_x, off_w, off_db, off_part;
 };
-// (the shares come last: their room takes the plans of all three products, which a call need not know)
-LinearLayout linear_layout(const moe_linear_shape& s) {
+// (the shares come last: their room takes the plans of all three products, which a call need not know.)  The
+// forward's own has no dz and no db, and so lies within the backward's.
+LinearLayout linear_layout(const moe_linear_shape& s, bool forward) {
   const size_t es = s.dtype == MOE_BF16 ? 2 : 4;
   LinearLayout L{};
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const bool pad = padded(s);
-  L.off_x = s.act == MOE_ACT_NONE && !(pad && s.N % 8 != 0) ? 0 : up((size_t)s.T * (pad ? up8(s.N) : s.N) * es);
+  L.off_x = forward || (s.act == MOE_ACT_NONE && !(pad && s.N % 8 != 0)) ? 0 : up((size_t)s.T * (pad ? up8(s.N) : s.N) * es);
   L.off_w = L.off_x + (pad && s.K % 8 != 0 ? up((size_t)s.T * up8(s.K) * es) : 0);
   L.off_db = L.off_w + (pad && s.N % 8 != 0 ? up((size_t)s.K * up8(s.N) * es) : 0);
-  L.off_part = L.off_db + up((size_t)ceil_div(s.T, dz_slab(s)) * s.N * 4);
+  L.off_part = L.off_db + (forward ? 0 : up((size_t)ceil_div(s.T, dz_slab(s)) * s.N * 4));
   return L;
 }
 
@@ -717,7 +718,7 @@ hipError_t fwd(const moe_linear_shape& s, const T* x, const T* w, const T* b, co
     launch_few<T>(x, w, s.T, s.K, s.N, e, st);
     return hipGetLastError();
   }
-  const LinearLayout L = linear_layout(s);
+  const LinearLayout L = linear_layout(s, true);
   float* const part = (float*)((char*)scratch + L.off_part);
   if constexpr (sizeof(T) == 2) {
     const bool wide = s.N % 8 == 0 && at16(b) && at16(res) && at16(z) && at16(y);
@@ -731,7 +732,7 @@ hipError_t fwd(const moe_linear_shape& s, const T* x, const T* w, const T* b, co
 template <typename T>
 hipError_t bwd(const moe_linear_shape& s, const T* dy, const T* x, const T* w, const T* z, const T* dx_in, T* dx,
                T* dw, T* db, void* scratch, hipStream_t st) {
-  const LinearLayout L = linear_layout(s);
+  const LinearLayout L = linear_layout(s, false);
   bool tiles = tiled<T>(s) && at16(dy) && at16(x) && at16(w) && at16(dx_in) && at16(dx) && at16(dw);
   if constexpr (sizeof(T) == 2)
     if (padded(s) && (s.N % 8 != 0 || at16(dy))) tiles = pad_operands(s, L, scratch, x, w, st);
@@ -777,18 +778,20 @@ hipError_t bwd(const moe_linear_shape& s, const T* dy, const T* x, const T* w, c
 
 }  // namespace
 
-size_t linear_scratch_bytes(const moe_linear_shape& s) {
-  size_t part = 0;   // of the largest of the three products, on the tiles or on the general kernel
+size_t linear_scratch_bytes(const moe_linear_shape& s, bool forward) {
+  if (forward && s.T <= FEW && s.N >= 8) return 0;
+  size_t part = 0;   // of the largest of the products, on the tiles or on the general kernel
   const bool tiles = padded(s) || (s.dtype == MOE_BF16 && tiled<bf16_t>(s));
   const int64_t of[3][3] = {{s.T, s.N, s.K}, {s.T, s.K, s.N}, {s.K, s.N, s.T}};
   for (const auto& d : of) {
+    if (forward && d != of[0]) break;
     const size_t a = tiles ? linear_part_bytes(d[0], d[1], d[2]) : 0;
     const size_t b = s.dtype == MOE_BF16 ? general_part_bytes<bf16_t>(d[0], d[1], d[2], false)
                                          : general_part_bytes<float>(d[0], d[1], d[2], s.act == MOE_ACT_RELU);
     part = a > part ? a : part;
     part = b > part ? b : part;
   }
-  return linear_layout(s).off_part + part;
+  return linear_layout(s, forward).off_part + part;
 }
 
 hipError_t launch_linear_fwd(const moe_linear_shape& s, const void* x, const void* w, const void* b, const void* res,

@@ -307,7 +307,7 @@ class Linear(_OnDevice):
 
     def __init__(self, T, K, N, act=L.MOE_ACT_NONE, dtype=L.MOE_BF16, train=True, device="cuda"):
         self.shape = L.MoeLinearShape(T, K, N, dtype, act)
-        scratch_b = L.moe_linear_scratch_bytes(self.shape)
+        scratch_b = L.moe_linear_scratch_bytes(self.shape) if train else L.moe_linear_fwd_scratch_bytes(self.shape)
         self._place(device)
         dev = self.device
         dt = self.dtype = _DT[dtype]

@@ -22,7 +22,7 @@ __all__ = [
     "moe_norm_scratch_bytes", "moe_norm_fwd", "moe_norm_bwd",
     "moe_orth_scratch_bytes", "moe_orthogonalize",
     "moe_gate_scratch_bytes", "moe_gate_fwd", "moe_gate_bwd", "moe_gate_update_bias",
-    "moe_linear_scratch_bytes", "moe_linear_fwd", "moe_linear_bwd", "moe_adamw",
+    "moe_linear_scratch_bytes", "moe_linear_fwd_scratch_bytes", "moe_linear_fwd", "moe_linear_bwd", "moe_adamw",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4
@@ -122,6 +122,7 @@ _SIG = {
     "moe_gate_bwd": (ctypes.c_int, [_GS] + [_P] * 5),
     "moe_gate_update_bias": (ctypes.c_int, [_GS, _P, _P, _F, _P, _P]),
     "moe_linear_scratch_bytes": (ctypes.c_int, [_LS, _SZ]),
+    "moe_linear_fwd_scratch_bytes": (ctypes.c_int, [_LS, _SZ]),
     "moe_linear_fwd": (ctypes.c_int, [_LS] + [_P] * 8),
     "moe_linear_bwd": (ctypes.c_int, [_LS] + [_P] * 10),
     "moe_adamw": (ctypes.c_int, [ctypes.POINTER(MoeAdamwParams), ctypes.POINTER(MoeAdamwTensor), ctypes.c_int32]
@@ -286,6 +287,10 @@ def moe_gate_update_bias(shape, counts, bias, rate, bias_out, stream=0):
 
 def moe_linear_scratch_bytes(shape: MoeLinearShape) -> int:
     return _scratch_bytes("moe_linear_scratch_bytes", shape)
+
+
+def moe_linear_fwd_scratch_bytes(shape: MoeLinearShape) -> int:
+    return _scratch_bytes("moe_linear_fwd_scratch_bytes", shape)
 
 
 def moe_linear_fwd(shape, x, w, b, res, z, y, scratch, stream=0):

@@ -419,6 +419,9 @@ typedef struct {
 /* Bytes of scratch of moe_linear_fwd and moe_linear_bwd.  Never 0. */
 int moe_linear_scratch_bytes(const moe_linear_shape* shape, size_t* scratch_bytes);
 
+/* Bytes of scratch that suffice for moe_linear_fwd alone, at most as many.  Never 0. */
+int moe_linear_fwd_scratch_bytes(const moe_linear_shape* shape, size_t* scratch_bytes);
+
 /* z = x W + b, y = act(z) + res, with x [T, K], W [K, N], b [N] (NULL: none), res [T, N] (NULL:
  * none).  The sums run in fp32 and y is rounded once.  z [T, N], rounded, is what moe_linear_bwd
  * needs of an activation; NULL: not kept.  In fp32 with relu a z that lies within its sum's rounding of
