@@ -247,7 +247,7 @@ __global__ __launch_bounds__(AT) void k_adamw(AdamwTable tab, AdamwHyper h) {
     load8(T.v, MOE_F32, i, n, full, v);
   }
   float s[VEC];
-  float probe = 0.f;   // stays 0 where every root and parameter is finite, and with them m
+  float probe = 0.f;   // 8 bits: stays 0 where every root and every m is finite, which encode's FINITE form asks for
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
     const float gj = g[j] * gs;
