@@ -25,13 +25,14 @@ namespace {
 // (|x| |W| + |b|) / 2.  With K such roundings, taken as independent, 3 sqrt(K) of them are five standard deviations.
 // The squares of both norms are added up beside the products.  Ordinary data have one such z in ten thousand
 // or so; with all of it the forward of 1003 x 769 x 333 takes 18.8 us (16.5 without), of 8192 x 1024 x 2048 340 (313), of
-// one row of 2048 x 768 4.6 (4.1).
+// one row of 2048 x 768 4.6 (4.1).  Where sums cancel in bulk (rows far off 0, one-hot rows and pruned weights),
+// whole blocks are formed again by the matrix cores in fp64 (8192 x 1024 x 2048 of nothing else: 1.4 ms).
 struct Corner {
   const float* a;
   const float* b;
   const float* bias;   // or null
   float* z;
-  int64_t am, ak, bk, bn, N, K;
+  int64_t am, ak, bk, bn, M, N, K;
 };
 
 // whether that z has to be formed again; b: its bias, sq: the product of the squared norms (3 2^-24 / 2 and 1 %
@@ -40,44 +41,83 @@ __device__ __forceinline__ bool corner_near(const Corner& c, float z, float b, f
   const float bound = 0x1.84p-24f * sqrtf((float)c.K + 64.f) * (sqrtf(sq) + fabsf(b));
   return fabsf(z) < bound && bound < __builtin_inff();
 }
-// A whole wave forms them, one at a time; near: a bit for each of a lane's elements, of which place gives
-// row and column; zero: those whose z came out as 0.  Where these are over a third of all `count` elements, the
-// products themselves are 0 (one-hot rows, pruned weights): their sums are exact and stay.
-template <int U, class F>   // U: products under way
-__device__ __forceinline__ void settle(const Corner& c, uint64_t near, uint64_t zero, int count, F&& place) {
-  uint64_t lanes = __ballot(near != 0);
-  if (lanes == 0) return;
-  int zeros = __popcll(zero);
+// One element by a whole wave, U products of a lane under way; lane src has it
+template <int U>
+__device__ __forceinline__ void settle_one(const Corner& c, int m, int n, int src) {
+  const float *const pa = c.a + m * c.am, *const pb = c.b + n * c.bn;
+  const int lane = threadIdx.x & 63, K = (int)c.K;
+  double s = 0.0;
+  for (int k = lane; k - lane < K; k += 64 * U) {
+    float u[U], v[U];
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) zeros += __shfl_xor(zeros, off, 64);
-  if (3 * zeros > count) {
-    near &= ~zero;
-    lanes = __ballot(near != 0);
+    for (int j = 0; j < U; ++j) {   // past the end the last again, for nothing
+      const int at = min(k + 64 * j, K - 1);
+      u[j] = pa[at * c.ak];
+      v[j] = pb[at * c.bk];
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) s = fma((double)(k + 64 * j < K ? u[j] : 0.f), (double)v[j], s);
   }
-  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
+  if (lane == src) c.z[m * c.N + n] = (float)(c.bias ? s + (double)c.bias[n] : s);
+}
+// Each lane its own element, if it has one (any of the matrices' for the others)
+__device__ __forceinline__ void settle_each(const Corner& c, bool near, int m, int n) {
+  const float *pa = c.a + m * c.am, *pb = c.b + n * c.bn;
+  double s = 0.0;
+#pragma unroll 8
+  for (int k = 0; k < (int)c.K; ++k, pa += c.ak, pb += c.bk) s = fma((double)*pa, (double)*pb, s);
+  if (near) c.z[m * c.N + n] = (float)(c.bias ? s + (double)c.bias[n] : s);
+}
+// One element (m, n) a lane
+__device__ __forceinline__ void settle_wave(const Corner& c, bool near, int m, int n) {
+  uint64_t lanes = __ballot(near);
+  if (__popcll(lanes) > 16) {
+    settle_each(c, near, m, n);
+    return;
+  }
   for (; lanes != 0; lanes &= lanes - 1) {
     const int src = __builtin_ctzll(lanes);
-#pragma unroll 1
-    for (uint64_t bits = __shfl((unsigned long long)near, src, 64); bits != 0; bits &= bits - 1) {
-      int m, n;
-      place(__builtin_ctzll(bits), src, m, n);
-      const float *const pa = c.a + m * c.am, *const pb = c.b + n * c.bn;
-      const int K = (int)c.K;
-      double s = 0.0;
-      for (int k = lane; k - lane < K; k += 64 * U) {
-        float u[U], v[U];
+    settle_one<16>(c, __shfl(m, src, 64), __shfl(n, src, 64), src);
+  }
+}
+// All of a block of 32 x 32 from (m0, n0) on, in fp64 by the matrix cores
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void settle_block(const Corner& c, int64_t m0, int64_t n0) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4, K = (int)c.K;
+  const float *pa[2], *pb[2];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {   // past the end the last again, for nothing
-          const int at = min(k + 64 * j, K - 1);
-          u[j] = pa[at * c.ak];
-          v[j] = pb[at * c.bk];
-        }
+  for (int i = 0; i < 2; ++i) {   // past the end the last row and column again, for nothing
+    pa[i] = c.a + min(m0 + 16 * i + r, c.M - 1) * c.am;
+    pb[i] = c.b + min(n0 + 16 * i + r, c.N - 1) * c.bn;
+  }
+  f64x4 acc[2][2];
 #pragma unroll
-        for (int j = 0; j < U; ++j) s = fma((double)(k + 64 * j < K ? u[j] : 0.f), (double)v[j], s);
-      }
+  for (int i = 0; i < 4; ++i) acc[i / 2][i % 2] = f64x4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+  for (int k = q; k - q < K; k += 4) {
+    const int at = min(k, K - 1);
+    double u[2], v[2];
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
-      if (lane == src) c.z[m * c.N + n] = (float)(c.bias ? s + (double)c.bias[n] : s);
+    for (int i = 0; i < 2; ++i) {
+      const float x = pa[i][at * c.ak], y = pb[i][at * c.bk];
+      u[i] = k < K ? x : 0.f;
+      v[i] = k < K ? y : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc[i / 2][i % 2] = __builtin_amdgcn_mfma_f64_16x16x4f64(u[i / 2], v[i % 2], acc[i / 2][i % 2], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = n0 + 16 * (i % 2) + r;
+    if (n >= c.N) continue;
+    const double b = c.bias ? (double)c.bias[n] : 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t m = m0 + 16 * (i / 2) + 4 * j + q;
+      if (m < c.M) c.z[m * c.N + n] = (float)(acc[i / 2][i % 2][j] + b);
     }
   }
 }
@@ -109,7 +149,7 @@ struct GeneralArgs {
   Epilogue<T> e;
 };
 inline __device__ Corner corner_of(const GeneralArgs<float>& g) {
-  return {g.a, g.b, g.e.bias, g.e.z, g.am, g.ak, g.bk, g.bn, g.N, g.K};
+  return {g.a, g.b, g.e.bias, g.e.z, g.am, g.ak, g.bk, g.bn, g.M, g.N, g.K};
 }
 
 // One operand's part of a thread: H times 8 elements along the axis that is contiguous, 64 rows or
@@ -180,7 +220,7 @@ struct GeneralLd {
 };
 
 // H: tiles of 64 H, waves of 32 H; DEPTH steps' loads are under way (four where the registers of four
-// workgroups on a CU hold them: in fp32 three workgroups with four steps were no faster); CORNER: see settle
+// workgroups on a CU hold them: in fp32 three workgroups with four steps were no faster); CORNER: relu's
 template <typename T, int H, bool CORNER = false>
 __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<T> g) {
   constexpr int LD = gstage<T>::LD, TILE = 64 * H, DEPTH = H == 1 && sizeof(T) == 2 ? 4 : 2;
@@ -297,7 +337,7 @@ __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<
     }
     __syncthreads();
     const Corner c = corner_of(g);
-    uint64_t near = 0, zero = 0;
+    uint32_t near[H * H] = {};   // a bit for each of the lane's elements of a block of 32 x 32
 #pragma unroll
     for (int i = 0; i < H * H; ++i) {
       const int nl = wn + 32 * (i % H) + (lane & 31);
@@ -306,18 +346,34 @@ __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int ml = wm + 32 * (i / H) + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
-        const float z = acc[i / H][i % H][j] + b;
-        if (m0 + ml < g.M && corner_near(c, z, b, an[ml] * bn[nl])) {
-          near |= 1ull << (16 * i + j);
-          if (z == 0.f) zero |= 1ull << (16 * i + j);
+        if (m0 + ml < g.M && corner_near(c, acc[i / H][i % H][j] + b, b, an[ml] * bn[nl])) near[i] |= 1u << j;
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // what is formed again is written over
+#pragma unroll 1
+    for (int i = 0; i < H * H; ++i) {
+      uint32_t bits = near[0];
+#pragma unroll
+      for (int h = 1; h < H * H; ++h) bits = i == h ? near[h] : bits;
+      uint64_t lanes = __ballot(bits != 0);
+      if (lanes == 0) continue;
+      const int64_t mb = m0 + wm + 32 * (i / H), nb = n0 + wn + 32 * (i % H);
+      int count = __popc(bits);
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) count += __shfl_xor(count, off, 64);
+      if (count > 12) {   // (a block takes about as long as 12 elements)
+        settle_block(c, mb, nb);
+        continue;
+      }
+      for (; lanes != 0; lanes &= lanes - 1) {
+        const int src = __builtin_ctzll(lanes);
+#pragma unroll 1
+        for (uint32_t left = __shfl(bits, src, 64); left != 0; left &= left - 1) {
+          const int j = __builtin_ctz(left);
+          settle_one<4>(c, (int)mb + 8 * (j >> 2) + 4 * (src >> 5) + (j & 3), (int)nb + (src & 31), src);
         }
       }
     }
-    settle<4>(c, near, zero, 64 * 16 * H * H, [&](int bit, int src, int& m, int& n) {
-      const int i = bit >> 4, j = bit & 15;
-      m = (int)m0 + wm + 32 * (i / H) + 8 * (j >> 2) + 4 * (src >> 5) + (j & 3);
-      n = (int)n0 + wn + 32 * (i % H) + (src & 31);
-    });
   }
 }
 
@@ -360,11 +416,7 @@ __global__ __launch_bounds__(256) void k_linear_corner_join(GeneralArgs<float> g
   if (in) g.e.store(m, n, g.N, s);
   const Corner c = corner_of(g);
   const float b = c.bias ? c.bias[n] : 0.f, z = s + b;
-  const bool near = in && corner_near(c, z, b, qa * qb);
-  settle<16>(c, near, near && z == 0.f, 64, [&](int, int src, int& row, int& col) {
-    row = __shfl(m, src, 64);
-    col = __shfl(n, src, 64);
-  });
+  settle_wave(c, in && corner_near(c, z, b, qa * qb), m, n);
 }
 
 constexpr PlanCost kAny16[2] = {{128, 128, 2, 1.1, 0.6, 6.0, 5.0, 6.0}, {64, 64, 4, 0.8, 0.26, 3.0, 5.0, 6.0}};
@@ -413,7 +465,7 @@ hipError_t general(const char* name, const T* a, const T* b, int64_t am, int64_t
 // MB) takes 4.9 us, one after another 7.0; 4 x 4096 x 4096 (33.6 MB) 10.1 and 25.5.
 constexpr int FEW = 4, FT = 512, FC = 16;
 
-// U: rows of W under way; CORNER: see settle
+// U: rows of W under way; CORNER: relu's
 template <typename T, int ROWS, bool CORNER = false, int U = (sizeof(T) == 2 ? 8 : 4) * (ROWS == 1 ? 2 : 1)>
 __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, const T* __restrict__ w, int rows, int K, int N,
                                                    Epilogue<T> e) {
@@ -516,13 +568,9 @@ __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, cons
         qa += xred[q][min(t, ROWS - 1)];
         qb += red[q][ROWS][threadIdx.x % FC];
       }
-      const Corner c{x, w, e.bias, e.z, K, 1, N, 1, N, K};
+      const Corner c{x, w, e.bias, e.z, K, 1, N, 1, rows, N, K};
       const float b = in && e.bias ? e.bias[m] : 0.f, z = s + b;
-      const bool near = in && corner_near(c, z, b, qa * qb);
-      settle<16>(c, near, near && z == 0.f, 64, [&](int, int src, int& row, int& col) {
-        row = src / FC;
-        col = n0 + src % FC;
-      });
+      settle_wave(c, in && corner_near(c, z, b, qa * qb), min(t, rows - 1), min(m, N - 1));
     }
 }
 

@@ -136,3 +136,32 @@ def test_sign_of_z_replayed():
         torch.cuda.synchronize()
         for p, q in zip(want, (op.y, op.z, op.dx, op.dw, op.db)):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("kind", ["offset", "one-hot"])
+@pytest.mark.parametrize("size", [(2, 96, 130), (4, 1000, 40), (3, 70, 7), (64, 2048, 200), (40, 100, 1), (1003, 769, 333), (8185, 261, 1021)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_sums_that_cancel_in_bulk(size, kind):
+    """Rows far off 0 against columns without a mean, all of whose sums lie within the rounding, and rows with
+    two entries of W that differ by less than that: the matrices' other way to fp64."""
+    T, K, N = size
+    g = torch.Generator().manual_seed(T + K)
+    w = torch.randn(K, N, generator=g) / K ** 0.5
+    if kind == "offset":
+        x, w = 1000.0 + torch.randn(T, K, generator=g), w - w.mean(0, keepdim=True)
+    else:
+        w[1::2] = w[0:K - K % 2:2] + 1e-7 * torch.randn(K // 2, N, generator=g)
+        x = torch.zeros(T, K)
+        at = 2 * torch.randint(0, K // 2, (T,), generator=g)
+        x[torch.arange(T), at], x[torch.arange(T), at + 1] = 1.1, -1.1
+    x, w, dy = x.cuda(), w.cuda(), torch.randn(T, N, generator=g).cuda()
+    op = _op(T, K, N)
+    y = op.forward(x, w)
+    grads = op.backward(dy)
+    z = x.double() @ w.double()
+    assert torch.equal(op.z > 0, z > 0)
+    dz = torch.where(z > 0, dy.double(), 0.0)
+    xt = x.double().t().contiguous()
+    assert ((grads["dw"].double() - xt @ dz).abs() <= (T + 8) * U * (xt.abs() @ dz.abs()) + 1e-40).all()
+    assert ((y.double() - z.clamp(min=0)).abs() <= (K + 8) * U * (x.double().abs() @ w.double().abs())).all()
+    assert torch.equal(_op(T, K, N, train=False).forward(x, w), y)
