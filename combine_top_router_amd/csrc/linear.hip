@@ -24,7 +24,7 @@ namespace {
 // |b| + |x_k+1..K| |W_k+1..K| too; the two products together are |x| |W| at most, so the smaller is
 // (|x| |W| + |b|) / 2.  With K such roundings, taken as independent, 3 sqrt(K) of them are five standard deviations.
 // The squares of both norms are added up beside the products.  Ordinary data have one such z in ten thousand
-// or so; with all of it the forward of 1003 x 769 x 333 takes 18.8 us (16.5 without), of 8192 x 1024 x 2048 340 (313), of
+// or so; with all of it the forward of 1003 x 769 x 333 takes 18.8 us (16.5 without), of 8192 x 1024 x 2048 333 (312), of
 // one row of 2048 x 768 4.6 (4.1).  Where sums cancel in bulk (rows far off 0, one-hot rows and pruned weights),
 // whole blocks are formed again by the matrix cores in fp64 (8192 x 1024 x 2048 of nothing else: 1.4 ms).
 struct Corner {
@@ -35,10 +35,10 @@ struct Corner {
   int64_t am, ak, bk, bn, M, N, K;
 };
 
-// whether that z has to be formed again; b: its bias, sq: the product of the squared norms (3 2^-24 / 2 and 1 %
-// for the norms' own rounding)
-__device__ __forceinline__ bool corner_near(const Corner& c, float z, float b, float sq) {
-  const float bound = 0x1.84p-24f * sqrtf((float)c.K + 64.f) * (sqrtf(sq) + fabsf(b));
+// whether that z has to be formed again; b: its bias, norms: |x_t| |W_n| (3 2^-24 / 2 and 1 % for the norms'
+// own rounding; where their squares leave fp32's range, above 10^19 or below 10^-20, the sum stays)
+__device__ __forceinline__ bool corner_near(const Corner& c, float z, float b, float norms) {
+  const float bound = 0x1.84p-24f * sqrtf((float)c.K + 64.f) * (norms + fabsf(b));
   return fabsf(z) < bound && bound < __builtin_inff();
 }
 // One element by a whole wave, U products of a lane under way; lane src has it
@@ -326,8 +326,8 @@ __global__ __launch_bounds__(256, H == 2 ? 2 : 4) void k_linear_any(GeneralArgs<
         qa += an[tid + p * TILE];
         qb += bn[tid + p * TILE];
       }
-      an[tid] = qa;
-      bn[tid] = qb;
+      an[tid] = sqrtf(qa);
+      bn[tid] = sqrtf(qb);
     }
     if (g.part) {   // rows by the first workgroup along N, columns by the first along M
       float* const to = g.squares + blockIdx.z * (g.M + g.N);
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(256) void k_linear_corner_join(GeneralArgs<float> g
   if (in) g.e.store(m, n, g.N, s);
   const Corner c = corner_of(g);
   const float b = c.bias ? c.bias[n] : 0.f, z = s + b;
-  settle_wave(c, in && corner_near(c, z, b, qa * qb), m, n);
+  settle_wave(c, in && corner_near(c, z, b, sqrtf(qa) * sqrtf(qb)), m, n);
 }
 
 constexpr PlanCost kAny16[2] = {{128, 128, 2, 1.1, 0.6, 6.0, 5.0, 6.0}, {64, 64, 4, 0.8, 0.26, 3.0, 5.0, 6.0}};
@@ -430,7 +430,7 @@ size_t general_part_bytes(int64_t M, int64_t N, int64_t K, bool corner) {
   const int s = general_plan<T>(M, N, K).splits;
   return s == 1 ? 0 : (size_t)s * (M * N + (corner ? M + N : 0)) * 4;
 }
-// what settle is for
+// whether relu's slope is decided beside the product
 template <typename T>
 bool has_corner(const Epilogue<T>& e) { return sizeof(T) == 4 && e.act == MOE_ACT_RELU && e.z; }
 
@@ -570,7 +570,7 @@ __global__ __launch_bounds__(FT) void k_linear_few(const T* __restrict__ x, cons
       }
       const Corner c{x, w, e.bias, e.z, K, 1, N, 1, rows, N, K};
       const float b = in && e.bias ? e.bias[m] : 0.f, z = s + b;
-      settle_wave(c, in && corner_near(c, z, b, qa * qb), min(t, rows - 1), min(m, N - 1));
+      settle_wave(c, in && corner_near(c, z, b, sqrtf(qa) * sqrtf(qb)), min(t, rows - 1), min(m, N - 1));
     }
 }
 

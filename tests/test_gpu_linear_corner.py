@@ -165,3 +165,15 @@ def test_sums_that_cancel_in_bulk(size, kind):
     assert ((grads["dw"].double() - xt @ dz).abs() <= (T + 8) * U * (xt.abs() @ dz.abs()) + 1e-40).all()
     assert ((y.double() - z.clamp(min=0)).abs() <= (K + 8) * U * (x.double().abs() @ w.double().abs())).all()
     assert torch.equal(_op(T, K, N, train=False).forward(x, w), y)
+
+
+@pytest.mark.parametrize("size", [(2, 96, 130), (64, 2048, 200), (1003, 769, 333)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("sx,sw", [(2.0 ** -50, 2.0 ** -50), (2.0 ** 50, 2.0 ** 50), (2.0 ** -40, 2.0 ** 60)])
+def test_sign_of_z_of_other_sizes(size, sx, sw):
+    """The same data times powers of two, of which the products of the squares leave fp32's range: the same signs."""
+    T, K, N = size
+    x, w, _, dy = _inputs(T, K, N, False, 5)
+    op = _op(T, K, N)
+    op.forward(x * sx, w * sw)
+    z = x.double() @ w.double()
+    assert torch.equal(op.z > 0, z > 0)
