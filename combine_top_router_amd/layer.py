@@ -502,7 +502,8 @@ class MoeLayer:
 
     ``gate``: a ``Gate`` of the same T, E and k routes in place of the softmax of the logits (and
     of ``renorm``); ``forward`` then takes its bias, its mask and ``count``, and tokens that the
-    mask leaves out get y = 0.  A gate is one layer's: the backward reads what it holds.
+    mask leaves out get y = 0.  ``balance`` has its own mask: without it such tokens' logits count
+    in the loss.  A gate is one layer's: the backward reads what it holds.
     """
 
     def __init__(self, T, H, I, E, k, e_begin=0, e_local=None, dtype=L.MOE_BF16, bwd=L.MOE_BWD_SAME,
